@@ -283,6 +283,203 @@ int gbtopk_varlen_static_ws(const void *logits, int dtype, int64_t num_rows, int
                             int32_t *out_indices, void *out_values, int deterministic,
                             void *stream);
 
+/* ------------------------------------------------------------------------
+ * The decode step after the selection: attention over a paged key/value
+ * cache, the weight each cached position accumulates, eviction by it, and
+ * the verification of drafted tokens.
+ *
+ * Shared conventions (those of the calls above): row r belongs to request
+ * i = r / next_n as its drafted token t = r % next_n, and seq_lens[i] counts
+ * the next_n newest tokens too, whose keys and values are in the cache
+ * already.  Position p of request i lies in cache slot
+ *     page_table[i, p / page_size] * page_size + p % page_size,
+ * the slot numbers that gbtopk_page_table_transform writes.  A position
+ * whose page-table column is >= pt_cols, whose page id is negative or whose
+ * slot is >= num_slots does not exist: it is never read or written.
+ * Row r sees position p when p < ctx, ctx = seq_lens[i] - next_n (the
+ * context), or when bit p - ctx of its tree mask is set: tree_mask[r] has
+ * bit j set when drafted token j is token t itself or one of its ancestors
+ * (or any other set the caller wants seen).  tree_mask NULL is a chain: row
+ * t sees tokens 0 .. t.
+ *
+ * The cache holds one key and one value row of head_dim elements for each
+ * (slot, kv head), with any slot and head strides (in elements) that are
+ * multiples of 8; bases 16-byte aligned (GBTOPK_EALIGN).  Query head h reads
+ * kv head h / (q_heads / kv_heads).  dtype is GBTOPK_BF16 or GBTOPK_F16 for
+ * queries, cache and output alike; head_dim is a multiple of 8, 8 .. 256;
+ * next_n is 1 .. 64; q_heads is a multiple of kv_heads (others:
+ * GBTOPK_EUNSUPPORTED for the dtype and the sizes, GBTOPK_EINVAL for the
+ * grouping).
+ */
+
+#define GBTOPK_MAX_NEXT_N 64    /* drafted tokens of a request (bits of a tree mask) */
+#define GBTOPK_MAX_HEAD_DIM 256
+
+/*
+ * gbtopk_tree_attention — attention of drafted tokens over a paged cache:
+ *     s(r,h,p) = scale * <q[r,h], k[slot(i,p), h / group]>  over visible p,
+ *     lse[r,h] = log sum_p exp s,   out[r,h] = sum_p exp(s - lse) v[slot(i,p)].
+ * A row that sees nothing gives zeros and lse = -infinity.  Keys and values
+ * of positions that no row of the request sees are not used, whatever they
+ * hold; those of a drafted token that some rows see and others do not have
+ * to be finite.
+ *
+ *  q            device [num_rows, q_heads, head_dim], inner stride 1, row and
+ *               head strides multiples of 8, 16-byte aligned.
+ *  page_table   device int32 [num_rows / next_n, pt_cols], row stride
+ *               pt_row_stride.
+ *  seq_lens     device int32 [num_rows / next_n].
+ *  tree_mask    device uint64 [num_rows] (as int64) or NULL.
+ *  out          device [num_rows, q_heads, head_dim], contiguous, 16-byte
+ *               aligned.
+ *  lse          device fp32 [num_rows, q_heads] or NULL.
+ *  workspace    as for gbtopk_varlen, gbtopk_attention_workspace_bytes(...)
+ *               bytes; its status word reports bounded waits that gave up
+ *               (bit 1: outputs not reliable).
+ */
+int gbtopk_tree_attention(const void *q, int dtype, int64_t num_rows, int64_t q_row_stride,
+                          int64_t q_head_stride, int32_t q_heads, int32_t kv_heads,
+                          int32_t head_dim, const void *k_cache, int64_t k_slot_stride,
+                          int64_t k_head_stride, const void *v_cache, int64_t v_slot_stride,
+                          int64_t v_head_stride, int64_t num_slots, const int32_t *page_table,
+                          int64_t pt_cols, int64_t pt_row_stride, int32_t page_size,
+                          const int32_t *seq_lens, int32_t next_n, const int64_t *tree_mask,
+                          float scale, void *out, float *lse, void *workspace,
+                          size_t workspace_bytes, void *stream);
+
+/*
+ * gbtopk_selected_attention — the same attention over a list of slots for
+ * each row: indices device int32 [num_rows, top_k] with row stride
+ * idx_row_stride, as gbtopk_page_table_transform writes them.  Entries < 0
+ * or >= num_slots are skipped wherever they stand; a slot listed twice
+ * counts twice.
+ */
+int gbtopk_selected_attention(const void *q, int dtype, int64_t num_rows, int64_t q_row_stride,
+                              int64_t q_head_stride, int32_t q_heads, int32_t kv_heads,
+                              int32_t head_dim, const void *k_cache, int64_t k_slot_stride,
+                              int64_t k_head_stride, const void *v_cache, int64_t v_slot_stride,
+                              int64_t v_head_stride, int64_t num_slots, const int32_t *indices,
+                              int64_t top_k, int64_t idx_row_stride, float scale, void *out,
+                              float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Scratch of the two attention calls (a pure function; 0 for invalid sizes). */
+size_t gbtopk_attention_workspace_bytes(int64_t num_rows, int32_t q_heads, int32_t kv_heads,
+                                        int32_t head_dim);
+
+/*
+ * gbtopk_cache_weights — adds to weights[i, w, p] the attention probability
+ * that the request's rows gave position p:
+ *     weights[i, w, p] += sum_{t, h} exp(s(r,h,p) - lse[r,h])
+ * over the rows t whose bit in accept_mask[i] is set (all rows when it is
+ * NULL) that see p, and over the query heads h of kv head w (weight_heads ==
+ * kv_heads) or all query heads (weight_heads == 1).  A row with lse =
+ * -infinity adds nothing.  Positions >= width are not counted.  The sum
+ * over rows and heads of one position has a fixed order.
+ *
+ *  lse          device fp32 [num_rows, q_heads]: gbtopk_tree_attention's.
+ *  accept_mask  device uint64 [num_rows / next_n] (as int64) or NULL.
+ *  weights      device fp32 [num_rows / next_n, weight_heads, width],
+ *               contiguous; updated in place.
+ */
+int gbtopk_cache_weights(const void *q, int dtype, int64_t num_rows, int64_t q_row_stride,
+                         int64_t q_head_stride, int32_t q_heads, int32_t kv_heads,
+                         int32_t head_dim, const void *k_cache, int64_t k_slot_stride,
+                         int64_t k_head_stride, int64_t num_slots, const float *lse,
+                         const int32_t *page_table, int64_t pt_cols, int64_t pt_row_stride,
+                         int32_t page_size, const int32_t *seq_lens, int32_t next_n,
+                         const int64_t *tree_mask, const int64_t *accept_mask, float scale,
+                         float *weights, int32_t weight_heads, int64_t width, void *workspace,
+                         size_t workspace_bytes, void *stream);
+
+/*
+ * gbtopk_cache_evict — keeps the positions of each request that carry the
+ * most weight and packs their keys and values, in order, into new pages.
+ *
+ * The survivors of request i are its positions p < min(seq_lens[i], width,
+ * pt_cols * page_size); with accept_mask, of the last next_n positions only
+ * the drafted tokens whose bit is set (the accepted path).  When more than
+ * `budget` survive, the last min(recent, budget) of them are kept and, of
+ * the others, those with the largest weight (ties: the lowest position) up
+ * to the budget.  The kept positions in ascending order become positions
+ * 0, 1, ... of out_page_table.  weight_heads == kv_heads makes the choice
+ * for each kv head by itself, weight_heads == 1 one choice for all.
+ *
+ *  weights      device fp32 [num_requests, weight_heads, width], contiguous;
+ *               ranked by float order (-0 equals +0; NaN order unspecified).
+ *  k_cache, v_cache  read at the pages of page_table and written at those of
+ *               out_page_table, which must not share a slot with any page
+ *               that page_table lists (pages of the source may be shared by
+ *               requests).  elem_bytes 2 or 4; head_dim * elem_bytes, the
+ *               strides' bytes and the bases multiples of 16 bytes.  A kept
+ *               position without a source slot is written as zeros; one
+ *               without a destination slot is not written.
+ *  out_page_table  device int32 [num_requests, out_pt_cols], out_pt_cols *
+ *               page_size >= budget.
+ *  kept         device int32 [num_requests, weight_heads, budget]: the kept
+ *               positions, padded with -1.
+ *  new_lens     device int32 [num_requests]: positions kept.
+ *  out_weights  device fp32 like weights, not overlapping it: the kept
+ *               positions' weights, zeros behind them.
+ */
+int gbtopk_cache_evict(const float *weights, int64_t num_requests, int32_t weight_heads,
+                       int64_t width, const int32_t *seq_lens, int32_t next_n,
+                       const int64_t *accept_mask, int32_t budget, int32_t recent, void *k_cache,
+                       int64_t k_slot_stride, int64_t k_head_stride, void *v_cache,
+                       int64_t v_slot_stride, int64_t v_head_stride, int64_t num_slots,
+                       int32_t kv_heads, int32_t head_dim, int32_t elem_bytes,
+                       const int32_t *page_table, int64_t pt_cols, int64_t pt_row_stride,
+                       const int32_t *out_page_table, int64_t out_pt_cols,
+                       int64_t out_pt_row_stride, int32_t page_size, int32_t *kept,
+                       int32_t *new_lens, float *out_weights, void *stream);
+
+/*
+ * gbtopk_verify_drafts — verifies a request's drafted tokens against the
+ * target model's distributions, losslessly, from given random numbers.
+ *
+ * Row n of request i is node n of its draft tree; node 0 is the last token
+ * already decided and logits row n is the target's distribution after node
+ * n: p_n = softmax(logits[n] / temperature[i]), or, where the temperature is
+ * <= 0, one at the largest logit (lowest index) and zero elsewhere.  The
+ * parent of node n is the highest bit below n of tree_mask[n] (NULL: n - 1);
+ * a node without one cannot be reached.  From node 0 the children c of the
+ * current node are tried in order:
+ *   draft_probs NULL:  accept when u_c * m < p(x_c), with m = 1 - the p of
+ *                      the children refused before (a token refused before
+ *                      has p = 0);
+ *   draft_probs given: accept when u_c * q(x_c) < p(x_c), q = row of the
+ *                      current node (what its child was drawn from; chains
+ *                      only: tree_mask must be NULL).
+ * The accepted child becomes the current node; where none is, the next token
+ * is argmax_v rest(v) / noise[i, v] (lowest index), which draws from rest
+ * when noise is standard exponential: rest is p without the refused tokens,
+ * or max(p - q, 0) after a refusal under draft_probs, or p.  -1 where rest
+ * is zero everywhere.  A token outside [0, vocab) is never accepted.
+ *
+ *  logits       device [num_rows, vocab] of dtype (any of the three), row
+ *               stride row_stride.  Logits of -infinity have p = 0.
+ *  tokens       device int32 [num_rows]; node 0's is not read.
+ *  uniforms     device fp32 [num_rows] in [0, 1); node 0's is not read.
+ *  noise        device fp32 [num_requests, vocab], positive, contiguous.
+ *  temperature  device fp32 [num_requests] or NULL (1).
+ *  draft_probs  device fp32 [num_rows, vocab], contiguous, or NULL.
+ *  accepted     device int32 [num_requests]: drafted tokens accepted.
+ *  path         device int32 [num_rows]: the nodes from 0 to the last
+ *               accepted, padded with -1.
+ *  next_token   device int32 [num_requests].
+ *  accept_mask  device uint64 [num_requests] (as int64): the path's bits, for
+ *               gbtopk_cache_weights and gbtopk_cache_evict.
+ *  workspace    gbtopk_verify_workspace_bytes(...) bytes, as for gbtopk_varlen.
+ */
+int gbtopk_verify_drafts(const void *logits, int dtype, int64_t num_rows, int64_t vocab,
+                         int64_t row_stride, const int32_t *tokens, const float *uniforms,
+                         const float *noise, int32_t next_n, const int64_t *tree_mask,
+                         const float *temperature, const float *draft_probs, int32_t *accepted,
+                         int32_t *path, int32_t *next_token, int64_t *accept_mask,
+                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* Scratch of gbtopk_verify_drafts (a pure function; 0 for invalid sizes). */
+size_t gbtopk_verify_workspace_bytes(int64_t num_rows, int64_t vocab, int32_t next_n);
+
 /* Human-readable name of a status code (static string).  The pages define no
  * such call; the codes follow the error cases of the FlashInfer
  * `top_k_varlen` page ("Raises") and the status convention above. */

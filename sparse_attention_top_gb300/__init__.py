@@ -11,6 +11,11 @@ Low-level entry points keep the C names (``gbtopk_varlen``,
 ``top_k_varlen`` and ``top_k_page_table_transform`` follow the Python
 signatures of the FlashInfer ``top_k_varlen`` page and of the compact
 page-table API quoted on the SGLang PR #33237 page.
+
+``decode`` holds the rest of a speculative decode step over the same paged
+cache (``tree_attention``, ``selected_attention``,
+``accumulate_cache_weights``, ``evict_cache``, ``verify_drafts``); its names
+are exported here too.
 """
 from __future__ import annotations
 
@@ -419,3 +424,9 @@ def top_k_page_table_transform_cu_seqlens(scores: torch.Tensor, lengths: torch.T
     gbtopk_page_table_transform_cu_seqlens(scores, lengths, row_starts, page_table, cu_seqlens_q,
                                            top_k, o, flags, ws)
     return o
+
+
+from . import decode  # noqa: E402
+from .decode import *  # noqa: E402,F401,F403
+
+__all__ += ["decode", *decode.__all__]

@@ -1,6 +1,6 @@
 """Builds the gbtopk shared library in-tree for sm_103a with nvcc.
 
-The two translation units are compiled in parallel and linked into
+The translation units are compiled in parallel and linked into
 ``sparse_attention_top_gb300/libgbtopk.so`` (CUDA runtime linked statically).
 """
 from __future__ import annotations
@@ -16,7 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgbtopk.so")
-SOURCES = ["gbtopk_api.cu", "gbtopk_kernels.cu", "gbtopk_static_ws.cu"]
+SOURCES = ["gbtopk_api.cu", "gbtopk_kernels.cu", "gbtopk_static_ws.cu", "gbtopk_attention.cu",
+           "gbtopk_cache.cu", "gbtopk_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

@@ -1,0 +1,111 @@
+// Shared by the decode-step kernels (gbtopk_attention.cu, gbtopk_cache.cu,
+// gbtopk_verify.cu): the paged cache's address arithmetic, 16-bit element
+// conversions, launch helpers and argument checks.  Not part of the ABI.
+#pragma once
+
+#include <cstddef>
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "gbtopk.h"
+#include "gbtopk_internal.h"
+
+namespace gbtopk {
+
+// Unsigned division by a launch-constant divisor: q = (x * mul) >> (32 +
+// shift) for 0 <= x < 2^31, with mul = ceil(2^(32+shift) / d) and shift =
+// ceil(log2 d) - 1 (Granlund and Montgomery, "Division by invariant integers
+// using multiplication", 1994): the rounding of mul adds less than x / 2^31
+// of 1/d, so the quotient is exact.  d = 1 uses mul = 0 (the identity).
+struct FastDiv {
+    uint32_t d, mul, shift;
+    __host__ void init(uint32_t divisor) {
+        d = divisor;
+        mul = 0;
+        shift = 0;
+        if (divisor > 1) {
+            uint32_t l = 0;
+            while ((1ull << l) < divisor) ++l;
+            shift = l - 1;
+            mul = static_cast<uint32_t>(((1ull << (32 + shift)) + divisor - 1) / divisor);
+        }
+    }
+    __device__ __forceinline__ uint32_t div(uint32_t x) const {
+        return mul ? __umulhi(x, mul) >> shift : x;
+    }
+};
+
+// The page table of a batch of requests over one cache.
+struct Paging {
+    const int32_t *table;
+    int64_t cols, row_stride;
+    int64_t num_slots;
+    FastDiv page;
+
+    // Cache slot of position p of request i, or -1 where there is none.
+    __device__ __forceinline__ int64_t slot(int64_t i, int32_t p) const {
+        const uint32_t c = page.div(static_cast<uint32_t>(p));
+        if (p < 0 || static_cast<int64_t>(c) >= cols) return -1;
+        const int64_t id = __ldg(table + i * row_stride + c);
+        const int64_t s = id * page.d + (static_cast<uint32_t>(p) - c * page.d);
+        return id >= 0 && s < num_slots ? s : -1;
+    }
+};
+
+template <bool BF16>
+struct Half2 {
+    using T = __nv_bfloat16;
+    __device__ __forceinline__ static float2 up(uint32_t v) {
+        return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    }
+    __device__ __forceinline__ static uint32_t down(float lo, float hi) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+};
+
+template <>
+struct Half2<false> {
+    using T = __half;
+    __device__ __forceinline__ static float2 up(uint32_t v) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&v));
+    }
+    __device__ __forceinline__ static uint32_t down(float lo, float hi) {
+        const __half2 h = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t *>(&h);
+    }
+};
+
+__device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void pdl_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Launch as a programmatic dependent of the stream's previous kernel: the
+// launch overlaps its tail, and the kernel waits (pdl_wait) before it reads
+// anything.
+template <typename... A, typename... B>
+cudaError_t launch_pdl(void (*kernel)(A...), dim3 grid, int threads, size_t smem, cudaStream_t stream,
+                       int cluster, B... args) {
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+inline bool multiple_of(int64_t v, int64_t a) { return v % a == 0; }
+
+}  // namespace gbtopk
