@@ -17,7 +17,7 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgbtopk.so")
 SOURCES = ["gbtopk_api.cu", "gbtopk_kernels.cu", "gbtopk_static_ws.cu", "gbtopk_attention.cu",
-           "gbtopk_cache.cu", "gbtopk_verify.cu"]
+           "gbtopk_weights.cu", "gbtopk_cache.cu", "gbtopk_verify.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

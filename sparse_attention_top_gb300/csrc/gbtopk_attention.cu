@@ -1,205 +1,489 @@
-// Attention of drafted tokens over a paged cache (gbtopk_tree_attention),
-// over selected slots (gbtopk_selected_attention), and the weight each
-// cached position accumulates (gbtopk_cache_weights).
-#include "gbtopk_decode.cuh"
+// Attention of drafted tokens over a paged cache (gbtopk_tree_attention) and
+// over selected slots (gbtopk_selected_attention).
+//
+// The rows that share a cached head - next_n tokens x the query heads of the
+// group - are the rows of one matrix tile, so each cached key and value is
+// read once for all of them.  Per tile of KT cached positions:
+//     S = Q K^T (tensor core, 32-bit accumulator in tensor memory),
+//     P = 2^(c S - m), the running maximum m and sum l in registers,
+//     O += P V (P from tensor memory, O stays there),
+// O being rescaled only when m rises by more than 8 (base 2).  The work of a
+// call is the list of all (request, kv head, row tile, position tile); block
+// c of a grid of one block per SM takes the c-th equal share of that list
+// whatever the lengths are, and a unit (request, head, row tile) that spans
+// blocks leaves partial O, m, l in the workspace for combine_kernel.
+//
+// A block: W warpgroups of softmax (one row a thread), a warpgroup whose first
+// warp issues the matrix products, a warpgroup that copies keys and values
+// from their pages (cp.async, 16 bytes a lane, any page size and stride) into
+// a ring of tiles.  Copies run ahead of the products by the whole ring.
+#include <cfloat>
+#include <cmath>
+
+#include "gbtopk_paged.cuh"
 
 namespace gbtopk {
 namespace {
 
-struct AttnParams {
-    const void *q, *k, *v;
-    int64_t q_row, q_head, k_slot, k_head, v_slot, v_head;
-    Paging pages;
-    const int32_t *seq_lens;     // null: selected slots
-    const int64_t *tree_mask;
-    const int64_t *accept_mask;
-    const int32_t *indices;
-    int64_t top_k, idx_row;
-    int64_t num_rows;
-    int32_t next_n, q_heads, kv_heads, dim;
-    float scale;
-    void *out;
-    float *lse;
-    const float *lse_in;
-    float *weights;
-    int32_t weight_heads;
-    int64_t width;
+constexpr int kMaxGrid = 160;       // blocks of the attention kernel (workspace bound)
+constexpr int kMaskRing = 8;        // tiles whose validity bits are kept (see attention_kernel)
+constexpr float kRescale = 8.f;     // rise of the running maximum (base 2) that rescales O
+
+template <int DP, int W>
+struct Shape {
+    static constexpr int KT = DP == 256 ? 64 : 128;         // positions a tile
+    static constexpr int kRows = 128 * W;                   // query rows a unit
+    static constexpr int kThreads = 128 * W + 256;
+    // registers a thread: what the launch gives each, and its split (a
+    // softmax row keeps its KT scores in registers)
+    static constexpr int kLaunchRegs = W == 2 ? 128 : 168;
+    static constexpr int kSoftmaxRegs = W == 2 ? 176 : 240, kOtherRegs = W == 2 ? 80 : 128;
+    static_assert(W * kSoftmaxRegs + 2 * kOtherRegs <= (W + 2) * kLaunchRegs, "register pool");
+    static constexpr int kStageBytes = KT * DP * 2;
+    static constexpr int kQBytes = kRows * DP * 2;
+    static constexpr int kFixed = 2048;                     // barriers, masks, scan scratch
+    static constexpr int kFit = (static_cast<int>(kMaxSmemBytes) - 1024 - kFixed - kQBytes) / kStageBytes;
+    static constexpr int kStages = kFit < 12 ? kFit : 12;   // half of it + 2 tiles fit the mask ring
+    static constexpr size_t kSmem = 1024 + kFixed + kQBytes + static_cast<size_t>(kStages) * kStageBytes;
+    static constexpr uint32_t kS = 0, kO = 2 * KT;          // tensor memory columns
+    static_assert(kO + W * DP <= 512, "tensor memory");
+    static_assert(kStages >= 4 && kStages / 2 + 2 <= kMaskRing, "ring");
 };
 
-// Positions a row may see: [0, n), slot() < 0 where it sees none.
-template <bool SELECTED>
-struct Row {
-    const AttnParams &p;
-    int64_t r, i;
-    int32_t ctx, n;
-    uint64_t tree;
-    __device__ Row(const AttnParams &p, int64_t r) : p(p), r(r) {
-        if constexpr (SELECTED) {
-            n = static_cast<int32_t>(p.top_k);
-        } else {
-            i = r / p.next_n;
-            const int t = static_cast<int>(r - i * p.next_n);
-            const int64_t len = p.seq_lens[i] > 0 ? p.seq_lens[i] : 0;
-            ctx = static_cast<int32_t>(len - p.next_n);
-            const int64_t room = p.pages.cols * p.pages.page.d;
-            n = static_cast<int32_t>(len < room ? len : room);
-            tree = p.tree_mask ? static_cast<uint64_t>(p.tree_mask[r]) : (~0ull >> (63 - t));
-        }
-    }
-    __device__ int64_t slot(int32_t pos) const {
-        if constexpr (SELECTED) {
-            const int32_t s = p.indices[r * p.idx_row + pos];
-            return s < p.pages.num_slots ? s : -1;
-        } else {
-            if (pos >= ctx && !((tree >> (pos - ctx)) & 1)) return -1;
-            return p.pages.slot(i, pos);
-        }
-    }
+struct Shared {
+    uint64_t full[12], empty[12];   // ring stages: K and V of a tile alternate
+    uint64_t mask_full[kMaskRing];  // validity bits written
+    uint64_t q_full, q_empty;
+    uint64_t s_full[2];             // S of a job is in tensor memory
+    uint64_t p_full[2];             // P of a job is
+    uint64_t pv_done[2];            // O holds the job's product
+    uint64_t drain;
+    uint32_t mask[kMaskRing][4];
+    ScanScratch scan;
+    uint32_t tmem;
+    uint32_t abort;
 };
+static_assert(sizeof(Shared) <= 2048, "shared block");
 
-template <bool BF16>
-__device__ float dot(const float *q, const uint4 *k, int dim) {
-    float s = 0;
-    for (int c = 0; c < dim / 8; ++c) {
-        const uint4 x = k[c];
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = Half2<BF16>::up(w[j]);
-            s = fmaf(f.x, q[c * 8 + 2 * j], s);
-            s = fmaf(f.y, q[c * 8 + 2 * j + 1], s);
+template <bool BF16, int DP, int W>
+__global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(const __grid_constant__ AttnParams p) {
+    using Sh = Shape<DP, W>;
+    constexpr int KT = Sh::KT;
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    Shared &sh = *reinterpret_cast<Shared *>(smem + Sh::kQBytes + Sh::kStages * Sh::kStageBytes);
+    const uint32_t q_smem = smem_addr(smem), ring = q_smem + Sh::kQBytes;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kMmaWarp = 4 * W;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Sh::kStages; ++i) {
+            bar_init(&sh.full[i], 128);
+            bar_init(&sh.empty[i], 1);
         }
+        for (int i = 0; i < kMaskRing; ++i) bar_init(&sh.mask_full[i], 4);
+        bar_init(&sh.q_full, 128);
+        bar_init(&sh.q_empty, 1);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&sh.s_full[i], 1);
+            bar_init(&sh.p_full[i], 4);
+            bar_init(&sh.pv_done[i], 1);
+        }
+        bar_init(&sh.drain, 1);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    return s;
-}
-
-__device__ float block_max(float v, float *red) {
-    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(~0u, v, o));
+    if (warp == kMmaWarp) tmem_alloc(&sh.tmem, 512);
+    tc_fence_before();
     __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    return fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-}
-__device__ float block_sum(float v, float *red) {
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(~0u, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    return (red[0] + red[1]) + (red[2] + red[3]);
-}
-
-// One block of 128 threads for each (row, query head): 128 positions at a
-// time, their scores by one thread each, then each thread sums two columns
-// of the values.
-template <bool BF16, bool SELECTED>
-__global__ void __launch_bounds__(128) attention_kernel(AttnParams p) {
-    using T = typename Half2<BF16>::T;
-    __shared__ float q[GBTOPK_MAX_HEAD_DIM], prob[128], red[4];
-    __shared__ int64_t where[128];
+    tc_fence_after();
     pdl_wait();
-    const int64_t r = blockIdx.x;
-    const int h = blockIdx.y, g = h / (p.q_heads / p.kv_heads);
-    for (int d = threadIdx.x; d < p.dim; d += 128)
-        q[d] = static_cast<float>(static_cast<const T *>(p.q)[r * p.q_row + h * p.q_head + d]);
-    const Row<SELECTED> row(p, r);
-    float m = -INFINITY, l = 0, o[2] = {0, 0};
-    for (int32_t p0 = 0; p0 < row.n; p0 += 128) {
-        __syncthreads();
-        const int32_t pos = p0 + static_cast<int32_t>(threadIdx.x);
-        const int64_t slot = pos < row.n ? row.slot(pos) : -1;
-        const float s = slot < 0 ? -INFINITY
-                                 : p.scale * dot<BF16>(q, reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k) +
-                                                                                          slot * p.k_slot + g * p.k_head),
-                                                       p.dim);
-        const float top = fmaxf(m, block_max(s, red));
-        if (top == -INFINITY) continue;
-        const float e = expf(s - top), f = expf(m - top);
-        prob[threadIdx.x] = e;
-        where[threadIdx.x] = slot;
-        l = l * f + block_sum(e, red);
-        m = top;
-        for (int c = 0; c < 2; ++c) {
-            const int d = static_cast<int>(threadIdx.x) + 128 * c;
-            if (d >= p.dim) break;
-            float a = o[c] * f;
-            for (int j = 0; j < 128; ++j)
-                if (where[j] >= 0)
-                    a += prob[j] * static_cast<float>(static_cast<const T *>(p.v)[where[j] * p.v_slot + g * p.v_head + d]);
-            o[c] = a;
+    pdl_release();
+
+    const Share share = block_share<KT, Sh::kThreads>(p, &sh.scan);
+    volatile uint32_t *abort = &sh.abort;
+    const uint32_t tmem = sh.tmem;
+    Walk<KT> walk(p, share);
+    const int32_t rows = p.next_n * p.group;   // of a (request, kv head)
+    const int32_t chunks = (p.dim + 15) / 16 * 2, loaded = p.dim / 8;
+
+    if (warp >= kMmaWarp + 4) {
+        // ------------------------------------------------ copies
+        regs_down<Sh::kOtherRegs>();
+        const int w = warp - kMmaWarp - 4;
+        const uint8_t *kb = static_cast<const uint8_t *>(p.k), *vb = static_cast<const uint8_t *>(p.v);
+        const int64_t k_bytes = p.k_slot * 2, v_bytes = p.v_slot * 2;
+        int32_t last_b = -1;
+        uint64_t seen = ~0ull;   // drafted tokens that some row of the request sees
+        // slot of this lane's row of tile t of unit u (KT / 4 rows a warp), -1 where there is none
+        auto slot_of = [&](const Unit &u, int32_t t) -> int32_t {
+            if (u.b != last_b) {
+                last_b = u.b;
+                if (p.seq_lens && p.tree_mask) {
+                    const int64_t *tm = p.tree_mask + static_cast<int64_t>(u.b) * p.next_n;
+                    uint64_t m = lane < p.next_n ? static_cast<uint64_t>(__ldg(tm + lane)) : 0;
+                    if (lane + 32 < p.next_n) m |= static_cast<uint64_t>(__ldg(tm + lane + 32));
+                    seen = static_cast<uint64_t>(__reduce_or_sync(~0u, static_cast<uint32_t>(m >> 32))) << 32 |
+                           __reduce_or_sync(~0u, static_cast<uint32_t>(m));
+                }
+            }
+            const int32_t pos = t * KT + w * (KT / 4) + (lane & (KT / 4 - 1));
+            if (pos >= u.span.n) return -1;
+            if (!p.seq_lens) {
+                const int32_t s = __ldg(p.indices + u.b * p.idx_row + pos);
+                return s < p.pages.num_slots ? s : -1;
+            }
+            if (pos >= u.span.ctx && !((seen >> (pos - u.span.ctx)) & 1)) return -1;
+            return static_cast<int32_t>(p.pages.slot(u.b, pos));
+        };
+        uint32_t unit = 0, g = 0, tile = 0;   // counters of units, ring stages and tiles
+        uint32_t stage = 0, lap = 0;
+        bool ok = true;
+        Walk<KT> ahead = walk;                // the tile after the one being copied
+        int32_t ahead_t = ahead.more() ? ahead.u.t0 : 0;
+        int32_t next_slot = ahead.more() ? slot_of(ahead.u, ahead_t) : -1;
+        for (; walk.more() && ok; walk.next(), ++unit) {
+            const Unit u = walk.u;
+            const int32_t h = u.hm / p.row_tiles, r0 = (u.hm - h * p.row_tiles) * Sh::kRows;
+            // the unit's queries
+            if (unit > 0) ok = __all_sync(~0u, bar_wait(&sh.q_empty, (unit - 1) & 1, abort));
+            if (!ok) break;
+            for (int x = w * 32 + lane; x < Sh::kRows * chunks; x += 128) {
+                const int32_t r = x / chunks, c = x - r * chunks, rho = r0 + r;
+                if (rho >= rows) break;
+                const int32_t t = rho / p.group, gq = rho - t * p.group;
+                const uint8_t *src = static_cast<const uint8_t *>(p.q) +
+                                     2 * ((static_cast<int64_t>(u.b) * p.next_n + t) * p.q_row + (h * p.group + gq) * p.q_head);
+                copy16(q_smem + tile_offset(Sh::kRows, r, c), c < loaded ? src + c * 16 : src, c < loaded ? 16u : 0u);
+            }
+            bar_arrive_copies(&sh.q_full);
+            for (int32_t t = u.t0; t < u.t1; ++t, ++tile) {
+                const int32_t slot = next_slot;
+                if (++ahead_t == ahead.u.t1) {
+                    ahead.next();
+                    ahead_t = ahead.more() ? ahead.u.t0 : 0;
+                }
+                next_slot = ahead.more() ? slot_of(ahead.u, ahead_t) : -1;
+                for (int kv = 0; kv < 2; ++kv, ++g) {
+                    if (g >= Sh::kStages) ok = __all_sync(~0u, bar_wait(&sh.empty[stage], (lap - 1) & 1, abort));
+                    if (!ok) break;
+                    if (kv == 0) {
+                        const uint32_t valid = __ballot_sync(~0u, slot >= 0);
+                        if (lane == 0) {
+                            if constexpr (KT == 128) sh.mask[tile % kMaskRing][w] = valid;
+                            else reinterpret_cast<uint16_t *>(sh.mask[tile % kMaskRing])[w] = static_cast<uint16_t>(valid);
+                            bar_arrive(&sh.mask_full[tile % kMaskRing]);
+                        }
+                    }
+                    copy_tile<DP, KT>(ring + stage * Sh::kStageBytes, (kv ? vb + 2 * h * p.v_head : kb + 2 * h * p.k_head),
+                                      kv ? v_bytes : k_bytes, slot, chunks, loaded, w, lane);
+                    bar_arrive_copies(&sh.full[stage]);
+                    if (++stage == Sh::kStages) {
+                        stage = 0;
+                        ++lap;
+                    }
+                }
+                if (!ok) break;
+            }
+        }
+        copies_land();
+    } else if (warp >= kMmaWarp) {
+        // ------------------------------------------------ matrix products
+        regs_down<Sh::kOtherRegs>();
+        if (warp == kMmaWarp && lane == 0) {
+            constexpr uint32_t kPanel = KT * 128;
+            const uint32_t qk_desc = mma_desc(BF16, 128, KT, false, p.negative != 0);
+            const uint32_t n_out = (p.dim + 15) / 16 * 16;
+            const uint32_t pv_desc = mma_desc(BF16, 128, n_out, true, false);
+            const int ksteps = chunks / 2;
+            uint32_t unit = 0, job0 = 0, gi = 0;   // gi: the unit's first tile since the start
+            bool ok = true;
+            // stage and parity of ring item i
+            auto wait_item = [&](uint32_t i) { return bar_wait(&sh.full[i % Sh::kStages], (i / Sh::kStages) & 1, abort); };
+            for (; walk.more() && ok; walk.next(), ++unit) {
+                const uint32_t nt = static_cast<uint32_t>(walk.u.t1 - walk.u.t0), jobs = nt * W;
+                ok = bar_wait(&sh.q_full, unit & 1, abort);
+                if (!ok) break;
+                auto issue_qk = [&](uint32_t j) {
+                    const uint32_t item = 2 * (gi + j / W), s = item % Sh::kStages, sb = (job0 + j) & 1;
+                    if (!wait_item(item)) return false;
+                    fence_async_reads();
+                    tc_fence_after();
+                    const uint32_t qa = q_smem + (W == 2 ? (j & 1) * 128 * 128 : 0), ka = ring + s * Sh::kStageBytes;
+                    for (int kk = 0; kk < ksteps; ++kk)
+                        mma_ss(tmem + Sh::kS + sb * KT,
+                               smem_desc(qa + (kk >> 2) * (Sh::kRows * 128) + (kk & 3) * 32, 16, 1024),
+                               smem_desc(ka + (kk >> 2) * kPanel + (kk & 3) * 32, 16, 1024), qk_desc, kk > 0);
+                    tc_commit(&sh.s_full[sb]);
+                    if (W == 1 || (j & 1)) tc_commit(&sh.empty[s]);
+                    if (j + 1 == jobs) tc_commit(&sh.q_empty);
+                    return true;
+                };
+                for (uint32_t j = 0; j < 2 && j < jobs && ok; ++j) ok = issue_qk(j);
+                for (uint32_t j = 0; j < jobs && ok; ++j) {
+                    const uint32_t job = job0 + j, sb = job & 1;
+                    const uint32_t item = 2 * (gi + j / W) + 1, s = item % Sh::kStages;
+                    ok = wait_item(item) && bar_wait(&sh.p_full[sb], (job >> 1) & 1, abort);
+                    if (!ok) break;
+                    fence_async_reads();
+                    tc_fence_after();
+                    const uint32_t va = ring + s * Sh::kStageBytes;
+                    for (int kk = 0; kk < KT / 16; ++kk)
+                        mma_ts(tmem + Sh::kO + (W == 2 ? (j & 1) * DP : 0), tmem + Sh::kS + sb * KT + kk * 8,
+                               smem_desc(va + kk * 2048, kPanel, 1024), pv_desc, j >= W || kk > 0);
+                    tc_commit(&sh.pv_done[sb]);
+                    if (W == 1 || (j & 1)) tc_commit(&sh.empty[s]);
+                    if (j + 2 < jobs) ok = issue_qk(j + 2);
+                }
+                job0 += jobs;
+                gi += nt;
+            }
+            // every product is done before the block gives its memory up
+            tc_commit(&sh.drain);
+            if (!bar_wait(&sh.drain, 0, abort)) {
+                const long long t0 = clock64();
+                while (!bar_try(&sh.drain, 0) && clock64() - t0 < kWaitCycles) {
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ softmax, output
+        regs_up<Sh::kSoftmaxRegs>();
+        const int wg = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // the warp's tensor memory lanes
+        const uint32_t t_o = tmem + lanes + Sh::kO + wg * DP;
+        uint32_t job = W == 2 ? wg : 0, tile = 0;
+        bool ok = true;
+        for (; walk.more() && ok; walk.next()) {
+            const Unit u = walk.u;
+            const int32_t h = u.hm / p.row_tiles, mt = u.hm - h * p.row_tiles;
+            const int32_t rho = mt * Sh::kRows + wg * 128 + row;
+            const bool mine = rho < rows;
+            const int32_t t = rho / p.group, gq = rho - t * p.group;
+            const int64_t r = static_cast<int64_t>(u.b) * p.next_n + t;
+            const bool active = mt * Sh::kRows + wg * 128 + (warp & 3) * 32 < rows;   // any row of the warp
+            uint64_t tree = 0;
+            if (mine && p.seq_lens) tree = p.tree_mask ? static_cast<uint64_t>(__ldg(p.tree_mask + r)) : (~0ull >> (63 - t));
+            float m = -INFINITY, l = 0.f;
+            for (int32_t i = u.t0; i < u.t1; ++i, ++tile, job += W) {
+                const uint32_t sb = job & 1, ph = (job >> 1) & 1;
+                ok = __all_sync(~0u, bar_wait(&sh.mask_full[tile % kMaskRing], (tile / kMaskRing) & 1, abort) &&
+                                         bar_wait(&sh.s_full[sb], ph, abort));
+                if (!ok) break;
+                if (active) {
+                    tc_fence_after();
+                    const uint32_t t_s = tmem + lanes + Sh::kS + sb * KT;
+                    uint32_t x[KT];
+#pragma unroll
+                    for (int c = 0; c < KT; c += 32) tmem_load32(t_s + c, x + c);
+                    // bits of the positions this row sees; all of them as a rule
+                    uint32_t bits[KT / 32];
+                    bool whole = true;
+#pragma unroll
+                    for (int c = 0; c < KT / 32; ++c) {
+                        bits[c] = reinterpret_cast<volatile uint32_t *>(sh.mask[tile % kMaskRing])[c];
+                        whole &= bits[c] == ~0u;
+                    }
+                    const bool drafts = i * KT + KT > u.span.ctx;
+                    if (drafts) {
+#pragma unroll
+                        for (int c = 0; c < KT / 32; ++c) {
+                            const int32_t j0 = i * KT + c * 32 - u.span.ctx;   // drafted token of the word's bit 0
+                            uint32_t see = 0;
+                            if (j0 <= -32) see = ~0u;
+                            else if (j0 < 0) see = static_cast<uint32_t>(tree << -j0) | ((1u << -j0) - 1);
+                            else if (j0 < 64) see = static_cast<uint32_t>(tree >> j0);
+                            bits[c] &= see;
+                        }
+                    }
+                    tc_wait_ld();
+                    if (!whole || drafts) {
+#pragma unroll
+                        for (int c = 0; c < KT; ++c)
+                            if (!((bits[c / 32] >> (c & 31)) & 1)) x[c] = 0xff800000u;
+                    }
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                    for (int c = 0; c < KT; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(x[c]));
+                    const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.c;
+                    const bool rise = best > m + kRescale;   // also from -inf
+                    if (__any_sync(~0u, rise)) {
+                        const float f = rise && l > 0.f ? exp2_fast(m - best) : 1.f;
+                        if (rise) {
+                            l *= f;
+                            m = best;
+                        }
+                        if (__any_sync(~0u, f != 1.f)) {
+                            // O is complete up to the row's last job
+                            const uint32_t prev = job - W;
+                            ok = __all_sync(~0u, bar_wait(&sh.pv_done[prev & 1], (prev >> 1) & 1, abort));
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < DP; c += 16) {
+                                uint32_t o[16];
+                                tmem_load16(t_o + c, o);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int d = 0; d < 16; ++d) o[d] = __float_as_uint(__uint_as_float(o[d]) * f);
+                                tmem_store16(t_o + c, o);
+                            }
+                        }
+                    }
+                    const float mm = m == -INFINITY ? 0.f : m;
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                    for (int c0 = 0; c0 < KT; c0 += 32) {   // P over the scores already in registers
+                        uint32_t y[16];
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            const float a = exp2_fast(fmaf(__uint_as_float(x[c0 + c]), p.c, -mm));
+                            const float b = exp2_fast(fmaf(__uint_as_float(x[c0 + c + 1]), p.c, -mm));
+                            sum[c & 2] += a;
+                            sum[(c & 2) + 1] += b;
+                            y[c / 2] = Half2<BF16>::down(a, b);
+                        }
+                        tmem_store16(t_s + c0 / 2, y);
+                    }
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    tc_wait_st();
+                    tc_fence_before();
+                }
+                __syncwarp();
+                if (lane == 0) bar_arrive(&sh.p_full[sb]);
+            }
+            if (!ok) break;
+            const uint32_t prev = job - W;
+            ok = __all_sync(~0u, bar_wait(&sh.pv_done[prev & 1], (prev >> 1) & 1, abort));
+            if (!ok) break;
+            if (!active) continue;
+            tc_fence_after();
+            const bool whole = u.t0 == 0 && u.t1 == u.tiles;
+            const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (u.t0 > 0 ? 0 : 1);
+            const int64_t part_row = part * Sh::kRows + wg * 128 + row;
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const int64_t q_at = r * p.q_heads + h * p.group + gq;
+            for (int c0 = 0; c0 < DP; c0 += 32) {
+                if (c0 >= p.dim) break;
+                uint32_t o[32];
+                tmem_load32(t_o + c0, o);
+                tc_wait_ld();
+                if (!mine) continue;
+                if (whole) {
+                    uint8_t *dst = static_cast<uint8_t *>(p.out) + 2 * (q_at * p.dim + c0);
+#pragma unroll
+                    for (int c = 0; c < 32; c += 8) {
+                        if (c0 + c >= p.dim) break;
+                        uint32_t y[4];
+#pragma unroll
+                        for (int d = 0; d < 4; ++d)
+                            y[d] = Half2<BF16>::down(__uint_as_float(o[c + 2 * d]) * inv, __uint_as_float(o[c + 2 * d + 1]) * inv);
+                        *reinterpret_cast<uint4 *>(dst + 2 * c) = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                } else {
+                    float *dst = p.part_o + part_row * DP + c0;
+#pragma unroll
+                    for (int c = 0; c < 32; c += 4)
+                        *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                }
+            }
+            if (mine) {
+                if (!whole) p.part_ml[part_row] = make_float2(m, l);
+                else if (p.lse) p.lse[q_at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            }
         }
     }
-    for (int c = 0; c < 2; ++c) {
-        const int d = static_cast<int>(threadIdx.x) + 128 * c;
-        if (d < p.dim)
-            static_cast<T *>(p.out)[(r * p.q_heads + h) * p.dim + d] = static_cast<T>(m == -INFINITY ? 0.f : o[c] / l);
-    }
-    if (p.lse && threadIdx.x == 0) p.lse[r * p.q_heads + h] = m == -INFINITY ? -INFINITY : m + logf(l);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_free(tmem, 512);
+    if (threadIdx.x == 0 && sh.abort) atomicOr(p.status, kStatusCopyLost);
 }
 
-// One thread for each (position, weight head) of a request.
-template <bool BF16>
-__global__ void __launch_bounds__(128) weights_kernel(AttnParams p) {
-    using T = typename Half2<BF16>::T;
-    __shared__ float q[GBTOPK_MAX_HEAD_DIM];
+// Joins the partial results of units that span blocks: blocks of one warp a
+// row, grid (units, row groups).
+constexpr int kCombineThreads = 256;
+
+template <bool BF16, int DP, int W>
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ AttnParams p, int32_t grid) {
+    constexpr int KT = Shape<DP, W>::KT, kRows = Shape<DP, W>::kRows;
+    __shared__ ScanScratch scan;
     pdl_wait();
-    const int64_t i = blockIdx.y;
-    const int w = blockIdx.z, group = p.q_heads / p.kv_heads, per = p.q_heads / p.weight_heads;
-    const int64_t pos = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
-    const uint64_t took = p.accept_mask ? static_cast<uint64_t>(p.accept_mask[i]) : ~0ull;
-    float sum = 0;
-    for (int t = 0; t < p.next_n; ++t) {
-        if (!((took >> t) & 1)) continue;
-        const int64_t r = i * p.next_n + t;
-        const Row<false> row(p, r);
-        const int64_t slot = pos < row.n && pos < p.width ? row.slot(static_cast<int32_t>(pos)) : -1;
-        for (int h = w * per; h < w * per + per; ++h) {
-            __syncthreads();
-            for (int d = threadIdx.x; d < p.dim; d += 128)
-                q[d] = static_cast<float>(static_cast<const T *>(p.q)[r * p.q_row + h * p.q_head + d]);
-            __syncthreads();
-            const float lse = p.lse_in[r * p.q_heads + h];
-            if (slot < 0 || lse == -INFINITY) continue;
-            sum += expf(p.scale * dot<BF16>(q, reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k) +
-                                                                               slot * p.k_slot + (h / group) * p.k_head),
-                                            p.dim) - lse);
+    const int32_t hms = p.request_units;
+    const int32_t b = static_cast<int32_t>(blockIdx.x / hms), hm = static_cast<int32_t>(blockIdx.x % hms);
+    const int64_t total = sum_tiles<KT, kCombineThreads>(p, p.requests, &scan);
+    const int64_t per = (total + grid - 1) / grid;
+    const int32_t tiles = tiles_of<KT>(span_of(p, b));
+    const int64_t start = sum_tiles<KT, kCombineThreads>(p, b, &scan) + static_cast<int64_t>(hm) * tiles;
+    const int64_t c0 = start / per, c1 = (start + tiles - 1) / per;
+    if (c0 == c1) return;
+    const int32_t h = hm / p.row_tiles, r0 = (hm - h * p.row_tiles) * kRows;
+    const int32_t rows = p.next_n * p.group;
+    const int lane = threadIdx.x & 31;
+    for (int32_t row = static_cast<int32_t>(blockIdx.y * (kCombineThreads / 32) + (threadIdx.x >> 5)); row < kRows && r0 + row < rows;
+         row += static_cast<int32_t>(gridDim.y * (kCombineThreads / 32))) {
+        auto at = [&](int64_t c) { return (2 * c + (c == c0 ? 1 : 0)) * kRows + row; };
+        float m = -INFINITY;
+        for (int64_t c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[at(c)].x);
+        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        const float mm = m == -INFINITY ? 0.f : m;
+        float l = 0.f, acc[DP / 32] = {};
+        for (int64_t c = c0; c <= c1; ++c) {
+            const float2 ml = p.part_ml[at(c)];
+            const float f = exp2f(ml.x - mm);
+            l += ml.y * f;
+            const float *o = p.part_o + at(c) * DP;
+#pragma unroll
+            for (int d = 0; d < DP / 32; ++d) acc[d] += f * o[d * 32 + lane];
         }
+        const int32_t t = (r0 + row) / p.group, gq = r0 + row - t * p.group;
+        const int64_t q_at = (static_cast<int64_t>(b) * p.next_n + t) * p.q_heads + h * p.group + gq;
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        using T = typename Half2<BF16>::T;
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d)
+            if (d * 32 + lane < p.dim) static_cast<T *>(p.out)[q_at * p.dim + d * 32 + lane] = static_cast<T>(acc[d] * inv);
+        if (p.lse && lane == 0) p.lse[q_at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
     }
-    if (pos < p.width) p.weights[(i * p.weight_heads + w) * p.width + pos] += sum;
 }
 
-int check_heads(int dtype, int64_t num_rows, int32_t q_heads, int32_t kv_heads, int32_t dim) {
-    if (dtype != GBTOPK_F32 && dtype != GBTOPK_BF16 && dtype != GBTOPK_F16) return GBTOPK_EINVAL;
-    if (num_rows < 0 || q_heads < 1 || kv_heads < 1 || dim < 1 || q_heads % kv_heads != 0) return GBTOPK_EINVAL;
-    if (dtype == GBTOPK_F32 || dim > GBTOPK_MAX_HEAD_DIM || dim % 8 != 0) return GBTOPK_EUNSUPPORTED;
-    if (num_rows > INT32_MAX || q_heads > 65535) return GBTOPK_EUNSUPPORTED;
-    return GBTOPK_OK;
-}
+int dim_class(int32_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-// Rows of 16-bit elements read in 16-byte pieces; `any`: there are some.
-int check_rows(const void *base, int64_t a, int64_t b, bool any) {
-    if (any && !base) return GBTOPK_EINVAL;
-    if (a < 0 || b < 0) return GBTOPK_EINVAL;
-    if (!aligned_to(base, 16) || !multiple_of(a, 8) || !multiple_of(b, 8)) return GBTOPK_EALIGN;
-    return GBTOPK_OK;
-}
+// Two row tiles a block where a head has more than 128 rows: they share each
+// copied tile, and one's softmax runs beside the other's products.
+int row_groups(int32_t dim, int64_t rows) { return dim <= 128 && rows > 128 ? 2 : 1; }
 
-int check_pages(const int32_t *table, int64_t cols, int64_t stride, int32_t page, int64_t num_slots,
-                int64_t requests, Paging *out) {
-    if (page < 1 || page > (1 << 30) || cols < 0 || num_slots < 0 || (requests > 1 && stride < cols)) return GBTOPK_EINVAL;
-    if (requests > 0 && cols > 0 && !table) return GBTOPK_EINVAL;
-    if (cols > INT32_MAX / page) cols = INT32_MAX / page;  // positions are 31-bit numbers
-    out->table = table;
-    out->cols = cols;
-    out->row_stride = stride;
-    out->num_slots = num_slots;
-    out->page.init(static_cast<uint32_t>(page));
-    return GBTOPK_OK;
+size_t partial_rows(int32_t) { return static_cast<size_t>(2 * kMaxGrid) * 256; }
+
+template <bool BF16, int DP, int W>
+cudaError_t launch_shape(AttnParams p, uint8_t *ws, int sms, cudaStream_t stream) {
+    using Sh = Shape<DP, W>;
+    const int64_t rows = static_cast<int64_t>(p.next_n) * p.group;
+    p.row_tiles = static_cast<int32_t>((rows + Sh::kRows - 1) / Sh::kRows);
+    p.request_units = p.kv_heads * p.row_tiles;
+    p.part_ml = reinterpret_cast<float2 *>(ws + kWsHeaderBytes);
+    p.part_o = reinterpret_cast<float *>(p.part_ml + partial_rows(p.dim));
+    cudaError_t e = cudaFuncSetAttribute(attention_kernel<BF16, DP, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         static_cast<int>(Sh::kSmem));
+    if (e != cudaSuccess) return e;
+    const int grid = sms < kMaxGrid ? sms : kMaxGrid;
+    e = launch_pdl(attention_kernel<BF16, DP, W>, dim3(static_cast<unsigned>(grid)), Sh::kThreads, Sh::kSmem, stream, 1, p);
+    if (e != cudaSuccess) return e;
+    const int64_t units = static_cast<int64_t>(p.requests) * p.kv_heads * p.row_tiles;
+    const int64_t each = rows < Sh::kRows ? rows : Sh::kRows;
+    const dim3 blocks(static_cast<unsigned>(units), static_cast<unsigned>((each + 7) / 8));
+    return launch_pdl(combine_kernel<BF16, DP, W>, blocks, kCombineThreads, 0, stream, 1, p, static_cast<int32_t>(grid));
 }
 
 template <bool BF16>
-cudaError_t launch_attention(const AttnParams &p, cudaStream_t stream) {
-    const dim3 grid(static_cast<unsigned>(p.num_rows), static_cast<unsigned>(p.q_heads));
-    return p.seq_lens ? launch_pdl(attention_kernel<BF16, false>, grid, 128, 0, stream, 1, p)
-                      : launch_pdl(attention_kernel<BF16, true>, grid, 128, 0, stream, 1, p);
+cudaError_t launch_attention(const AttnParams &p, uint8_t *ws, int sms, cudaStream_t s) {
+    const int w = row_groups(p.dim, static_cast<int64_t>(p.next_n) * p.group);
+    switch (dim_class(p.dim)) {
+        case 64: return w == 2 ? launch_shape<BF16, 64, 2>(p, ws, sms, s) : launch_shape<BF16, 64, 1>(p, ws, sms, s);
+        case 128: return w == 2 ? launch_shape<BF16, 128, 2>(p, ws, sms, s) : launch_shape<BF16, 128, 1>(p, ws, sms, s);
+        default: return launch_shape<BF16, 256, 1>(p, ws, sms, s);
+    }
 }
 
 }  // namespace
@@ -215,6 +499,7 @@ int attend(AttnParams &p, int dtype, const void *q, int64_t num_rows, int64_t q_
            void *out, float *lse, void *workspace, size_t workspace_bytes, void *stream) {
     int rc;
     const int64_t num_slots = p.pages.num_slots;
+    if (num_slots > INT32_MAX) return GBTOPK_EUNSUPPORTED;
     if ((rc = check_rows(q, q_row_stride, q_head_stride, true)) != GBTOPK_OK) return rc;
     if ((rc = check_rows(k_cache, k_slot_stride, k_head_stride, num_slots > 0)) != GBTOPK_OK) return rc;
     if ((rc = check_rows(v_cache, v_slot_stride, v_head_stride, num_slots > 0)) != GBTOPK_OK) return rc;
@@ -232,15 +517,24 @@ int attend(AttnParams &p, int dtype, const void *q, int64_t num_rows, int64_t q_
     p.v = v_cache;
     p.v_slot = v_slot_stride;
     p.v_head = v_head_stride;
-    p.num_rows = num_rows;
+    p.requests = static_cast<int32_t>(num_rows / p.next_n);
     p.q_heads = q_heads;
     p.kv_heads = kv_heads;
+    p.group = q_heads / kv_heads;
     p.dim = head_dim;
-    p.scale = scale;
+    p.c = fmaxf(fabsf(scale) * kLog2e, FLT_MIN);   // a scale of 0 stays a product that ignores no mask
+    p.negative = scale < 0.f;
     p.out = out;
     p.lse = lse;
+    p.status = static_cast<uint32_t *>(workspace);
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return GBTOPK_ECUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    return (dtype == GBTOPK_BF16 ? launch_attention<true>(p, s) : launch_attention<false>(p, s)) == cudaSuccess
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    return (dtype == GBTOPK_BF16 ? launch_attention<true>(p, ws, sms, s) : launch_attention<false>(p, ws, sms, s)) ==
+                   cudaSuccess
                ? GBTOPK_OK
                : GBTOPK_ECUDA;
 }
@@ -251,7 +545,7 @@ extern "C" {
 
 size_t gbtopk_attention_workspace_bytes(int64_t num_rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
     if (check_heads(GBTOPK_BF16, num_rows, q_heads, kv_heads, head_dim) != GBTOPK_OK) return 0;
-    return kWsHeaderBytes;
+    return kWsHeaderBytes + partial_rows(head_dim) * (8 + 4 * static_cast<size_t>(dim_class(head_dim)));
 }
 
 int gbtopk_tree_attention(const void *q, int dtype, int64_t num_rows, int64_t q_row_stride, int64_t q_head_stride,
@@ -292,61 +586,11 @@ int gbtopk_selected_attention(const void *q, int dtype, int64_t num_rows, int64_
     AttnParams p{};
     p.pages.num_slots = num_slots;
     p.indices = indices;
-    p.top_k = top_k;
+    p.top_k = static_cast<int32_t>(top_k);
     p.idx_row = idx_row_stride;
     p.next_n = 1;
     return attend(p, dtype, q, num_rows, q_row_stride, q_head_stride, q_heads, kv_heads, head_dim, k_cache, k_slot_stride,
                   k_head_stride, v_cache, v_slot_stride, v_head_stride, scale, out, lse, workspace, workspace_bytes, stream);
-}
-
-int gbtopk_cache_weights(const void *q, int dtype, int64_t num_rows, int64_t q_row_stride, int64_t q_head_stride,
-                         int32_t q_heads, int32_t kv_heads, int32_t head_dim, const void *k_cache,
-                         int64_t k_slot_stride, int64_t k_head_stride, int64_t num_slots, const float *lse,
-                         const int32_t *page_table, int64_t pt_cols, int64_t pt_row_stride, int32_t page_size,
-                         const int32_t *seq_lens, int32_t next_n, const int64_t *tree_mask,
-                         const int64_t *accept_mask, float scale, float *weights, int32_t weight_heads, int64_t width,
-                         void *workspace, size_t workspace_bytes, void *stream) {
-    int rc = check_heads(dtype, num_rows, q_heads, kv_heads, head_dim);
-    if (rc != GBTOPK_OK) return rc;
-    if (next_n < 1 || num_rows % next_n != 0 || width < 0) return GBTOPK_EINVAL;
-    if (weight_heads != 1 && weight_heads != kv_heads) return GBTOPK_EINVAL;
-    if (next_n > GBTOPK_MAX_NEXT_N || width > INT32_MAX) return GBTOPK_EUNSUPPORTED;
-    AttnParams p{};
-    if ((rc = check_pages(page_table, pt_cols, pt_row_stride, page_size, num_slots, num_rows / next_n, &p.pages)) != GBTOPK_OK)
-        return rc;
-    if (num_rows == 0 || width == 0) return GBTOPK_OK;
-    if (!seq_lens || !lse || !weights) return GBTOPK_EINVAL;
-    if ((rc = check_rows(q, q_row_stride, q_head_stride, true)) != GBTOPK_OK) return rc;
-    if ((rc = check_rows(k_cache, k_slot_stride, k_head_stride, num_slots > 0)) != GBTOPK_OK) return rc;
-    if (!aligned_to(lse, 4) || !aligned_to(weights, 16)) return GBTOPK_EALIGN;
-    if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < kWsHeaderBytes) return GBTOPK_EWORKSPACE;
-    p.q = q;
-    p.q_row = q_row_stride;
-    p.q_head = q_head_stride;
-    p.k = k_cache;
-    p.k_slot = k_slot_stride;
-    p.k_head = k_head_stride;
-    p.num_rows = num_rows;
-    p.q_heads = q_heads;
-    p.kv_heads = kv_heads;
-    p.dim = head_dim;
-    p.scale = scale;
-    p.seq_lens = seq_lens;
-    p.next_n = next_n;
-    p.tree_mask = tree_mask;
-    p.accept_mask = accept_mask;
-    p.lse_in = lse;
-    p.weights = weights;
-    p.weight_heads = weight_heads;
-    p.width = width;
-    cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid(static_cast<unsigned>((width + 127) / 128), static_cast<unsigned>(num_rows / next_n),
-                    static_cast<unsigned>(weight_heads));
-    if (grid.y > 65535) return GBTOPK_EUNSUPPORTED;
-    return (dtype == GBTOPK_BF16 ? launch_pdl(weights_kernel<true>, grid, 128, 0, s, 1, p)
-                                 : launch_pdl(weights_kernel<false>, grid, 128, 0, s, 1, p)) == cudaSuccess
-               ? GBTOPK_OK
-               : GBTOPK_ECUDA;
 }
 
 }  // extern "C"

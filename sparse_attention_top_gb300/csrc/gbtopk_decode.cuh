@@ -108,4 +108,33 @@ cudaError_t launch_pdl(void (*kernel)(A...), dim3 grid, int threads, size_t smem
 inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 inline bool multiple_of(int64_t v, int64_t a) { return v % a == 0; }
 
+inline int check_heads(int dtype, int64_t num_rows, int32_t q_heads, int32_t kv_heads, int32_t dim) {
+    if (dtype != GBTOPK_F32 && dtype != GBTOPK_BF16 && dtype != GBTOPK_F16) return GBTOPK_EINVAL;
+    if (num_rows < 0 || q_heads < 1 || kv_heads < 1 || dim < 1 || q_heads % kv_heads != 0) return GBTOPK_EINVAL;
+    if (dtype == GBTOPK_F32 || dim > GBTOPK_MAX_HEAD_DIM || dim % 8 != 0) return GBTOPK_EUNSUPPORTED;
+    if (num_rows > INT32_MAX || q_heads > 65535) return GBTOPK_EUNSUPPORTED;
+    return GBTOPK_OK;
+}
+
+// Rows of 16-bit elements read in 16-byte pieces; `any`: there are some.
+inline int check_rows(const void *base, int64_t a, int64_t b, bool any) {
+    if (any && !base) return GBTOPK_EINVAL;
+    if (a < 0 || b < 0) return GBTOPK_EINVAL;
+    if (!aligned_to(base, 16) || !multiple_of(a, 8) || !multiple_of(b, 8)) return GBTOPK_EALIGN;
+    return GBTOPK_OK;
+}
+
+inline int check_pages(const int32_t *table, int64_t cols, int64_t stride, int32_t page, int64_t num_slots,
+                int64_t requests, Paging *out) {
+    if (page < 1 || page > (1 << 30) || cols < 0 || num_slots < 0 || (requests > 1 && stride < cols)) return GBTOPK_EINVAL;
+    if (requests > 0 && cols > 0 && !table) return GBTOPK_EINVAL;
+    if (cols > (INT32_MAX - 1024) / page) cols = (INT32_MAX - 1024) / page;  // positions and a tile more are 31-bit numbers
+    out->table = table;
+    out->cols = cols;
+    out->row_stride = stride;
+    out->num_slots = num_slots;
+    out->page.init(static_cast<uint32_t>(page));
+    return GBTOPK_OK;
+}
+
 }  // namespace gbtopk

@@ -1,0 +1,187 @@
+// Shared by the tensor-core kernels over a paged cache (gbtopk_attention.cu,
+// gbtopk_weights.cu): their arguments, the equal split of a ragged batch's
+// tiles over the blocks, and the copies of cached rows.  Not part of the ABI.
+#pragma once
+
+#include "gbtopk_decode.cuh"
+#include "gbtopk_mma.cuh"
+
+namespace gbtopk {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct AttnParams {
+    const void *q, *k, *v;
+    int64_t q_row, q_head, k_slot, k_head, v_slot, v_head;  // strides in elements
+    Paging pages;
+    const int32_t *seq_lens;     // null: selected slots
+    const int64_t *tree_mask;
+    const int32_t *indices;
+    int64_t idx_row;
+    int32_t top_k;
+    int32_t requests;            // selected: rows
+    int32_t next_n, q_heads, kv_heads, group, dim;
+    int32_t row_tiles;           // row tiles of a (request, kv head)
+    int32_t request_units;       // units of a request
+    float c;                     // |scale| log2 e
+    int32_t negative;            // scale < 0: the products are negated
+    void *out;
+    float *lse;
+    uint32_t *status;
+    float *part_o;               // [2 grid][rows of a tile][DP]
+    float2 *part_ml;             // [2 grid][rows of a tile]
+};
+
+// Cached positions of request b, and the first drafted one.
+struct Span {
+    int32_t n, ctx;
+};
+
+__device__ __forceinline__ Span span_of(const AttnParams &p, int32_t b) {
+    if (!p.seq_lens) return Span{p.top_k, INT32_MAX};
+    const int32_t raw = __ldg(p.seq_lens + b);
+    const int32_t len = raw > 0 ? raw : 0;
+    const int64_t room = p.pages.cols * p.pages.page.d;
+    return Span{static_cast<int32_t>(len < room ? len : room), len - p.next_n};
+}
+
+// Every request has at least one tile, so that rows that see nothing are
+// written too.
+template <int KT>
+__device__ __forceinline__ int32_t tiles_of(const Span &s) {
+    return s.n > KT ? (s.n - 1) / KT + 1 : 1;
+}
+
+// The block's part of one unit: position tiles t0 .. t1 - 1 of `tiles`.
+struct Unit {
+    int32_t b, hm, t0, t1, tiles;
+    Span span;
+};
+
+struct ScanScratch {
+    int64_t warps[16];
+    int64_t off;
+    int32_t b;
+};
+
+// A block's share of the call's tiles: `tiles` of them from tile `off` of
+// request b's units on.
+struct Share {
+    int64_t off, tiles;
+    int32_t b;
+};
+
+// Walks the units of a share of `left` tiles.
+template <int KT>
+struct Walk {
+    const AttnParams &p;
+    int64_t left;
+    Unit u;
+    __device__ Walk(const AttnParams &p, const Share &s) : p(p), left(s.tiles) {
+        if (left <= 0) return;
+        u.b = s.b;
+        u.span = span_of(p, u.b);
+        u.tiles = tiles_of<KT>(u.span);
+        u.hm = static_cast<int32_t>(s.off / u.tiles);
+        u.t0 = static_cast<int32_t>(s.off - static_cast<int64_t>(u.hm) * u.tiles);
+        clip();
+    }
+    __device__ void clip() {
+        const int64_t end = u.t0 + left;
+        u.t1 = end < u.tiles ? static_cast<int32_t>(end) : u.tiles;
+    }
+    __device__ bool more() const { return left > 0; }
+    __device__ void next() {
+        left -= u.t1 - u.t0;
+        if (left <= 0) return;
+        if (++u.hm == p.request_units) {
+            u.hm = 0;
+            u.span = span_of(p, ++u.b);
+            u.tiles = tiles_of<KT>(u.span);
+        }
+        u.t0 = 0;
+        clip();
+    }
+};
+
+// Total tiles of the call over requests [0, upto), summed by the block.
+template <int KT, int THREADS>
+__device__ int64_t sum_tiles(const AttnParams &p, int32_t upto, ScanScratch *scratch) {
+    if (!p.seq_lens) return static_cast<int64_t>(upto) * tiles_of<KT>(span_of(p, 0)) * p.request_units;
+    int64_t s = 0;
+    for (int32_t b = threadIdx.x; b < upto; b += THREADS) s += tiles_of<KT>(span_of(p, b));
+    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
+    if ((threadIdx.x & 31) == 0) scratch->warps[threadIdx.x >> 5] = s;
+    __syncthreads();
+    s = 0;
+    for (int w = 0; w < (THREADS + 31) / 32; ++w) s += scratch->warps[w];
+    __syncthreads();
+    return s * p.request_units;
+}
+
+// The blockIdx.x-th of gridDim.x equal shares.
+template <int KT, int THREADS>
+__device__ Share block_share(const AttnParams &p, ScanScratch *scratch) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t total = sum_tiles<KT, THREADS>(p, p.requests, scratch);
+    const int64_t per = (total + gridDim.x - 1) / gridDim.x, start = per * blockIdx.x;
+    Share s{0, start >= total ? 0 : (start + per < total ? per : total - start), 0};
+    if (s.tiles == 0) return s;
+    if (!p.seq_lens) {
+        const int64_t each = static_cast<int64_t>(tiles_of<KT>(span_of(p, 0))) * p.request_units;
+        s.b = static_cast<int32_t>(start / each);
+        s.off = start - s.b * each;
+        return s;
+    }
+    int64_t base = 0;
+    for (int32_t b0 = 0; b0 < p.requests; b0 += THREADS) {
+        const int32_t b = b0 + static_cast<int32_t>(threadIdx.x);
+        const int64_t v = b < p.requests ? static_cast<int64_t>(tiles_of<KT>(span_of(p, b))) * p.request_units : 0;
+        int64_t inc = v;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(~0u, inc, o);
+            if (lane >= o) inc += x;
+        }
+        if (lane == 31) scratch->warps[warp] = inc;
+        __syncthreads();
+        int64_t all = 0, before = base;
+        for (int w = 0; w < THREADS / 32; ++w) {
+            before += w < warp ? scratch->warps[w] : 0;
+            all += scratch->warps[w];
+        }
+        const int64_t at = before + inc - v;
+        if (start >= at && start < at + v) {
+            scratch->b = b;
+            scratch->off = start - at;
+        }
+        base += all;
+        __syncthreads();
+        if (start < base) break;
+    }
+    s.b = scratch->b;
+    s.off = scratch->off;
+    return s;
+}
+
+// Copies one tile's rows: each warp its 32 (or 16) rows, consecutive lanes
+// consecutive 16-byte chunks; rows without a slot become zeros.
+template <int DP, int KT>
+__device__ __forceinline__ void copy_tile(uint32_t dst, const uint8_t *base, int64_t slot_bytes, int32_t slot,
+                                          int32_t chunks, int32_t loaded, int warp, int lane) {
+    constexpr int kChunks = DP / 8 < 32 ? DP / 8 : 32;   // of a row; lanes of a row
+    constexpr int kPer = 32 / kChunks;                   // rows an instruction
+    constexpr int kMine = KT / 4;                        // rows of the warp
+    const int c = lane % kChunks;
+#pragma unroll 4
+    for (int r0 = 0; r0 < kMine; r0 += kPer) {
+        const int r = r0 + lane / kChunks;
+        const int32_t s = __shfl_sync(~0u, slot, r);
+        if (c < chunks) {
+            const bool ok = s >= 0 && c < loaded;
+            copy16(dst + tile_offset(KT, warp * kMine + r, c), ok ? base + s * slot_bytes + c * 16 : base, ok ? 16u : 0u);
+        }
+    }
+}
+
+}  // namespace gbtopk
