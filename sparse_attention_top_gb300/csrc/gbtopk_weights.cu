@@ -1,104 +1,373 @@
-// The weight each cached position accumulates (gbtopk_cache_weights).
-#include "gbtopk_decode.cuh"
+// The weight each cached position accumulates (gbtopk_cache_weights):
+// w[p] += sum over rows of 2^(c s(row, p) - lse2(row)), c = |scale| log2 e.
+//
+// The scores are computed transposed, S^T = K Q^T (tensor core): a tile of
+// 128 cached positions is the rows of the matrix, so one thread owns one
+// position and sums its rows alone, in a fixed order and without atomics;
+// the softmax's sum is known (lse), so one pass over the keys does it and
+// the values are not read.  Only accepted rows enter the product.
+//
+// Work is split as in the attention kernel: block c takes the c-th equal
+// share of the list of (request, weight head, position tile).  Within a
+// share, up to kSpan tiles of one (request, weight head) at a time: for each
+// kv head and each group of up to NQ rows (a phase, one queries' buffer) its
+// tiles one after the other (a job each), the even and odd jobs summed by two
+// warpgroups, each into its own sums in shared memory.
+#include <cfloat>
+#include <cmath>
+
+#include "gbtopk_paged.cuh"
 
 namespace gbtopk {
 namespace {
 
+constexpr int kSpan = 16;        // tiles whose sums are held at a time
+constexpr int kMaskRing = 8;     // tiles whose validity bits are kept
+constexpr int KT = 128;          // positions a tile
+
 struct WeightParams {
-    const void *q, *k, *v;
-    int64_t q_row, q_head, k_slot, k_head, v_slot, v_head;
-    Paging pages;
-    const int32_t *seq_lens;     // null: selected slots
-    const int64_t *tree_mask;
+    AttnParams a;                // request_units: weight heads
     const int64_t *accept_mask;
-    const int32_t *indices;
-    int64_t top_k, idx_row;
-    int64_t num_rows;
-    int32_t next_n, q_heads, kv_heads, dim;
-    float scale;
-    void *out;
-    float *lse;
-    const float *lse_in;
+    const float *lse;
     float *weights;
     int32_t weight_heads;
     int64_t width;
 };
 
-// Positions a row may see: [0, n), slot() < 0 where it sees none.
-template <bool SELECTED>
-struct Row {
+template <int DP>
+struct Shape {
+    static constexpr int NQ = DP == 256 ? 64 : 128;         // query rows of a phase
+    static constexpr int kThreads = 512;                    // 2 summing warpgroups, products, copies
+    static constexpr int kLaunchRegs = 128, kSumRegs = 152, kOtherRegs = 96;
+    static_assert(2 * kSumRegs + 2 * kOtherRegs <= 4 * kLaunchRegs, "register pool");
+    static constexpr int kQBytes = NQ * DP * 2;             // one of two buffers
+    static constexpr int kStageBytes = KT * DP * 2;
+    static constexpr int kSums = 2 * kSpan * KT * 4;
+    static constexpr int kFixed = 4096;
+    static constexpr int kFit = (static_cast<int>(kMaxSmemBytes) - 1024 - kFixed - kSums - 2 * kQBytes) / kStageBytes;
+    static constexpr int kStages = kFit < 6 ? kFit : 6;
+    static constexpr size_t kSmem = 1024 + kFixed + kSums + 2 * kQBytes + static_cast<size_t>(kStages) * kStageBytes;
+    static_assert(kStages >= 2 && kStages + 2 <= kMaskRing, "ring");
+};
+
+struct Shared {
+    uint64_t full[6], empty[6];     // ring stages, one key tile each
+    uint64_t mask_full[kMaskRing];
+    uint64_t q_full[2], q_empty[2]; // phase buffers
+    uint64_t s_full[2], s_empty[2];
+    uint64_t drain;
+    uint32_t mask[kMaskRing][4];
+    alignas(16) float lse2[2][128]; // base-2 lse of the phase's rows; +inf: adds nothing
+    uint64_t tree[GBTOPK_MAX_NEXT_N];
+    ScanScratch scan;
+    uint32_t tmem;
+    uint32_t abort;
+};
+static_assert(sizeof(Shared) <= 4096, "shared block");
+static_assert(offsetof(Shared, lse2) % 16 == 0, "vector loads of the rows' lse");
+
+// One span of a share: tiles t0 .. t1 - 1 of a (request, weight head), and
+// its phases.
+struct Span16 {
+    int32_t b, w, t0, t1, n, ctx;
+    uint64_t took;     // accepted tokens
+    int32_t rows;      // accepted rows of a kv head
+    int32_t groups;    // row groups of a kv head
+    int32_t phases;
+};
+
+// Walks the spans of the block's share; every role sees the same sequence.
+template <int NQ>
+struct Spans {
     const WeightParams &p;
-    int64_t r, i;
-    int32_t ctx, n;
-    uint64_t tree;
-    __device__ Row(const WeightParams &p, int64_t r) : p(p), r(r) {
-        if constexpr (SELECTED) {
-            n = static_cast<int32_t>(p.top_k);
-        } else {
-            i = r / p.next_n;
-            const int t = static_cast<int>(r - i * p.next_n);
-            const int64_t len = p.seq_lens[i] > 0 ? p.seq_lens[i] : 0;
-            ctx = static_cast<int32_t>(len - p.next_n);
-            const int64_t room = p.pages.cols * p.pages.page.d;
-            n = static_cast<int32_t>(len < room ? len : room);
-            tree = p.tree_mask ? static_cast<uint64_t>(p.tree_mask[r]) : (~0ull >> (63 - t));
+    Walk<KT> walk;
+    int32_t t;
+    __device__ Spans(const WeightParams &p, const Share &s) : p(p), walk(p.a, s), t(walk.more() ? walk.u.t0 : 0) {}
+    __device__ bool next(Span16 *s) {
+        while (walk.more()) {
+            if (t == walk.u.t1) {
+                walk.next();
+                if (!walk.more()) return false;
+                t = walk.u.t0;
+            }
+            s->b = walk.u.b;
+            s->w = walk.u.hm;
+            s->n = walk.u.span.n;
+            s->ctx = walk.u.span.ctx;
+            s->t0 = t;
+            s->t1 = walk.u.t1 - t > kSpan ? t + kSpan : walk.u.t1;
+            t = s->t1;
+            const uint64_t all = ~0ull >> (64 - p.a.next_n);
+            s->took = p.accept_mask ? static_cast<uint64_t>(__ldg(p.accept_mask + s->b)) & all : all;
+            s->rows = __popcll(s->took) * p.a.group;
+            s->groups = (s->rows + NQ - 1) / NQ;
+            s->phases = s->groups * (p.a.kv_heads / p.weight_heads);
+            if (s->phases > 0 && s->n > 0 && static_cast<int64_t>(s->t0) * KT < p.width) return true;
         }
-    }
-    __device__ int64_t slot(int32_t pos) const {
-        if constexpr (SELECTED) {
-            const int32_t s = p.indices[r * p.idx_row + pos];
-            return s < p.pages.num_slots ? s : -1;
-        } else {
-            if (pos >= ctx && !((tree >> (pos - ctx)) & 1)) return -1;
-            return p.pages.slot(i, pos);
-        }
+        return false;
     }
 };
 
-template <bool BF16>
-__device__ float dot(const float *q, const uint4 *k, int dim) {
-    float s = 0;
-    for (int c = 0; c < dim / 8; ++c) {
-        const uint4 x = k[c];
-        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
-        for (int j = 0; j < 4; ++j) {
-            const float2 f = Half2<BF16>::up(w[j]);
-            s = fmaf(f.x, q[c * 8 + 2 * j], s);
-            s = fmaf(f.y, q[c * 8 + 2 * j + 1], s);
-        }
-    }
-    return s;
+// The k-th accepted token.
+__device__ __forceinline__ int nth_bit(uint64_t bits, int k) {
+    for (; k > 0; --k) bits &= bits - 1;
+    return __ffsll(static_cast<long long>(bits)) - 1;
 }
 
-// One thread for each (position, weight head) of a request.
-template <bool BF16>
-__global__ void __launch_bounds__(128) weights_kernel(WeightParams p) {
-    using T = typename Half2<BF16>::T;
-    __shared__ float q[GBTOPK_MAX_HEAD_DIM];
+// Barrier of the two summing warpgroups; true for all when `v` is for one.
+__device__ __forceinline__ bool sums_barrier_or(bool v) {
+    uint32_t any;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, 1, 256, p;\n selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(any)
+        : "r"(static_cast<uint32_t>(v))
+        : "memory");
+    return any != 0;
+}
+
+template <bool BF16, int DP>
+__global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const __grid_constant__ WeightParams p) {
+    using Sh = Shape<DP>;
+    constexpr int NQ = Sh::NQ;
+    extern __shared__ uint8_t raw[];
+    uint8_t *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    const uint32_t q_smem = smem_addr(smem), ring = q_smem + 2 * Sh::kQBytes;
+    float *sums = reinterpret_cast<float *>(smem + 2 * Sh::kQBytes + Sh::kStages * Sh::kStageBytes);   // [2][kSpan][KT]
+    Shared &sh = *reinterpret_cast<Shared *>(reinterpret_cast<uint8_t *>(sums) + Sh::kSums);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int kMmaWarp = 8;
+    const AttnParams &a = p.a;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < Sh::kStages; ++i) {
+            bar_init(&sh.full[i], 128);
+            bar_init(&sh.empty[i], 1);
+        }
+        for (int i = 0; i < kMaskRing; ++i) bar_init(&sh.mask_full[i], 4);
+        for (int i = 0; i < 2; ++i) {
+            bar_init(&sh.q_full[i], 128 + 4);   // copies, and the lse values of each copying warp
+            bar_init(&sh.q_empty[i], 1 + 8);    // products, and the summing warps
+            bar_init(&sh.s_full[i], 1);
+            bar_init(&sh.s_empty[i], 4);
+        }
+        bar_init(&sh.drain, 1);
+        sh.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == kMmaWarp) tmem_alloc(&sh.tmem, 256);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
     pdl_wait();
-    const int64_t i = blockIdx.y;
-    const int w = blockIdx.z, group = p.q_heads / p.kv_heads, per = p.q_heads / p.weight_heads;
-    const int64_t pos = static_cast<int64_t>(blockIdx.x) * 128 + threadIdx.x;
-    const uint64_t took = p.accept_mask ? static_cast<uint64_t>(p.accept_mask[i]) : ~0ull;
-    float sum = 0;
-    for (int t = 0; t < p.next_n; ++t) {
-        if (!((took >> t) & 1)) continue;
-        const int64_t r = i * p.next_n + t;
-        const Row<false> row(p, r);
-        const int64_t slot = pos < row.n && pos < p.width ? row.slot(static_cast<int32_t>(pos)) : -1;
-        for (int h = w * per; h < w * per + per; ++h) {
-            __syncthreads();
-            for (int d = threadIdx.x; d < p.dim; d += 128)
-                q[d] = static_cast<float>(static_cast<const T *>(p.q)[r * p.q_row + h * p.q_head + d]);
-            __syncthreads();
-            const float lse = p.lse_in[r * p.q_heads + h];
-            if (slot < 0 || lse == -INFINITY) continue;
-            sum += expf(p.scale * dot<BF16>(q, reinterpret_cast<const uint4 *>(static_cast<const T *>(p.k) +
-                                                                               slot * p.k_slot + (h / group) * p.k_head),
-                                            p.dim) - lse);
+    pdl_release();
+    const Share share = block_share<KT, Sh::kThreads>(a, &sh.scan);
+    volatile uint32_t *abort = &sh.abort;
+    const uint32_t tmem = sh.tmem;
+    Spans<NQ> spans(p, share);
+    const int32_t per = a.kv_heads / p.weight_heads;   // kv heads of a weight head
+    const int32_t chunks = (a.dim + 15) / 16 * 2, loaded = a.dim / 8;
+    Span16 s;
+    bool ok = true;
+
+    if (warp >= kMmaWarp + 4) {
+        // ------------------------------------------------ copies
+        regs_down<Sh::kOtherRegs>();
+        const int w = warp - kMmaWarp - 4;
+        uint32_t phase = 0, job = 0;
+        while (ok && spans.next(&s)) {
+            uint64_t seen = ~0ull;   // drafted tokens that an accepted row sees
+            if (a.tree_mask && s.t1 * KT > s.ctx) {
+                seen = 0;
+                for (int j = lane; j < a.next_n; j += 32)
+                    if ((s.took >> j) & 1) seen |= static_cast<uint64_t>(__ldg(a.tree_mask + static_cast<int64_t>(s.b) * a.next_n + j));
+                seen = static_cast<uint64_t>(__reduce_or_sync(~0u, static_cast<uint32_t>(seen >> 32))) << 32 |
+                       __reduce_or_sync(~0u, static_cast<uint32_t>(seen));
+            }
+            auto slot_of = [&](int32_t t) -> int32_t {
+                const int32_t pos = t * KT + w * 32 + lane;
+                if (pos >= s.n || pos >= p.width) return -1;
+                if (pos >= s.ctx && !((seen >> (pos - s.ctx)) & 1)) return -1;
+                return static_cast<int32_t>(a.pages.slot(s.b, pos));
+            };
+            int32_t next_slot = slot_of(s.t0);
+            for (int32_t ph = 0; ph < s.phases && ok; ++ph, ++phase) {
+                const int32_t h = s.w * per + ph / s.groups, r0 = (ph % s.groups) * NQ;
+                const int32_t rows = s.rows - r0 < NQ ? s.rows - r0 : NQ, padded = (rows + 15) / 16 * 16;
+                const uint32_t qb = phase & 1;
+                if (phase >= 2) ok = __all_sync(~0u, bar_wait(&sh.q_empty[qb], (phase / 2 - 1) & 1, abort));
+                if (!ok) break;
+                for (int x = w * 32 + lane; x < padded * chunks; x += 128) {
+                    const int32_t r = x / chunks, c = x - r * chunks;
+                    const uint8_t *src = static_cast<const uint8_t *>(a.q);
+                    const bool have = r < rows && c < loaded;
+                    if (have) {
+                        const int32_t k = (r0 + r) / a.group, gq = r0 + r - k * a.group;
+                        src += 2 * ((static_cast<int64_t>(s.b) * a.next_n + nth_bit(s.took, k)) * a.q_row + (h * a.group + gq) * a.q_head) + c * 16;
+                    }
+                    copy16(q_smem + qb * Sh::kQBytes + tile_offset(NQ, r, c), src, have ? 16u : 0u);
+                }
+                bar_arrive_copies(&sh.q_full[qb]);
+                for (int r = w * 32 + lane; r < padded; r += 128) {
+                    float v = INFINITY;
+                    if (r < rows) {
+                        const int32_t k = (r0 + r) / a.group, gq = r0 + r - k * a.group;
+                        const float lse = __ldg(p.lse + (static_cast<int64_t>(s.b) * a.next_n + nth_bit(s.took, k)) * a.q_heads + h * a.group + gq);
+                        v = lse == -INFINITY ? INFINITY : lse * kLog2e;
+                    }
+                    sh.lse2[qb][r] = v;
+                }
+                __syncwarp();
+                if (lane == 0) bar_arrive(&sh.q_full[qb]);
+                for (int32_t t = s.t0; t < s.t1; ++t, ++job) {
+                    const int32_t slot = next_slot;
+                    next_slot = slot_of(t + 1 < s.t1 ? t + 1 : s.t0);
+                    const uint32_t stage = job % Sh::kStages;
+                    if (job >= Sh::kStages) ok = __all_sync(~0u, bar_wait(&sh.empty[stage], (job / Sh::kStages - 1) & 1, abort));
+                    if (!ok) break;
+                    const uint32_t valid = __ballot_sync(~0u, slot >= 0);
+                    if (lane == 0) {
+                        sh.mask[job % kMaskRing][w] = valid;
+                        bar_arrive(&sh.mask_full[job % kMaskRing]);
+                    }
+                    copy_tile<DP, KT>(ring + stage * Sh::kStageBytes, static_cast<const uint8_t *>(a.k) + 2 * h * a.k_head, a.k_slot * 2,
+                                      slot, chunks, loaded, w, lane);
+                    bar_arrive_copies(&sh.full[stage]);
+                }
+            }
+        }
+        copies_land();
+    } else if (warp >= kMmaWarp) {
+        // ------------------------------------------------ matrix products
+        regs_down<Sh::kOtherRegs>();
+        if (warp == kMmaWarp && lane == 0) {
+            uint32_t phase = 0, job = 0;
+            while (ok && spans.next(&s)) {
+                for (int32_t ph = 0; ph < s.phases && ok; ++ph, ++phase) {
+                    const int32_t r0 = (ph % s.groups) * NQ;
+                    const int32_t rows = s.rows - r0 < NQ ? s.rows - r0 : NQ, padded = (rows + 15) / 16 * 16;
+                    const uint32_t desc = mma_desc(BF16, 128, static_cast<uint32_t>(padded), false, a.negative != 0);
+                    const uint32_t qa = q_smem + (phase & 1) * Sh::kQBytes;
+                    ok = bar_wait(&sh.q_full[phase & 1], (phase / 2) & 1, abort);
+                    for (int32_t t = s.t0; t < s.t1 && ok; ++t, ++job) {
+                        const uint32_t stage = job % Sh::kStages, sb = job & 1;
+                        ok = bar_wait(&sh.full[stage], (job / Sh::kStages) & 1, abort);
+                        if (ok && job >= 2) ok = bar_wait(&sh.s_empty[sb], (job / 2 - 1) & 1, abort);
+                        if (!ok) break;
+                        fence_async_reads();
+                        tc_fence_after();
+                        const uint32_t ka = ring + stage * Sh::kStageBytes;
+                        for (int kk = 0; kk < chunks / 2; ++kk)
+                            mma_ss(tmem + sb * 128, smem_desc(ka + (kk >> 2) * (KT * 128) + (kk & 3) * 32, 16, 1024),
+                                   smem_desc(qa + (kk >> 2) * (NQ * 128) + (kk & 3) * 32, 16, 1024), desc, kk > 0);
+                        tc_commit(&sh.s_full[sb]);
+                        tc_commit(&sh.empty[stage]);
+                    }
+                    if (ok) tc_commit(&sh.q_empty[phase & 1]);
+                }
+            }
+            tc_commit(&sh.drain);
+            if (!bar_wait(&sh.drain, 0, abort)) {
+                const long long t0 = clock64();
+                while (!bar_try(&sh.drain, 0) && clock64() - t0 < kWaitCycles) {
+                }
+            }
+        }
+        __syncwarp();
+    } else {
+        // ------------------------------------------------ sums
+        regs_up<Sh::kSumRegs>();
+        const int wg = warp >> 2, key = threadIdx.x & 127;
+        const uint32_t t_s = tmem + (static_cast<uint32_t>(warp & 3) << 21) + wg * 128;
+        float *mine = sums + wg * kSpan * KT + key;
+        uint32_t phase = 0, job = 0;
+        while (ok && spans.next(&s)) {
+            for (int i = 0; i < s.t1 - s.t0; ++i) mine[i * KT] = 0.f;
+            // trees of the accepted tokens, where the span reaches the drafts
+            const bool drafts = s.t1 * KT > s.ctx;
+            if (drafts) {
+                sums_barrier_or(false);
+                const int k = threadIdx.x;
+                if (k < __popcll(s.took)) {
+                    const int t = nth_bit(s.took, k);
+                    sh.tree[k] = a.tree_mask ? static_cast<uint64_t>(__ldg(a.tree_mask + static_cast<int64_t>(s.b) * a.next_n + t))
+                                             : ~0ull >> (63 - t);
+                }
+                sums_barrier_or(false);
+            }
+            for (int32_t ph = 0; ph < s.phases && ok; ++ph, ++phase) {
+                const int32_t r0 = (ph % s.groups) * NQ;
+                const int32_t rows = s.rows - r0 < NQ ? s.rows - r0 : NQ, padded = (rows + 15) / 16 * 16;
+                const float *lse2 = sh.lse2[phase & 1];
+                ok = __all_sync(~0u, bar_wait(&sh.q_full[phase & 1], (phase / 2) & 1, abort));
+                for (int32_t t = s.t0; t < s.t1 && ok; ++t, ++job) {
+                    if ((job & 1) != static_cast<uint32_t>(wg)) continue;
+                    ok = __all_sync(~0u, bar_wait(&sh.mask_full[job % kMaskRing], (job / kMaskRing) & 1, abort) &&
+                                             bar_wait(&sh.s_full[wg], (job / 2) & 1, abort));
+                    if (!ok) break;
+                    tc_fence_after();
+                    const bool valid = (reinterpret_cast<volatile uint32_t *>(sh.mask[job % kMaskRing])[warp & 3] >> lane) & 1;
+                    const int32_t j = t * KT + key - s.ctx;   // the position's drafted token
+                    float add = 0.f;
+                    for (int c0 = 0; c0 < padded; c0 += 16) {
+                        uint32_t x[16];
+                        tmem_load16(t_s + c0, x);
+                        float e[16];
+#pragma unroll
+                        for (int c = 0; c < 16; c += 4) *reinterpret_cast<float4 *>(e + c) = *reinterpret_cast<const float4 *>(lse2 + c0 + c);
+                        tc_wait_ld();
+                        if (t * KT + KT > s.ctx && j >= 0) {
+#pragma unroll
+                            for (int c = 0; c < 16; ++c) {
+                                const int32_t k = (r0 + c0 + c) / a.group;
+                                if (j > 63 || r0 + c0 + c >= s.rows || !((sh.tree[k] >> j) & 1)) e[c] = INFINITY;
+                            }
+                        }
+                        float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int c = 0; c < 16; ++c) part[c & 3] += exp2_fast(fmaf(__uint_as_float(x[c]), a.c, -e[c]));
+                        add += (part[0] + part[1]) + (part[2] + part[3]);
+                    }
+                    if (valid) mine[(t - s.t0) * KT] += add;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&sh.s_empty[wg]);
+                }
+                if (!ok) break;
+                __syncwarp();
+                if (lane == 0) bar_arrive(&sh.q_empty[phase & 1]);
+            }
+            // the two warpgroups' sums, in order; all leave together when one gave up
+            ok = !sums_barrier_or(!ok);
+            if (ok) {
+                float *w = p.weights + (static_cast<int64_t>(s.b) * p.weight_heads + s.w) * p.width;
+                for (int x = threadIdx.x; x < (s.t1 - s.t0) * KT; x += 256) {
+                    const int64_t pos = static_cast<int64_t>(s.t0) * KT + x;
+                    if (pos < s.n && pos < p.width) w[pos] += sums[x] + sums[kSpan * KT + x];
+                }
+            }
+            sums_barrier_or(false);
         }
     }
-    if (pos < p.width) p.weights[(i * p.weight_heads + w) * p.width + pos] += sum;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == kMmaWarp) tmem_free(tmem, 256);
+    if (threadIdx.x == 0 && sh.abort) atomicOr(a.status, kStatusCopyLost);
+}
+
+template <bool BF16, int DP>
+cudaError_t launch_shape(const WeightParams &p, int sms, cudaStream_t stream) {
+    const cudaError_t e = cudaFuncSetAttribute(weights_kernel<BF16, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               static_cast<int>(Shape<DP>::kSmem));
+    if (e != cudaSuccess) return e;
+    return launch_pdl(weights_kernel<BF16, DP>, dim3(static_cast<unsigned>(sms)), Shape<DP>::kThreads, Shape<DP>::kSmem, stream, 1, p);
+}
+
+template <bool BF16>
+cudaError_t launch_weights(const WeightParams &p, int sms, cudaStream_t s) {
+    if (p.a.dim <= 64) return launch_shape<BF16, 64>(p, sms, s);
+    if (p.a.dim <= 128) return launch_shape<BF16, 128>(p, sms, s);
+    return launch_shape<BF16, 256>(p, sms, s);
 }
 
 }  // namespace
@@ -106,20 +375,21 @@ __global__ void __launch_bounds__(128) weights_kernel(WeightParams p) {
 
 using namespace gbtopk;
 
-extern "C" int gbtopk_cache_weights(const void *q, int dtype, int64_t num_rows, int64_t q_row_stride, int64_t q_head_stride,
-                         int32_t q_heads, int32_t kv_heads, int32_t head_dim, const void *k_cache,
-                         int64_t k_slot_stride, int64_t k_head_stride, int64_t num_slots, const float *lse,
-                         const int32_t *page_table, int64_t pt_cols, int64_t pt_row_stride, int32_t page_size,
-                         const int32_t *seq_lens, int32_t next_n, const int64_t *tree_mask,
-                         const int64_t *accept_mask, float scale, float *weights, int32_t weight_heads, int64_t width,
-                         void *workspace, size_t workspace_bytes, void *stream) {
+extern "C" int gbtopk_cache_weights(const void *q, int dtype, int64_t num_rows, int64_t q_row_stride,
+                                    int64_t q_head_stride, int32_t q_heads, int32_t kv_heads, int32_t head_dim,
+                                    const void *k_cache, int64_t k_slot_stride, int64_t k_head_stride, int64_t num_slots,
+                                    const float *lse, const int32_t *page_table, int64_t pt_cols, int64_t pt_row_stride,
+                                    int32_t page_size, const int32_t *seq_lens, int32_t next_n, const int64_t *tree_mask,
+                                    const int64_t *accept_mask, float scale, float *weights, int32_t weight_heads,
+                                    int64_t width, void *workspace, size_t workspace_bytes, void *stream) {
     int rc = check_heads(dtype, num_rows, q_heads, kv_heads, head_dim);
     if (rc != GBTOPK_OK) return rc;
     if (next_n < 1 || num_rows % next_n != 0 || width < 0) return GBTOPK_EINVAL;
     if (weight_heads != 1 && weight_heads != kv_heads) return GBTOPK_EINVAL;
-    if (next_n > GBTOPK_MAX_NEXT_N || width > INT32_MAX) return GBTOPK_EUNSUPPORTED;
+    if (next_n > GBTOPK_MAX_NEXT_N || width > INT32_MAX || num_slots > INT32_MAX) return GBTOPK_EUNSUPPORTED;
     WeightParams p{};
-    if ((rc = check_pages(page_table, pt_cols, pt_row_stride, page_size, num_slots, num_rows / next_n, &p.pages)) != GBTOPK_OK)
+    AttnParams &a = p.a;
+    if ((rc = check_pages(page_table, pt_cols, pt_row_stride, page_size, num_slots, num_rows / next_n, &a.pages)) != GBTOPK_OK)
         return rc;
     if (num_rows == 0 || width == 0) return GBTOPK_OK;
     if (!seq_lens || !lse || !weights) return GBTOPK_EINVAL;
@@ -127,32 +397,36 @@ extern "C" int gbtopk_cache_weights(const void *q, int dtype, int64_t num_rows, 
     if ((rc = check_rows(k_cache, k_slot_stride, k_head_stride, num_slots > 0)) != GBTOPK_OK) return rc;
     if (!aligned_to(lse, 4) || !aligned_to(weights, 16)) return GBTOPK_EALIGN;
     if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < kWsHeaderBytes) return GBTOPK_EWORKSPACE;
-    p.q = q;
-    p.q_row = q_row_stride;
-    p.q_head = q_head_stride;
-    p.k = k_cache;
-    p.k_slot = k_slot_stride;
-    p.k_head = k_head_stride;
-    p.num_rows = num_rows;
-    p.q_heads = q_heads;
-    p.kv_heads = kv_heads;
-    p.dim = head_dim;
-    p.scale = scale;
-    p.seq_lens = seq_lens;
-    p.next_n = next_n;
-    p.tree_mask = tree_mask;
+    a.q = q;
+    a.q_row = q_row_stride;
+    a.q_head = q_head_stride;
+    a.k = k_cache;
+    a.k_slot = k_slot_stride;
+    a.k_head = k_head_stride;
+    a.seq_lens = seq_lens;
+    a.tree_mask = tree_mask;
+    a.requests = static_cast<int32_t>(num_rows / next_n);
+    a.next_n = next_n;
+    a.q_heads = q_heads;
+    a.kv_heads = kv_heads;
+    a.group = q_heads / kv_heads;
+    a.dim = head_dim;
+    a.row_tiles = 1;
+    a.request_units = weight_heads;
+    a.c = fmaxf(fabsf(scale) * kLog2e, FLT_MIN);
+    a.negative = scale < 0.f;
+    a.status = static_cast<uint32_t *>(workspace);
     p.accept_mask = accept_mask;
-    p.lse_in = lse;
+    p.lse = lse;
     p.weights = weights;
     p.weight_heads = weight_heads;
     p.width = width;
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+        return GBTOPK_ECUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const dim3 grid(static_cast<unsigned>((width + 127) / 128), static_cast<unsigned>(num_rows / next_n),
-                    static_cast<unsigned>(weight_heads));
-    if (grid.y > 65535) return GBTOPK_EUNSUPPORTED;
-    return (dtype == GBTOPK_BF16 ? launch_pdl(weights_kernel<true>, grid, 128, 0, s, 1, p)
-                                 : launch_pdl(weights_kernel<false>, grid, 128, 0, s, 1, p)) == cudaSuccess
+    return (dtype == GBTOPK_BF16 ? launch_weights<true>(p, sms, s) : launch_weights<false>(p, sms, s)) == cudaSuccess
                ? GBTOPK_OK
                : GBTOPK_ECUDA;
 }
-
