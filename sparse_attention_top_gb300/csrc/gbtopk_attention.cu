@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(co
                 last_b = u.b;
                 if (p.seq_lens && p.tree_mask) {
                     const int64_t *tm = p.tree_mask + static_cast<int64_t>(u.b) * p.next_n;
-                    uint64_t m = lane < p.next_n ? static_cast<uint64_t>(__ldg(tm + lane)) : 0;
-                    if (lane + 32 < p.next_n) m |= static_cast<uint64_t>(__ldg(tm + lane + 32));
+                    uint64_t m = lane < p.next_n ? static_cast<uint64_t>(fetch(tm + lane)) : 0;
+                    if (lane + 32 < p.next_n) m |= static_cast<uint64_t>(fetch(tm + lane + 32));
                     seen = static_cast<uint64_t>(__reduce_or_sync(~0u, static_cast<uint32_t>(m >> 32))) << 32 |
                            __reduce_or_sync(~0u, static_cast<uint32_t>(m));
                 }
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(co
             const int32_t pos = t * KT + w * (KT / 4) + (lane & (KT / 4 - 1));
             if (pos >= u.span.n) return -1;
             if (!p.seq_lens) {
-                const int32_t s = __ldg(p.indices + u.b * p.idx_row + pos);
+                const int32_t s = fetch(p.indices + u.b * p.idx_row + pos);
                 return s < p.pages.num_slots ? s : -1;
             }
             if (pos >= u.span.ctx && !((seen >> (pos - u.span.ctx)) & 1)) return -1;
@@ -264,7 +264,7 @@ __global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(co
             const int64_t r = static_cast<int64_t>(u.b) * p.next_n + t;
             const bool active = mt * Sh::kRows + wg * 128 + (warp & 3) * 32 < rows;   // any row of the warp
             uint64_t tree = 0;
-            if (mine && p.seq_lens) tree = p.tree_mask ? static_cast<uint64_t>(__ldg(p.tree_mask + r)) : (~0ull >> (63 - t));
+            if (mine && p.seq_lens) tree = p.tree_mask ? static_cast<uint64_t>(fetch(p.tree_mask + r)) : (~0ull >> (63 - t));
             float m = -INFINITY, l = 0.f;
             for (int32_t i = u.t0; i < u.t1; ++i, ++tile, job += W) {
                 const uint32_t sb = job & 1, ph = (job >> 1) & 1;

@@ -1,11 +1,26 @@
 // Eviction from a paged cache by accumulated weight (gbtopk_cache_evict).
+//
+// evict_select_kernel: a cluster of 1 to 8 blocks for each (request, weight
+// head).  Each block stages the order-preserving keys of its slice of the
+// survivors in shared memory, four rounds of 8-bit radix histograms (summed
+// over the cluster through distributed shared memory) give the key at the
+// budget, and one ordered pass (warp segments, ballots) writes the kept
+// positions in place.  evict_move_kernel then copies the kept rows, blocks of
+// about 32 KB of keys and values.
+#include <cooperative_groups.h>
+
 #include "gbtopk_decode.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace gbtopk {
 namespace {
 
-constexpr int kEvictThreads = 1024;
+constexpr int kSelectThreads = 1024;
+constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kMoveThreads = 256;
+constexpr int kStagedKeys = 49152;   // keys a block can stage (192 KB)
+constexpr int kMaxCluster = 8;
 
 struct EvictParams {
     const float *weights;
@@ -19,6 +34,9 @@ struct EvictParams {
     int32_t kv_heads, row_chunks;  // 16-byte chunks of one (slot, head) row
     int32_t *kept, *new_lens;
     float *out_weights;
+    int32_t move_rows;     // kept positions a block of evict_move_kernel copies
+    int32_t row_blocks;
+    int32_t staged;        // keys staged in shared memory (else read again)
 };
 
 __device__ __forceinline__ uint32_t weight_key(float w) {
@@ -26,117 +44,220 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-// Sum over the block of `v` and, in *before, the sum over lower threads.
-__device__ uint32_t block_scan(uint32_t v, uint32_t *warps, uint32_t *before) {
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint32_t s = v;
-    for (int o = 1; o < 32; o <<= 1) {
-        const uint32_t x = __shfl_up_sync(~0u, s, o);
-        if (lane >= static_cast<uint32_t>(o)) s += x;
-    }
-    __syncthreads();
-    if (lane == 31) warps[warp] = s;
-    __syncthreads();
-    uint32_t base = 0, all = 0;
-    for (uint32_t w = 0; w < kEvictThreads / 32; ++w) {
-        base += w < warp ? warps[w] : 0;
-        all += warps[w];
-    }
-    *before = base + s - v;
-    return all;
-}
+struct SelectShared {
+    uint32_t hist[256];
+    uint32_t gt[kSelectWarps], eq[kSelectWarps];   // kept for sure, equal to the key: by warp, then before each
+    uint32_t all_gt[kMaxCluster], all_eq[kMaxCluster];
+    int32_t draft[64];
+    uint32_t bin, need, count;
+};
 
-// One block for each (request, weight head).
-__global__ void __launch_bounds__(kEvictThreads) evict_select_kernel(EvictParams p) {
-    __shared__ uint32_t hist[256], scan[kEvictThreads / 32], pick[2];
-    __shared__ int32_t draft[64];
+__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
+    extern __shared__ uint32_t keys[];
+    __shared__ SelectShared sh;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int size = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
+    const int tid = static_cast<int>(threadIdx.x), warp = tid >> 5, lane = tid & 31;
     pdl_wait();
-    const int64_t i = blockIdx.x / p.heads, row = blockIdx.x;
+    pdl_release();
+    const int64_t row = blockIdx.x / size, i = row / p.heads;
     const float *w = p.weights + row * p.width;
     int32_t *kept = p.kept + row * p.budget;
     float *out_w = p.out_weights + row * p.width;
-    const int64_t len = p.seq_lens[i] > 0 ? p.seq_lens[i] : 0;
+    const int32_t raw = p.seq_lens[i], len = raw > 0 ? raw : 0;
     const int64_t room = p.from.cols * p.from.page.d < p.width ? p.from.cols * p.from.page.d : p.width;
     const int32_t lim = static_cast<int32_t>(len < room ? len : room);
     // survivors in order: positions 0 .. a - 1, then draft[0 .. nd - 1]
     int32_t a = lim, nd = 0;
     if (p.accept_mask) {
-        const int32_t ctx = static_cast<int32_t>(len - p.next_n);
+        const int32_t ctx = len - p.next_n;
         a = ctx < 0 ? 0 : (ctx < lim ? ctx : lim);
-        const uint64_t bits = static_cast<uint64_t>(p.accept_mask[i]);
-        for (int j = 0; j < p.next_n; ++j) {
-            if (!((bits >> j) & 1) || ctx + j < 0 || ctx + j >= lim) continue;
-            if (threadIdx.x == 0) draft[nd] = ctx + j;
-            ++nd;
-        }
-        __syncthreads();
+        const int32_t lo = ctx < 0 ? -ctx : 0, hi = lim - ctx < p.next_n ? lim - ctx : p.next_n;
+        uint64_t bits = static_cast<uint64_t>(p.accept_mask[i]);
+        bits = hi > lo ? bits & (~0ull >> (64 - hi)) & (~0ull << lo) : 0;
+        nd = __popcll(bits);
+        if (tid < 64 && ((bits >> tid) & 1)) sh.draft[__popcll(bits & ((1ull << tid) - 1))] = ctx + tid;
     }
     const int32_t n = a + nd, m = n < p.budget ? n : p.budget;
     const int32_t recent = p.recent < p.budget ? p.recent : p.budget;
-    const int32_t cut = n <= p.budget ? 0 : n - recent;  // survivors below the cut compete
-    uint32_t t = 0, need = static_cast<uint32_t>(n <= p.budget ? 0 : p.budget - recent);
-    auto pos = [&](int32_t s) { return s < a ? s : draft[s - a]; };
-    for (int shift = 24; shift >= 0 && need; shift -= 8) {
-        for (int b = threadIdx.x; b < 256; b += kEvictThreads) hist[b] = 0;
+    const int32_t cut = n <= p.budget ? 0 : n - recent;   // survivors below the cut compete
+    uint32_t need = n <= p.budget ? 0u : static_cast<uint32_t>(p.budget - recent);
+    // the block's slice of the survivors
+    const int32_t each = (n + size - 1) / size;
+    const int32_t s0 = rank * each < n ? rank * each : n, s1 = s0 + each < n ? s0 + each : n;
+    const int32_t c1 = s1 < cut ? s1 : (s0 < cut ? cut : s0);   // its competitors: s0 .. c1 - 1
+    // also: every block of the cluster runs before any other writes to it
+    if (size > 1) cluster.sync();
+    else __syncthreads();
+    auto pos = [&](int32_t s) { return s < a ? s : sh.draft[s - a]; };
+    auto key = [&](int32_t s) { return p.staged ? keys[s - s0] : weight_key(w[pos(s)]); };
+    if (p.staged && need)
+        for (int32_t s = s0 + tid; s < c1; s += kSelectThreads) keys[s - s0] = weight_key(w[pos(s)]);
+    // the key t at the budget: keys above it are kept, and the first `ties`
+    // equal to it (with `whole` every key of at least t)
+    uint32_t t = 0;
+    bool whole = false;
+    for (int shift = 24; shift >= 0 && need && !whole; shift -= 8) {
+        if (tid < 256) sh.hist[tid] = 0;
         __syncthreads();
-        for (int32_t s = threadIdx.x; s < cut; s += kEvictThreads) {
-            const uint32_t k = weight_key(w[pos(s)]);
-            if (shift == 24 || (k >> (shift + 8)) == (t >> (shift + 8))) atomicAdd(hist + ((k >> shift) & 255), 1u);
+        for (int32_t s = s0 + tid; s < c1; s += kSelectThreads) {
+            const uint32_t k = key(s);
+            if (shift == 24 || (k >> (shift + 8)) == (t >> (shift + 8))) atomicAdd(&sh.hist[(k >> shift) & 255], 1u);
         }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            int b = 255;
-            for (; b > 0 && need > hist[b]; --b) need -= hist[b];
-            pick[0] = static_cast<uint32_t>(b);
-            pick[1] = need;
+        if (size > 1) cluster.sync();
+        else __syncthreads();
+        if (warp == 0) {
+            // eight bins a lane, the highest in lane 0
+            uint32_t h[8], sum = 0;
+            for (int b = 0; b < 8; ++b) {
+                h[b] = 0;
+                for (int r = 0; r < size; ++r) h[b] += cluster.map_shared_rank(sh.hist, r)[255 - (lane * 8 + b)];
+                sum += h[b];
+            }
+            uint32_t inc = sum;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(~0u, inc, o);
+                if (lane >= o) inc += x;
+            }
+            const int owner = __ffs(__ballot_sync(~0u, inc >= need)) - 1;
+            if (lane == owner) {
+                uint32_t left = need - (inc - sum);
+                int b = 0;
+                while (left > h[b]) left -= h[b++];
+                sh.bin = static_cast<uint32_t>(255 - (lane * 8 + b));
+                sh.need = left;
+                sh.count = h[b];
+            }
         }
-        __syncthreads();
-        t |= pick[0] << shift;
-        need = pick[1];
+        if (size > 1) cluster.sync();
+        else __syncthreads();
+        t |= sh.bin << shift;
+        need = sh.need;
+        whole = need == sh.count;
     }
-    const bool any = p.budget > recent && cut > 0;  // keys above t, and the first `need` equal to it
-    uint32_t ties = 0, at = 0;
-    for (int32_t s0 = 0; s0 < n; s0 += kEvictThreads) {
-        const int32_t s = s0 + static_cast<int32_t>(threadIdx.x);
-        const uint32_t k = s < cut ? weight_key(w[pos(s)]) : 0;
-        const bool tie = s < cut && any && k == t;
-        uint32_t before, nb;
-        const uint32_t all_ties = block_scan(tie ? 1u : 0u, scan, &before);
-        const bool keep = s < n && (s >= cut || (any && k > t) || (tie && ties + before < need));
-        const uint32_t all = block_scan(keep ? 1u : 0u, scan, &nb);
-        if (keep) {
-            kept[at + nb] = pos(s);
-            out_w[at + nb] = w[pos(s)];
-        }
-        ties += all_ties;
-        at += all;
+    const bool compete = cut > 0 && p.budget > recent;
+    // ordered pass: each warp a segment of the slice
+    const int32_t seg = ((s1 - s0 + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
+    const int32_t b0 = s0 + warp * seg < s1 ? s0 + warp * seg : s1, b1 = b0 + seg < s1 ? b0 + seg : s1;
+    auto classify = [&](int32_t s, bool *eq) {
+        *eq = false;
+        if (s >= b1) return false;
+        if (s >= cut) return true;
+        if (!compete) return false;
+        const uint32_t k = key(s);
+        *eq = !whole && k == t;
+        return whole ? k >= t : k > t;
+    };
+    uint32_t gt = 0, eq = 0;
+    for (int32_t s = b0; s < b1; s += 32) {
+        bool e;
+        const bool g = classify(s + lane, &e);
+        gt += __popc(__ballot_sync(~0u, g));
+        eq += __popc(__ballot_sync(~0u, e));
     }
-    for (int64_t j = m + threadIdx.x; j < p.budget; j += kEvictThreads) kept[j] = -1;
-    for (int64_t j = m + threadIdx.x; j < p.width; j += kEvictThreads) out_w[j] = 0.f;
-    if (threadIdx.x == 0 && row % p.heads == 0) p.new_lens[i] = m;
+    if (lane == 0) {
+        sh.gt[warp] = gt;
+        sh.eq[warp] = eq;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        uint32_t g = sh.gt[lane], e = sh.eq[lane], gi = g, ei = e;
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t x = __shfl_up_sync(~0u, gi, o), y = __shfl_up_sync(~0u, ei, o);
+            if (lane >= o) {
+                gi += x;
+                ei += y;
+            }
+        }
+        sh.gt[lane] = gi - g;
+        sh.eq[lane] = ei - e;
+        if (lane == 31)
+            for (int r = 0; r < size; ++r) {
+                cluster.map_shared_rank(sh.all_gt, r)[rank] = gi;
+                cluster.map_shared_rank(sh.all_eq, r)[rank] = ei;
+            }
+    }
+    if (size > 1) cluster.sync();
+    else __syncthreads();
+    gt = sh.gt[warp];
+    eq = sh.eq[warp];
+    for (int r = 0; r < rank; ++r) {
+        gt += sh.all_gt[r];
+        eq += sh.all_eq[r];
+    }
+    const uint32_t below = (1u << lane) - 1;
+    for (int32_t s = b0; s < b1; s += 32) {
+        bool e;
+        const bool g = classify(s + lane, &e);
+        const uint32_t gm = __ballot_sync(~0u, g), em = __ballot_sync(~0u, e);
+        const uint32_t eb = eq + __popc(em & below);   // equal keys before this one
+        if (g || (e && eb < need)) {
+            const uint32_t at = gt + __popc(gm & below) + (eb < need ? eb : need);
+            const int32_t q = pos(s + lane);
+            kept[at] = q;
+            out_w[at] = w[q];
+        }
+        gt += __popc(gm);
+        eq += __popc(em);
+    }
+    for (int64_t j = m + rank * kSelectThreads + tid; j < p.budget; j += size * kSelectThreads) kept[j] = -1;
+    for (int64_t j = m + rank * kSelectThreads + tid; j < p.width; j += size * kSelectThreads) out_w[j] = 0.f;
+    if (rank == 0 && tid == 0 && row % p.heads == 0) p.new_lens[i] = m;
 }
 
-// One thread for each 16-byte chunk of the kept rows of keys and values.
-__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictParams p) {
+// Copies kept rows: row_blocks blocks of move_rows kept positions for each
+// (request, weight head).  Consecutive threads copy consecutive 16-byte chunks of a
+// position's heads; two keys' and two values' chunks are in flight a thread.
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_constant__ EvictParams p) {
+    constexpr int kUnroll = 2;
+    __shared__ int64_t src[64], dst[64];
     pdl_wait();
-    const int64_t i = blockIdx.y;
+    pdl_release();
+    const int64_t row = blockIdx.x / p.row_blocks, i = row / p.heads;
+    const int32_t j0 = static_cast<int32_t>(blockIdx.x % p.row_blocks) * p.move_rows;
     const int32_t m = p.new_lens[i];
-    const int32_t per = p.kv_heads * p.row_chunks;
-    const int64_t total = static_cast<int64_t>(m) * per;
-    for (int64_t x = static_cast<int64_t>(blockIdx.x) * kMoveThreads + threadIdx.x; x < total;
-         x += static_cast<int64_t>(gridDim.x) * kMoveThreads) {
-        const int32_t j = static_cast<int32_t>(x / per), c = static_cast<int32_t>(x % per);
-        const int32_t h = c / p.row_chunks, b = c % p.row_chunks;
-        const int32_t pos = p.kept[(i * p.heads + (p.heads == 1 ? 0 : h)) * p.budget + j];
-        const int64_t src = p.from.slot(i, pos), dst = p.to.slot(i, j);
-        if (dst < 0) continue;
-        for (int kv = 0; kv < 2; ++kv) {
-            uint8_t *base = p.cache[kv] + h * p.head_bytes[kv] + b * 16;
-            const uint4 v = src < 0 ? make_uint4(0, 0, 0, 0)
-                                    : *reinterpret_cast<const uint4 *>(base + src * p.slot_bytes[kv]);
-            *reinterpret_cast<uint4 *>(base + dst * p.slot_bytes[kv]) = v;
-        }
+    const int32_t rows = m - j0 < p.move_rows ? m - j0 : p.move_rows;
+    if (rows <= 0) return;
+    if (static_cast<int32_t>(threadIdx.x) < rows) {
+        const int32_t j = j0 + static_cast<int32_t>(threadIdx.x);
+        src[threadIdx.x] = p.from.slot(i, p.kept[row * p.budget + j]);
+        dst[threadIdx.x] = p.to.slot(i, j);
     }
+    __syncthreads();
+    const int32_t h0 = p.heads == 1 ? 0 : static_cast<int32_t>(row % p.heads), heads = p.heads == 1 ? p.kv_heads : 1;
+    const int32_t per = heads * p.row_chunks, total = rows * per;
+    for (int32_t x0 = threadIdx.x; x0 < total; x0 += kMoveThreads * kUnroll) {
+        uint4 v[kUnroll][2];
+        uint8_t *to[kUnroll][2];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const int32_t x = x0 + u * kMoveThreads;
+            to[u][0] = nullptr;
+            if (x >= total) continue;
+            const int32_t j = x / per, c = x - j * per, h = h0 + c / p.row_chunks, b = c % p.row_chunks;
+            const int64_t s = src[j], d = dst[j];
+            if (d < 0) continue;
+#pragma unroll
+            for (int kv = 0; kv < 2; ++kv) {
+                uint8_t *base = p.cache[kv] + h * p.head_bytes[kv] + b * 16;
+                v[u][kv] = s < 0 ? make_uint4(0, 0, 0, 0) : *reinterpret_cast<const uint4 *>(base + s * p.slot_bytes[kv]);
+                to[u][kv] = base + d * p.slot_bytes[kv];
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u)
+            if (to[u][0])
+#pragma unroll
+                for (int kv = 0; kv < 2; ++kv) *reinterpret_cast<uint4 *>(to[u][kv]) = v[u][kv];
+    }
+}
+
+// Blocks of a selection's cluster: enough to stage the row, and for few rows
+// as many as leave each block 4096 weights.
+int select_cluster(int64_t rows, int64_t width) {
+    int c = 1;
+    while (c < kMaxCluster && ((width + c - 1) / c > kStagedKeys || (rows * c * 2 <= 152 && width / c > 4096))) c *= 2;
+    return c;
 }
 
 bool overlap(const void *a, size_t an, const void *b, size_t bn) {
@@ -164,8 +285,7 @@ extern "C" int gbtopk_cache_evict(const float *weights, int64_t num_requests, in
     if (num_requests > 1 && (pt_row_stride < pt_cols || out_pt_row_stride < out_pt_cols)) return GBTOPK_EINVAL;
     if (out_pt_cols < (static_cast<int64_t>(budget) + page_size - 1) / page_size) return GBTOPK_EINVAL;
     if (elem_bytes != 2 && elem_bytes != 4) return GBTOPK_EUNSUPPORTED;
-    if (next_n > GBTOPK_MAX_NEXT_N || width > INT32_MAX || num_requests > 65535 ||
-        num_requests * weight_heads > INT32_MAX || head_dim > (1 << 20) || kv_heads > 65535 ||
+    if (next_n > GBTOPK_MAX_NEXT_N || width > INT32_MAX || num_requests > INT32_MAX / weight_heads || head_dim > (1 << 20) || kv_heads > 65535 ||
         static_cast<int64_t>(kv_heads) * head_dim > (1 << 26))
         return GBTOPK_EUNSUPPORTED;
     if (num_requests == 0) return GBTOPK_OK;
@@ -212,10 +332,20 @@ extern "C" int gbtopk_cache_evict(const float *weights, int64_t num_requests, in
     p.new_lens = new_lens;
     p.out_weights = out_weights;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (launch_pdl(evict_select_kernel, dim3(static_cast<unsigned>(num_requests * weight_heads)), kEvictThreads, 0, s, 1,
-                   p) != cudaSuccess)
+    const int64_t rows = num_requests * weight_heads;
+    const int cluster = select_cluster(rows, width);
+    const int64_t slice = (width + cluster - 1) / cluster;
+    p.staged = slice <= kStagedKeys;
+    const size_t smem = p.staged ? static_cast<size_t>(slice) * 4 : 0;
+    // 32 KB of keys and values a block, at most 64 positions
+    const int64_t bytes = 2ll * head_dim * es * (weight_heads == 1 ? kv_heads : 1);
+    p.move_rows = static_cast<int32_t>(bytes >= 32768 ? 1 : 32768 / bytes > 64 ? 64 : 32768 / bytes);
+    p.row_blocks = (budget + p.move_rows - 1) / p.move_rows;
+    if (rows * p.row_blocks > INT32_MAX || rows * cluster > INT32_MAX) return GBTOPK_EUNSUPPORTED;
+    if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedKeys * 4) != cudaSuccess)
         return GBTOPK_ECUDA;
-    const int64_t most = (static_cast<int64_t>(budget) * kv_heads * p.row_chunks + kMoveThreads - 1) / kMoveThreads;
-    const dim3 grid(static_cast<unsigned>(most < 4096 ? most : 4096), static_cast<unsigned>(num_requests));
-    return launch_pdl(evict_move_kernel, grid, kMoveThreads, 0, s, 1, p) == cudaSuccess ? GBTOPK_OK : GBTOPK_ECUDA;
+    if (launch_pdl(evict_select_kernel, dim3(static_cast<unsigned>(rows * cluster)), kSelectThreads, smem, s, cluster, p) !=
+        cudaSuccess)
+        return GBTOPK_ECUDA;
+    return launch_pdl(evict_move_kernel, dim3(static_cast<unsigned>(rows * p.row_blocks)), kMoveThreads, 0, s, 1, p) == cudaSuccess ? GBTOPK_OK : GBTOPK_ECUDA;
 }

@@ -15,6 +15,9 @@
 
 namespace gbtopk {
 
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
 // Unsigned division by a launch-constant divisor: q = (x * mul) >> (32 +
 // shift) for 0 <= x < 2^31, with mul = ceil(2^(32+shift) / d) and shift =
 // ceil(log2 d) - 1 (Granlund and Montgomery, "Division by invariant integers
@@ -38,6 +41,13 @@ struct FastDiv {
     }
 };
 
+// An ordinary load of data that the stream's previous kernel may have
+// written: it stays behind pdl_wait, which a load of constant data need not.
+template <typename T>
+__device__ __forceinline__ T fetch(const T *p) {
+    return *p;
+}
+
 // The page table of a batch of requests over one cache.
 struct Paging {
     const int32_t *table;
@@ -49,7 +59,7 @@ struct Paging {
     __device__ __forceinline__ int64_t slot(int64_t i, int32_t p) const {
         const uint32_t c = page.div(static_cast<uint32_t>(p));
         if (p < 0 || static_cast<int64_t>(c) >= cols) return -1;
-        const int64_t id = __ldg(table + i * row_stride + c);
+        const int64_t id = fetch(table + i * row_stride + c);
         const int64_t s = id * page.d + (static_cast<uint32_t>(p) - c * page.d);
         return id >= 0 && s < num_slots ? s : -1;
     }

@@ -8,9 +8,6 @@
 
 namespace gbtopk {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
-
 struct AttnParams {
     const void *q, *k, *v;
     int64_t q_row, q_head, k_slot, k_head, v_slot, v_head;  // strides in elements
@@ -40,7 +37,7 @@ struct Span {
 
 __device__ __forceinline__ Span span_of(const AttnParams &p, int32_t b) {
     if (!p.seq_lens) return Span{p.top_k, INT32_MAX};
-    const int32_t raw = __ldg(p.seq_lens + b);
+    const int32_t raw = fetch(p.seq_lens + b);
     const int32_t len = raw > 0 ? raw : 0;
     const int64_t room = p.pages.cols * p.pages.page.d;
     return Span{static_cast<int32_t>(len < room ? len : room), len - p.next_n};

@@ -98,7 +98,7 @@ struct Spans {
             s->t1 = walk.u.t1 - t > kSpan ? t + kSpan : walk.u.t1;
             t = s->t1;
             const uint64_t all = ~0ull >> (64 - p.a.next_n);
-            s->took = p.accept_mask ? static_cast<uint64_t>(__ldg(p.accept_mask + s->b)) & all : all;
+            s->took = p.accept_mask ? static_cast<uint64_t>(fetch(p.accept_mask + s->b)) & all : all;
             s->rows = __popcll(s->took) * p.a.group;
             s->groups = (s->rows + NQ - 1) / NQ;
             s->phases = s->groups * (p.a.kv_heads / p.weight_heads);
@@ -179,7 +179,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
             if (a.tree_mask && s.t1 * KT > s.ctx) {
                 seen = 0;
                 for (int j = lane; j < a.next_n; j += 32)
-                    if ((s.took >> j) & 1) seen |= static_cast<uint64_t>(__ldg(a.tree_mask + static_cast<int64_t>(s.b) * a.next_n + j));
+                    if ((s.took >> j) & 1) seen |= static_cast<uint64_t>(fetch(a.tree_mask + static_cast<int64_t>(s.b) * a.next_n + j));
                 seen = static_cast<uint64_t>(__reduce_or_sync(~0u, static_cast<uint32_t>(seen >> 32))) << 32 |
                        __reduce_or_sync(~0u, static_cast<uint32_t>(seen));
             }
@@ -211,7 +211,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
                     float v = INFINITY;
                     if (r < rows) {
                         const int32_t k = (r0 + r) / a.group, gq = r0 + r - k * a.group;
-                        const float lse = __ldg(p.lse + (static_cast<int64_t>(s.b) * a.next_n + nth_bit(s.took, k)) * a.q_heads + h * a.group + gq);
+                        const float lse = fetch(p.lse + (static_cast<int64_t>(s.b) * a.next_n + nth_bit(s.took, k)) * a.q_heads + h * a.group + gq);
                         v = lse == -INFINITY ? INFINITY : lse * kLog2e;
                     }
                     sh.lse2[qb][r] = v;
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
                 const int k = threadIdx.x;
                 if (k < __popcll(s.took)) {
                     const int t = nth_bit(s.took, k);
-                    sh.tree[k] = a.tree_mask ? static_cast<uint64_t>(__ldg(a.tree_mask + static_cast<int64_t>(s.b) * a.next_n + t))
+                    sh.tree[k] = a.tree_mask ? static_cast<uint64_t>(fetch(a.tree_mask + static_cast<int64_t>(s.b) * a.next_n + t))
                                              : ~0ull >> (63 - t);
                 }
                 sums_barrier_or(false);
