@@ -115,8 +115,8 @@ __global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(co
         const int64_t k_bytes = p.k_slot * 2, v_bytes = p.v_slot * 2;
         int32_t last_b = -1;
         uint64_t seen = ~0ull;   // drafted tokens that some row of the request sees
-        // slot of this lane's row of tile t of unit u (KT / 4 rows a warp), -1 where there is none
-        auto slot_of = [&](const Unit &u, int32_t t) -> int32_t {
+        // where this lane's row of tile t of unit u lies (KT / 4 rows a warp)
+        auto place_of = [&](const Unit &u, int32_t t) -> Paging::Place {
             if (u.b != last_b) {
                 last_b = u.b;
                 if (p.seq_lens && p.tree_mask) {
@@ -128,20 +128,18 @@ __global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(co
                 }
             }
             const int32_t pos = t * KT + w * (KT / 4) + (lane & (KT / 4 - 1));
-            if (pos >= u.span.n) return -1;
-            if (!p.seq_lens) {
-                const int32_t s = fetch(p.indices + u.b * p.idx_row + pos);
-                return s < p.pages.num_slots ? s : -1;
-            }
-            if (pos >= u.span.ctx && !((seen >> (pos - u.span.ctx)) & 1)) return -1;
-            return static_cast<int32_t>(p.pages.slot(u.b, pos));
+            if (pos >= u.span.n) return Paging::Place{-1, 0};
+            if (!p.seq_lens) return Paging::Place{fetch(p.indices + u.b * p.idx_row + pos), 0};   // pages of one slot
+            if (pos >= u.span.ctx && !((seen >> (pos - u.span.ctx)) & 1)) return Paging::Place{-1, 0};
+            return p.pages.place(u.b, pos);
         };
         uint32_t unit = 0, g = 0, tile = 0;   // counters of units, ring stages and tiles
         uint32_t stage = 0, lap = 0;
         bool ok = true;
         Walk<KT> ahead = walk;                // the tile after the one being copied
         int32_t ahead_t = ahead.more() ? ahead.u.t0 : 0;
-        int32_t next_slot = ahead.more() ? slot_of(ahead.u, ahead_t) : -1;
+        Paging::Place next{-1, 0};
+        if (ahead.more()) next = place_of(ahead.u, ahead_t);
         for (; walk.more() && ok; walk.next(), ++unit) {
             const Unit u = walk.u;
             const int32_t h = u.hm / p.row_tiles, r0 = (u.hm - h * p.row_tiles) * Sh::kRows;
@@ -158,12 +156,13 @@ __global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(co
             }
             bar_arrive_copies(&sh.q_full);
             for (int32_t t = u.t0; t < u.t1; ++t, ++tile) {
-                const int32_t slot = next_slot;
+                const int32_t slot = static_cast<int32_t>(p.pages.slot(next));
                 if (++ahead_t == ahead.u.t1) {
                     ahead.next();
                     ahead_t = ahead.more() ? ahead.u.t0 : 0;
                 }
-                next_slot = ahead.more() ? slot_of(ahead.u, ahead_t) : -1;
+                next.id = -1;
+                if (ahead.more()) next = place_of(ahead.u, ahead_t);
                 for (int kv = 0; kv < 2; ++kv, ++g) {
                     if (g >= Sh::kStages) ok = __all_sync(~0u, bar_wait(&sh.empty[stage], (lap - 1) & 1, abort));
                     if (!ok) break;
@@ -401,42 +400,54 @@ __global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(co
     if (threadIdx.x == 0 && sh.abort) atomicOr(p.status, kStatusCopyLost);
 }
 
-// Joins the partial results of units that span blocks: blocks of one warp a
-// row, grid (units, row groups).
+// Joins the partial results of units that span blocks: one warp a row, blocks
+// of kCombineRows rows, grid (units, row blocks).
 constexpr int kCombineThreads = 256;
+constexpr int kCombineRows = 32;
 
 template <bool BF16, int DP, int W>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ AttnParams p, int32_t grid) {
     constexpr int KT = Shape<DP, W>::KT, kRows = Shape<DP, W>::kRows;
     __shared__ ScanScratch scan;
     pdl_wait();
+    pdl_release();
     const int32_t hms = p.request_units;
     const int32_t b = static_cast<int32_t>(blockIdx.x / hms), hm = static_cast<int32_t>(blockIdx.x % hms);
-    const int64_t total = sum_tiles<KT, kCombineThreads>(p, p.requests, &scan);
+    int64_t before;
+    const int64_t total = sum_tiles<KT, kCombineThreads>(p, b, &before, &scan);
     const int64_t per = (total + grid - 1) / grid;
     const int32_t tiles = tiles_of<KT>(span_of(p, b));
-    const int64_t start = sum_tiles<KT, kCombineThreads>(p, b, &scan) + static_cast<int64_t>(hm) * tiles;
-    const int64_t c0 = start / per, c1 = (start + tiles - 1) / per;
+    const int64_t start = before + static_cast<int64_t>(hm) * tiles;
+    const int32_t c0 = static_cast<int32_t>(start / per), c1 = static_cast<int32_t>((start + tiles - 1) / per);
     if (c0 == c1) return;
     const int32_t h = hm / p.row_tiles, r0 = (hm - h * p.row_tiles) * kRows;
-    const int32_t rows = p.next_n * p.group;
+    const int32_t rows = p.next_n * p.group - r0 < kRows ? p.next_n * p.group - r0 : kRows;
     const int lane = threadIdx.x & 31;
-    for (int32_t row = static_cast<int32_t>(blockIdx.y * (kCombineThreads / 32) + (threadIdx.x >> 5)); row < kRows && r0 + row < rows;
-         row += static_cast<int32_t>(gridDim.y * (kCombineThreads / 32))) {
-        auto at = [&](int64_t c) { return (2 * c + (c == c0 ? 1 : 0)) * kRows + row; };
+    const int32_t first = static_cast<int32_t>(blockIdx.y) * kCombineRows;
+    for (int32_t row = first + static_cast<int32_t>(threadIdx.x >> 5); row < rows && row < first + kCombineRows; row += kCombineThreads / 32) {
+        auto at = [&](int32_t c) { return (2ll * c + (c == c0 ? 1 : 0)) * kRows + row; };
         float m = -INFINITY;
-        for (int64_t c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[at(c)].x);
+        for (int32_t c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[at(c)].x);
         for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
         const float mm = m == -INFINITY ? 0.f : m;
         float l = 0.f, acc[DP / 32] = {};
-        for (int64_t c = c0; c <= c1; ++c) {
-            const float2 ml = p.part_ml[at(c)];
-            const float f = exp2f(ml.x - mm);
-            l += ml.y * f;
-            const float *o = p.part_o + at(c) * DP;
+        for (int32_t g0 = c0; g0 <= c1; g0 += 32) {
+            float f = 0.f;   // of the lane's part
+            if (g0 + lane <= c1) {
+                const float2 ml = p.part_ml[at(g0 + lane)];
+                f = exp2f(ml.x - mm);
+                l += ml.y * f;
+            }
+            const int32_t n = c1 - g0 + 1 < 32 ? c1 - g0 + 1 : 32;
+#pragma unroll 4
+            for (int32_t k = 0; k < n; ++k) {
+                const float fk = __shfl_sync(~0u, f, k);
+                const float *o = p.part_o + at(g0 + k) * DP;
 #pragma unroll
-            for (int d = 0; d < DP / 32; ++d) acc[d] += f * o[d * 32 + lane];
+                for (int d = 0; d < DP / 32; ++d) acc[d] += fk * o[d * 32 + lane];
+            }
         }
+        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
         const int32_t t = (r0 + row) / p.group, gq = r0 + row - t * p.group;
         const int64_t q_at = (static_cast<int64_t>(b) * p.next_n + t) * p.q_heads + h * p.group + gq;
         const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -472,7 +483,7 @@ cudaError_t launch_shape(AttnParams p, uint8_t *ws, int sms, cudaStream_t stream
     if (e != cudaSuccess) return e;
     const int64_t units = static_cast<int64_t>(p.requests) * p.kv_heads * p.row_tiles;
     const int64_t each = rows < Sh::kRows ? rows : Sh::kRows;
-    const dim3 blocks(static_cast<unsigned>(units), static_cast<unsigned>((each + 7) / 8));
+    const dim3 blocks(static_cast<unsigned>(units), static_cast<unsigned>((each + kCombineRows - 1) / kCombineRows));
     return launch_pdl(combine_kernel<BF16, DP, W>, blocks, kCombineThreads, 0, stream, 1, p, static_cast<int32_t>(grid));
 }
 
@@ -585,6 +596,7 @@ int gbtopk_selected_attention(const void *q, int dtype, int64_t num_rows, int64_
     if (top_k > 0 && !indices) return GBTOPK_EINVAL;
     AttnParams p{};
     p.pages.num_slots = num_slots;
+    p.pages.page.init(1);
     p.indices = indices;
     p.top_k = static_cast<int32_t>(top_k);
     p.idx_row = idx_row_stride;

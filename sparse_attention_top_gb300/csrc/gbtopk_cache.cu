@@ -45,7 +45,7 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 }
 
 struct SelectShared {
-    uint32_t hist[256];
+    uint32_t hist[256], total[256];   // of the block, of the cluster
     uint32_t gt[kSelectWarps], eq[kSelectWarps];   // kept for sure, equal to the key: by warp, then before each
     uint32_t all_gt[kMaxCluster], all_eq[kMaxCluster];
     int32_t draft[64];
@@ -106,12 +106,18 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
         }
         if (size > 1) cluster.sync();
         else __syncthreads();
+        if (tid < 256) {
+            uint32_t x = 0;
+            for (int r = 0; r < size; ++r) x += cluster.map_shared_rank(sh.hist, r)[tid];
+            sh.total[tid] = x;
+        }
+        __syncthreads();
         if (warp == 0) {
             // eight bins a lane, the highest in lane 0
             uint32_t h[8], sum = 0;
+#pragma unroll
             for (int b = 0; b < 8; ++b) {
-                h[b] = 0;
-                for (int r = 0; r < size; ++r) h[b] += cluster.map_shared_rank(sh.hist, r)[255 - (lane * 8 + b)];
+                h[b] = sh.total[255 - (lane * 8 + b)];
                 sum += h[b];
             }
             uint32_t inc = sum;
@@ -122,11 +128,19 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
             const int owner = __ffs(__ballot_sync(~0u, inc >= need)) - 1;
             if (lane == owner) {
                 uint32_t left = need - (inc - sum);
-                int b = 0;
-                while (left > h[b]) left -= h[b++];
-                sh.bin = static_cast<uint32_t>(255 - (lane * 8 + b));
-                sh.need = left;
-                sh.count = h[b];
+                bool found = false;
+#pragma unroll
+                for (int b = 0; b < 8; ++b) {
+                    if (found) continue;
+                    if (left > h[b]) {
+                        left -= h[b];
+                        continue;
+                    }
+                    found = true;
+                    sh.bin = static_cast<uint32_t>(255 - (lane * 8 + b));
+                    sh.need = left;
+                    sh.count = h[b];
+                }
             }
         }
         if (size > 1) cluster.sync();

@@ -55,14 +55,24 @@ struct Paging {
     int64_t num_slots;
     FastDiv page;
 
-    // Cache slot of position p of request i, or -1 where there is none.
-    __device__ __forceinline__ int64_t slot(int64_t i, int32_t p) const {
+    // Page id and offset in it of a position; the id's load is in flight
+    // until slot() looks at it.
+    struct Place {
+        int32_t id;
+        uint32_t rest;
+    };
+    __device__ __forceinline__ Place place(int64_t i, int32_t p) const {
         const uint32_t c = page.div(static_cast<uint32_t>(p));
-        if (p < 0 || static_cast<int64_t>(c) >= cols) return -1;
-        const int64_t id = fetch(table + i * row_stride + c);
-        const int64_t s = id * page.d + (static_cast<uint32_t>(p) - c * page.d);
-        return id >= 0 && s < num_slots ? s : -1;
+        Place at{-1, static_cast<uint32_t>(p) - c * page.d};
+        if (p >= 0 && static_cast<int64_t>(c) < cols) at.id = fetch(table + i * row_stride + c);
+        return at;
     }
+    // The cache slot, or -1 where there is none.
+    __device__ __forceinline__ int64_t slot(const Place &at) const {
+        const int64_t s = static_cast<int64_t>(at.id) * page.d + at.rest;
+        return at.id >= 0 && s < num_slots ? s : -1;
+    }
+    __device__ __forceinline__ int64_t slot(int64_t i, int32_t p) const { return slot(place(i, p)); }
 };
 
 template <bool BF16>

@@ -57,7 +57,7 @@ struct Unit {
 };
 
 struct ScanScratch {
-    int64_t warps[16];
+    int64_t warps[16], low[16];
     int64_t off;
     int32_t b;
 };
@@ -102,26 +102,46 @@ struct Walk {
     }
 };
 
-// Total tiles of the call over requests [0, upto), summed by the block.
+// Tiles of the call, and in *before those of the requests below b, summed by
+// the block.
 template <int KT, int THREADS>
-__device__ int64_t sum_tiles(const AttnParams &p, int32_t upto, ScanScratch *scratch) {
-    if (!p.seq_lens) return static_cast<int64_t>(upto) * tiles_of<KT>(span_of(p, 0)) * p.request_units;
-    int64_t s = 0;
-    for (int32_t b = threadIdx.x; b < upto; b += THREADS) s += tiles_of<KT>(span_of(p, b));
-    for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(~0u, s, o);
-    if ((threadIdx.x & 31) == 0) scratch->warps[threadIdx.x >> 5] = s;
+__device__ int64_t sum_tiles(const AttnParams &p, int32_t b, int64_t *before, ScanScratch *scratch) {
+    if (!p.seq_lens) {
+        const int64_t each = static_cast<int64_t>(tiles_of<KT>(span_of(p, 0))) * p.request_units;
+        *before = b * each;
+        return p.requests * each;
+    }
+    int64_t all = 0, low = 0;
+    for (int32_t x = threadIdx.x; x < p.requests; x += THREADS) {
+        const int32_t v = tiles_of<KT>(span_of(p, x));
+        all += v;
+        low += x < b ? v : 0;
+    }
+    for (int o = 16; o; o >>= 1) {
+        all += __shfl_xor_sync(~0u, all, o);
+        low += __shfl_xor_sync(~0u, low, o);
+    }
+    if ((threadIdx.x & 31) == 0) {
+        scratch->warps[threadIdx.x >> 5] = all;
+        scratch->low[threadIdx.x >> 5] = low;
+    }
     __syncthreads();
-    s = 0;
-    for (int w = 0; w < (THREADS + 31) / 32; ++w) s += scratch->warps[w];
+    all = low = 0;
+    for (int w = 0; w < THREADS / 32; ++w) {
+        all += scratch->warps[w];
+        low += scratch->low[w];
+    }
     __syncthreads();
-    return s * p.request_units;
+    *before = low * p.request_units;
+    return all * p.request_units;
 }
 
 // The blockIdx.x-th of gridDim.x equal shares.
 template <int KT, int THREADS>
 __device__ Share block_share(const AttnParams &p, ScanScratch *scratch) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t total = sum_tiles<KT, THREADS>(p, p.requests, scratch);
+    int64_t before;
+    const int64_t total = sum_tiles<KT, THREADS>(p, 0, &before, scratch);
     const int64_t per = (total + gridDim.x - 1) / gridDim.x, start = per * blockIdx.x;
     Share s{0, start >= total ? 0 : (start + per < total ? per : total - start), 0};
     if (s.tiles == 0) return s;
@@ -142,7 +162,8 @@ __device__ Share block_share(const AttnParams &p, ScanScratch *scratch) {
         }
         if (lane == 31) scratch->warps[warp] = inc;
         __syncthreads();
-        int64_t all = 0, before = base;
+        int64_t all = 0;
+        before = base;
         for (int w = 0; w < THREADS / 32; ++w) {
             before += w < warp ? scratch->warps[w] : 0;
             all += scratch->warps[w];
@@ -161,23 +182,28 @@ __device__ Share block_share(const AttnParams &p, ScanScratch *scratch) {
     return s;
 }
 
-// Copies one tile's rows: each warp its 32 (or 16) rows, consecutive lanes
-// consecutive 16-byte chunks; rows without a slot become zeros.
+// Copies one tile's rows, of which each of four warps has KT / 4: eight lanes
+// a row of a 128-byte panel, four rows an instruction, so that a row's address
+// is computed once for all its panels.  `slot` is the slot of the warp's row
+// `lane`; rows without one, and columns at or beyond `loaded` chunks, become
+// zeros.  (One lane group a whole row, two rows an instruction, took 62 cycles
+// an instruction and bound the attention kernel at 3.9 TB/s.)
 template <int DP, int KT>
 __device__ __forceinline__ void copy_tile(uint32_t dst, const uint8_t *base, int64_t slot_bytes, int32_t slot,
                                           int32_t chunks, int32_t loaded, int warp, int lane) {
-    constexpr int kChunks = DP / 8 < 32 ? DP / 8 : 32;   // of a row; lanes of a row
-    constexpr int kPer = 32 / kChunks;                   // rows an instruction
-    constexpr int kMine = KT / 4;                        // rows of the warp
-    const int c = lane % kChunks;
-#pragma unroll 4
-    for (int r0 = 0; r0 < kMine; r0 += kPer) {
-        const int r = r0 + lane / kChunks;
-        const int32_t s = __shfl_sync(~0u, slot, r);
-        if (c < chunks) {
-            const bool ok = s >= 0 && c < loaded;
-            copy16(dst + tile_offset(KT, warp * kMine + r, c), ok ? base + s * slot_bytes + c * 16 : base, ok ? 16u : 0u);
-        }
+    constexpr int kMine = KT / 4, kPanels = DP / 64;
+    const int c0 = lane & 7, sub = lane >> 3;
+    base += c0 * 16;
+    dst += (warp * kMine + sub) * 128;
+    const uint32_t off[2] = {static_cast<uint32_t>((c0 ^ sub) << 4), static_cast<uint32_t>((c0 ^ (sub + 4)) << 4)};
+#pragma unroll
+    for (int it = 0; it < kMine / 4; ++it) {
+        const int32_t s = __shfl_sync(~0u, slot, it * 4 + sub);
+        const uint8_t *src = base + static_cast<int64_t>(s < 0 ? 0 : s) * slot_bytes;
+#pragma unroll
+        for (int n = 0; n < kPanels; ++n)
+            if (n * 8 + c0 < chunks)
+                copy16(dst + it * 512 + off[it & 1] + n * (KT * 128), src + n * 128, s >= 0 && n * 8 + c0 < loaded ? 16u : 0u);
     }
 }
 

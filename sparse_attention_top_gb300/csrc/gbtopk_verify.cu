@@ -10,22 +10,25 @@ namespace cg = cooperative_groups;
 namespace gbtopk {
 namespace {
 
-// Two kernels.  verify_stat_kernel reads every row of logits once: blocks of
-// (row, piece of the vocabulary) leave the piece's largest logit and its sum
-// of exponentials (a running pair per thread, rescaled when the maximum
-// rises), or for greedy requests the largest logit's lowest index.
-// verify_walk_kernel runs a cluster of kWalkCluster blocks for each request:
-// every block joins the pieces' pairs, looks up the probability that each
-// node's parent gives it (one thread a node), walks the tree in shared memory,
-// then draws over its part of the vocabulary; the cluster's first block takes
-// the best of the parts through distributed shared memory.
-constexpr int kStatThreads = 256;
-constexpr int kWalkThreads = 512;
-constexpr int kWalkCluster = 8;
+// verify_path_kernel: a cluster of kCluster blocks for each request, every
+// block an equal part of the vocabulary.  A step of the walk reads the current
+// node's row of logits once (each block its part: a running maximum and sum of
+// exponentials per thread, joined over the cluster through distributed shared
+// memory), decides its children in order, and goes on from the accepted one;
+// the last node's row is then drawn from.  Rows that the path does not reach
+// are not read.  A step costs about 3 us of latency, so where all rows of the
+// call are read sooner than its steps would take (kLazyBytes),
+// verify_stat_kernel reads them all first, blocks of (row, piece of the
+// vocabulary), and the path kernel only joins the pieces.
+constexpr int kThreads = 256;
+constexpr int kCluster = 8;
 constexpr int kMaxPieces = 32;
-// A piece: 32 KB of a row, so that a block has 16 KB or more in flight and
-// the sum of a row's pieces stays short (131073 bf16 logits: 9 pieces).
-constexpr int kPieceBytes = 32768;
+// A piece: 64 KB of a row, fewer for few rows (see piece_of).
+constexpr int kPieceBytes = 65536;
+// One row of logits of every request: above this many bytes the walk reads
+// rows as it reaches them.  (Half of next_n steps of 3 us at 6.5 TB/s against
+// next_n rows of all requests.)
+constexpr int64_t kLazyBytes = 10 << 20;
 
 // Of a row, or a piece of one: the largest logit, its lowest index (greedy
 // requests) and the sum of exp((x - top) / temperature).
@@ -87,49 +90,42 @@ __device__ __forceinline__ void unpack(const uint4 &v, float *x) {
     }
 }
 
-// grid: pieces of row 0, of row 1, ...
+struct StatScratch {
+    float top[kThreads / 32], sum[kThreads / 32];
+    int32_t first[kThreads / 32];
+};
+
+// The stat of logits [e0, e1) of a row, by the block; thread 0 has it.
 template <int DT>
-__global__ void __launch_bounds__(kStatThreads) verify_stat_kernel(const __grid_constant__ VerifyParams p) {
+__device__ RowStat block_stat(const uint8_t *row, int64_t e0, int64_t e1, bool greedy, float c, StatScratch &sh) {
     constexpr int kBytes = DT == GBTOPK_F32 ? 4 : 2, kVec = 16 / kBytes, kUnroll = 4;
-    __shared__ float s_top[kStatThreads / 32], s_sum[kStatThreads / 32];
-    __shared__ int32_t s_first[kStatThreads / 32];
-    pdl_wait();
-    pdl_release();
-    const int64_t r = blockIdx.x / p.pieces;
-    const int32_t piece = static_cast<int32_t>(blockIdx.x % p.pieces);
-    const float t = p.temperature ? fetch(p.temperature + r / p.next_n) : 1.f;
-    const bool greedy = t <= 0.f;
-    const float c = greedy ? 0.f : kLog2e / t;
-    const uint8_t *row = static_cast<const uint8_t *>(p.logits) + r * p.row_stride * kBytes;
-    // the piece's logits [e0, e1); whole 16-byte vectors from `skip` logits on
-    const int64_t e0 = piece * p.piece;
-    const int64_t e1 = e0 + p.piece < p.vocab ? e0 + p.piece : p.vocab;
-    const int32_t n = static_cast<int32_t>(e1 - e0);
+    const int32_t n = static_cast<int32_t>(e1 - e0), tid = static_cast<int32_t>(threadIdx.x);
     const uint8_t *base = row + e0 * kBytes;
+    // whole 16-byte vectors from `skip` logits on
     int32_t skip = static_cast<int32_t>((16 - (reinterpret_cast<uintptr_t>(base) & 15)) & 15) / kBytes;
     if (skip > n) skip = n;
     const int32_t vecs = (n - skip) / kVec;
     const uint4 *body = reinterpret_cast<const uint4 *>(base + skip * kBytes);
     float top = -INFINITY, sum = 0.f;
     int32_t first = INT32_MAX;
-    auto one = [&](int32_t e) {   // logit e of the piece
+    auto one = [&](int32_t e) {   // logit e of the part
         const float x = logit<DT>(base, e);
         if (greedy) better(top, first, x, static_cast<int32_t>(e0) + e);
         else if (x > -INFINITY) join(top, sum, x, 1.f, c);
     };
-    if (static_cast<int32_t>(threadIdx.x) < skip) one(threadIdx.x);
+    if (tid < skip) one(tid);
     const int32_t tail = skip + vecs * kVec;
-    if (static_cast<int32_t>(threadIdx.x) < n - tail) one(tail + threadIdx.x);
-    for (int32_t v0 = 0; v0 < vecs; v0 += kStatThreads * kUnroll) {
+    if (tid < n - tail) one(tail + tid);
+    for (int32_t v0 = 0; v0 < vecs; v0 += kThreads * kUnroll) {
         uint4 raw[kUnroll];
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int32_t v = v0 + u * kStatThreads + static_cast<int32_t>(threadIdx.x);
+            const int32_t v = v0 + u * kThreads + tid;
             if (v < vecs) raw[u] = fetch(body + v);
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const int32_t v = v0 + u * kStatThreads + static_cast<int32_t>(threadIdx.x);
+            const int32_t v = v0 + u * kThreads + tid;
             if (v >= vecs) break;
             float x[kVec];
             unpack<DT>(raw[u], x);
@@ -145,13 +141,13 @@ __global__ void __launch_bounds__(kStatThreads) verify_stat_kernel(const __grid_
                 continue;
             }
             if (m > top) {
-                sum *= exp2f((top - m) * c);
+                sum *= exp2_fast((top - m) * c);
                 top = m;
             }
-            const float base = top == -INFINITY ? 0.f : top;
+            const float base_x = top == -INFINITY ? 0.f : top;
             float part = 0.f;
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) part += exp2_fast((x[i] - base) * c);
+            for (int i = 0; i < kVec; ++i) part += exp2_fast((x[i] - base_x) * c);
             sum += part;
         }
     }
@@ -161,116 +157,177 @@ __global__ void __launch_bounds__(kStatThreads) verify_stat_kernel(const __grid_
         if (greedy) better(top, first, t2, f2);
         else join(top, sum, t2, s2, c);
     }
-    if ((threadIdx.x & 31) == 0) {
-        s_top[threadIdx.x >> 5] = top;
-        s_sum[threadIdx.x >> 5] = sum;
-        s_first[threadIdx.x >> 5] = first;
+    if ((tid & 31) == 0) {
+        sh.top[tid >> 5] = top;
+        sh.sum[tid >> 5] = sum;
+        sh.first[tid >> 5] = first;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kStatThreads / 32; ++w) {
-            if (greedy) better(top, first, s_top[w], s_first[w]);
-            else join(top, sum, s_top[w], s_sum[w], c);
+    if (tid == 0)
+        for (int w = 1; w < kThreads / 32; ++w) {
+            if (greedy) better(top, first, sh.top[w], sh.first[w]);
+            else join(top, sum, sh.top[w], sh.sum[w], c);
         }
-        p.stats[r * p.pieces + piece] = RowStat{top, sum, first};
-    }
+    return RowStat{top, sum, first};
 }
 
-struct WalkShared {
-    RowStat stat[GBTOPK_MAX_NEXT_N];
-    int32_t parent[GBTOPK_MAX_NEXT_N], token[GBTOPK_MAX_NEXT_N];
+// grid: pieces of row 0, of row 1, ...
+template <int DT>
+__global__ void __launch_bounds__(kThreads) verify_stat_kernel(const __grid_constant__ VerifyParams p) {
+    __shared__ StatScratch sh;
+    pdl_wait();
+    pdl_release();
+    const int64_t r = blockIdx.x / p.pieces;
+    const int32_t piece = static_cast<int32_t>(blockIdx.x % p.pieces);
+    const float t = p.temperature ? fetch(p.temperature + r / p.next_n) : 1.f;
+    const int64_t e0 = piece * p.piece, e1 = e0 + p.piece < p.vocab ? e0 + p.piece : p.vocab;
+    const RowStat st = block_stat<DT>(static_cast<const uint8_t *>(p.logits) + r * p.row_stride * (DT == GBTOPK_F32 ? 4 : 2), e0, e1,
+                                      t <= 0.f, t <= 0.f ? 0.f : kLog2e / t, sh);
+    if (threadIdx.x == 0) p.stats[r * p.pieces + piece] = st;
+}
+
+struct PathShared {
+    RowStat part[2][kCluster];         // each block's part of a step's row
+    RowStat stat[GBTOPK_MAX_NEXT_N];   // rows' stats (sum: its reciprocal)
+    uint64_t children[GBTOPK_MAX_NEXT_N];
+    int32_t token[GBTOPK_MAX_NEXT_N];
     float u[GBTOPK_MAX_NEXT_N], have[GBTOPK_MAX_NEXT_N], q[GBTOPK_MAX_NEXT_N];
     int32_t refused[GBTOPK_MAX_NEXT_N], path[GBTOPK_MAX_NEXT_N];
     int32_t n_refused, cur, count;
     uint64_t took;
-    float best[kWalkThreads / 32];
-    int32_t index[kWalkThreads / 32];
-    float all_best[kWalkCluster];      // of the cluster's first block
-    int32_t all_index[kWalkCluster];
+    StatScratch scratch;
+    float best[kThreads / 32];
+    int32_t index[kThreads / 32];
+    float all_best[kCluster];          // of the cluster's first block
+    int32_t all_index[kCluster];
 };
 
-// A cluster of kWalkCluster blocks for each request.
-template <int DT>
-__global__ void __launch_bounds__(kWalkThreads) verify_walk_kernel(const __grid_constant__ VerifyParams p) {
-    __shared__ WalkShared sh;
-    const int rank = static_cast<int>(blockIdx.x % kWalkCluster), tid = static_cast<int>(threadIdx.x);
-    const int64_t i = blockIdx.x / kWalkCluster, r0 = i * p.next_n;
+template <int DT, bool LAZY>
+__global__ void __launch_bounds__(kThreads, 4) verify_path_kernel(const __grid_constant__ VerifyParams p) {
+    __shared__ PathShared sh;
+    const int rank = static_cast<int>(blockIdx.x % kCluster), tid = static_cast<int>(threadIdx.x);
+    const int64_t i = blockIdx.x / kCluster, r0 = i * p.next_n;
+    cg::cluster_group cluster = cg::this_cluster();
+    if (tid < GBTOPK_MAX_NEXT_N) sh.children[tid] = 0;
     pdl_wait();
     pdl_release();
     const float t = p.temperature ? fetch(p.temperature + i) : 1.f;
     const bool greedy = t <= 0.f;
     const float c = greedy ? 0.f : kLog2e / t;
-    // p of token v under row n of the request, 1 / sum and top given
-    auto prob = [&](int64_t row, float top, float inv, int32_t first, int64_t v) -> float {
-        if (top == -INFINITY) return 0.f;
-        if (greedy) return v == first ? 1.f : 0.f;
-        return exp2f((logit<DT>(p.logits, row * p.row_stride + v) - top) * c) * inv;
+    const int32_t part = static_cast<int32_t>((p.vocab + kCluster - 1) / kCluster);
+    const int32_t v0 = rank * part < p.vocab ? rank * part : static_cast<int32_t>(p.vocab);
+    const int32_t v1 = v0 + part < p.vocab ? v0 + part : static_cast<int32_t>(p.vocab);
+    // of a logit under a stat whose sum is a reciprocal
+    auto prob = [&](const RowStat &st, float x, int32_t v) -> float {
+        if (st.top == -INFINITY) return 0.f;
+        if (greedy) return v == st.first ? 1.f : 0.f;
+        return exp2f((x - st.top) * c) * st.sum;
     };
-    cg::cluster_group cluster = cg::this_cluster();
-    // each row's pieces joined, eight lanes a row
-    for (int n = tid >> 3; n < p.next_n; n += kWalkThreads / 8) {
-        float top = -INFINITY, sum = 0.f;
-        int32_t first = INT32_MAX;
-        for (int k = tid & 7; k < p.pieces; k += 8) {
-            const RowStat st = p.stats[(r0 + n) * p.pieces + k];
-            if (greedy) better(top, first, st.top, st.first);
-            else join(top, sum, st.top, st.sum, c);
-        }
-        const uint32_t lanes = 0xffu << (tid & 24);
-        for (int o = 4; o; o >>= 1) {
-            const float t2 = __shfl_xor_sync(lanes, top, o), s2 = __shfl_xor_sync(lanes, sum, o);
-            const int32_t f2 = __shfl_xor_sync(lanes, first, o);
-            if (greedy) better(top, first, t2, f2);
-            else join(top, sum, t2, s2, c);
-        }
-        if ((tid & 7) == 0) sh.stat[n] = RowStat{top, sum > 0.f ? 1.f / sum : 0.f, first};
-    }
-    cluster.sync();   // also: every block of the cluster runs before any other writes to it
+    __syncthreads();
+    int32_t parent = -1;
     if (tid < p.next_n && tid > 0) {
-        int32_t parent = tid - 1;
+        parent = tid - 1;
         if (p.tree_mask) {
             const uint64_t above = static_cast<uint64_t>(fetch(p.tree_mask + r0 + tid)) & ((1ull << tid) - 1);
             parent = above ? 63 - __clzll(static_cast<long long>(above)) : -1;
         }
-        const int32_t x = fetch(p.tokens + r0 + tid);
-        const bool known = parent >= 0 && x >= 0 && x < p.vocab;
-        sh.parent[tid] = parent;
-        sh.token[tid] = x;
+        sh.token[tid] = fetch(p.tokens + r0 + tid);
         sh.u[tid] = fetch(p.uniforms + r0 + tid);
-        const RowStat st = sh.stat[parent >= 0 ? parent : 0];
-        sh.have[tid] = known ? prob(r0 + parent, st.top, st.sum, st.first, x) : 0.f;
-        sh.q[tid] = known && p.draft_probs ? fetch(p.draft_probs + (r0 + parent) * p.vocab + x) : 1.f;
+        if (parent >= 0) atomicOr(reinterpret_cast<unsigned long long *>(&sh.children[parent]), 1ull << tid);
     }
-    __syncthreads();
-    if (tid == 0) {
-        int cur = 0, count = 0, n_ref = 0;
-        uint64_t took = 1;
-        float mass = 1.f;
-        sh.path[0] = 0;
-        for (int n = 1; n < p.next_n; ++n) {
-            if (sh.parent[n] != cur) continue;
-            const int32_t x = sh.token[n];
-            float have = sh.have[n];
-            for (int k = 0; k < n_ref; ++k)
-                if (sh.refused[k] == x) have = 0.f;
-            const float q = p.draft_probs ? sh.q[n] : mass;
-            if (sh.u[n] * q < have) {
-                cur = n;
-                took |= 1ull << n;
-                sh.path[++count] = n;
-                n_ref = 0;
-                mass = 1.f;
-            } else {
-                sh.refused[n_ref++] = x;
-                mass -= have;
+    if (!LAZY) {   // each row's pieces joined, eight lanes a row
+        for (int n = tid >> 3; n < p.next_n; n += kThreads / 8) {
+            float top = -INFINITY, sum = 0.f;
+            int32_t first = INT32_MAX;
+            for (int k = tid & 7; k < p.pieces; k += 8) {
+                const RowStat st = p.stats[(r0 + n) * p.pieces + k];
+                if (greedy) better(top, first, st.top, st.first);
+                else join(top, sum, st.top, st.sum, c);
             }
+            const uint32_t lanes = 0xffu << (tid & 24);
+            for (int o = 4; o; o >>= 1) {
+                const float t2 = __shfl_xor_sync(lanes, top, o), s2 = __shfl_xor_sync(lanes, sum, o);
+                const int32_t f2 = __shfl_xor_sync(lanes, first, o);
+                if (greedy) better(top, first, t2, f2);
+                else join(top, sum, t2, s2, c);
+            }
+            if ((tid & 7) == 0) sh.stat[n] = RowStat{top, sum > 0.f ? 1.f / sum : 0.f, first};
         }
-        sh.cur = cur;
-        sh.count = count;
-        sh.n_refused = n_ref;
-        sh.took = took;
     }
-    __syncthreads();
+    if (tid == 0) {
+        sh.cur = sh.count = sh.n_refused = 0;
+        sh.took = 1;
+        sh.path[0] = 0;
+    }
+    cluster.sync();   // also: every block of the cluster runs before any other writes to it
+    const int32_t x_tok = tid < p.next_n && parent >= 0 ? sh.token[tid] : -1;
+    const bool known = x_tok >= 0 && x_tok < p.vocab;
+    if (!LAZY) {
+        if (parent >= 0) {
+            sh.have[tid] = known ? prob(sh.stat[parent], logit<DT>(p.logits, (r0 + parent) * p.row_stride + x_tok), x_tok) : 0.f;
+            sh.q[tid] = known && p.draft_probs ? fetch(p.draft_probs + (r0 + parent) * p.vocab + x_tok) : 1.f;
+        }
+        __syncthreads();
+    }
+    for (uint32_t step = 0;; ++step) {
+        const int cur = sh.cur;
+        if (LAZY) {
+            // the node's row, and what it gives its children
+            const uint8_t *row = static_cast<const uint8_t *>(p.logits) + (r0 + cur) * p.row_stride * (DT == GBTOPK_F32 ? 4 : 2);
+            const bool child = parent == cur && known;
+            const float x = child ? logit<DT>(row, x_tok) : 0.f;
+            const float q = child && p.draft_probs ? fetch(p.draft_probs + (r0 + cur) * p.vocab + x_tok) : 1.f;
+            const RowStat mine = block_stat<DT>(row, v0, v1, greedy, c, sh.scratch);
+            if (tid == 0)
+                for (int k = 0; k < kCluster; ++k) cluster.map_shared_rank(&sh, k)->part[step & 1][rank] = mine;
+            cluster.sync();
+            RowStat st = sh.part[step & 1][0];
+            for (int k = 1; k < kCluster; ++k) {
+                const RowStat o = sh.part[step & 1][k];
+                if (greedy) better(st.top, st.first, o.top, o.first);
+                else join(st.top, st.sum, o.top, o.sum, c);
+            }
+            st.sum = st.sum > 0.f ? 1.f / st.sum : 0.f;
+            if (tid == 0) sh.stat[cur] = st;
+            if (parent == cur) {
+                sh.have[tid] = child ? prob(st, x, x_tok) : 0.f;
+                sh.q[tid] = q;
+            }
+            __syncthreads();
+        }
+        if (tid == 0) {
+            int at = cur, count = sh.count, n_ref;
+            uint64_t took = sh.took;
+            bool moved;
+            do {
+                moved = false;
+                n_ref = 0;
+                float mass = 1.f;
+                for (uint64_t left = sh.children[at]; left; left &= left - 1) {
+                    const int n = __ffsll(static_cast<long long>(left)) - 1;
+                    float have = sh.have[n];
+                    for (int k = 0; k < n_ref; ++k)
+                        if (sh.refused[k] == sh.token[n]) have = 0.f;
+                    if (sh.u[n] * (p.draft_probs ? sh.q[n] : mass) < have) {
+                        at = n;
+                        took |= 1ull << n;
+                        sh.path[++count] = n;
+                        moved = true;
+                        break;
+                    }
+                    sh.refused[n_ref++] = sh.token[n];
+                    mass -= have;
+                }
+            } while (moved && !LAZY);
+            if (moved) n_ref = 0;
+            sh.cur = at;
+            sh.count = count;
+            sh.n_refused = moved ? -1 : n_ref;
+            sh.took = took;
+        }
+        __syncthreads();
+        if (sh.n_refused >= 0) break;
+    }
     const int cur = sh.cur, n_ref = sh.n_refused;
     if (rank == 0) {
         if (tid < p.next_n) p.path[r0 + tid] = tid <= sh.count ? sh.path[tid] : -1;
@@ -282,40 +339,45 @@ __global__ void __launch_bounds__(kWalkThreads) verify_walk_kernel(const __grid_
     // the draw: this block's part of the vocabulary
     const RowStat st = sh.stat[cur];
     const int64_t row = r0 + cur;
-    const int64_t part = (p.vocab + kWalkCluster - 1) / kWalkCluster;
-    const int64_t v1 = (rank + 1) * part < p.vocab ? (rank + 1) * part : p.vocab;
     const float *noise = p.noise + i * p.vocab, *q = p.draft_probs && n_ref ? p.draft_probs + row * p.vocab : nullptr;
     float best = 0.f;
     int32_t token = INT32_MAX;
-    auto consider = [&](float rest, float e, int64_t v) {
-        const float race = rest / e;
-        if (rest > 0.f && (race > best || (race == best && v < token))) {
-            if (!q)
-                for (int k = 0; k < n_ref; ++k)
-                    if (sh.refused[k] == v) return;
-            best = race;
-            token = static_cast<int32_t>(v);
-        }
+    auto refused = [&](int32_t v) {
+        for (int k = 0; k < n_ref; ++k)
+            if (sh.refused[k] == v) return true;
+        return false;
     };
-    if (st.top > -INFINITY) {
+    if (st.top == -INFINITY) {
+    } else if (greedy) {   // all of p is at one word
+        if (rank == 0 && tid == 0 && (q ? 1.f - fetch(q + st.first) > 0.f : !refused(st.first))) {
+            best = 1.f;
+            token = st.first;
+        }
+    } else {
         constexpr int kUnroll = 8;
-        for (int64_t v0 = rank * part + tid; v0 < v1; v0 += kWalkThreads * kUnroll) {
+        for (int32_t b0 = v0 + tid; b0 < v1; b0 += kThreads * kUnroll) {
             float x[kUnroll], e[kUnroll], d[kUnroll];
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int64_t v = v0 + u * kWalkThreads;
+                const int32_t v = b0 + u * kThreads;
+                x[u] = -INFINITY;
+                e[u] = 1.f;
+                d[u] = 0.f;
                 if (v < v1) {
                     x[u] = logit<DT>(p.logits, row * p.row_stride + v);
                     e[u] = fetch(noise + v);
-                    d[u] = q ? fetch(q + v) : 0.f;
+                    if (q) d[u] = fetch(q + v);
                 }
             }
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                const int64_t v = v0 + u * kWalkThreads;
-                if (v >= v1) break;
-                const float pr = greedy ? (v == st.first ? 1.f : 0.f) : exp2f((x[u] - st.top) * c) * st.sum;
-                consider(pr - d[u], e[u], v);
+                const float rest = exp2_fast((x[u] - st.top) * c) * st.sum - d[u];
+                const float race = __fdividef(rest, e[u]);
+                const int32_t v = b0 + u * kThreads;
+                if (race > best && (q || !refused(v))) {   // a thread's words ascend: ties keep the lowest
+                    best = race;
+                    token = v;
+                }
             }
         }
     }
@@ -326,14 +388,14 @@ __global__ void __launch_bounds__(kWalkThreads) verify_walk_kernel(const __grid_
     }
     __syncthreads();
     if (tid == 0) {
-        for (int w = 1; w < kWalkThreads / 32; ++w) better(best, token, sh.best[w], sh.index[w]);
-        WalkShared *home = cluster.map_shared_rank(&sh, 0);
+        for (int w = 1; w < kThreads / 32; ++w) better(best, token, sh.best[w], sh.index[w]);
+        PathShared *home = cluster.map_shared_rank(&sh, 0);
         home->all_best[rank] = best;
         home->all_index[rank] = token;
     }
     cluster.sync();
     if (rank == 0 && tid == 0) {
-        for (int k = 0; k < kWalkCluster; ++k) better(best, token, sh.all_best[k], sh.all_index[k]);
+        for (int k = 0; k < kCluster; ++k) better(best, token, sh.all_best[k], sh.all_index[k]);
         p.next_token[i] = best > 0.f ? token : -1;
     }
 }
@@ -351,11 +413,12 @@ int64_t piece_of(int64_t num_rows, int64_t vocab, int es) {
 
 template <int DT>
 cudaError_t launch_verify(const VerifyParams &p, cudaStream_t s) {
-    const cudaError_t e = launch_pdl(verify_stat_kernel<DT>, dim3(static_cast<unsigned>(p.num_rows * p.pieces)),
-                                     kStatThreads, 0, s, 1, p);
+    const dim3 clusters(static_cast<unsigned>(p.num_rows / p.next_n * kCluster));
+    if (p.num_rows / p.next_n * p.vocab * (DT == GBTOPK_F32 ? 4 : 2) > kLazyBytes)
+        return launch_pdl(verify_path_kernel<DT, true>, clusters, kThreads, 0, s, kCluster, p);
+    const cudaError_t e = launch_pdl(verify_stat_kernel<DT>, dim3(static_cast<unsigned>(p.num_rows * p.pieces)), kThreads, 0, s, 1, p);
     if (e != cudaSuccess) return e;
-    return launch_pdl(verify_walk_kernel<DT>, dim3(static_cast<unsigned>(p.num_rows / p.next_n * kWalkCluster)), kWalkThreads, 0, s,
-                      kWalkCluster, p);
+    return launch_pdl(verify_path_kernel<DT, false>, clusters, kThreads, 0, s, kCluster, p);
 }
 
 }  // namespace

@@ -183,13 +183,13 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
                 seen = static_cast<uint64_t>(__reduce_or_sync(~0u, static_cast<uint32_t>(seen >> 32))) << 32 |
                        __reduce_or_sync(~0u, static_cast<uint32_t>(seen));
             }
-            auto slot_of = [&](int32_t t) -> int32_t {
+            auto place_of = [&](int32_t t) -> Paging::Place {
                 const int32_t pos = t * KT + w * 32 + lane;
-                if (pos >= s.n || pos >= p.width) return -1;
-                if (pos >= s.ctx && !((seen >> (pos - s.ctx)) & 1)) return -1;
-                return static_cast<int32_t>(a.pages.slot(s.b, pos));
+                if (pos >= s.n || pos >= p.width) return Paging::Place{-1, 0};
+                if (pos >= s.ctx && !((seen >> (pos - s.ctx)) & 1)) return Paging::Place{-1, 0};
+                return a.pages.place(s.b, pos);
             };
-            int32_t next_slot = slot_of(s.t0);
+            Paging::Place next = place_of(s.t0);
             for (int32_t ph = 0; ph < s.phases && ok; ++ph, ++phase) {
                 const int32_t h = s.w * per + ph / s.groups, r0 = (ph % s.groups) * NQ;
                 const int32_t rows = s.rows - r0 < NQ ? s.rows - r0 : NQ, padded = (rows + 15) / 16 * 16;
@@ -219,8 +219,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
                 __syncwarp();
                 if (lane == 0) bar_arrive(&sh.q_full[qb]);
                 for (int32_t t = s.t0; t < s.t1; ++t, ++job) {
-                    const int32_t slot = next_slot;
-                    next_slot = slot_of(t + 1 < s.t1 ? t + 1 : s.t0);
+                    const int32_t slot = static_cast<int32_t>(a.pages.slot(next));
+                    next = place_of(t + 1 < s.t1 ? t + 1 : s.t0);
                     const uint32_t stage = job % Sh::kStages;
                     if (job >= Sh::kStages) ok = __all_sync(~0u, bar_wait(&sh.empty[stage], (job / Sh::kStages - 1) & 1, abort));
                     if (!ok) break;
