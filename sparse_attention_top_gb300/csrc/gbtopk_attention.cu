@@ -29,10 +29,17 @@ constexpr int kMaxGrid = 160;       // blocks of the attention kernel (workspace
 constexpr int kMaskRing = 8;        // tiles whose validity bits are kept (see attention_kernel)
 constexpr float kRescale = 8.f;     // rise of the running maximum (base 2) that rescales O
 
-template <int DP, int W>
+// DP: head dimension rounded up to 64, 128 or 256.  W: softmax warpgroups.
+// SPLIT (W = 2): both have the same 128 query rows and take the position
+// tiles in turn, each with an O of its own, joined at the unit's end; else
+// each has a 128-row tile of queries.  (A warp needs about 2000 cycles for
+// the softmax of a tile of 128 columns, whose copies take 2800 at dimension
+// 128 and 1400 at 64.)
+template <int DP, int W, bool SPLIT>
 struct Shape {
     static constexpr int KT = DP == 256 ? 64 : 128;         // positions a tile
-    static constexpr int kRows = 128 * W;                   // query rows a unit
+    static constexpr int kRows = SPLIT ? 128 : 128 * W;     // query rows a unit
+    static constexpr int kJobs = SPLIT ? 1 : W;             // products (jobs) a tile
     static constexpr int kThreads = 128 * W + 256;
     // registers a thread: what the launch gives each, and its split (a
     // softmax row keeps its KT scores in registers)
@@ -41,13 +48,15 @@ struct Shape {
     static_assert(W * kSoftmaxRegs + 2 * kOtherRegs <= (W + 2) * kLaunchRegs, "register pool");
     static constexpr int kStageBytes = KT * DP * 2;
     static constexpr int kQBytes = kRows * DP * 2;
+    static constexpr int kJoin = SPLIT ? 128 * 33 * 4 : 0;  // 32 columns of the second O
     static constexpr int kFixed = 2048;                     // barriers, masks, scan scratch
-    static constexpr int kFit = (static_cast<int>(kMaxSmemBytes) - 1024 - kFixed - kQBytes) / kStageBytes;
+    static constexpr int kFit = (static_cast<int>(kMaxSmemBytes) - 1024 - kFixed - kJoin - kQBytes) / kStageBytes;
     static constexpr int kStages = kFit < 12 ? kFit : 12;   // half of it + 2 tiles fit the mask ring
-    static constexpr size_t kSmem = 1024 + kFixed + kQBytes + static_cast<size_t>(kStages) * kStageBytes;
+    static constexpr size_t kSmem = 1024 + kFixed + kJoin + kQBytes + static_cast<size_t>(kStages) * kStageBytes;
     static constexpr uint32_t kS = 0, kO = 2 * KT;          // tensor memory columns
     static_assert(kO + W * DP <= 512, "tensor memory");
     static_assert(kStages >= 4 && kStages / 2 + 2 <= kMaskRing, "ring");
+    static_assert(!SPLIT || W == 2, "split");
 };
 
 struct Shared {
@@ -59,19 +68,34 @@ struct Shared {
     uint64_t pv_done[2];            // O holds the job's product
     uint64_t drain;
     uint32_t mask[kMaskRing][4];
+    float2 ml[128];                 // (m, l) of the second warpgroup's rows
     ScanScratch scan;
     uint32_t tmem;
     uint32_t abort;
 };
 static_assert(sizeof(Shared) <= 2048, "shared block");
 
-template <bool BF16, int DP, int W>
-__global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(const __grid_constant__ AttnParams p) {
-    using Sh = Shape<DP, W>;
+// Barrier of the two softmax warps that share rows; true for both when `v`
+// is for one.
+__device__ __forceinline__ bool pair_barrier_or(int id, bool v) {
+    uint32_t any;
+    __syncwarp();
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %1, 0;\n bar.red.or.pred q, %2, 64, p;\n selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(any)
+        : "r"(static_cast<uint32_t>(v)), "r"(id)
+        : "memory");
+    return any != 0;
+}
+
+template <bool BF16, int DP, int W, bool SPLIT>
+__global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_kernel(const __grid_constant__ AttnParams p) {
+    using Sh = Shape<DP, W, SPLIT>;
     constexpr int KT = Sh::KT;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-    Shared &sh = *reinterpret_cast<Shared *>(smem + Sh::kQBytes + Sh::kStages * Sh::kStageBytes);
+    float *join = reinterpret_cast<float *>(smem + Sh::kQBytes + Sh::kStages * Sh::kStageBytes);   // [128][33]
+    Shared &sh = *reinterpret_cast<Shared *>(reinterpret_cast<uint8_t *>(join) + Sh::kJoin);
     const uint32_t q_smem = smem_addr(smem), ring = q_smem + Sh::kQBytes;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kMmaWarp = 4 * W;
@@ -189,7 +213,8 @@ __global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(co
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------ matrix products
         regs_down<Sh::kOtherRegs>();
-        if (warp == kMmaWarp && lane == 0) {
+        if (warp == kMmaWarp) {   // all lanes alike, see elect_lane
+            const bool lead = elect_lane();
             constexpr uint32_t kPanel = KT * 128;
             const uint32_t qk_desc = mma_desc(BF16, 128, KT, false, p.negative != 0);
             const uint32_t n_out = (p.dim + 15) / 16 * 16;
@@ -198,47 +223,57 @@ __global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(co
             uint32_t unit = 0, job0 = 0, gi = 0;   // gi: the unit's first tile since the start
             bool ok = true;
             // stage and parity of ring item i
-            auto wait_item = [&](uint32_t i) { return bar_wait(&sh.full[i % Sh::kStages], (i / Sh::kStages) & 1, abort); };
+            auto wait_item = [&](uint32_t i) { return __all_sync(~0u, bar_wait(&sh.full[i % Sh::kStages], (i / Sh::kStages) & 1, abort)); };
             for (; walk.more() && ok; walk.next(), ++unit) {
-                const uint32_t nt = static_cast<uint32_t>(walk.u.t1 - walk.u.t0), jobs = nt * W;
-                ok = bar_wait(&sh.q_full, unit & 1, abort);
+                const uint32_t nt = static_cast<uint32_t>(walk.u.t1 - walk.u.t0), jobs = nt * Sh::kJobs;
+                ok = __all_sync(~0u, bar_wait(&sh.q_full, unit & 1, abort));
                 if (!ok) break;
                 auto issue_qk = [&](uint32_t j) {
-                    const uint32_t item = 2 * (gi + j / W), s = item % Sh::kStages, sb = (job0 + j) & 1;
+                    const uint32_t item = 2 * (gi + j / Sh::kJobs), s = item % Sh::kStages, sb = (job0 + j) & 1;
                     if (!wait_item(item)) return false;
                     fence_async_reads();
                     tc_fence_after();
-                    const uint32_t qa = q_smem + (W == 2 ? (j & 1) * 128 * 128 : 0), ka = ring + s * Sh::kStageBytes;
-                    for (int kk = 0; kk < ksteps; ++kk)
-                        mma_ss(tmem + Sh::kS + sb * KT,
-                               smem_desc(qa + (kk >> 2) * (Sh::kRows * 128) + (kk & 3) * 32, 16, 1024),
-                               smem_desc(ka + (kk >> 2) * kPanel + (kk & 3) * 32, 16, 1024), qk_desc, kk > 0);
-                    tc_commit(&sh.s_full[sb]);
-                    if (W == 1 || (j & 1)) tc_commit(&sh.empty[s]);
-                    if (j + 1 == jobs) tc_commit(&sh.q_empty);
+                    const uint32_t qa = q_smem + (Sh::kJobs == 2 ? (j & 1) * 128 * 128 : 0), ka = ring + s * Sh::kStageBytes;
+                    if (lead) {   // unrolled: one thread issues, and its instructions bound the products' rate
+#pragma unroll
+                        for (int kk = 0; kk < DP / 16; ++kk)
+                            if (kk < ksteps)
+                                mma_ss(tmem + Sh::kS + sb * KT,
+                                       smem_desc(qa + (kk >> 2) * (Sh::kRows * 128) + (kk & 3) * 32, 16, 1024),
+                                       smem_desc(ka + (kk >> 2) * kPanel + (kk & 3) * 32, 16, 1024), qk_desc, kk > 0);
+                        tc_commit(&sh.s_full[sb]);
+                        if (Sh::kJobs == 1 || (j & 1)) tc_commit(&sh.empty[s]);
+                        if (j + 1 == jobs) tc_commit(&sh.q_empty);
+                    }
+                    __syncwarp();
                     return true;
                 };
                 for (uint32_t j = 0; j < 2 && j < jobs && ok; ++j) ok = issue_qk(j);
                 for (uint32_t j = 0; j < jobs && ok; ++j) {
                     const uint32_t job = job0 + j, sb = job & 1;
-                    const uint32_t item = 2 * (gi + j / W) + 1, s = item % Sh::kStages;
-                    ok = wait_item(item) && bar_wait(&sh.p_full[sb], (job >> 1) & 1, abort);
+                    const uint32_t item = 2 * (gi + j / Sh::kJobs) + 1, s = item % Sh::kStages;
+                    ok = wait_item(item) && __all_sync(~0u, bar_wait(&sh.p_full[sb], (job >> 1) & 1, abort));
                     if (!ok) break;
                     fence_async_reads();
                     tc_fence_after();
                     const uint32_t va = ring + s * Sh::kStageBytes;
-                    for (int kk = 0; kk < KT / 16; ++kk)
-                        mma_ts(tmem + Sh::kO + (W == 2 ? (j & 1) * DP : 0), tmem + Sh::kS + sb * KT + kk * 8,
-                               smem_desc(va + kk * 2048, kPanel, 1024), pv_desc, j >= W || kk > 0);
-                    tc_commit(&sh.pv_done[sb]);
-                    if (W == 1 || (j & 1)) tc_commit(&sh.empty[s]);
+                    if (lead) {
+#pragma unroll
+                        for (int kk = 0; kk < KT / 16; ++kk)
+                            mma_ts(tmem + Sh::kO + (W == 2 ? sb * DP : 0), tmem + Sh::kS + sb * KT + kk * 8,
+                                   smem_desc(va + kk * 2048, kPanel, 1024), pv_desc, j >= W || kk > 0);
+                        tc_commit(&sh.pv_done[sb]);
+                        if (Sh::kJobs == 1 || (j & 1)) tc_commit(&sh.empty[s]);
+                    }
+                    __syncwarp();
                     if (j + 2 < jobs) ok = issue_qk(j + 2);
                 }
                 job0 += jobs;
                 gi += nt;
             }
             // every product is done before the block gives its memory up
-            tc_commit(&sh.drain);
+            if (lead) tc_commit(&sh.drain);
+            __syncwarp();
             if (!bar_wait(&sh.drain, 0, abort)) {
                 const long long t0 = clock64();
                 while (!bar_try(&sh.drain, 0) && clock64() - t0 < kWaitCycles) {
@@ -252,21 +287,24 @@ __global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(co
         const int wg = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // the warp's tensor memory lanes
         const uint32_t t_o = tmem + lanes + Sh::kO + wg * DP;
-        uint32_t job = W == 2 ? wg : 0, tile = 0;
+        const int row_wg = SPLIT ? 0 : wg * 128;   // the warpgroup's first row of a unit
+        uint32_t job = Sh::kJobs == 2 ? wg : 0, tile = 0;
         bool ok = true;
         for (; walk.more() && ok; walk.next()) {
             const Unit u = walk.u;
             const int32_t h = u.hm / p.row_tiles, mt = u.hm - h * p.row_tiles;
-            const int32_t rho = mt * Sh::kRows + wg * 128 + row;
+            const int32_t rho = mt * Sh::kRows + row_wg + row;
             const bool mine = rho < rows;
             const int32_t t = rho / p.group, gq = rho - t * p.group;
             const int64_t r = static_cast<int64_t>(u.b) * p.next_n + t;
-            const bool active = mt * Sh::kRows + wg * 128 + (warp & 3) * 32 < rows;   // any row of the warp
+            const bool active = mt * Sh::kRows + row_wg + (warp & 3) * 32 < rows;   // any row of the warp
             uint64_t tree = 0;
             if (mine && p.seq_lens) tree = p.tree_mask ? static_cast<uint64_t>(fetch(p.tree_mask + r)) : (~0ull >> (63 - t));
             float m = -INFINITY, l = 0.f;
-            for (int32_t i = u.t0; i < u.t1; ++i, ++tile, job += W) {
+            uint32_t last = ~0u;   // the unit's latest job of this warpgroup
+            for (int32_t i = u.t0; i < u.t1; ++i, ++tile, job += Sh::kJobs) {
                 const uint32_t sb = job & 1, ph = (job >> 1) & 1;
+                if (SPLIT && sb != static_cast<uint32_t>(wg)) continue;
                 ok = __all_sync(~0u, bar_wait(&sh.mask_full[tile % kMaskRing], (tile / kMaskRing) & 1, abort) &&
                                          bar_wait(&sh.s_full[sb], ph, abort));
                 if (!ok) break;
@@ -315,8 +353,7 @@ __global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(co
                         }
                         if (__any_sync(~0u, f != 1.f)) {
                             // O is complete up to the row's last job
-                            const uint32_t prev = job - W;
-                            ok = __all_sync(~0u, bar_wait(&sh.pv_done[prev & 1], (prev >> 1) & 1, abort));
+                            ok = __all_sync(~0u, bar_wait(&sh.pv_done[last & 1], (last >> 1) & 1, abort));
                             if (!ok) break;
                             tc_fence_after();
 #pragma unroll 1
@@ -349,26 +386,65 @@ __global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(co
                     tc_wait_st();
                     tc_fence_before();
                 }
+                last = job;
                 __syncwarp();
                 if (lane == 0) bar_arrive(&sh.p_full[sb]);
             }
-            if (!ok) break;
-            const uint32_t prev = job - W;
-            ok = __all_sync(~0u, bar_wait(&sh.pv_done[prev & 1], (prev >> 1) & 1, abort));
-            if (!ok) break;
-            if (!active) continue;
+            if (ok && last != ~0u) ok = __all_sync(~0u, bar_wait(&sh.pv_done[last & 1], (last >> 1) & 1, abort));
+            if (!SPLIT && !ok) break;
+            if (threadIdx.x == 0 && ok) {   // the blocks that share the unit
+                int32_t *ends = p.unit_ends + 2 * (static_cast<int64_t>(u.b) * p.request_units + u.hm);
+                if (u.t0 == 0) ends[0] = static_cast<int32_t>(blockIdx.x);
+                if (u.t1 == u.tiles) ends[1] = static_cast<int32_t>(blockIdx.x);
+            }
+            __syncwarp();
+            float f0 = 1.f, f1 = 0.f;   // SPLIT: factors of the two O
+            if constexpr (SPLIT) {
+                if (wg == 1) sh.ml[row] = make_float2(m, l);
+                ok = !pair_barrier_or(1 + (warp & 3), !ok);   // both leave when one gave up
+                if (!ok) break;
+                if (wg == 0) {
+                    const float2 other = sh.ml[row];
+                    const float top = fmaxf(m, other.x);
+                    f0 = m == -INFINITY ? 0.f : exp2_fast(m - top);
+                    f1 = other.x == -INFINITY ? 0.f : exp2_fast(other.x - top);
+                    l = l * f0 + other.y * f1;
+                    m = top;
+                }
+            }
+            if (!active) {
+                if constexpr (SPLIT) pair_barrier_or(1 + (warp & 3), false);
+                continue;
+            }
             tc_fence_after();
             const bool whole = u.t0 == 0 && u.t1 == u.tiles;
             const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (u.t0 > 0 ? 0 : 1);
-            const int64_t part_row = part * Sh::kRows + wg * 128 + row;
+            const int64_t part_row = part * Sh::kRows + row_wg + row;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const int64_t q_at = r * p.q_heads + h * p.group + gq;
             for (int c0 = 0; c0 < DP; c0 += 32) {
                 if (c0 >= p.dim) break;
+                __syncwarp();
                 uint32_t o[32];
                 tmem_load32(t_o + c0, o);
                 tc_wait_ld();
-                if (!mine) continue;
+                if constexpr (SPLIT) {   // the second warpgroup's columns through shared memory
+                    if (wg == 1) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) join[row * 33 + c] = __uint_as_float(o[c]);
+                    }
+                    pair_barrier_or(1 + (warp & 3), false);
+                    if (wg == 0) {
+#pragma unroll
+                        for (int c = 0; c < 32; ++c) {
+                            // an O without a job holds what an earlier unit left there
+                            const float a = f0 > 0.f ? __uint_as_float(o[c]) * f0 : 0.f, b = f1 > 0.f ? join[row * 33 + c] * f1 : 0.f;
+                            o[c] = __float_as_uint(a + b);
+                        }
+                    }
+                    pair_barrier_or(1 + (warp & 3), false);
+                }
+                if (!mine || (SPLIT && wg == 1)) continue;
                 if (whole) {
                     uint8_t *dst = static_cast<uint8_t *>(p.out) + 2 * (q_at * p.dim + c0);
 #pragma unroll
@@ -387,7 +463,8 @@ __global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(co
                         *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
                 }
             }
-            if (mine) {
+            if constexpr (SPLIT) pair_barrier_or(1 + (warp & 3), false);   // ml is read
+            if (mine && !(SPLIT && wg == 1)) {
                 if (!whole) p.part_ml[part_row] = make_float2(m, l);
                 else if (p.lse) p.lse[q_at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
             }
@@ -400,100 +477,113 @@ __global__ void __launch_bounds__(Shape<DP, W>::kThreads, 1) attention_kernel(co
     if (threadIdx.x == 0 && sh.abort) atomicOr(p.status, kStatusCopyLost);
 }
 
-// Joins the partial results of units that span blocks: one warp a row, blocks
-// of kCombineRows rows, grid (units, row blocks).
-constexpr int kCombineThreads = 256;
-constexpr int kCombineRows = 32;
+// Joins the partial results of units that span blocks: one warp a row, grid
+// (units, groups of kCombineRows rows).  All of a row's parts are loaded at
+// once where there are at most eight, else eight at a time.
+constexpr int kCombineRows = 8;
 
-template <bool BF16, int DP, int W>
-__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ AttnParams p, int32_t grid) {
-    constexpr int KT = Shape<DP, W>::KT, kRows = Shape<DP, W>::kRows;
-    __shared__ ScanScratch scan;
+template <bool BF16, int DP>
+__global__ void __launch_bounds__(kCombineRows * 32) combine_kernel(const __grid_constant__ AttnParams p, int32_t unit_rows) {
     pdl_wait();
     pdl_release();
-    const int32_t hms = p.request_units;
-    const int32_t b = static_cast<int32_t>(blockIdx.x / hms), hm = static_cast<int32_t>(blockIdx.x % hms);
-    int64_t before;
-    const int64_t total = sum_tiles<KT, kCombineThreads>(p, b, &before, &scan);
-    const int64_t per = (total + grid - 1) / grid;
-    const int32_t tiles = tiles_of<KT>(span_of(p, b));
-    const int64_t start = before + static_cast<int64_t>(hm) * tiles;
-    const int32_t c0 = static_cast<int32_t>(start / per), c1 = static_cast<int32_t>((start + tiles - 1) / per);
-    if (c0 == c1) return;
-    const int32_t h = hm / p.row_tiles, r0 = (hm - h * p.row_tiles) * kRows;
-    const int32_t rows = p.next_n * p.group - r0 < kRows ? p.next_n * p.group - r0 : kRows;
+    const int2 ends = reinterpret_cast<const int2 *>(p.unit_ends)[blockIdx.x];
+    const int32_t c0 = ends.x, c1 = ends.y;
+    if (c0 == c1 || c0 < 0 || c1 < c0 || c1 >= kMaxGrid) return;   // whole, or not written by a block that gave up
+    const int32_t b = static_cast<int32_t>(blockIdx.x / p.request_units), hm = static_cast<int32_t>(blockIdx.x % p.request_units);
+    const int32_t h = hm / p.row_tiles, r0 = (hm - h * p.row_tiles) * unit_rows;
     const int lane = threadIdx.x & 31;
-    const int32_t first = static_cast<int32_t>(blockIdx.y) * kCombineRows;
-    for (int32_t row = first + static_cast<int32_t>(threadIdx.x >> 5); row < rows && row < first + kCombineRows; row += kCombineThreads / 32) {
-        auto at = [&](int32_t c) { return (2ll * c + (c == c0 ? 1 : 0)) * kRows + row; };
-        float m = -INFINITY;
-        for (int32_t c = c0 + lane; c <= c1; c += 32) m = fmaxf(m, p.part_ml[at(c)].x);
-        for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        const float mm = m == -INFINITY ? 0.f : m;
-        float l = 0.f, acc[DP / 32] = {};
-        for (int32_t g0 = c0; g0 <= c1; g0 += 32) {
-            float f = 0.f;   // of the lane's part
-            if (g0 + lane <= c1) {
-                const float2 ml = p.part_ml[at(g0 + lane)];
-                f = exp2f(ml.x - mm);
-                l += ml.y * f;
-            }
-            const int32_t n = c1 - g0 + 1 < 32 ? c1 - g0 + 1 : 32;
-#pragma unroll 4
-            for (int32_t k = 0; k < n; ++k) {
-                const float fk = __shfl_sync(~0u, f, k);
-                const float *o = p.part_o + at(g0 + k) * DP;
+    const int32_t row = static_cast<int32_t>(blockIdx.y) * kCombineRows + static_cast<int32_t>(threadIdx.x >> 5);
+    if (row >= unit_rows || r0 + row >= p.next_n * p.group) return;
+    auto at = [&](int32_t c) { return (2ll * c + (c == c0 ? 1 : 0)) * unit_rows + row; };
+    constexpr int kCols = DP / 32, kBatch = DP == 256 ? 4 : 8;
+    float m = -INFINITY, l = 0.f, acc[kCols] = {};
+    for (int32_t g0 = c0; g0 <= c1; g0 += kBatch) {
+        float2 ml[kBatch];
+        float o[kBatch][kCols];
 #pragma unroll
-                for (int d = 0; d < DP / 32; ++d) acc[d] += fk * o[d * 32 + lane];
-            }
+        for (int k = 0; k < kBatch; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
+            if (g0 + k > c1) continue;
+            const int64_t x = at(g0 + k);
+            ml[k] = p.part_ml[x];
+#pragma unroll
+            for (int d = 0; d < kCols; ++d) o[k][d] = p.part_o[x * DP + d * 32 + lane];
         }
-        for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(~0u, l, o);
-        const int32_t t = (r0 + row) / p.group, gq = r0 + row - t * p.group;
-        const int64_t q_at = (static_cast<int64_t>(b) * p.next_n + t) * p.q_heads + h * p.group + gq;
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        using T = typename Half2<BF16>::T;
+        float top = m;
 #pragma unroll
-        for (int d = 0; d < DP / 32; ++d)
-            if (d * 32 + lane < p.dim) static_cast<T *>(p.out)[q_at * p.dim + d * 32 + lane] = static_cast<T>(acc[d] * inv);
-        if (p.lse && lane == 0) p.lse[q_at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);
+        if (top == -INFINITY) continue;
+        const float f = exp2_fast(m - top);
+        m = top;
+        l *= f;
+#pragma unroll
+        for (int d = 0; d < kCols; ++d) acc[d] *= f;
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) {
+            if (ml[k].x == -INFINITY) continue;
+            const float fk = exp2_fast(ml[k].x - top);
+            l += ml[k].y * fk;
+#pragma unroll
+            for (int d = 0; d < kCols; ++d) acc[d] += fk * o[k][d];
+        }
     }
+    const int32_t t = (r0 + row) / p.group, gq = r0 + row - t * p.group;
+    const int64_t q_at = (static_cast<int64_t>(b) * p.next_n + t) * p.q_heads + h * p.group + gq;
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    using T = typename Half2<BF16>::T;
+#pragma unroll
+    for (int d = 0; d < kCols; ++d)
+        if (d * 32 + lane < p.dim) static_cast<T *>(p.out)[q_at * p.dim + d * 32 + lane] = static_cast<T>(acc[d] * inv);
+    if (p.lse && lane == 0) p.lse[q_at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 int dim_class(int32_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-// Two row tiles a block where a head has more than 128 rows: they share each
-// copied tile, and one's softmax runs beside the other's products.
-int row_groups(int32_t dim, int64_t rows) { return dim <= 128 && rows > 128 ? 2 : 1; }
+size_t partial_rows() { return static_cast<size_t>(2 * kMaxGrid) * 256; }
+size_t unit_bytes(int64_t num_rows, int32_t q_heads) {   // a unit has a row or more
+    return (static_cast<size_t>(num_rows) * q_heads * 8 + 255) / 256 * 256;
+}
 
-size_t partial_rows(int32_t) { return static_cast<size_t>(2 * kMaxGrid) * 256; }
-
-template <bool BF16, int DP, int W>
+template <bool BF16, int DP, int W, bool SPLIT>
 cudaError_t launch_shape(AttnParams p, uint8_t *ws, int sms, cudaStream_t stream) {
-    using Sh = Shape<DP, W>;
+    using Sh = Shape<DP, W, SPLIT>;
     const int64_t rows = static_cast<int64_t>(p.next_n) * p.group;
     p.row_tiles = static_cast<int32_t>((rows + Sh::kRows - 1) / Sh::kRows);
     p.request_units = p.kv_heads * p.row_tiles;
-    p.part_ml = reinterpret_cast<float2 *>(ws + kWsHeaderBytes);
-    p.part_o = reinterpret_cast<float *>(p.part_ml + partial_rows(p.dim));
-    cudaError_t e = cudaFuncSetAttribute(attention_kernel<BF16, DP, W>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    p.unit_ends = reinterpret_cast<int32_t *>(ws + kWsHeaderBytes);
+    p.part_ml = reinterpret_cast<float2 *>(ws + kWsHeaderBytes + unit_bytes(static_cast<int64_t>(p.requests) * p.next_n, p.q_heads));
+    p.part_o = reinterpret_cast<float *>(p.part_ml + partial_rows());
+    cudaError_t e = cudaFuncSetAttribute(attention_kernel<BF16, DP, W, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          static_cast<int>(Sh::kSmem));
     if (e != cudaSuccess) return e;
     const int grid = sms < kMaxGrid ? sms : kMaxGrid;
-    e = launch_pdl(attention_kernel<BF16, DP, W>, dim3(static_cast<unsigned>(grid)), Sh::kThreads, Sh::kSmem, stream, 1, p);
+    e = launch_pdl(attention_kernel<BF16, DP, W, SPLIT>, dim3(static_cast<unsigned>(grid)), Sh::kThreads, Sh::kSmem, stream, 1, p);
     if (e != cudaSuccess) return e;
-    const int64_t units = static_cast<int64_t>(p.requests) * p.kv_heads * p.row_tiles;
+    const int64_t units = static_cast<int64_t>(p.requests) * p.request_units;
     const int64_t each = rows < Sh::kRows ? rows : Sh::kRows;
     const dim3 blocks(static_cast<unsigned>(units), static_cast<unsigned>((each + kCombineRows - 1) / kCombineRows));
-    return launch_pdl(combine_kernel<BF16, DP, W>, blocks, kCombineThreads, 0, stream, 1, p, static_cast<int32_t>(grid));
+    return launch_pdl(combine_kernel<BF16, DP>, blocks, kCombineRows * 32, 0, stream, 1, p, Sh::kRows);
+}
+
+// Up to 128 rows a head: two warpgroups take the tiles in turn.  More: each
+// has a row tile, they share each copied tile, and one's softmax runs beside
+// the other's products.  Above dimension 128 tensor memory has room for one O.
+template <bool BF16, int DP>
+cudaError_t launch_dim(const AttnParams &p, uint8_t *ws, int sms, cudaStream_t s) {
+    if constexpr (DP == 256) {
+        return launch_shape<BF16, DP, 1, false>(p, ws, sms, s);
+    } else {
+        if (static_cast<int64_t>(p.next_n) * p.group <= 128) return launch_shape<BF16, DP, 2, true>(p, ws, sms, s);
+        return launch_shape<BF16, DP, 2, false>(p, ws, sms, s);
+    }
 }
 
 template <bool BF16>
 cudaError_t launch_attention(const AttnParams &p, uint8_t *ws, int sms, cudaStream_t s) {
-    const int w = row_groups(p.dim, static_cast<int64_t>(p.next_n) * p.group);
     switch (dim_class(p.dim)) {
-        case 64: return w == 2 ? launch_shape<BF16, 64, 2>(p, ws, sms, s) : launch_shape<BF16, 64, 1>(p, ws, sms, s);
-        case 128: return w == 2 ? launch_shape<BF16, 128, 2>(p, ws, sms, s) : launch_shape<BF16, 128, 1>(p, ws, sms, s);
-        default: return launch_shape<BF16, 256, 1>(p, ws, sms, s);
+        case 64: return launch_dim<BF16, 64>(p, ws, sms, s);
+        case 128: return launch_dim<BF16, 128>(p, ws, sms, s);
+        default: return launch_dim<BF16, 256>(p, ws, sms, s);
     }
 }
 
@@ -556,7 +646,7 @@ extern "C" {
 
 size_t gbtopk_attention_workspace_bytes(int64_t num_rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
     if (check_heads(GBTOPK_BF16, num_rows, q_heads, kv_heads, head_dim) != GBTOPK_OK) return 0;
-    return kWsHeaderBytes + partial_rows(head_dim) * (8 + 4 * static_cast<size_t>(dim_class(head_dim)));
+    return kWsHeaderBytes + unit_bytes(num_rows, q_heads) + partial_rows() * (8 + 4 * static_cast<size_t>(dim_class(head_dim)));
 }
 
 int gbtopk_tree_attention(const void *q, int dtype, int64_t num_rows, int64_t q_row_stride, int64_t q_head_stride,

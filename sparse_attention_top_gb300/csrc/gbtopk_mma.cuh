@@ -115,6 +115,16 @@ __device__ __forceinline__ uint32_t mma_desc(bool bf16, uint32_t m, uint32_t n, 
            (n >> 3) << 17 | (m >> 4) << 24;
 }
 
+// One lane of the (converged) warp.  The warp that issues products runs its
+// loop with all lanes on equal values and puts only the instructions
+// themselves under this: their descriptors go through warp-uniform registers,
+// and in a branch of one lane the compiler may take another lane's stale copy.
+__device__ __forceinline__ bool elect_lane() {
+    uint32_t p;
+    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+    return p != 0;
+}
+
 // D (tensor memory) = A B, + D when `add`; A and B in shared memory.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
@@ -155,6 +165,12 @@ __device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t *v) {
           "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
         : "r"(addr)
         : "memory");
+}
+
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t *v) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t *v) {

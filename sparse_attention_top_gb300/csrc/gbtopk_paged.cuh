@@ -26,6 +26,7 @@ struct AttnParams {
     void *out;
     float *lse;
     uint32_t *status;
+    int32_t *unit_ends;          // first and last block of each unit
     float *part_o;               // [2 grid][rows of a tile][DP]
     float2 *part_ml;             // [2 grid][rows of a tile]
 };

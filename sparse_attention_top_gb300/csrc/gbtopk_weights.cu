@@ -239,7 +239,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------ matrix products
         regs_down<Sh::kOtherRegs>();
-        if (warp == kMmaWarp && lane == 0) {
+        if (warp == kMmaWarp) {   // all lanes alike, see elect_lane
+            const bool lead = elect_lane();
             uint32_t phase = 0, job = 0;
             while (ok && spans.next(&s)) {
                 for (int32_t ph = 0; ph < s.phases && ok; ++ph, ++phase) {
@@ -247,25 +248,32 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
                     const int32_t rows = s.rows - r0 < NQ ? s.rows - r0 : NQ, padded = (rows + 15) / 16 * 16;
                     const uint32_t desc = mma_desc(BF16, 128, static_cast<uint32_t>(padded), false, a.negative != 0);
                     const uint32_t qa = q_smem + (phase & 1) * Sh::kQBytes;
-                    ok = bar_wait(&sh.q_full[phase & 1], (phase / 2) & 1, abort);
+                    ok = __all_sync(~0u, bar_wait(&sh.q_full[phase & 1], (phase / 2) & 1, abort));
                     for (int32_t t = s.t0; t < s.t1 && ok; ++t, ++job) {
                         const uint32_t stage = job % Sh::kStages, sb = job & 1;
-                        ok = bar_wait(&sh.full[stage], (job / Sh::kStages) & 1, abort);
-                        if (ok && job >= 2) ok = bar_wait(&sh.s_empty[sb], (job / 2 - 1) & 1, abort);
+                        ok = __all_sync(~0u, bar_wait(&sh.full[stage], (job / Sh::kStages) & 1, abort));
+                        if (ok && job >= 2) ok = __all_sync(~0u, bar_wait(&sh.s_empty[sb], (job / 2 - 1) & 1, abort));
                         if (!ok) break;
                         fence_async_reads();
                         tc_fence_after();
                         const uint32_t ka = ring + stage * Sh::kStageBytes;
-                        for (int kk = 0; kk < chunks / 2; ++kk)
-                            mma_ss(tmem + sb * 128, smem_desc(ka + (kk >> 2) * (KT * 128) + (kk & 3) * 32, 16, 1024),
-                                   smem_desc(qa + (kk >> 2) * (NQ * 128) + (kk & 3) * 32, 16, 1024), desc, kk > 0);
-                        tc_commit(&sh.s_full[sb]);
-                        tc_commit(&sh.empty[stage]);
+                        if (lead) {
+#pragma unroll
+                            for (int kk = 0; kk < DP / 16; ++kk)
+                                if (kk < chunks / 2)
+                                    mma_ss(tmem + sb * 128, smem_desc(ka + (kk >> 2) * (KT * 128) + (kk & 3) * 32, 16, 1024),
+                                           smem_desc(qa + (kk >> 2) * (NQ * 128) + (kk & 3) * 32, 16, 1024), desc, kk > 0);
+                            tc_commit(&sh.s_full[sb]);
+                            tc_commit(&sh.empty[stage]);
+                        }
+                        __syncwarp();
                     }
-                    if (ok) tc_commit(&sh.q_empty[phase & 1]);
+                    if (ok && lead) tc_commit(&sh.q_empty[phase & 1]);
+                    __syncwarp();
                 }
             }
-            tc_commit(&sh.drain);
+            if (lead) tc_commit(&sh.drain);
+            __syncwarp();
             if (!bar_wait(&sh.drain, 0, abort)) {
                 const long long t0 = clock64();
                 while (!bar_try(&sh.drain, 0) && clock64() - t0 < kWaitCycles) {
