@@ -41,11 +41,6 @@ struct Shape {
     static constexpr int kRows = SPLIT ? 128 : 128 * W;     // query rows a unit
     static constexpr int kJobs = SPLIT ? 1 : W;             // products (jobs) a tile
     static constexpr int kThreads = 128 * W + 256;
-    // registers a thread: what the launch gives each, and its split (a
-    // softmax row keeps its KT scores in registers)
-    static constexpr int kLaunchRegs = W == 2 ? 128 : 168;
-    static constexpr int kSoftmaxRegs = W == 2 ? 176 : 240, kOtherRegs = W == 2 ? 80 : 128;
-    static_assert(W * kSoftmaxRegs + 2 * kOtherRegs <= (W + 2) * kLaunchRegs, "register pool");
     static constexpr int kStageBytes = KT * DP * 2;
     static constexpr int kQBytes = kRows * DP * 2;
     static constexpr int kJoin = SPLIT ? 128 * 33 * 4 : 0;  // 32 columns of the second O
@@ -133,15 +128,14 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
 
     if (warp >= kMmaWarp + 4) {
         // ------------------------------------------------ copies
-        regs_down<Sh::kOtherRegs>();
         const int w = warp - kMmaWarp - 4;
         const uint8_t *kb = static_cast<const uint8_t *>(p.k), *vb = static_cast<const uint8_t *>(p.v);
         const int64_t k_bytes = p.k_slot * 2, v_bytes = p.v_slot * 2;
         int32_t last_b = -1;
         uint64_t seen = ~0ull;   // drafted tokens that some row of the request sees
         // where this lane's row of tile t of unit u lies (KT / 4 rows a warp)
-        auto place_of = [&](const Unit &u, int32_t t) -> Paging::Place {
-            if (u.b != last_b) {
+        auto place_of = [&](const Unit &u, int32_t t, bool more) {
+            if (more && u.b != last_b) {
                 last_b = u.b;
                 if (p.seq_lens && p.tree_mask) {
                     const int64_t *tm = p.tree_mask + static_cast<int64_t>(u.b) * p.next_n;
@@ -152,18 +146,15 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
                 }
             }
             const int32_t pos = t * KT + w * (KT / 4) + (lane & (KT / 4 - 1));
-            if (pos >= u.span.n) return Paging::Place{-1, 0};
-            if (!p.seq_lens) return Paging::Place{fetch(p.indices + u.b * p.idx_row + pos), 0};   // pages of one slot
-            if (pos >= u.span.ctx && !((seen >> (pos - u.span.ctx)) & 1)) return Paging::Place{-1, 0};
-            return p.pages.place(u.b, pos);
+            const bool is = more && pos < u.span.n && (pos < u.span.ctx || ((seen >> (pos - u.span.ctx)) & 1));
+            return p.seq_lens ? p.pages.place(u.b, pos, is) : p.pages.listed(p.indices + u.b * p.idx_row + pos, is);
         };
         uint32_t unit = 0, g = 0, tile = 0;   // counters of units, ring stages and tiles
         uint32_t stage = 0, lap = 0;
         bool ok = true;
         Walk<KT> ahead = walk;                // the tile after the one being copied
         int32_t ahead_t = ahead.more() ? ahead.u.t0 : 0;
-        Paging::Place next{-1, 0};
-        if (ahead.more()) next = place_of(ahead.u, ahead_t);
+        Paging::Place next = place_of(ahead.u, ahead_t, ahead.more());
         for (; walk.more() && ok; walk.next(), ++unit) {
             const Unit u = walk.u;
             const int32_t h = u.hm / p.row_tiles, r0 = (u.hm - h * p.row_tiles) * Sh::kRows;
@@ -185,8 +176,7 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
                     ahead.next();
                     ahead_t = ahead.more() ? ahead.u.t0 : 0;
                 }
-                next.id = -1;
-                if (ahead.more()) next = place_of(ahead.u, ahead_t);
+                next = place_of(ahead.u, ahead_t, ahead.more());
                 for (int kv = 0; kv < 2; ++kv, ++g) {
                     if (g >= Sh::kStages) ok = __all_sync(~0u, bar_wait(&sh.empty[stage], (lap - 1) & 1, abort));
                     if (!ok) break;
@@ -212,7 +202,6 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
         copies_land();
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------ matrix products
-        regs_down<Sh::kOtherRegs>();
         if (warp == kMmaWarp) {   // all lanes alike, see elect_lane
             const bool lead = elect_lane();
             constexpr uint32_t kPanel = KT * 128;
@@ -224,8 +213,10 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
             bool ok = true;
             // stage and parity of ring item i
             auto wait_item = [&](uint32_t i) { return __all_sync(~0u, bar_wait(&sh.full[i % Sh::kStages], (i / Sh::kStages) & 1, abort)); };
-            for (; walk.more() && ok; walk.next(), ++unit) {
-                const uint32_t nt = static_cast<uint32_t>(walk.u.t1 - walk.u.t0), jobs = nt * Sh::kJobs;
+            // (broadcasts: values known to be warp-uniform need no move to
+            // uniform registers for every product)
+            for (; __any_sync(~0u, walk.more()) && ok; walk.next(), ++unit) {
+                const uint32_t nt = __shfl_sync(~0u, static_cast<uint32_t>(walk.u.t1 - walk.u.t0), 0), jobs = nt * Sh::kJobs;
                 ok = __all_sync(~0u, bar_wait(&sh.q_full, unit & 1, abort));
                 if (!ok) break;
                 auto issue_qk = [&](uint32_t j) {
@@ -283,7 +274,6 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
         __syncwarp();
     } else {
         // ------------------------------------------------ softmax, output
-        regs_up<Sh::kSoftmaxRegs>();
         const int wg = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // the warp's tensor memory lanes
         const uint32_t t_o = tmem + lanes + Sh::kO + wg * DP;
@@ -311,9 +301,12 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
                 if (active) {
                     tc_fence_after();
                     const uint32_t t_s = tmem + lanes + Sh::kS + sb * KT;
-                    uint32_t x[KT];
-#pragma unroll
-                    for (int c = 0; c < KT; c += 32) tmem_load32(t_s + c, x + c);
+                    // Half of the tile's scores are held at a time, so that 128
+                    // registers do for every role: the upper half is read for its
+                    // maximum, then the lower half, whose P goes over its own
+                    // columns, then the upper half again.
+                    constexpr int kHalf = KT / 2;
+                    uint32_t x[kHalf];
                     // bits of the positions this row sees; all of them as a rule
                     uint32_t bits[KT / 32];
                     bool whole = true;
@@ -322,8 +315,8 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
                         bits[c] = reinterpret_cast<volatile uint32_t *>(sh.mask[tile % kMaskRing])[c];
                         whole &= bits[c] == ~0u;
                     }
-                    const bool drafts = i * KT + KT > u.span.ctx;
-                    if (drafts) {
+                    if (i * KT + KT > u.span.ctx) {
+                        whole = false;
 #pragma unroll
                         for (int c = 0; c < KT / 32; ++c) {
                             const int32_t j0 = i * KT + c * 32 - u.span.ctx;   // drafted token of the word's bit 0
@@ -334,15 +327,25 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
                             bits[c] &= see;
                         }
                     }
-                    tc_wait_ld();
-                    if (!whole || drafts) {
+                    auto load_half = [&](int half) {
 #pragma unroll
-                        for (int c = 0; c < KT; ++c)
-                            if (!((bits[c / 32] >> (c & 31)) & 1)) x[c] = 0xff800000u;
-                    }
+                        for (int c = 0; c < kHalf; c += 32) tmem_load32(t_s + half * kHalf + c, x + c);
+                        tc_wait_ld();
+                        if (!whole) {
+#pragma unroll
+                            for (int c = 0; c < kHalf; ++c)
+                                if (!((bits[(half * kHalf + c) / 32] >> (c & 31)) & 1)) x[c] = 0xff800000u;
+                        }
+                    };
                     float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    auto max_half = [&]() {
 #pragma unroll
-                    for (int c = 0; c < KT; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(x[c]));
+                        for (int c = 0; c < kHalf; ++c) top[c & 3] = fmaxf(top[c & 3], __uint_as_float(x[c]));
+                    };
+                    load_half(1);
+                    max_half();
+                    load_half(0);
+                    max_half();
                     const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.c;
                     const bool rise = best > m + kRescale;   // also from -inf
                     if (__any_sync(~0u, rise)) {
@@ -369,19 +372,24 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
                     }
                     const float mm = m == -INFINITY ? 0.f : m;
                     float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    auto exp_half = [&](int half) {
 #pragma unroll
-                    for (int c0 = 0; c0 < KT; c0 += 32) {   // P over the scores already in registers
-                        uint32_t y[16];
+                        for (int c0 = 0; c0 < kHalf; c0 += 32) {
+                            uint32_t y[16];
 #pragma unroll
-                        for (int c = 0; c < 32; c += 2) {
-                            const float a = exp2_fast(fmaf(__uint_as_float(x[c0 + c]), p.c, -mm));
-                            const float b = exp2_fast(fmaf(__uint_as_float(x[c0 + c + 1]), p.c, -mm));
-                            sum[c & 2] += a;
-                            sum[(c & 2) + 1] += b;
-                            y[c / 2] = Half2<BF16>::down(a, b);
+                            for (int c = 0; c < 32; c += 2) {
+                                const float a = exp2_fast(fmaf(__uint_as_float(x[c0 + c]), p.c, -mm));
+                                const float b = exp2_fast(fmaf(__uint_as_float(x[c0 + c + 1]), p.c, -mm));
+                                sum[c & 2] += a;
+                                sum[(c & 2) + 1] += b;
+                                y[c / 2] = Half2<BF16>::down(a, b);
+                            }
+                            tmem_store16(t_s + (half * kHalf + c0) / 2, y);
                         }
-                        tmem_store16(t_s + c0 / 2, y);
-                    }
+                    };
+                    exp_half(0);
+                    load_half(1);
+                    exp_half(1);
                     l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     tc_wait_st();
                     tc_fence_before();
@@ -628,6 +636,7 @@ int attend(AttnParams &p, int dtype, const void *q, int64_t num_rows, int64_t q_
     p.out = out;
     p.lse = lse;
     p.status = static_cast<uint32_t *>(workspace);
+    p.pages.spare = static_cast<const int32_t *>(workspace);
     int dev = 0, sms = 0;
     if (cudaGetDevice(&dev) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)

@@ -47,6 +47,11 @@ __device__ __forceinline__ uint32_t weight_key(float w) {
 
 constexpr int kBins11 = 2048;
 
+// The weight of a key (+0 for either zero).
+__device__ __forceinline__ float key_weight(uint32_t k) {
+    return __uint_as_float((k & 0x80000000u) ? k & 0x7fffffffu : ~k);
+}
+
 struct SelectShared {
     uint32_t hist[kBins11];
     uint32_t scan[kSelectWarps];
@@ -95,8 +100,19 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
     else __syncthreads();
     auto pos = [&](int32_t s) { return s < a ? s : sh.draft[s - a]; };
     auto key = [&](int32_t s) { return p.staged ? keys[s - s0] : weight_key(w[pos(s)]); };
-    if (p.staged && need)
-        for (int32_t s = s0 + tid; s < c1; s += kSelectThreads) keys[s - s0] = weight_key(w[pos(s)]);
+    if (p.staged) {   // eight loads in flight a thread
+        constexpr int kUnroll = 8;
+        for (int32_t b = s0 + tid; b < s1; b += kSelectThreads * kUnroll) {
+            float x[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (b + u * kSelectThreads < s1) x[u] = w[pos(b + u * kSelectThreads)];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (b + u * kSelectThreads < s1) keys[b + u * kSelectThreads - s0] = weight_key(x[u]);
+        }
+        __syncthreads();
+    }
     // the key t at the budget: keys above it are kept, and the first `ties`
     // equal to it (with `whole` every key of at least t)
     uint32_t t = 0;
@@ -137,8 +153,8 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
         }
         if (lane == 31) sh.scan[warp] = inc;
         __syncthreads();
-        uint32_t above = 0;   // in higher bins
-        for (int w = 0; w < kSelectWarps; ++w) above += w < warp ? sh.scan[w] : 0;
+        uint32_t above = lane < warp ? sh.scan[lane] : 0;   // in higher bins
+        for (int o = 16; o; o >>= 1) above += __shfl_xor_sync(~0u, above, o);
         above += inc - h0 - h1;
         if (above < need && above + h0 + h1 >= need) {
             const bool first = above + h0 >= need;
@@ -212,7 +228,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
             const uint32_t at = gt + __popc(gm & below) + (eb < need ? eb : need);
             const int32_t q = pos(s + lane);
             kept[at] = q;
-            out_w[at] = w[q];
+            out_w[at] = p.staged ? key_weight(keys[s + lane - s0]) : w[q];
         }
         gt += __popc(gm);
         eq += __popc(em);
@@ -332,6 +348,7 @@ extern "C" int gbtopk_cache_evict(const float *weights, int64_t num_requests, in
     p.from.cols = pt_cols < INT32_MAX / page_size ? pt_cols : INT32_MAX / page_size;
     p.from.row_stride = pt_row_stride;
     p.from.num_slots = num_slots;
+    p.from.spare = seq_lens;
     p.from.page.init(static_cast<uint32_t>(page_size));
     p.to = p.from;
     p.to.table = out_page_table;

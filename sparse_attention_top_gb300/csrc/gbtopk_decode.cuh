@@ -51,28 +51,34 @@ __device__ __forceinline__ T fetch(const T *p) {
 // The page table of a batch of requests over one cache.
 struct Paging {
     const int32_t *table;
+    const int32_t *spare;   // any readable word
     int64_t cols, row_stride;
     int64_t num_slots;
     FastDiv page;
 
-    // Page id and offset in it of a position; the id's load is in flight
-    // until slot() looks at it.
+    // Page id and offset in it of a position.  The id's load is in flight
+    // until slot() looks at it: it is unconditional (from
+    // `spare` where there is no position),
+    // because a load that is merged with a constant is waited for at once.
     struct Place {
         int32_t id;
         uint32_t rest;
+        bool is;
     };
-    __device__ __forceinline__ Place place(int64_t i, int32_t p) const {
+    __device__ __forceinline__ Place place(int64_t i, int32_t p, bool is) const {
         const uint32_t c = page.div(static_cast<uint32_t>(p));
-        Place at{-1, static_cast<uint32_t>(p) - c * page.d};
-        if (p >= 0 && static_cast<int64_t>(c) < cols) at.id = fetch(table + i * row_stride + c);
-        return at;
+        is = is && p >= 0 && static_cast<int64_t>(c) < cols;
+        return listed(table + i * row_stride + c, is, static_cast<uint32_t>(p) - c * page.d);
+    }
+    __device__ __forceinline__ Place listed(const int32_t *at, bool is, uint32_t rest = 0) const {
+        return Place{fetch(is ? at : spare), rest, is};
     }
     // The cache slot, or -1 where there is none.
     __device__ __forceinline__ int64_t slot(const Place &at) const {
         const int64_t s = static_cast<int64_t>(at.id) * page.d + at.rest;
-        return at.id >= 0 && s < num_slots ? s : -1;
+        return at.is && at.id >= 0 && s < num_slots ? s : -1;
     }
-    __device__ __forceinline__ int64_t slot(int64_t i, int32_t p) const { return slot(place(i, p)); }
+    __device__ __forceinline__ int64_t slot(int64_t i, int32_t p) const { return slot(place(i, p, true)); }
 };
 
 template <bool BF16>

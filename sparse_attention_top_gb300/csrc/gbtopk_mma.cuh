@@ -181,18 +181,6 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t *v) {
         : "memory");
 }
 
-// Moves registers between the warpgroups of a block (every warp of the
-// warpgroup calls it).  The sum over the block may not exceed what the launch
-// gave: an increase beyond it would wait forever.
-template <int N>
-__device__ __forceinline__ void regs_up() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void regs_down() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));

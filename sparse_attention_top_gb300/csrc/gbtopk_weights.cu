@@ -38,8 +38,6 @@ template <int DP>
 struct Shape {
     static constexpr int NQ = DP == 256 ? 64 : 128;         // query rows of a phase
     static constexpr int kThreads = 512;                    // 2 summing warpgroups, products, copies
-    static constexpr int kLaunchRegs = 128, kSumRegs = 152, kOtherRegs = 96;
-    static_assert(2 * kSumRegs + 2 * kOtherRegs <= 4 * kLaunchRegs, "register pool");
     static constexpr int kQBytes = NQ * DP * 2;             // one of two buffers
     static constexpr int kStageBytes = KT * DP * 2;
     static constexpr int kSums = 2 * kSpan * KT * 4;
@@ -171,7 +169,6 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
 
     if (warp >= kMmaWarp + 4) {
         // ------------------------------------------------ copies
-        regs_down<Sh::kOtherRegs>();
         const int w = warp - kMmaWarp - 4;
         uint32_t phase = 0, job = 0;
         while (ok && spans.next(&s)) {
@@ -183,11 +180,9 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
                 seen = static_cast<uint64_t>(__reduce_or_sync(~0u, static_cast<uint32_t>(seen >> 32))) << 32 |
                        __reduce_or_sync(~0u, static_cast<uint32_t>(seen));
             }
-            auto place_of = [&](int32_t t) -> Paging::Place {
+            auto place_of = [&](int32_t t) {
                 const int32_t pos = t * KT + w * 32 + lane;
-                if (pos >= s.n || pos >= p.width) return Paging::Place{-1, 0};
-                if (pos >= s.ctx && !((seen >> (pos - s.ctx)) & 1)) return Paging::Place{-1, 0};
-                return a.pages.place(s.b, pos);
+                return a.pages.place(s.b, pos, pos < s.n && pos < p.width && (pos < s.ctx || ((seen >> (pos - s.ctx)) & 1)));
             };
             Paging::Place next = place_of(s.t0);
             for (int32_t ph = 0; ph < s.phases && ok; ++ph, ++phase) {
@@ -238,11 +233,16 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
         copies_land();
     } else if (warp >= kMmaWarp) {
         // ------------------------------------------------ matrix products
-        regs_down<Sh::kOtherRegs>();
         if (warp == kMmaWarp) {   // all lanes alike, see elect_lane
             const bool lead = elect_lane();
             uint32_t phase = 0, job = 0;
-            while (ok && spans.next(&s)) {
+            while (ok && __any_sync(~0u, spans.next(&s))) {
+                // broadcasts: values known to be warp-uniform
+                s.phases = __shfl_sync(~0u, s.phases, 0);
+                s.groups = __shfl_sync(~0u, s.groups, 0);
+                s.rows = __shfl_sync(~0u, s.rows, 0);
+                s.t0 = __shfl_sync(~0u, s.t0, 0);
+                s.t1 = __shfl_sync(~0u, s.t1, 0);
                 for (int32_t ph = 0; ph < s.phases && ok; ++ph, ++phase) {
                     const int32_t r0 = (ph % s.groups) * NQ;
                     const int32_t rows = s.rows - r0 < NQ ? s.rows - r0 : NQ, padded = (rows + 15) / 16 * 16;
@@ -283,7 +283,6 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
         __syncwarp();
     } else {
         // ------------------------------------------------ sums
-        regs_up<Sh::kSumRegs>();
         const int wg = warp >> 2, key = threadIdx.x & 127;
         const uint32_t t_s = tmem + (static_cast<uint32_t>(warp & 3) << 21) + wg * 128;
         float *mine = sums + wg * kSpan * KT + key;
@@ -424,6 +423,7 @@ extern "C" int gbtopk_cache_weights(const void *q, int dtype, int64_t num_rows, 
     a.c = fmaxf(fabsf(scale) * kLog2e, FLT_MIN);
     a.negative = scale < 0.f;
     a.status = static_cast<uint32_t *>(workspace);
+    a.pages.spare = static_cast<const int32_t *>(workspace);
     p.accept_mask = accept_mask;
     p.lse = lse;
     p.weights = weights;
