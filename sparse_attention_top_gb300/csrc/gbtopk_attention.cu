@@ -561,13 +561,16 @@ cudaError_t launch_shape(AttnParams p, uint8_t *ws, int sms, cudaStream_t stream
     p.unit_ends = reinterpret_cast<int32_t *>(ws + kWsHeaderBytes);
     p.part_ml = reinterpret_cast<float2 *>(ws + kWsHeaderBytes + unit_bytes(static_cast<int64_t>(p.requests) * p.next_n, p.q_heads));
     p.part_o = reinterpret_cast<float *>(p.part_ml + partial_rows());
-    cudaError_t e = cudaFuncSetAttribute(attention_kernel<BF16, DP, W, SPLIT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         static_cast<int>(Sh::kSmem));
+    static std::atomic<uint64_t> allowed{0};
+    cudaError_t e = allow_smem(attention_kernel<BF16, DP, W, SPLIT>, Sh::kSmem, allowed);
     if (e != cudaSuccess) return e;
     const int grid = sms < kMaxGrid ? sms : kMaxGrid;
     e = launch_pdl(attention_kernel<BF16, DP, W, SPLIT>, dim3(static_cast<unsigned>(grid)), Sh::kThreads, Sh::kSmem, stream, 1, p);
     if (e != cudaSuccess) return e;
     const int64_t units = static_cast<int64_t>(p.requests) * p.request_units;
+    // no unit spans blocks where none has more than one tile
+    const int64_t longest = p.seq_lens ? p.pages.cols * p.pages.page.d : p.top_k;
+    if (longest <= Sh::KT) return cudaSuccess;
     const int64_t each = rows < Sh::kRows ? rows : Sh::kRows;
     const dim3 blocks(static_cast<unsigned>(units), static_cast<unsigned>((each + kCombineRows - 1) / kCombineRows));
     return launch_pdl(combine_kernel<BF16, DP>, blocks, kCombineRows * 32, 0, stream, 1, p, Sh::kRows);
@@ -637,10 +640,8 @@ int attend(AttnParams &p, int dtype, const void *q, int64_t num_rows, int64_t q_
     p.lse = lse;
     p.status = static_cast<uint32_t *>(workspace);
     p.pages.spare = static_cast<const int32_t *>(workspace);
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return GBTOPK_ECUDA;
+    const int sms = device_sms();
+    if (sms == 0) return GBTOPK_ECUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     return (dtype == GBTOPK_BF16 ? launch_attention<true>(p, ws, sms, s) : launch_attention<false>(p, ws, sms, s)) ==

@@ -376,8 +376,8 @@ extern "C" int gbtopk_cache_evict(const float *weights, int64_t num_requests, in
     p.move_rows = static_cast<int32_t>(bytes >= 32768 ? 1 : 32768 / bytes > 64 ? 64 : 32768 / bytes);
     p.row_blocks = (budget + p.move_rows - 1) / p.move_rows;
     if (rows * p.row_blocks > INT32_MAX || rows * cluster > INT32_MAX) return GBTOPK_EUNSUPPORTED;
-    if (cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kStagedKeys * 4) != cudaSuccess)
-        return GBTOPK_ECUDA;
+    static std::atomic<uint64_t> allowed{0};
+    if (allow_smem(evict_select_kernel, kStagedKeys * 4, allowed) != cudaSuccess) return GBTOPK_ECUDA;
     if (launch_pdl(evict_select_kernel, dim3(static_cast<unsigned>(rows * cluster)), kSelectThreads, smem, s, cluster, p) !=
         cudaSuccess)
         return GBTOPK_ECUDA;

@@ -364,8 +364,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
 
 template <bool BF16, int DP>
 cudaError_t launch_shape(const WeightParams &p, int sms, cudaStream_t stream) {
-    const cudaError_t e = cudaFuncSetAttribute(weights_kernel<BF16, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               static_cast<int>(Shape<DP>::kSmem));
+    static std::atomic<uint64_t> allowed{0};
+    const cudaError_t e = allow_smem(weights_kernel<BF16, DP>, Shape<DP>::kSmem, allowed);
     if (e != cudaSuccess) return e;
     return launch_pdl(weights_kernel<BF16, DP>, dim3(static_cast<unsigned>(sms)), Shape<DP>::kThreads, Shape<DP>::kSmem, stream, 1, p);
 }
@@ -429,10 +429,8 @@ extern "C" int gbtopk_cache_weights(const void *q, int dtype, int64_t num_rows, 
     p.weights = weights;
     p.weight_heads = weight_heads;
     p.width = width;
-    int dev = 0, sms = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess ||
-        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-        return GBTOPK_ECUDA;
+    const int sms = device_sms();
+    if (sms == 0) return GBTOPK_ECUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     return (dtype == GBTOPK_BF16 ? launch_weights<true>(p, sms, s) : launch_weights<false>(p, sms, s)) == cudaSuccess
                ? GBTOPK_OK

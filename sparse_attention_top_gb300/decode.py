@@ -13,6 +13,7 @@ p % page_size`` - the numbers ``top_k_page_table_transform`` returns.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -70,38 +71,57 @@ def gbtopk_verify_workspace_bytes(num_rows: int, vocab: int, next_n: int) -> int
     return int(_lib().gbtopk_verify_workspace_bytes(num_rows, vocab, next_n))
 
 
-def _tensor(t, name: str, device, dtype, shape=None, contiguous: bool = True):
-    if not isinstance(t, torch.Tensor) or t.device != device:
-        raise ValueError(f"{name} must be a tensor on {device}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}")
-    if contiguous and not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+# Each call tests its arguments in one expression of cheap attribute reads (a
+# call's host time is what a small batch waits for); only where that fails does
+# _refuse look for the reason.
+
+_HALF = (torch.bfloat16, torch.float16)
+_F32, _I32, _I64 = torch.float32, torch.int32, torch.int64
+
+
+def _refuse(*rules):
+    for ok, message in rules:
+        if not ok:
+            raise ValueError(message)
+    raise ValueError("invalid arguments")
+
+
+def _dense(t, dev, dtype, shape) -> bool:
+    return isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == dev and t.shape == shape \
+        and t.is_contiguous()
+
+
+def _maybe(t, dev, dtype, shape) -> bool:
+    return t is None or _dense(t, dev, dtype, shape)
+
+
+def _table(t, dev, rows) -> bool:
+    """An int32 matrix of `rows` rows with inner stride 1."""
+    return isinstance(t, torch.Tensor) and t.dtype is _I32 and t.device == dev and t.dim() == 2 \
+        and t.shape[0] == rows and (t.stride(1) == 1 or t.shape[1] < 2)
 
 
 def _query(q):
-    _gb._require_cuda(q, "q")
-    if q.dim() != 3 or q.dtype not in (torch.bfloat16, torch.float16) or (q.shape[2] > 1 and q.stride(2) != 1):
-        raise ValueError("q must be a 3-D bf16/fp16 tensor [num_rows, q_heads, head_dim], inner stride 1")
+    """(rows, heads, dim), device, strides of the queries."""
+    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3 and q.dtype in _HALF):
+        _gb._require_cuda(q, "q")
+        raise ValueError("q must be a 3-D bf16/fp16 tensor [num_rows, q_heads, head_dim]")
+    strides = q.stride()
+    if strides[2] != 1 and q.shape[2] > 1:
+        raise ValueError("q must have inner stride 1")
+    return q.shape, q.device, strides
 
 
-def _cache(t, name: str, q, like=None):
-    if not isinstance(t, torch.Tensor) or t.device != q.device or t.dtype != q.dtype:
-        raise ValueError(f"{name} must be a {q.dtype} tensor on {q.device}")
-    if t.dim() != 3 or t.shape[2] != q.shape[2] or (t.shape[2] > 1 and t.stride(2) != 1):
-        raise ValueError(f"{name} must be [num_slots, kv_heads, head_dim] with inner stride 1")
-    if like is not None and t.shape != like.shape:
-        raise ValueError("k_cache and v_cache must have one shape")
-    if t.shape[1] < 1 or q.shape[1] % t.shape[1] != 0:
-        raise ValueError("q_heads must be a multiple of kv_heads")
-
-
-def _table(t, name: str, device, requests: int):
-    if not isinstance(t, torch.Tensor) or t.device != device or t.dtype != torch.int32 or t.dim() != 2 \
-            or t.shape[0] != requests or (t.shape[1] > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} must be an int32 [num_requests, pt_cols] tensor on {device}, inner stride 1")
+def _cache(t, q, dev, dim):
+    """(slots, kv heads) and strides of a cache for `q`."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is q.dtype and t.device == dev and t.dim() == 3):
+        raise ValueError(f"the caches must be 3-D {q.dtype} tensors on {dev}")
+    slots, heads, d = t.shape
+    strides = t.stride()
+    if d != dim or (strides[2] != 1 and d > 1) or heads < 1 or q.shape[1] % heads != 0:
+        raise ValueError("the caches must be [num_slots, kv_heads, head_dim] with inner stride 1, q_heads a "
+                         "multiple of kv_heads")
+    return slots, heads, strides
 
 
 def _requests(rows: int, next_n: int) -> int:
@@ -110,32 +130,38 @@ def _requests(rows: int, next_n: int) -> int:
     return rows // next_n
 
 
-def _outputs(q, out, lse, return_lse: bool):
-    rows, heads, _ = q.shape
+def _outputs(q, shape, dev, out, lse, return_lse: bool):
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-    else:
-        _tensor(out, "out", q.device, q.dtype, tuple(q.shape))
-    if lse is not None:
-        _tensor(lse, "lse", q.device, torch.float32, (rows, heads))
-    elif return_lse:
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=q.device)
+        out = torch.empty(shape, dtype=q.dtype, device=dev)
+    elif not _dense(out, dev, q.dtype, shape):
+        raise ValueError("out must be a contiguous tensor like q")
+    if lse is None:
+        if return_lse:
+            lse = torch.empty(shape[:2], dtype=_F32, device=dev)
+    elif not _dense(lse, dev, _F32, shape[:2]):
+        raise ValueError("lse must be a contiguous fp32 [num_rows, q_heads] tensor on q's device")
     return out, lse
 
 
-def _scratch(workspace, device, nbytes: int):
+try:   # the handle alone, without a Stream object
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
+_attention_bytes = functools.lru_cache(maxsize=None)(gbtopk_attention_workspace_bytes)
+_verify_bytes = functools.lru_cache(maxsize=None)(gbtopk_verify_workspace_bytes)
+
+
+def _scratch(workspace, dev, stream, nbytes: int):
+    """Address and size of the caller's workspace, or of the stream's."""
     if workspace is None:
-        return _gb._workspace(device, nbytes)
+        workspace = _gb._WS.get((dev.index, stream))
+        if workspace is None or workspace.numel() < nbytes:
+            workspace = _gb._workspace(dev, nbytes)
+        return workspace.data_ptr(), workspace.numel()
     _gb._require_cuda(workspace, "workspace")
-    return workspace
-
-
-def _ws_args(ws):
-    return ws.data_ptr(), ws.numel() * ws.element_size()
-
-
-def _strides(t):
-    return t.data_ptr(), t.stride(0), t.stride(1)
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -155,25 +181,29 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     ``scale`` defaults to ``head_dim ** -0.5``.  Returns ``out`` (like ``q``),
     or ``(out, lse)`` with ``return_lse`` or a given ``lse``; a row that sees
     nothing is zero with ``lse`` -inf."""
-    _query(q)
-    rows, heads, dim = q.shape
+    shape, dev, qs = _query(q)
+    rows, heads, dim = shape
     requests = _requests(rows, next_n)
-    _cache(k_cache, "k_cache", q)
-    _cache(v_cache, "v_cache", q, k_cache)
-    _table(page_table, "page_table", q.device, requests)
-    _tensor(seq_lens, "seq_lens", q.device, torch.int32, (requests,))
-    if tree_mask is not None:
-        _tensor(tree_mask, "tree_mask", q.device, torch.int64, (rows,))
-    out, lse = _outputs(q, out, lse, return_lse)
-    kv = k_cache.shape[1]
-    lib = _lib()
-    ws = _scratch(workspace, q.device, lib.gbtopk_attention_workspace_bytes(rows, heads, kv, dim))
-    _gb._check(lib.gbtopk_tree_attention(
-        q.data_ptr(), _gb._DTYPES[q.dtype], rows, q.stride(0), q.stride(1), heads, kv, dim,
-        *_strides(k_cache), *_strides(v_cache), k_cache.shape[0], page_table.data_ptr(),
-        page_table.shape[1], page_table.stride(0), page_size, seq_lens.data_ptr(), next_n,
-        _gb._ptr(tree_mask), dim ** -0.5 if scale is None else scale, out.data_ptr(), _gb._ptr(lse),
-        *_ws_args(ws), _gb._stream_handle(q.device)))
+    slots, kv, ks = _cache(k_cache, q, dev, dim)
+    vslots, vkv, vs = _cache(v_cache, q, dev, dim)
+    if not (slots == vslots and kv == vkv and _table(page_table, dev, requests)
+            and _dense(seq_lens, dev, _I32, (requests,)) and _maybe(tree_mask, dev, _I64, (rows,))):
+        _refuse((slots == vslots and kv == vkv, "k_cache and v_cache must have one shape"),
+                (_table(page_table, dev, requests), "page_table must be int32 [num_requests, pt_cols], inner stride 1"),
+                (_dense(seq_lens, dev, _I32, (requests,)), "seq_lens must be contiguous int32 [num_requests]"),
+                (False, "tree_mask must be contiguous int64 [num_rows]"))
+    out, lse = _outputs(q, shape, dev, out, lse, return_lse)
+    lib = _calls or _lib()
+    stream = _raw_stream(dev.index)
+    ws, ws_bytes = _scratch(workspace, dev, stream, _attention_bytes(rows, heads, kv, dim))
+    status = lib.gbtopk_tree_attention(
+        q.data_ptr(), _gb._DTYPES[q.dtype], rows, qs[0], qs[1], heads, kv, dim, k_cache.data_ptr(), ks[0], ks[1],
+        v_cache.data_ptr(), vs[0], vs[1], slots, page_table.data_ptr(), page_table.shape[1], page_table.stride(0),
+        page_size, seq_lens.data_ptr(), next_n, None if tree_mask is None else tree_mask.data_ptr(),
+        dim ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(), ws, ws_bytes,
+        stream)
+    if status < 0:
+        _gb._check(status)
     return out if lse is None else (out, lse)
 
 
@@ -186,20 +216,24 @@ def selected_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
     ``indices`` int32 [num_rows, top_k], as ``top_k_page_table_transform``
     returns them: entries < 0 or beyond the cache are skipped.  Everything
     else as for ``tree_attention``."""
-    _query(q)
-    rows, heads, dim = q.shape
-    _cache(k_cache, "k_cache", q)
-    _cache(v_cache, "v_cache", q, k_cache)
-    _table(indices, "indices", q.device, rows)
-    out, lse = _outputs(q, out, lse, return_lse)
-    kv = k_cache.shape[1]
-    lib = _lib()
-    ws = _scratch(workspace, q.device, lib.gbtopk_attention_workspace_bytes(rows, heads, kv, dim))
-    _gb._check(lib.gbtopk_selected_attention(
-        q.data_ptr(), _gb._DTYPES[q.dtype], rows, q.stride(0), q.stride(1), heads, kv, dim,
-        *_strides(k_cache), *_strides(v_cache), k_cache.shape[0], indices.data_ptr(),
-        indices.shape[1], indices.stride(0), dim ** -0.5 if scale is None else scale,
-        out.data_ptr(), _gb._ptr(lse), *_ws_args(ws), _gb._stream_handle(q.device)))
+    shape, dev, qs = _query(q)
+    rows, heads, dim = shape
+    slots, kv, ks = _cache(k_cache, q, dev, dim)
+    vslots, vkv, vs = _cache(v_cache, q, dev, dim)
+    if not (slots == vslots and kv == vkv and _table(indices, dev, rows)):
+        _refuse((slots == vslots and kv == vkv, "k_cache and v_cache must have one shape"),
+                (False, "indices must be int32 [num_rows, top_k], inner stride 1"))
+    out, lse = _outputs(q, shape, dev, out, lse, return_lse)
+    lib = _calls or _lib()
+    stream = _raw_stream(dev.index)
+    ws, ws_bytes = _scratch(workspace, dev, stream, _attention_bytes(rows, heads, kv, dim))
+    status = lib.gbtopk_selected_attention(
+        q.data_ptr(), _gb._DTYPES[q.dtype], rows, qs[0], qs[1], heads, kv, dim, k_cache.data_ptr(), ks[0], ks[1],
+        v_cache.data_ptr(), vs[0], vs[1], slots, indices.data_ptr(), indices.shape[1], indices.stride(0),
+        dim ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(), ws, ws_bytes,
+        stream)
+    if status < 0:
+        _gb._check(status)
     return out if lse is None else (out, lse)
 
 
@@ -215,30 +249,32 @@ def accumulate_cache_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.
     ``tree_attention``'s ``lse``: all rows, or those whose bit is set in
     ``accept_mask`` (int64 [num_requests], ``verify_drafts``'s).  Returns
     ``weights``."""
-    _query(q)
-    rows, heads, dim = q.shape
+    shape, dev, qs = _query(q)
+    rows, heads, dim = shape
     requests = _requests(rows, next_n)
-    _cache(k_cache, "k_cache", q)
-    _table(page_table, "page_table", q.device, requests)
-    _tensor(seq_lens, "seq_lens", q.device, torch.int32, (requests,))
-    _tensor(lse, "lse", q.device, torch.float32, (rows, heads))
-    kv = k_cache.shape[1]
-    _tensor(weights, "weights", q.device, torch.float32)
-    if weights.dim() != 3 or weights.shape[0] != requests or weights.shape[1] not in (1, kv):
-        raise ValueError("weights must be [num_requests, 1 or kv_heads, width]")
-    if tree_mask is not None:
-        _tensor(tree_mask, "tree_mask", q.device, torch.int64, (rows,))
-    if accept_mask is not None:
-        _tensor(accept_mask, "accept_mask", q.device, torch.int64, (requests,))
-    lib = _lib()
-    ws = _scratch(workspace, q.device, lib.gbtopk_attention_workspace_bytes(rows, heads, kv, dim))
-    _gb._check(lib.gbtopk_cache_weights(
-        q.data_ptr(), _gb._DTYPES[q.dtype], rows, q.stride(0), q.stride(1), heads, kv, dim,
-        *_strides(k_cache), k_cache.shape[0], lse.data_ptr(), page_table.data_ptr(),
-        page_table.shape[1], page_table.stride(0), page_size, seq_lens.data_ptr(), next_n,
-        _gb._ptr(tree_mask), _gb._ptr(accept_mask), dim ** -0.5 if scale is None else scale,
-        weights.data_ptr(), weights.shape[1], weights.shape[2], *_ws_args(ws),
-        _gb._stream_handle(q.device)))
+    slots, kv, ks = _cache(k_cache, q, dev, dim)
+    wshape = weights.shape if isinstance(weights, torch.Tensor) and weights.dim() == 3 else (-1, -1, -1)
+    fits = wshape[0] == requests and wshape[1] in (1, kv) and _dense(weights, dev, _F32, wshape)
+    if not (fits and _table(page_table, dev, requests) and _dense(seq_lens, dev, _I32, (requests,))
+            and _dense(lse, dev, _F32, shape[:2]) and _maybe(tree_mask, dev, _I64, (rows,))
+            and _maybe(accept_mask, dev, _I64, (requests,))):
+        _refuse((fits, "weights must be contiguous fp32 [num_requests, 1 or kv_heads, width]"),
+                (_table(page_table, dev, requests), "page_table must be int32 [num_requests, pt_cols], inner stride 1"),
+                (_dense(seq_lens, dev, _I32, (requests,)), "seq_lens must be contiguous int32 [num_requests]"),
+                (_dense(lse, dev, _F32, shape[:2]), "lse must be contiguous fp32 [num_rows, q_heads]"),
+                (_maybe(tree_mask, dev, _I64, (rows,)), "tree_mask must be contiguous int64 [num_rows]"),
+                (False, "accept_mask must be contiguous int64 [num_requests]"))
+    lib = _calls or _lib()
+    stream = _raw_stream(dev.index)
+    ws, ws_bytes = _scratch(workspace, dev, stream, _attention_bytes(rows, heads, kv, dim))
+    status = lib.gbtopk_cache_weights(
+        q.data_ptr(), _gb._DTYPES[q.dtype], rows, qs[0], qs[1], heads, kv, dim, k_cache.data_ptr(), ks[0], ks[1], slots,
+        lse.data_ptr(), page_table.data_ptr(), page_table.shape[1], page_table.stride(0), page_size, seq_lens.data_ptr(),
+        next_n, None if tree_mask is None else tree_mask.data_ptr(),
+        None if accept_mask is None else accept_mask.data_ptr(), dim ** -0.5 if scale is None else scale,
+        weights.data_ptr(), wshape[1], wshape[2], ws, ws_bytes, stream)
+    if status < 0:
+        _gb._check(status)
     return weights
 
 
@@ -265,39 +301,43 @@ def evict_cache(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     elements."""
     _gb._require_cuda(weights, "weights")
     dev = weights.device
-    _tensor(weights, "weights", dev, torch.float32)
-    if weights.dim() != 3:
-        raise ValueError("weights must be [num_requests, 1 or kv_heads, width]")
-    requests, wheads, width = weights.shape
-    for t, name in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if not isinstance(t, torch.Tensor) or t.device != dev or t.dim() != 3 \
-                or t.element_size() not in (2, 4) or (t.shape[2] > 1 and t.stride(2) != 1):
-            raise ValueError(f"{name} must be [num_slots, kv_heads, head_dim] of 2- or 4-byte elements "
-                             f"on {dev}, inner stride 1")
-    if k_cache.shape != v_cache.shape or k_cache.dtype != v_cache.dtype:
-        raise ValueError("k_cache and v_cache must have one shape and type")
-    if wheads not in (1, k_cache.shape[1]):
-        raise ValueError("weights must be [num_requests, 1 or kv_heads, width]")
-    _table(page_table, "page_table", dev, requests)
-    _table(out_page_table, "out_page_table", dev, requests)
-    _tensor(seq_lens, "seq_lens", dev, torch.int32, (requests,))
-    if accept_mask is not None:
-        _tensor(accept_mask, "accept_mask", dev, torch.int64, (requests,))
-    if budget < 1 or recent < 0 or page_size < 1 or out_page_table.shape[1] * page_size < budget:
-        raise ValueError("budget >= 1, recent >= 0 and room for budget positions in out_page_table are required")
+    if weights.dtype is not _F32 or weights.dim() != 3 or not weights.is_contiguous():
+        raise ValueError("weights must be contiguous fp32 [num_requests, 1 or kv_heads, width]")
+    wshape = weights.shape
+    requests, wheads, width = wshape
+    for t in (k_cache, v_cache):
+        if not (isinstance(t, torch.Tensor) and t.device == dev and t.dim() == 3 and t.element_size() in (2, 4)
+                and (t.stride(2) == 1 or t.shape[2] < 2)):
+            raise ValueError(f"the caches must be [num_slots, kv_heads, head_dim] of 2- or 4-byte elements on {dev}, "
+                             "inner stride 1")
+    slots, kv, dim = k_cache.shape
+    one = k_cache.shape == v_cache.shape and k_cache.dtype is v_cache.dtype
+    if not (one and wheads in (1, kv) and _table(page_table, dev, requests) and _table(out_page_table, dev, requests)
+            and _dense(seq_lens, dev, _I32, (requests,)) and _maybe(accept_mask, dev, _I64, (requests,))
+            and budget >= 1 and recent >= 0 and page_size >= 1 and out_page_table.shape[1] * page_size >= budget
+            and _maybe(out_weights, dev, _F32, wshape)):
+        _refuse((one, "k_cache and v_cache must have one shape and type"),
+                (wheads in (1, kv), "weights must be [num_requests, 1 or kv_heads, width]"),
+                (_table(page_table, dev, requests), "page_table must be int32 [num_requests, pt_cols], inner stride 1"),
+                (_table(out_page_table, dev, requests), "out_page_table must be int32 [num_requests, cols], inner stride 1"),
+                (_dense(seq_lens, dev, _I32, (requests,)), "seq_lens must be contiguous int32 [num_requests]"),
+                (_maybe(accept_mask, dev, _I64, (requests,)), "accept_mask must be contiguous int64 [num_requests]"),
+                (_maybe(out_weights, dev, _F32, wshape), "out_weights must be contiguous fp32 like weights"),
+                (False, "budget >= 1, recent >= 0 and room for budget positions in out_page_table are required"))
     if out_weights is None:
-        out_weights = torch.empty_like(weights)
-    else:
-        _tensor(out_weights, "out_weights", dev, torch.float32, tuple(weights.shape))
-    kept = torch.empty((requests, wheads, budget), dtype=torch.int32, device=dev)
-    new_lens = torch.empty((requests,), dtype=torch.int32, device=dev)
-    _gb._check(_lib().gbtopk_cache_evict(
+        out_weights = torch.empty(wshape, dtype=_F32, device=dev)
+    kept = torch.empty((requests, wheads, budget), dtype=_I32, device=dev)
+    new_lens = torch.empty((requests,), dtype=_I32, device=dev)
+    ks, vs = k_cache.stride(), v_cache.stride()
+    status = (_calls or _lib()).gbtopk_cache_evict(
         weights.data_ptr(), requests, wheads, width, seq_lens.data_ptr(), next_n,
-        _gb._ptr(accept_mask), budget, recent, *_strides(k_cache), *_strides(v_cache),
-        k_cache.shape[0], k_cache.shape[1], k_cache.shape[2], k_cache.element_size(),
-        page_table.data_ptr(), page_table.shape[1], page_table.stride(0),
-        out_page_table.data_ptr(), out_page_table.shape[1], out_page_table.stride(0), page_size,
-        kept.data_ptr(), new_lens.data_ptr(), out_weights.data_ptr(), _gb._stream_handle(dev)))
+        None if accept_mask is None else accept_mask.data_ptr(), budget, recent, k_cache.data_ptr(), ks[0], ks[1],
+        v_cache.data_ptr(), vs[0], vs[1], slots, kv, dim, k_cache.element_size(), page_table.data_ptr(),
+        page_table.shape[1], page_table.stride(0), out_page_table.data_ptr(), out_page_table.shape[1],
+        out_page_table.stride(0), page_size, kept.data_ptr(), new_lens.data_ptr(), out_weights.data_ptr(),
+        _raw_stream(dev.index))
+    if status < 0:
+        _gb._check(status)
     return Evicted(kept, new_lens, out_weights)
 
 
@@ -330,26 +370,29 @@ def verify_drafts(logits: torch.Tensor, tokens: torch.Tensor, uniforms: torch.Te
         raise ValueError("logits must be a 2-D fp32/bf16/fp16 tensor with inner stride 1")
     rows, vocab = logits.shape
     requests = _requests(rows, next_n)
-    _tensor(tokens, "tokens", dev, torch.int32, (rows,))
-    _tensor(uniforms, "uniforms", dev, torch.float32, (rows,))
-    _tensor(noise, "noise", dev, torch.float32, (requests, vocab))
-    if tree_mask is not None:
-        _tensor(tree_mask, "tree_mask", dev, torch.int64, (rows,))
-    if temperature is not None:
-        _tensor(temperature, "temperature", dev, torch.float32, (requests,))
-    if draft_probs is not None:
-        if tree_mask is not None:
-            raise ValueError("draft_probs needs a chain of drafts (tree_mask None)")
-        _tensor(draft_probs, "draft_probs", dev, torch.float32, (rows, vocab))
-    accepted = torch.empty((requests,), dtype=torch.int32, device=dev)
-    path = torch.empty((requests, next_n), dtype=torch.int32, device=dev)
-    next_token = torch.empty((requests,), dtype=torch.int32, device=dev)
-    accept_mask = torch.empty((requests,), dtype=torch.int64, device=dev)
-    lib = _lib()
-    ws = _scratch(workspace, dev, lib.gbtopk_verify_workspace_bytes(rows, vocab, next_n))
-    _gb._check(lib.gbtopk_verify_drafts(
-        logits.data_ptr(), _gb._DTYPES[logits.dtype], rows, vocab, logits.stride(0),
-        tokens.data_ptr(), uniforms.data_ptr(), noise.data_ptr(), next_n, _gb._ptr(tree_mask),
-        _gb._ptr(temperature), _gb._ptr(draft_probs), accepted.data_ptr(), path.data_ptr(),
-        next_token.data_ptr(), accept_mask.data_ptr(), *_ws_args(ws), _gb._stream_handle(dev)))
+    if not (_dense(tokens, dev, _I32, (rows,)) and _dense(uniforms, dev, _F32, (rows,))
+            and _dense(noise, dev, _F32, (requests, vocab)) and _maybe(tree_mask, dev, _I64, (rows,))
+            and _maybe(temperature, dev, _F32, (requests,)) and _maybe(draft_probs, dev, _F32, (rows, vocab))
+            and (draft_probs is None or tree_mask is None)):
+        _refuse((_dense(tokens, dev, _I32, (rows,)), "tokens must be contiguous int32 [num_rows]"),
+                (_dense(uniforms, dev, _F32, (rows,)), "uniforms must be contiguous fp32 [num_rows]"),
+                (_dense(noise, dev, _F32, (requests, vocab)), "noise must be contiguous fp32 [num_requests, vocab]"),
+                (_maybe(tree_mask, dev, _I64, (rows,)), "tree_mask must be contiguous int64 [num_rows]"),
+                (_maybe(temperature, dev, _F32, (requests,)), "temperature must be contiguous fp32 [num_requests]"),
+                (draft_probs is None or tree_mask is None, "draft_probs needs a chain of drafts (tree_mask None)"),
+                (False, "draft_probs must be contiguous fp32 [num_rows, vocab]"))
+    accepted = torch.empty((requests,), dtype=_I32, device=dev)
+    path = torch.empty((requests, next_n), dtype=_I32, device=dev)
+    next_token = torch.empty((requests,), dtype=_I32, device=dev)
+    accept_mask = torch.empty((requests,), dtype=_I64, device=dev)
+    lib = _calls or _lib()
+    stream = _raw_stream(dev.index)
+    ws, ws_bytes = _scratch(workspace, dev, stream, _verify_bytes(rows, vocab, next_n))
+    status = lib.gbtopk_verify_drafts(
+        logits.data_ptr(), _gb._DTYPES[logits.dtype], rows, vocab, logits.stride(0), tokens.data_ptr(),
+        uniforms.data_ptr(), noise.data_ptr(), next_n, None if tree_mask is None else tree_mask.data_ptr(),
+        None if temperature is None else temperature.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(),
+        accepted.data_ptr(), path.data_ptr(), next_token.data_ptr(), accept_mask.data_ptr(), ws, ws_bytes, stream)
+    if status < 0:
+        _gb._check(status)
     return Verified(accepted, path, next_token, accept_mask)
