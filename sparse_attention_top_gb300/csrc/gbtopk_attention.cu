@@ -153,27 +153,30 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
         uint32_t stage = 0, lap = 0;
         bool ok = true;
         Walk<KT> ahead = walk;                // the tile after the one being copied
+        while (ahead.more() && ahead.u.span.n == 0) ahead.next();
         int32_t ahead_t = ahead.more() ? ahead.u.t0 : 0;
         Paging::Place next = place_of(ahead.u, ahead_t, ahead.more());
-        for (; walk.more() && ok; walk.next(), ++unit) {
+        for (; walk.more() && ok; walk.next()) {
             const Unit u = walk.u;
+            if (u.span.n == 0) continue;   // nothing to see: the rows' zeros need no products
             const int32_t h = u.hm / p.row_tiles, r0 = (u.hm - h * p.row_tiles) * Sh::kRows;
             // the unit's queries
             if (unit > 0) ok = __all_sync(~0u, bar_wait(&sh.q_empty, (unit - 1) & 1, abort));
             if (!ok) break;
-            for (int x = w * 32 + lane; x < Sh::kRows * chunks; x += 128) {
-                const int32_t r = x / chunks, c = x - r * chunks, rho = r0 + r;
-                if (rho >= rows) break;
-                const int32_t t = rho / p.group, gq = rho - t * p.group;
+            constexpr int kRowChunks = DP / 8 < 32 ? DP / 8 : 32, kStep = 128 / kRowChunks;   // lanes a row, rows a step
+            for (int32_t r = (w * 32 + lane) / kRowChunks; r < Sh::kRows && r0 + r < rows; r += kStep) {
+                const int32_t c = lane % kRowChunks, t = (r0 + r) / p.group, gq = r0 + r - t * p.group;
                 const uint8_t *src = static_cast<const uint8_t *>(p.q) +
                                      2 * ((static_cast<int64_t>(u.b) * p.next_n + t) * p.q_row + (h * p.group + gq) * p.q_head);
-                copy16(q_smem + tile_offset(Sh::kRows, r, c), c < loaded ? src + c * 16 : src, c < loaded ? 16u : 0u);
+                if (c < chunks) copy16(q_smem + tile_offset(Sh::kRows, r, c), c < loaded ? src + c * 16 : src, c < loaded ? 16u : 0u);
             }
             bar_arrive_copies(&sh.q_full);
+            ++unit;
             for (int32_t t = u.t0; t < u.t1; ++t, ++tile) {
                 const int32_t slot = static_cast<int32_t>(p.pages.slot(next));
                 if (++ahead_t == ahead.u.t1) {
-                    ahead.next();
+                    do ahead.next();
+                    while (ahead.more() && ahead.u.span.n == 0);
                     ahead_t = ahead.more() ? ahead.u.t0 : 0;
                 }
                 next = place_of(ahead.u, ahead_t, ahead.more());
@@ -215,7 +218,8 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
             auto wait_item = [&](uint32_t i) { return __all_sync(~0u, bar_wait(&sh.full[i % Sh::kStages], (i / Sh::kStages) & 1, abort)); };
             // (broadcasts: values known to be warp-uniform need no move to
             // uniform registers for every product)
-            for (; __any_sync(~0u, walk.more()) && ok; walk.next(), ++unit) {
+            for (; __any_sync(~0u, walk.more()) && ok; walk.next()) {
+                if (__any_sync(~0u, walk.u.span.n == 0)) continue;
                 const uint32_t nt = __shfl_sync(~0u, static_cast<uint32_t>(walk.u.t1 - walk.u.t0), 0), jobs = nt * Sh::kJobs;
                 ok = __all_sync(~0u, bar_wait(&sh.q_full, unit & 1, abort));
                 if (!ok) break;
@@ -261,6 +265,7 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
                 }
                 job0 += jobs;
                 gi += nt;
+                ++unit;
             }
             // every product is done before the block gives its memory up
             if (lead) tc_commit(&sh.drain);
@@ -288,6 +293,16 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
             const int32_t t = rho / p.group, gq = rho - t * p.group;
             const int64_t r = static_cast<int64_t>(u.b) * p.next_n + t;
             const bool active = mt * Sh::kRows + row_wg + (warp & 3) * 32 < rows;   // any row of the warp
+            if (u.span.n == 0) {
+                if (threadIdx.x < 2) p.unit_ends[2 * (static_cast<int64_t>(u.b) * p.request_units + u.hm) + threadIdx.x] = static_cast<int32_t>(blockIdx.x);
+                if (mine && !(SPLIT && wg == 1)) {
+                    const int64_t at = r * p.q_heads + h * p.group + gq;
+                    for (int c = 0; c < p.dim; c += 8)
+                        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + 2 * (at * p.dim + c)) = make_uint4(0, 0, 0, 0);
+                    if (p.lse) p.lse[at] = -INFINITY;
+                }
+                continue;
+            }
             uint64_t tree = 0;
             if (mine && p.seq_lens) tree = p.tree_mask ? static_cast<uint64_t>(fetch(p.tree_mask + r)) : (~0ull >> (63 - t));
             float m = -INFINITY, l = 0.f;
@@ -371,18 +386,17 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
                         }
                     }
                     const float mm = m == -INFINITY ? 0.f : m;
-                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
                     auto exp_half = [&](int half) {
 #pragma unroll
                         for (int c0 = 0; c0 < kHalf; c0 += 32) {
                             uint32_t y[16];
 #pragma unroll
                             for (int c = 0; c < 32; c += 2) {
-                                const float a = exp2_fast(fmaf(__uint_as_float(x[c0 + c]), p.c, -mm));
-                                const float b = exp2_fast(fmaf(__uint_as_float(x[c0 + c + 1]), p.c, -mm));
-                                sum[c & 2] += a;
-                                sum[(c & 2) + 1] += b;
-                                y[c / 2] = Half2<BF16>::down(a, b);
+                                const float2 z = fma2(x[c0 + c], x[c0 + c + 1], p.c, -mm);
+                                const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
+                                sum[c >> 1 & 1] = add2(sum[c >> 1 & 1], e);
+                                y[c / 2] = Half2<BF16>::down(e.x, e.y);
                             }
                             tmem_store16(t_s + (half * kHalf + c0) / 2, y);
                         }
@@ -390,7 +404,7 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
                     exp_half(0);
                     load_half(1);
                     exp_half(1);
-                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                     tc_wait_st();
                     tc_fence_before();
                 }
@@ -427,7 +441,7 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
             tc_fence_after();
             const bool whole = u.t0 == 0 && u.t1 == u.tiles;
             const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (u.t0 > 0 ? 0 : 1);
-            const int64_t part_row = part * Sh::kRows + row_wg + row;
+            const int32_t part_row = row_wg + row;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const int64_t q_at = r * p.q_heads + h * p.group + gq;
             for (int c0 = 0; c0 < DP; c0 += 32) {
@@ -465,15 +479,15 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
                         *reinterpret_cast<uint4 *>(dst + 2 * c) = make_uint4(y[0], y[1], y[2], y[3]);
                     }
                 } else {
-                    float *dst = p.part_o + part_row * DP + c0;
+                    // column by column: a warp's rows are 128 consecutive bytes
+                    float *dst = p.part_o + (part * DP + c0) * Sh::kRows + part_row;
 #pragma unroll
-                    for (int c = 0; c < 32; c += 4)
-                        *reinterpret_cast<uint4 *>(dst + c) = make_uint4(o[c], o[c + 1], o[c + 2], o[c + 3]);
+                    for (int c = 0; c < 32; ++c) dst[c * Sh::kRows] = __uint_as_float(o[c]);
                 }
             }
             if constexpr (SPLIT) pair_barrier_or(1 + (warp & 3), false);   // ml is read
             if (mine && !(SPLIT && wg == 1)) {
-                if (!whole) p.part_ml[part_row] = make_float2(m, l);
+                if (!whole) p.part_ml[part * Sh::kRows + part_row] = make_float2(m, l);
                 else if (p.lse) p.lse[q_at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
             }
         }
@@ -485,13 +499,12 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
     if (threadIdx.x == 0 && sh.abort) atomicOr(p.status, kStatusCopyLost);
 }
 
-// Joins the partial results of units that span blocks: one warp a row, grid
-// (units, groups of kCombineRows rows).  All of a row's parts are loaded at
-// once where there are at most eight, else eight at a time.
-constexpr int kCombineRows = 8;
+// Joins the partial results of units that span blocks: blocks of 32 rows (a
+// lane each) and eight warps, each DP / 8 columns; grid (units, row groups).
+constexpr int kCombineRows = 32, kCombineThreads = 256;
 
 template <bool BF16, int DP>
-__global__ void __launch_bounds__(kCombineRows * 32) combine_kernel(const __grid_constant__ AttnParams p, int32_t unit_rows) {
+__global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ AttnParams p, int32_t unit_rows) {
     pdl_wait();
     pdl_release();
     const int2 ends = reinterpret_cast<const int2 *>(p.unit_ends)[blockIdx.x];
@@ -499,11 +512,10 @@ __global__ void __launch_bounds__(kCombineRows * 32) combine_kernel(const __grid
     if (c0 == c1 || c0 < 0 || c1 < c0 || c1 >= kMaxGrid) return;   // whole, or not written by a block that gave up
     const int32_t b = static_cast<int32_t>(blockIdx.x / p.request_units), hm = static_cast<int32_t>(blockIdx.x % p.request_units);
     const int32_t h = hm / p.row_tiles, r0 = (hm - h * p.row_tiles) * unit_rows;
-    const int lane = threadIdx.x & 31;
-    const int32_t row = static_cast<int32_t>(blockIdx.y) * kCombineRows + static_cast<int32_t>(threadIdx.x >> 5);
+    const int32_t row = static_cast<int32_t>(blockIdx.y) * kCombineRows + static_cast<int32_t>(threadIdx.x & 31);
     if (row >= unit_rows || r0 + row >= p.next_n * p.group) return;
-    auto at = [&](int32_t c) { return (2ll * c + (c == c0 ? 1 : 0)) * unit_rows + row; };
-    constexpr int kCols = DP / 32, kBatch = DP == 256 ? 4 : 8;
+    constexpr int kCols = DP / 8, kBatch = DP == 256 ? 2 : 4;
+    const int32_t col = static_cast<int32_t>(threadIdx.x >> 5) * kCols;
     float m = -INFINITY, l = 0.f, acc[kCols] = {};
     for (int32_t g0 = c0; g0 <= c1; g0 += kBatch) {
         float2 ml[kBatch];
@@ -512,10 +524,10 @@ __global__ void __launch_bounds__(kCombineRows * 32) combine_kernel(const __grid
         for (int k = 0; k < kBatch; ++k) {
             ml[k] = make_float2(-INFINITY, 0.f);
             if (g0 + k > c1) continue;
-            const int64_t x = at(g0 + k);
-            ml[k] = p.part_ml[x];
+            const int64_t part = 2ll * (g0 + k) + (g0 + k == c0 ? 1 : 0);
+            ml[k] = p.part_ml[part * unit_rows + row];
 #pragma unroll
-            for (int d = 0; d < kCols; ++d) o[k][d] = p.part_o[x * DP + d * 32 + lane];
+            for (int d = 0; d < kCols; ++d) o[k][d] = p.part_o[(part * DP + col + d) * unit_rows + row];
         }
         float top = m;
 #pragma unroll
@@ -538,11 +550,15 @@ __global__ void __launch_bounds__(kCombineRows * 32) combine_kernel(const __grid
     const int32_t t = (r0 + row) / p.group, gq = r0 + row - t * p.group;
     const int64_t q_at = (static_cast<int64_t>(b) * p.next_n + t) * p.q_heads + h * p.group + gq;
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    using T = typename Half2<BF16>::T;
 #pragma unroll
-    for (int d = 0; d < kCols; ++d)
-        if (d * 32 + lane < p.dim) static_cast<T *>(p.out)[q_at * p.dim + d * 32 + lane] = static_cast<T>(acc[d] * inv);
-    if (p.lse && lane == 0) p.lse[q_at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    for (int d = 0; d < kCols; d += 8) {
+        if (col + d >= p.dim) break;
+        uint32_t y[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) y[k] = Half2<BF16>::down(acc[d + 2 * k] * inv, acc[d + 2 * k + 1] * inv);
+        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + 2 * (q_at * p.dim + col + d)) = make_uint4(y[0], y[1], y[2], y[3]);
+    }
+    if (p.lse && col == 0) p.lse[q_at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
 int dim_class(int32_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
@@ -573,7 +589,7 @@ cudaError_t launch_shape(AttnParams p, uint8_t *ws, int sms, cudaStream_t stream
     if (longest <= Sh::KT) return cudaSuccess;
     const int64_t each = rows < Sh::kRows ? rows : Sh::kRows;
     const dim3 blocks(static_cast<unsigned>(units), static_cast<unsigned>((each + kCombineRows - 1) / kCombineRows));
-    return launch_pdl(combine_kernel<BF16, DP>, blocks, kCombineRows * 32, 0, stream, 1, p, Sh::kRows);
+    return launch_pdl(combine_kernel<BF16, DP>, blocks, kCombineThreads, 0, stream, 1, p, Sh::kRows);
 }
 
 // Up to 128 rows a head: two warpgroups take the tiles in turn.  More: each
