@@ -30,20 +30,23 @@ constexpr int kMaskRing = 8;        // tiles whose validity bits are kept (see a
 constexpr float kRescale = 8.f;     // rise of the running maximum (base 2) that rescales O
 
 // DP: head dimension rounded up to 64, 128 or 256.  W: softmax warpgroups.
-// SPLIT (W = 2): both have the same 128 query rows and take the position
-// tiles in turn, each with an O of its own, joined at the unit's end; else
-// each has a 128-row tile of queries.  (A warp needs about 2000 cycles for
-// the softmax of a tile of 128 columns, whose copies take 2800 at dimension
-// 128 and 1400 at 64.)
-template <int DP, int W, bool SPLIT>
+// ROWS: query rows of a unit.  With two warpgroups and up to 128 rows both
+// have the same rows and take the position tiles in turn (kSplit), each with
+// an O of its own, joined at the unit's end; with 256 each has 128 of them.
+// (A warp needs about 1000 to 2000 cycles for the softmax of a tile of 128
+// columns, whose copies take 2800 at dimension 128 and 1400 at 64.)  A tile
+// of 32 query rows leaves a stage more to the ring; the product reads 128
+// rows all the same, the ring's bytes behind them, whose results no one reads.
+template <int DP, int W, int ROWS>
 struct Shape {
+    static constexpr bool kSplit = W == 2 && ROWS <= 128;
     static constexpr int KT = DP == 256 ? 64 : 128;         // positions a tile
-    static constexpr int kRows = SPLIT ? 128 : 128 * W;     // query rows a unit
-    static constexpr int kJobs = SPLIT ? 1 : W;             // products (jobs) a tile
+    static constexpr int kRows = ROWS;
+    static constexpr int kJobs = kSplit ? 1 : W;            // products (jobs) a tile
     static constexpr int kThreads = 128 * W + 256;
     static constexpr int kStageBytes = KT * DP * 2;
     static constexpr int kQBytes = kRows * DP * 2;
-    static constexpr int kJoin = SPLIT ? 128 * 33 * 4 : 0;  // 32 columns of the second O
+    static constexpr int kJoin = kSplit ? (ROWS * 33 * 4 + 127) / 128 * 128 : 0;   // 32 columns of the second O
     static constexpr int kFixed = 2048;                     // barriers, masks, scan scratch
     static constexpr int kFit = (static_cast<int>(kMaxSmemBytes) - 1024 - kFixed - kJoin - kQBytes) / kStageBytes;
     static constexpr int kStages = kFit < 12 ? kFit : 12;   // half of it + 2 tiles fit the mask ring
@@ -51,7 +54,7 @@ struct Shape {
     static constexpr uint32_t kS = 0, kO = 2 * KT;          // tensor memory columns
     static_assert(kO + W * DP <= 512, "tensor memory");
     static_assert(kStages >= 4 && kStages / 2 + 2 <= kMaskRing, "ring");
-    static_assert(!SPLIT || W == 2, "split");
+    static_assert(kSplit || ROWS == 128 * W, "rows");
 };
 
 struct Shared {
@@ -83,9 +86,10 @@ __device__ __forceinline__ bool pair_barrier_or(int id, bool v) {
     return any != 0;
 }
 
-template <bool BF16, int DP, int W, bool SPLIT>
-__global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_kernel(const __grid_constant__ AttnParams p) {
-    using Sh = Shape<DP, W, SPLIT>;
+template <bool BF16, int DP, int W, int ROWS>
+__global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_kernel(const __grid_constant__ AttnParams p) {
+    using Sh = Shape<DP, W, ROWS>;
+    constexpr bool SPLIT = Sh::kSplit;
     constexpr int KT = Sh::KT;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
@@ -386,17 +390,18 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
                         }
                     }
                     const float mm = m == -INFINITY ? 0.f : m;
-                    float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+                    float sum[4] = {0.f, 0.f, 0.f, 0.f};
                     auto exp_half = [&](int half) {
 #pragma unroll
                         for (int c0 = 0; c0 < kHalf; c0 += 32) {
                             uint32_t y[16];
 #pragma unroll
                             for (int c = 0; c < 32; c += 2) {
-                                const float2 z = fma2(x[c0 + c], x[c0 + c + 1], p.c, -mm);
-                                const float2 e = make_float2(exp2_fast(z.x), exp2_fast(z.y));
-                                sum[c >> 1 & 1] = add2(sum[c >> 1 & 1], e);
-                                y[c / 2] = Half2<BF16>::down(e.x, e.y);
+                                const float a = exp2_fast(fmaf(__uint_as_float(x[c0 + c]), p.c, -mm));
+                                const float b = exp2_fast(fmaf(__uint_as_float(x[c0 + c + 1]), p.c, -mm));
+                                sum[c & 2] += a;
+                                sum[(c & 2) + 1] += b;
+                                y[c / 2] = Half2<BF16>::down(a, b);
                             }
                             tmem_store16(t_s + (half * kHalf + c0) / 2, y);
                         }
@@ -404,7 +409,7 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
                     exp_half(0);
                     load_half(1);
                     exp_half(1);
-                    l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                    l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                     tc_wait_st();
                     tc_fence_before();
                 }
@@ -500,8 +505,9 @@ __global__ void __launch_bounds__(Shape<DP, W, SPLIT>::kThreads, 1) attention_ke
 }
 
 // Joins the partial results of units that span blocks: blocks of 32 rows (a
-// lane each) and eight warps, each DP / 8 columns; grid (units, row groups).
-constexpr int kCombineRows = 32, kCombineThreads = 256;
+// lane each) and sixteen warps, each DP / 16 columns; grid (units, row
+// groups).  A batch of parts is loaded at once.
+constexpr int kCombineRows = 32, kCombineThreads = 512;
 
 template <bool BF16, int DP>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ AttnParams p, int32_t unit_rows) {
@@ -514,7 +520,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
     const int32_t h = hm / p.row_tiles, r0 = (hm - h * p.row_tiles) * unit_rows;
     const int32_t row = static_cast<int32_t>(blockIdx.y) * kCombineRows + static_cast<int32_t>(threadIdx.x & 31);
     if (row >= unit_rows || r0 + row >= p.next_n * p.group) return;
-    constexpr int kCols = DP / 8, kBatch = DP == 256 ? 2 : 4;
+    constexpr int kCols = DP / 16, kBatch = DP == 256 ? 4 : 8;
     const int32_t col = static_cast<int32_t>(threadIdx.x >> 5) * kCols;
     float m = -INFINITY, l = 0.f, acc[kCols] = {};
     for (int32_t g0 = c0; g0 <= c1; g0 += kBatch) {
@@ -551,12 +557,10 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
     const int64_t q_at = (static_cast<int64_t>(b) * p.next_n + t) * p.q_heads + h * p.group + gq;
     const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
-    for (int d = 0; d < kCols; d += 8) {
+    for (int d = 0; d < kCols; d += 4) {
         if (col + d >= p.dim) break;
-        uint32_t y[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) y[k] = Half2<BF16>::down(acc[d + 2 * k] * inv, acc[d + 2 * k + 1] * inv);
-        *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + 2 * (q_at * p.dim + col + d)) = make_uint4(y[0], y[1], y[2], y[3]);
+        *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) + 2 * (q_at * p.dim + col + d)) =
+            make_uint2(Half2<BF16>::down(acc[d] * inv, acc[d + 1] * inv), Half2<BF16>::down(acc[d + 2] * inv, acc[d + 3] * inv));
     }
     if (p.lse && col == 0) p.lse[q_at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
@@ -568,9 +572,9 @@ size_t unit_bytes(int64_t num_rows, int32_t q_heads) {   // a unit has a row or 
     return (static_cast<size_t>(num_rows) * q_heads * 8 + 255) / 256 * 256;
 }
 
-template <bool BF16, int DP, int W, bool SPLIT>
+template <bool BF16, int DP, int W, int ROWS>
 cudaError_t launch_shape(AttnParams p, uint8_t *ws, int sms, cudaStream_t stream) {
-    using Sh = Shape<DP, W, SPLIT>;
+    using Sh = Shape<DP, W, ROWS>;
     const int64_t rows = static_cast<int64_t>(p.next_n) * p.group;
     p.row_tiles = static_cast<int32_t>((rows + Sh::kRows - 1) / Sh::kRows);
     p.request_units = p.kv_heads * p.row_tiles;
@@ -578,10 +582,10 @@ cudaError_t launch_shape(AttnParams p, uint8_t *ws, int sms, cudaStream_t stream
     p.part_ml = reinterpret_cast<float2 *>(ws + kWsHeaderBytes + unit_bytes(static_cast<int64_t>(p.requests) * p.next_n, p.q_heads));
     p.part_o = reinterpret_cast<float *>(p.part_ml + partial_rows());
     static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_smem(attention_kernel<BF16, DP, W, SPLIT>, Sh::kSmem, allowed);
+    cudaError_t e = allow_smem(attention_kernel<BF16, DP, W, ROWS>, Sh::kSmem, allowed);
     if (e != cudaSuccess) return e;
     const int grid = sms < kMaxGrid ? sms : kMaxGrid;
-    e = launch_pdl(attention_kernel<BF16, DP, W, SPLIT>, dim3(static_cast<unsigned>(grid)), Sh::kThreads, Sh::kSmem, stream, 1, p);
+    e = launch_pdl(attention_kernel<BF16, DP, W, ROWS>, dim3(static_cast<unsigned>(grid)), Sh::kThreads, Sh::kSmem, stream, 1, p);
     if (e != cudaSuccess) return e;
     const int64_t units = static_cast<int64_t>(p.requests) * p.request_units;
     // no unit spans blocks where none has more than one tile
@@ -592,16 +596,19 @@ cudaError_t launch_shape(AttnParams p, uint8_t *ws, int sms, cudaStream_t stream
     return launch_pdl(combine_kernel<BF16, DP>, blocks, kCombineThreads, 0, stream, 1, p, Sh::kRows);
 }
 
-// Up to 128 rows a head: two warpgroups take the tiles in turn.  More: each
-// has a row tile, they share each copied tile, and one's softmax runs beside
-// the other's products.  Above dimension 128 tensor memory has room for one O.
+// By the rows of a head: up to 32, up to 128 (both warpgroups on them), more
+// (each its row tile; they share each copied tile, and one's softmax runs
+// beside the other's products).  Above dimension 128 tensor memory has room
+// for one O.
 template <bool BF16, int DP>
 cudaError_t launch_dim(const AttnParams &p, uint8_t *ws, int sms, cudaStream_t s) {
     if constexpr (DP == 256) {
-        return launch_shape<BF16, DP, 1, false>(p, ws, sms, s);
+        return launch_shape<BF16, DP, 1, 128>(p, ws, sms, s);
     } else {
-        if (static_cast<int64_t>(p.next_n) * p.group <= 128) return launch_shape<BF16, DP, 2, true>(p, ws, sms, s);
-        return launch_shape<BF16, DP, 2, false>(p, ws, sms, s);
+        const int64_t rows = static_cast<int64_t>(p.next_n) * p.group;
+        if (rows <= 32) return launch_shape<BF16, DP, 2, 32>(p, ws, sms, s);
+        if (rows <= 128) return launch_shape<BF16, DP, 2, 128>(p, ws, sms, s);
+        return launch_shape<BF16, DP, 2, 256>(p, ws, sms, s);
     }
 }
 

@@ -181,24 +181,6 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t *v) {
         : "memory");
 }
 
-// Two 32-bit operations in one instruction: x * c + d, and a + b.
-__device__ __forceinline__ float2 fma2(uint32_t x0, uint32_t x1, float c, float d) {
-    float2 y;
-    asm("{\n .reg .b64 a, b, e, f;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %4};\n mov.b64 e, {%5, %5};\n"
-        " fma.rn.f32x2 f, a, b, e;\n mov.b64 {%0, %1}, f;\n}"
-        : "=f"(y.x), "=f"(y.y)
-        : "r"(x0), "r"(x1), "f"(c), "f"(d));
-    return y;
-}
-
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-    float2 y;
-    asm("{\n .reg .b64 a, b, f;\n mov.b64 a, {%2, %3};\n mov.b64 b, {%4, %5};\n add.rn.f32x2 f, a, b;\n mov.b64 {%0, %1}, f;\n}"
-        : "=f"(y.x), "=f"(y.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return y;
-}
-
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
