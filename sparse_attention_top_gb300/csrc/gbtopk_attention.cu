@@ -14,9 +14,10 @@
 // blocks leaves partial O, m, l in the workspace for combine_kernel.
 //
 // A block: W warpgroups of softmax (one row a thread), a warpgroup whose first
-// warp issues the matrix products, a warpgroup that copies keys and values
-// from their pages (cp.async, 16 bytes a lane, any page size and stride) into
-// a ring of tiles.  Copies run ahead of the products by the whole ring.
+// warp issues the matrix products and whose others look up the cache slots of
+// the tiles to come, a warpgroup that copies keys and values from those slots
+// (cp.async, 16 bytes a lane, any page size and stride) into a ring of tiles.
+// Copies run ahead of the products by the whole ring.
 #include <cfloat>
 #include <cmath>
 
@@ -26,7 +27,7 @@ namespace gbtopk {
 namespace {
 
 constexpr int kMaxGrid = 160;       // blocks of the attention kernel (workspace bound)
-constexpr int kMaskRing = 8;        // tiles whose validity bits are kept (see attention_kernel)
+constexpr int kMaskRing = 8;        // tiles whose slots and validity bits are looked up ahead
 constexpr float kRescale = 8.f;     // rise of the running maximum (base 2) that rescales O
 
 // DP: head dimension rounded up to 64, 128 or 256.  W: softmax warpgroups.
@@ -36,42 +37,48 @@ constexpr float kRescale = 8.f;     // rise of the running maximum (base 2) that
 // (A warp needs about 1000 to 2000 cycles for the softmax of a tile of 128
 // columns, whose copies take 2800 at dimension 128 and 1400 at 64.)  A tile
 // of 32 query rows leaves a stage more to the ring; the product reads 128
-// rows all the same, the ring's bytes behind them, whose results no one reads.
+// rows all the same, the ring's bytes around them, whose results no one
+// reads.  The second warpgroup's products then start 32 rows early, so that
+// its rows lie in the tensor memory of its second warp: each of the two warps
+// that have rows, and the one that issues products, has an SM quarter to
+// itself.
 template <int DP, int W, int ROWS>
 struct Shape {
     static constexpr bool kSplit = W == 2 && ROWS <= 128;
     static constexpr int KT = DP == 256 ? 64 : 128;         // positions a tile
     static constexpr int kRows = ROWS;
     static constexpr int kJobs = kSplit ? 1 : W;            // products (jobs) a tile
+    static constexpr int kShift = ROWS == 32 ? 32 : 0;      // tensor memory rows before the second warpgroup's
     static constexpr int kThreads = 128 * W + 256;
     static constexpr int kStageBytes = KT * DP * 2;
     static constexpr int kQBytes = kRows * DP * 2;
     static constexpr int kJoin = kSplit ? (ROWS * 33 * 4 + 127) / 128 * 128 : 0;   // 32 columns of the second O
-    static constexpr int kFixed = 2048;                     // barriers, masks, scan scratch
+    static constexpr int kFixed = 6144;                     // barriers, slots and masks, scan scratch
     static constexpr int kFit = (static_cast<int>(kMaxSmemBytes) - 1024 - kFixed - kJoin - kQBytes) / kStageBytes;
-    static constexpr int kStages = kFit < 12 ? kFit : 12;   // half of it + 2 tiles fit the mask ring
+    static constexpr int kStages = kFit < 12 ? kFit : 12;
     static constexpr size_t kSmem = 1024 + kFixed + kJoin + kQBytes + static_cast<size_t>(kStages) * kStageBytes;
     static constexpr uint32_t kS = 0, kO = 2 * KT;          // tensor memory columns
     static_assert(kO + W * DP <= 512, "tensor memory");
-    static_assert(kStages >= 4 && kStages / 2 + 2 <= kMaskRing, "ring");
+    static_assert(kStages >= 4 && kStages / 2 + 1 <= kMaskRing, "ring");   // copies never wait for slots behind the softmax
     static_assert(kSplit || ROWS == 128 * W, "rows");
 };
 
 struct Shared {
     uint64_t full[12], empty[12];   // ring stages: K and V of a tile alternate
-    uint64_t mask_full[kMaskRing];  // validity bits written
+    uint64_t slots_full[kMaskRing], slots_empty[kMaskRing];   // slots and validity bits of a tile
     uint64_t q_full, q_empty;
     uint64_t s_full[2];             // S of a job is in tensor memory
     uint64_t p_full[2];             // P of a job is
     uint64_t pv_done[2];            // O holds the job's product
     uint64_t drain;
-    uint32_t mask[kMaskRing][4];
+    int32_t slots[kMaskRing][128];  // cache slot of each position, -1 where there is none
+    uint32_t mask[kMaskRing][4];    // positions with a slot, as bits
     float2 ml[128];                 // (m, l) of the second warpgroup's rows
     ScanScratch scan;
     uint32_t tmem;
     uint32_t abort;
 };
-static_assert(sizeof(Shared) <= 2048, "shared block");
+static_assert(sizeof(Shared) <= 6144, "shared block");
 
 // Barrier of the two softmax warps that share rows; true for both when `v`
 // is for one.
@@ -95,16 +102,22 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
     uint8_t *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     float *join = reinterpret_cast<float *>(smem + Sh::kQBytes + Sh::kStages * Sh::kStageBytes);   // [128][33]
     Shared &sh = *reinterpret_cast<Shared *>(reinterpret_cast<uint8_t *>(join) + Sh::kJoin);
-    const uint32_t q_smem = smem_addr(smem), ring = q_smem + Sh::kQBytes;
+    // stage 0, the queries, the other stages (the products of kShift read
+    // around the queries)
+    const uint32_t ring = smem_addr(smem), q_smem = ring + Sh::kStageBytes;
+    auto stage_at = [&](uint32_t s) { return ring + s * Sh::kStageBytes + (s ? Sh::kQBytes : 0); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    constexpr int kMmaWarp = 4 * W;
+    constexpr int kRoleWarp = 4 * W, kMmaWarp = kRoleWarp + 2;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < Sh::kStages; ++i) {
             bar_init(&sh.full[i], 128);
             bar_init(&sh.empty[i], 1);
         }
-        for (int i = 0; i < kMaskRing; ++i) bar_init(&sh.mask_full[i], 4);
+        for (int i = 0; i < kMaskRing; ++i) {
+            bar_init(&sh.slots_full[i], 1);
+            bar_init(&sh.slots_empty[i], 4 * Sh::kJobs);
+        }
         bar_init(&sh.q_full, 128);
         bar_init(&sh.q_empty, 1);
         for (int i = 0; i < 2; ++i) {
@@ -130,36 +143,14 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
     const int32_t rows = p.next_n * p.group;   // of a (request, kv head)
     const int32_t chunks = (p.dim + 15) / 16 * 2, loaded = p.dim / 8;
 
-    if (warp >= kMmaWarp + 4) {
+    if (warp >= kRoleWarp + 4) {
         // ------------------------------------------------ copies
-        const int w = warp - kMmaWarp - 4;
+        const int w = warp - kRoleWarp - 4;
         const uint8_t *kb = static_cast<const uint8_t *>(p.k), *vb = static_cast<const uint8_t *>(p.v);
         const int64_t k_bytes = p.k_slot * 2, v_bytes = p.v_slot * 2;
-        int32_t last_b = -1;
-        uint64_t seen = ~0ull;   // drafted tokens that some row of the request sees
-        // where this lane's row of tile t of unit u lies (KT / 4 rows a warp)
-        auto place_of = [&](const Unit &u, int32_t t, bool more) {
-            if (more && u.b != last_b) {
-                last_b = u.b;
-                if (p.seq_lens && p.tree_mask) {
-                    const int64_t *tm = p.tree_mask + static_cast<int64_t>(u.b) * p.next_n;
-                    uint64_t m = lane < p.next_n ? static_cast<uint64_t>(fetch(tm + lane)) : 0;
-                    if (lane + 32 < p.next_n) m |= static_cast<uint64_t>(fetch(tm + lane + 32));
-                    seen = static_cast<uint64_t>(__reduce_or_sync(~0u, static_cast<uint32_t>(m >> 32))) << 32 |
-                           __reduce_or_sync(~0u, static_cast<uint32_t>(m));
-                }
-            }
-            const int32_t pos = t * KT + w * (KT / 4) + (lane & (KT / 4 - 1));
-            const bool is = more && pos < u.span.n && (pos < u.span.ctx || ((seen >> (pos - u.span.ctx)) & 1));
-            return p.seq_lens ? p.pages.place(u.b, pos, is) : p.pages.listed(p.indices + u.b * p.idx_row + pos, is);
-        };
         uint32_t unit = 0, g = 0, tile = 0;   // counters of units, ring stages and tiles
         uint32_t stage = 0, lap = 0;
         bool ok = true;
-        Walk<KT> ahead = walk;                // the tile after the one being copied
-        while (ahead.more() && ahead.u.span.n == 0) ahead.next();
-        int32_t ahead_t = ahead.more() ? ahead.u.t0 : 0;
-        Paging::Place next = place_of(ahead.u, ahead_t, ahead.more());
         for (; walk.more() && ok; walk.next()) {
             const Unit u = walk.u;
             if (u.span.n == 0) continue;   // nothing to see: the rows' zeros need no products
@@ -177,25 +168,13 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
             bar_arrive_copies(&sh.q_full);
             ++unit;
             for (int32_t t = u.t0; t < u.t1; ++t, ++tile) {
-                const int32_t slot = static_cast<int32_t>(p.pages.slot(next));
-                if (++ahead_t == ahead.u.t1) {
-                    do ahead.next();
-                    while (ahead.more() && ahead.u.span.n == 0);
-                    ahead_t = ahead.more() ? ahead.u.t0 : 0;
-                }
-                next = place_of(ahead.u, ahead_t, ahead.more());
+                ok = __all_sync(~0u, bar_wait(&sh.slots_full[tile % kMaskRing], (tile / kMaskRing) & 1, abort));
+                if (!ok) break;
+                const int32_t slot = reinterpret_cast<volatile int32_t *>(sh.slots[tile % kMaskRing])[w * (KT / 4) + (lane & (KT / 4 - 1))];
                 for (int kv = 0; kv < 2; ++kv, ++g) {
                     if (g >= Sh::kStages) ok = __all_sync(~0u, bar_wait(&sh.empty[stage], (lap - 1) & 1, abort));
                     if (!ok) break;
-                    if (kv == 0) {
-                        const uint32_t valid = __ballot_sync(~0u, slot >= 0);
-                        if (lane == 0) {
-                            if constexpr (KT == 128) sh.mask[tile % kMaskRing][w] = valid;
-                            else reinterpret_cast<uint16_t *>(sh.mask[tile % kMaskRing])[w] = static_cast<uint16_t>(valid);
-                            bar_arrive(&sh.mask_full[tile % kMaskRing]);
-                        }
-                    }
-                    copy_tile<DP, KT>(ring + stage * Sh::kStageBytes, (kv ? vb + 2 * h * p.v_head : kb + 2 * h * p.k_head),
+                    copy_tile<DP, KT>(stage_at(stage), (kv ? vb + 2 * h * p.v_head : kb + 2 * h * p.k_head),
                                       kv ? v_bytes : k_bytes, slot, chunks, loaded, w, lane);
                     bar_arrive_copies(&sh.full[stage]);
                     if (++stage == Sh::kStages) {
@@ -207,7 +186,7 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
             }
         }
         copies_land();
-    } else if (warp >= kMmaWarp) {
+    } else if (warp >= kRoleWarp) {
         // ------------------------------------------------ matrix products
         if (warp == kMmaWarp) {   // all lanes alike, see elect_lane
             const bool lead = elect_lane();
@@ -232,7 +211,7 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                     if (!wait_item(item)) return false;
                     fence_async_reads();
                     tc_fence_after();
-                    const uint32_t qa = q_smem + (Sh::kJobs == 2 ? (j & 1) * 128 * 128 : 0), ka = ring + s * Sh::kStageBytes;
+                    const uint32_t qa = q_smem + (Sh::kJobs == 2 ? (j & 1) * 128 * 128 : 0) - sb * Sh::kShift * 128, ka = stage_at(s);
                     if (lead) {   // unrolled: one thread issues, and its instructions bound the products' rate
 #pragma unroll
                         for (int kk = 0; kk < DP / 16; ++kk)
@@ -255,7 +234,7 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                     if (!ok) break;
                     fence_async_reads();
                     tc_fence_after();
-                    const uint32_t va = ring + s * Sh::kStageBytes;
+                    const uint32_t va = stage_at(s);
                     if (lead) {
 #pragma unroll
                         for (int kk = 0; kk < KT / 16; ++kk)
@@ -280,10 +259,55 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                 }
             }
         }
+        else {
+            // -------------------------------------------- slots of the tiles to come
+            // Three warps take the tiles in turn, up to kMaskRing tiles ahead of
+            // the softmax: the page-table reads (DRAM latency where pages are
+            // small) are then behind neither the copies nor one another.
+            const int turn = warp == kRoleWarp + 3 ? 2 : warp - kRoleWarp;
+            int32_t last_b = -1;
+            uint64_t seen = ~0ull;   // drafted tokens that some row of the request sees
+            uint32_t tile = 0;
+            bool ok = true;
+            for (; walk.more() && ok; walk.next()) {
+                const Unit u = walk.u;
+                if (u.span.n == 0) continue;
+                if (u.b != last_b && p.seq_lens && p.tree_mask) {
+                    const int64_t *tm = p.tree_mask + static_cast<int64_t>(u.b) * p.next_n;
+                    uint64_t m = lane < p.next_n ? static_cast<uint64_t>(fetch(tm + lane)) : 0;
+                    if (lane + 32 < p.next_n) m |= static_cast<uint64_t>(fetch(tm + lane + 32));
+                    seen = static_cast<uint64_t>(__reduce_or_sync(~0u, static_cast<uint32_t>(m >> 32))) << 32 |
+                           __reduce_or_sync(~0u, static_cast<uint32_t>(m));
+                }
+                last_b = u.b;
+                for (int32_t t = u.t0; t < u.t1; ++t, ++tile) {
+                    if (tile % 3 != static_cast<uint32_t>(turn)) continue;
+                    const uint32_t r = tile % kMaskRing;
+                    Paging::Place at[KT / 32];
+#pragma unroll
+                    for (int k = 0; k < KT / 32; ++k) {
+                        const int32_t pos = t * KT + k * 32 + lane;
+                        const bool is = pos < u.span.n && (pos < u.span.ctx || ((seen >> (pos - u.span.ctx)) & 1));
+                        at[k] = p.seq_lens ? p.pages.place(u.b, pos, is) : p.pages.listed(p.indices + u.b * p.idx_row + pos, is);
+                    }
+                    if (tile >= kMaskRing) ok = __all_sync(~0u, bar_wait(&sh.slots_empty[r], (tile / kMaskRing - 1) & 1, abort));
+                    if (!ok) break;
+#pragma unroll
+                    for (int k = 0; k < KT / 32; ++k) {
+                        const int32_t slot = static_cast<int32_t>(p.pages.slot(at[k]));
+                        const uint32_t valid = __ballot_sync(~0u, slot >= 0);
+                        sh.slots[r][k * 32 + lane] = slot;
+                        if (lane == 0) sh.mask[r][k] = valid;
+                    }
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&sh.slots_full[r]);
+                }
+            }
+        }
         __syncwarp();
     } else {
         // ------------------------------------------------ softmax, output
-        const int wg = warp >> 2, row = threadIdx.x & 127;
+        const int wg = warp >> 2, row0 = (warp & 3) * 32 - wg * Sh::kShift, row = row0 + lane;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // the warp's tensor memory lanes
         const uint32_t t_o = tmem + lanes + Sh::kO + wg * DP;
         const int row_wg = SPLIT ? 0 : wg * 128;   // the warpgroup's first row of a unit
@@ -293,10 +317,10 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
             const Unit u = walk.u;
             const int32_t h = u.hm / p.row_tiles, mt = u.hm - h * p.row_tiles;
             const int32_t rho = mt * Sh::kRows + row_wg + row;
-            const bool mine = rho < rows;
+            const bool mine = row >= 0 && rho < rows;
             const int32_t t = rho / p.group, gq = rho - t * p.group;
             const int64_t r = static_cast<int64_t>(u.b) * p.next_n + t;
-            const bool active = mt * Sh::kRows + row_wg + (warp & 3) * 32 < rows;   // any row of the warp
+            const bool active = row0 >= 0 && mt * Sh::kRows + row_wg + row0 < rows;   // any row of the warp
             if (u.span.n == 0) {
                 if (threadIdx.x < 2) p.unit_ends[2 * (static_cast<int64_t>(u.b) * p.request_units + u.hm) + threadIdx.x] = static_cast<int32_t>(blockIdx.x);
                 if (mine && !(SPLIT && wg == 1)) {
@@ -314,7 +338,7 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
             for (int32_t i = u.t0; i < u.t1; ++i, ++tile, job += Sh::kJobs) {
                 const uint32_t sb = job & 1, ph = (job >> 1) & 1;
                 if (SPLIT && sb != static_cast<uint32_t>(wg)) continue;
-                ok = __all_sync(~0u, bar_wait(&sh.mask_full[tile % kMaskRing], (tile / kMaskRing) & 1, abort) &&
+                ok = __all_sync(~0u, bar_wait(&sh.slots_full[tile % kMaskRing], (tile / kMaskRing) & 1, abort) &&
                                          bar_wait(&sh.s_full[sb], ph, abort));
                 if (!ok) break;
                 if (active) {
@@ -415,7 +439,10 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                 }
                 last = job;
                 __syncwarp();
-                if (lane == 0) bar_arrive(&sh.p_full[sb]);
+                if (lane == 0) {
+                    bar_arrive(&sh.p_full[sb]);
+                    bar_arrive(&sh.slots_empty[tile % kMaskRing]);
+                }
             }
             if (ok && last != ~0u) ok = __all_sync(~0u, bar_wait(&sh.pv_done[last & 1], (last >> 1) & 1, abort));
             if (!SPLIT && !ok) break;
@@ -425,10 +452,15 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                 if (u.t1 == u.tiles) ends[1] = static_cast<int32_t>(blockIdx.x);
             }
             __syncwarp();
-            float f0 = 1.f, f1 = 0.f;   // SPLIT: factors of the two O
+            if (!active) {
+                if (!ok) break;
+                continue;
+            }
+            const int pair = 1 + row0 / 32;   // barrier of the two warps that have these rows
+            float f0 = 1.f, f1 = 0.f;         // SPLIT: factors of the two O
             if constexpr (SPLIT) {
                 if (wg == 1) sh.ml[row] = make_float2(m, l);
-                ok = !pair_barrier_or(1 + (warp & 3), !ok);   // both leave when one gave up
+                ok = !pair_barrier_or(pair, !ok);   // both leave when one gave up
                 if (!ok) break;
                 if (wg == 0) {
                     const float2 other = sh.ml[row];
@@ -438,10 +470,6 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                     l = l * f0 + other.y * f1;
                     m = top;
                 }
-            }
-            if (!active) {
-                if constexpr (SPLIT) pair_barrier_or(1 + (warp & 3), false);
-                continue;
             }
             tc_fence_after();
             const bool whole = u.t0 == 0 && u.t1 == u.tiles;
@@ -460,7 +488,7 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
 #pragma unroll
                         for (int c = 0; c < 32; ++c) join[row * 33 + c] = __uint_as_float(o[c]);
                     }
-                    pair_barrier_or(1 + (warp & 3), false);
+                    pair_barrier_or(pair, false);
                     if (wg == 0) {
 #pragma unroll
                         for (int c = 0; c < 32; ++c) {
@@ -469,7 +497,7 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                             o[c] = __float_as_uint(a + b);
                         }
                     }
-                    pair_barrier_or(1 + (warp & 3), false);
+                    pair_barrier_or(pair, false);
                 }
                 if (!mine || (SPLIT && wg == 1)) continue;
                 if (whole) {
@@ -490,7 +518,7 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                     for (int c = 0; c < 32; ++c) dst[c * Sh::kRows] = __uint_as_float(o[c]);
                 }
             }
-            if constexpr (SPLIT) pair_barrier_or(1 + (warp & 3), false);   // ml is read
+            if constexpr (SPLIT) pair_barrier_or(pair, false);   // ml is read
             if (mine && !(SPLIT && wg == 1)) {
                 if (!whole) p.part_ml[part * Sh::kRows + part_row] = make_float2(m, l);
                 else if (p.lse) p.lse[q_at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
