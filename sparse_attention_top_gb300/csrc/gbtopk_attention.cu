@@ -52,11 +52,12 @@ struct Shape {
     static constexpr int kThreads = 128 * W + 256;
     static constexpr int kStageBytes = KT * DP * 2;
     static constexpr int kQBytes = kRows * DP * 2;
+    static constexpr int kQBufs = ROWS == 32 ? 2 : 1;       // units whose queries are held
     static constexpr int kJoin = kSplit ? (ROWS * 33 * 4 + 127) / 128 * 128 : 0;   // 32 columns of the second O
     static constexpr int kFixed = 6144;                     // barriers, slots and masks, scan scratch
-    static constexpr int kFit = (static_cast<int>(kMaxSmemBytes) - 1024 - kFixed - kJoin - kQBytes) / kStageBytes;
+    static constexpr int kFit = (static_cast<int>(kMaxSmemBytes) - 1024 - kFixed - kJoin - kQBufs * kQBytes) / kStageBytes;
     static constexpr int kStages = kFit < 12 ? kFit : 12;
-    static constexpr size_t kSmem = 1024 + kFixed + kJoin + kQBytes + static_cast<size_t>(kStages) * kStageBytes;
+    static constexpr size_t kSmem = 1024 + kFixed + kJoin + kQBufs * kQBytes + static_cast<size_t>(kStages) * kStageBytes;
     static constexpr uint32_t kS = 0, kO = 2 * KT;          // tensor memory columns
     static_assert(kO + W * DP <= 512, "tensor memory");
     static_assert(kStages >= 4 && kStages / 2 + 1 <= kMaskRing, "ring");   // copies never wait for slots behind the softmax
@@ -66,7 +67,7 @@ struct Shape {
 struct Shared {
     uint64_t full[12], empty[12];   // ring stages: K and V of a tile alternate
     uint64_t slots_full[kMaskRing], slots_empty[kMaskRing];   // slots and validity bits of a tile
-    uint64_t q_full, q_empty;
+    uint64_t q_full[2], q_empty[2];
     uint64_t s_full[2];             // S of a job is in tensor memory
     uint64_t p_full[2];             // P of a job is
     uint64_t pv_done[2];            // O holds the job's product
@@ -100,12 +101,12 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
     constexpr int KT = Sh::KT;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-    float *join = reinterpret_cast<float *>(smem + Sh::kQBytes + Sh::kStages * Sh::kStageBytes);   // [128][33]
+    float *join = reinterpret_cast<float *>(smem + Sh::kQBufs * Sh::kQBytes + Sh::kStages * Sh::kStageBytes);   // [128][33]
     Shared &sh = *reinterpret_cast<Shared *>(reinterpret_cast<uint8_t *>(join) + Sh::kJoin);
     // stage 0, the queries, the other stages (the products of kShift read
     // around the queries)
     const uint32_t ring = smem_addr(smem), q_smem = ring + Sh::kStageBytes;
-    auto stage_at = [&](uint32_t s) { return ring + s * Sh::kStageBytes + (s ? Sh::kQBytes : 0); };
+    auto stage_at = [&](uint32_t s) { return ring + s * Sh::kStageBytes + (s ? Sh::kQBufs * Sh::kQBytes : 0); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kRoleWarp = 4 * W, kMmaWarp = kRoleWarp + 2;
 
@@ -118,9 +119,9 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
             bar_init(&sh.slots_full[i], 1);
             bar_init(&sh.slots_empty[i], 4 * Sh::kJobs);
         }
-        bar_init(&sh.q_full, 128);
-        bar_init(&sh.q_empty, 1);
         for (int i = 0; i < 2; ++i) {
+            bar_init(&sh.q_full[i], 128);
+            bar_init(&sh.q_empty[i], 1);
             bar_init(&sh.s_full[i], 1);
             bar_init(&sh.p_full[i], 4);
             bar_init(&sh.pv_done[i], 1);
@@ -156,16 +157,17 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
             if (u.span.n == 0) continue;   // nothing to see: the rows' zeros need no products
             const int32_t h = u.hm / p.row_tiles, r0 = (u.hm - h * p.row_tiles) * Sh::kRows;
             // the unit's queries
-            if (unit > 0) ok = __all_sync(~0u, bar_wait(&sh.q_empty, (unit - 1) & 1, abort));
+            const uint32_t qb = unit % Sh::kQBufs;
+            if (unit >= Sh::kQBufs) ok = __all_sync(~0u, bar_wait(&sh.q_empty[qb], (unit / Sh::kQBufs - 1) & 1, abort));
             if (!ok) break;
             constexpr int kRowChunks = DP / 8 < 32 ? DP / 8 : 32, kStep = 128 / kRowChunks;   // lanes a row, rows a step
             for (int32_t r = (w * 32 + lane) / kRowChunks; r < Sh::kRows && r0 + r < rows; r += kStep) {
                 const int32_t c = lane % kRowChunks, t = (r0 + r) / p.group, gq = r0 + r - t * p.group;
                 const uint8_t *src = static_cast<const uint8_t *>(p.q) +
                                      2 * ((static_cast<int64_t>(u.b) * p.next_n + t) * p.q_row + (h * p.group + gq) * p.q_head);
-                if (c < chunks) copy16(q_smem + tile_offset(Sh::kRows, r, c), c < loaded ? src + c * 16 : src, c < loaded ? 16u : 0u);
+                if (c < chunks) copy16(q_smem + qb * Sh::kQBytes + tile_offset(Sh::kRows, r, c), c < loaded ? src + c * 16 : src, c < loaded ? 16u : 0u);
             }
-            bar_arrive_copies(&sh.q_full);
+            bar_arrive_copies(&sh.q_full[qb]);
             ++unit;
             for (int32_t t = u.t0; t < u.t1; ++t, ++tile) {
                 ok = __all_sync(~0u, bar_wait(&sh.slots_full[tile % kMaskRing], (tile / kMaskRing) & 1, abort));
@@ -204,14 +206,15 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
             for (; __any_sync(~0u, walk.more()) && ok; walk.next()) {
                 if (__any_sync(~0u, walk.u.span.n == 0)) continue;
                 const uint32_t nt = __shfl_sync(~0u, static_cast<uint32_t>(walk.u.t1 - walk.u.t0), 0), jobs = nt * Sh::kJobs;
-                ok = __all_sync(~0u, bar_wait(&sh.q_full, unit & 1, abort));
+                const uint32_t qb = unit % Sh::kQBufs;
+                ok = __all_sync(~0u, bar_wait(&sh.q_full[qb], (unit / Sh::kQBufs) & 1, abort));
                 if (!ok) break;
                 auto issue_qk = [&](uint32_t j) {
                     const uint32_t item = 2 * (gi + j / Sh::kJobs), s = item % Sh::kStages, sb = (job0 + j) & 1;
                     if (!wait_item(item)) return false;
                     fence_async_reads();
                     tc_fence_after();
-                    const uint32_t qa = q_smem + (Sh::kJobs == 2 ? (j & 1) * 128 * 128 : 0) - sb * Sh::kShift * 128, ka = stage_at(s);
+                    const uint32_t qa = q_smem + qb * Sh::kQBytes + (Sh::kJobs == 2 ? (j & 1) * 128 * 128 : 0) - sb * Sh::kShift * 128, ka = stage_at(s);
                     if (lead) {   // unrolled: one thread issues, and its instructions bound the products' rate
 #pragma unroll
                         for (int kk = 0; kk < DP / 16; ++kk)
@@ -221,7 +224,7 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                                        smem_desc(ka + (kk >> 2) * kPanel + (kk & 3) * 32, 16, 1024), qk_desc, kk > 0);
                         tc_commit(&sh.s_full[sb]);
                         if (Sh::kJobs == 1 || (j & 1)) tc_commit(&sh.empty[s]);
-                        if (j + 1 == jobs) tc_commit(&sh.q_empty);
+                        if (j + 1 == jobs) tc_commit(&sh.q_empty[qb]);
                     }
                     __syncwarp();
                     return true;
@@ -534,10 +537,13 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
 
 // Joins the partial results of units that span blocks: blocks of 32 rows (a
 // lane each) and sixteen warps, each DP / 16 columns; grid (units, row
-// groups).  A batch of parts is loaded at once.
+// groups).  A batch of BATCH parts is loaded at once: more for few blocks,
+// where a batch's latency counts (one request of 1027 positions: 15.7 us a
+// call with 4, 14.1 with 8), fewer for many, where registers bound the blocks
+// an SM holds (16 wide trees: 102.9 us with 4, 107.1 with 8).
 constexpr int kCombineRows = 32, kCombineThreads = 512;
 
-template <bool BF16, int DP>
+template <bool BF16, int DP, int BATCH>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ AttnParams p, int32_t unit_rows) {
     pdl_wait();
     pdl_release();
@@ -548,7 +554,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
     const int32_t h = hm / p.row_tiles, r0 = (hm - h * p.row_tiles) * unit_rows;
     const int32_t row = static_cast<int32_t>(blockIdx.y) * kCombineRows + static_cast<int32_t>(threadIdx.x & 31);
     if (row >= unit_rows || r0 + row >= p.next_n * p.group) return;
-    constexpr int kCols = DP / 16, kBatch = DP == 256 ? 4 : 8;
+    constexpr int kCols = DP / 16, kBatch = BATCH;
     const int32_t col = static_cast<int32_t>(threadIdx.x >> 5) * kCols;
     float m = -INFINITY, l = 0.f, acc[kCols] = {};
     for (int32_t g0 = c0; g0 <= c1; g0 += kBatch) {
@@ -621,7 +627,9 @@ cudaError_t launch_shape(AttnParams p, uint8_t *ws, int sms, cudaStream_t stream
     if (longest <= Sh::KT) return cudaSuccess;
     const int64_t each = rows < Sh::kRows ? rows : Sh::kRows;
     const dim3 blocks(static_cast<unsigned>(units), static_cast<unsigned>((each + kCombineRows - 1) / kCombineRows));
-    return launch_pdl(combine_kernel<BF16, DP>, blocks, kCombineThreads, 0, stream, 1, p, Sh::kRows);
+    const bool few = units * blocks.y <= sms && DP <= 128;
+    return few ? launch_pdl(combine_kernel<BF16, DP, DP <= 128 ? 8 : 4>, blocks, kCombineThreads, 0, stream, 1, p, Sh::kRows)
+               : launch_pdl(combine_kernel<BF16, DP, 4>, blocks, kCombineThreads, 0, stream, 1, p, Sh::kRows);
 }
 
 // By the rows of a head: up to 32, up to 128 (both warpgroups on them), more

@@ -17,7 +17,7 @@ namespace cg = cooperative_groups;
 namespace gbtopk {
 namespace {
 
-constexpr int kSelectThreads = 1024;
+constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kMoveThreads = 256;
 constexpr int kStagedKeys = 49152;   // keys a block can stage (192 KB)
@@ -53,7 +53,7 @@ __device__ __forceinline__ float key_weight(uint32_t k) {
 }
 
 struct SelectShared {
-    uint32_t hist[kBins11];
+    alignas(16) uint32_t hist[kBins11];
     uint32_t scan[kSelectWarps];
     uint32_t gt[kSelectWarps], eq[kSelectWarps];   // kept for sure, equal to the key: by warp, then before each
     uint32_t all_gt[kMaxCluster], all_eq[kMaxCluster];
@@ -61,7 +61,7 @@ struct SelectShared {
     uint32_t bin, need, count;
 };
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __grid_constant__ EvictParams p) {
+__global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(const __grid_constant__ EvictParams p) {
     extern __shared__ uint32_t keys[];
     __shared__ SelectShared sh;
     cg::cluster_group cluster = cg::this_cluster();
@@ -138,15 +138,19 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
         }
         if (size > 1) cluster.sync();
         else __syncthreads();
-        // two bins a thread, the highest in thread 0
-        const int hi = kBins11 - 1 - 2 * tid;
-        uint32_t h0 = 0, h1 = 0;
+        // four bins a thread, the highest in thread 0
+        const int hi = kBins11 - 1 - 4 * tid;
+        uint32_t h[4] = {}, mine = 0;
         for (int r = 0; r < size; ++r) {
-            const uint32_t *h = cluster.map_shared_rank(sh.hist, r);
-            h0 += h[hi];
-            h1 += h[hi - 1];
+            const uint4 x = *reinterpret_cast<const uint4 *>(cluster.map_shared_rank(sh.hist, r) + hi - 3);
+            h[0] += x.w;
+            h[1] += x.z;
+            h[2] += x.y;
+            h[3] += x.x;
         }
-        uint32_t inc = h0 + h1;
+#pragma unroll
+        for (int b = 0; b < 4; ++b) mine += h[b];
+        uint32_t inc = mine;
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t x = __shfl_up_sync(~0u, inc, o);
             if (lane >= o) inc += x;
@@ -155,12 +159,22 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
         __syncthreads();
         uint32_t above = lane < warp ? sh.scan[lane] : 0;   // in higher bins
         for (int o = 16; o; o >>= 1) above += __shfl_xor_sync(~0u, above, o);
-        above += inc - h0 - h1;
-        if (above < need && above + h0 + h1 >= need) {
-            const bool first = above + h0 >= need;
-            sh.bin = static_cast<uint32_t>(first ? hi : hi - 1);
-            sh.need = need - above - (first ? 0 : h0);
-            sh.count = first ? h0 : h1;
+        above += inc - mine;
+        if (above < need && above + mine >= need) {
+            uint32_t left = need - above;
+            bool found = false;
+#pragma unroll
+            for (int b = 0; b < 4; ++b) {
+                if (found) continue;
+                if (left > h[b]) {
+                    left -= h[b];
+                    continue;
+                }
+                found = true;
+                sh.bin = static_cast<uint32_t>(hi - b);
+                sh.need = left;
+                sh.count = h[b];
+            }
         }
         if (size > 1) cluster.sync();
         else __syncthreads();
@@ -194,7 +208,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
     }
     __syncthreads();
     if (warp == 0) {
-        uint32_t g = sh.gt[lane], e = sh.eq[lane], gi = g, ei = e;
+        uint32_t g = lane < kSelectWarps ? sh.gt[lane] : 0, e = lane < kSelectWarps ? sh.eq[lane] : 0, gi = g, ei = e;
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t x = __shfl_up_sync(~0u, gi, o), y = __shfl_up_sync(~0u, ei, o);
             if (lane >= o) {
@@ -202,8 +216,10 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const __gr
                 ei += y;
             }
         }
-        sh.gt[lane] = gi - g;
-        sh.eq[lane] = ei - e;
+        if (lane < kSelectWarps) {
+            sh.gt[lane] = gi - g;
+            sh.eq[lane] = ei - e;
+        }
         if (lane == 31)
             for (int r = 0; r < size; ++r) {
                 cluster.map_shared_rank(sh.all_gt, r)[rank] = gi;
@@ -285,11 +301,12 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
     }
 }
 
-// Blocks of a selection's cluster: enough to stage the row, and for few rows
-// as many as leave each block 4096 weights.
+// Blocks of a selection's cluster: enough for two blocks an SM to stage their
+// slices (256 rows of 32768 weights, one block each of 1024 threads: 56 us),
+// and for few rows as many as leave each block 4096 weights.
 int select_cluster(int64_t rows, int64_t width) {
     int c = 1;
-    while (c < kMaxCluster && ((width + c - 1) / c > kStagedKeys || (rows * c * 2 <= 152 && width / c > 4096))) c *= 2;
+    while (c < kMaxCluster && ((width + c - 1) / c > 24576 || (rows * c * 2 <= 152 && width / c > 4096))) c *= 2;
     return c;
 }
 

@@ -34,34 +34,38 @@ struct WeightParams {
     int64_t width;
 };
 
-template <int DP>
+// NQ: query rows of a phase; few rows leave room for the queries of eight
+// phases, so that a request's heads (one weight for all) follow one another
+// without a wait for each head's queries.
+template <int DP, int NQ>
 struct Shape {
-    static constexpr int NQ = DP == 256 ? 64 : 128;         // query rows of a phase
+    static constexpr int kQBufs = NQ == 32 ? (DP == 256 ? 4 : 8) : 2;
     static constexpr int kThreads = 512;                    // 2 summing warpgroups, products, copies
-    static constexpr int kQBytes = NQ * DP * 2;             // one of two buffers
+    static constexpr int kQBytes = NQ * DP * 2;             // of a phase
     static constexpr int kStageBytes = KT * DP * 2;
     static constexpr int kSums = 2 * kSpan * KT * 4;
-    static constexpr int kFixed = 4096;
-    static constexpr int kFit = (static_cast<int>(kMaxSmemBytes) - 1024 - kFixed - kSums - 2 * kQBytes) / kStageBytes;
+    static constexpr int kFixed = 8192;                     // barriers, slots and masks, lse, trees
+    static constexpr int kFit = (static_cast<int>(kMaxSmemBytes) - 1024 - kFixed - kSums - kQBufs * kQBytes) / kStageBytes;
     static constexpr int kStages = kFit < 6 ? kFit : 6;
-    static constexpr size_t kSmem = 1024 + kFixed + kSums + 2 * kQBytes + static_cast<size_t>(kStages) * kStageBytes;
-    static_assert(kStages >= 2 && kStages + 2 <= kMaskRing, "ring");
+    static constexpr size_t kSmem = 1024 + kFixed + kSums + kQBufs * kQBytes + static_cast<size_t>(kStages) * kStageBytes;
+    static_assert(kStages >= 2 && kStages <= kMaskRing && NQ * kQBufs <= 256, "ring");
 };
 
 struct Shared {
     uint64_t full[6], empty[6];     // ring stages, one key tile each
-    uint64_t mask_full[kMaskRing];
-    uint64_t q_full[2], q_empty[2]; // phase buffers
+    uint64_t slots_full[kMaskRing], slots_empty[kMaskRing];   // slots and validity bits of a job's tile
+    uint64_t q_full[8], q_empty[8]; // phase buffers
     uint64_t s_full[2], s_empty[2];
     uint64_t drain;
     uint32_t mask[kMaskRing][4];
-    alignas(16) float lse2[2][128]; // base-2 lse of the phase's rows; +inf: adds nothing
+    int32_t slots[kMaskRing][KT];   // cache slot of each position, -1 where there is none
+    alignas(16) float lse2[256];    // base-2 lse of the phases' rows; +inf: adds nothing
     uint64_t tree[GBTOPK_MAX_NEXT_N];
     ScanScratch scan;
     uint32_t tmem;
     uint32_t abort;
 };
-static_assert(sizeof(Shared) <= 4096, "shared block");
+static_assert(sizeof(Shared) <= 8192, "shared block");
 static_assert(offsetof(Shared, lse2) % 16 == 0, "vector loads of the rows' lse");
 
 // One span of a share: tiles t0 .. t1 - 1 of a (request, weight head), and
@@ -123,14 +127,13 @@ __device__ __forceinline__ bool sums_barrier_or(bool v) {
     return any != 0;
 }
 
-template <bool BF16, int DP>
-__global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const __grid_constant__ WeightParams p) {
-    using Sh = Shape<DP>;
-    constexpr int NQ = Sh::NQ;
+template <bool BF16, int DP, int NQ>
+__global__ void __launch_bounds__(Shape<DP, NQ>::kThreads, 1) weights_kernel(const __grid_constant__ WeightParams p) {
+    using Sh = Shape<DP, NQ>;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-    const uint32_t q_smem = smem_addr(smem), ring = q_smem + 2 * Sh::kQBytes;
-    float *sums = reinterpret_cast<float *>(smem + 2 * Sh::kQBytes + Sh::kStages * Sh::kStageBytes);   // [2][kSpan][KT]
+    const uint32_t q_smem = smem_addr(smem), ring = q_smem + Sh::kQBufs * Sh::kQBytes;
+    float *sums = reinterpret_cast<float *>(smem + Sh::kQBufs * Sh::kQBytes + Sh::kStages * Sh::kStageBytes);   // [2][kSpan][KT]
     Shared &sh = *reinterpret_cast<Shared *>(reinterpret_cast<uint8_t *>(sums) + Sh::kSums);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr int kMmaWarp = 8;
@@ -141,10 +144,15 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
             bar_init(&sh.full[i], 128);
             bar_init(&sh.empty[i], 1);
         }
-        for (int i = 0; i < kMaskRing; ++i) bar_init(&sh.mask_full[i], 4);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kMaskRing; ++i) {
+            bar_init(&sh.slots_full[i], 1);
+            bar_init(&sh.slots_empty[i], 4);
+        }
+        for (int i = 0; i < Sh::kQBufs; ++i) {
             bar_init(&sh.q_full[i], 128 + 4);   // copies, and the lse values of each copying warp
             bar_init(&sh.q_empty[i], 1 + 8);    // products, and the summing warps
+        }
+        for (int i = 0; i < 2; ++i) {
             bar_init(&sh.s_full[i], 1);
             bar_init(&sh.s_empty[i], 4);
         }
@@ -172,24 +180,11 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
         const int w = warp - kMmaWarp - 4;
         uint32_t phase = 0, job = 0;
         while (ok && spans.next(&s)) {
-            uint64_t seen = ~0ull;   // drafted tokens that an accepted row sees
-            if (a.tree_mask && s.t1 * KT > s.ctx) {
-                seen = 0;
-                for (int j = lane; j < a.next_n; j += 32)
-                    if ((s.took >> j) & 1) seen |= static_cast<uint64_t>(fetch(a.tree_mask + static_cast<int64_t>(s.b) * a.next_n + j));
-                seen = static_cast<uint64_t>(__reduce_or_sync(~0u, static_cast<uint32_t>(seen >> 32))) << 32 |
-                       __reduce_or_sync(~0u, static_cast<uint32_t>(seen));
-            }
-            auto place_of = [&](int32_t t) {
-                const int32_t pos = t * KT + w * 32 + lane;
-                return a.pages.place(s.b, pos, pos < s.n && pos < p.width && (pos < s.ctx || ((seen >> (pos - s.ctx)) & 1)));
-            };
-            Paging::Place next = place_of(s.t0);
             for (int32_t ph = 0; ph < s.phases && ok; ++ph, ++phase) {
                 const int32_t h = s.w * per + ph / s.groups, r0 = (ph % s.groups) * NQ;
                 const int32_t rows = s.rows - r0 < NQ ? s.rows - r0 : NQ, padded = (rows + 15) / 16 * 16;
-                const uint32_t qb = phase & 1;
-                if (phase >= 2) ok = __all_sync(~0u, bar_wait(&sh.q_empty[qb], (phase / 2 - 1) & 1, abort));
+                const uint32_t qb = phase % Sh::kQBufs;
+                if (phase >= Sh::kQBufs) ok = __all_sync(~0u, bar_wait(&sh.q_empty[qb], (phase / Sh::kQBufs - 1) & 1, abort));
                 if (!ok) break;
                 for (int x = w * 32 + lane; x < padded * chunks; x += 128) {
                     const int32_t r = x / chunks, c = x - r * chunks;
@@ -209,21 +204,17 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
                         const float lse = fetch(p.lse + (static_cast<int64_t>(s.b) * a.next_n + nth_bit(s.took, k)) * a.q_heads + h * a.group + gq);
                         v = lse == -INFINITY ? INFINITY : lse * kLog2e;
                     }
-                    sh.lse2[qb][r] = v;
+                    sh.lse2[qb * NQ + r] = v;
                 }
                 __syncwarp();
                 if (lane == 0) bar_arrive(&sh.q_full[qb]);
                 for (int32_t t = s.t0; t < s.t1; ++t, ++job) {
-                    const int32_t slot = static_cast<int32_t>(a.pages.slot(next));
-                    next = place_of(t + 1 < s.t1 ? t + 1 : s.t0);
+                    ok = __all_sync(~0u, bar_wait(&sh.slots_full[job % kMaskRing], (job / kMaskRing) & 1, abort));
+                    if (!ok) break;
+                    const int32_t slot = reinterpret_cast<volatile int32_t *>(sh.slots[job % kMaskRing])[w * 32 + lane];
                     const uint32_t stage = job % Sh::kStages;
                     if (job >= Sh::kStages) ok = __all_sync(~0u, bar_wait(&sh.empty[stage], (job / Sh::kStages - 1) & 1, abort));
                     if (!ok) break;
-                    const uint32_t valid = __ballot_sync(~0u, slot >= 0);
-                    if (lane == 0) {
-                        sh.mask[job % kMaskRing][w] = valid;
-                        bar_arrive(&sh.mask_full[job % kMaskRing]);
-                    }
                     copy_tile<DP, KT>(ring + stage * Sh::kStageBytes, static_cast<const uint8_t *>(a.k) + 2 * h * a.k_head, a.k_slot * 2,
                                       slot, chunks, loaded, w, lane);
                     bar_arrive_copies(&sh.full[stage]);
@@ -247,8 +238,8 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
                     const int32_t r0 = (ph % s.groups) * NQ;
                     const int32_t rows = s.rows - r0 < NQ ? s.rows - r0 : NQ, padded = (rows + 15) / 16 * 16;
                     const uint32_t desc = mma_desc(BF16, 128, static_cast<uint32_t>(padded), false, a.negative != 0);
-                    const uint32_t qa = q_smem + (phase & 1) * Sh::kQBytes;
-                    ok = __all_sync(~0u, bar_wait(&sh.q_full[phase & 1], (phase / 2) & 1, abort));
+                    const uint32_t qb = phase % Sh::kQBufs, qa = q_smem + qb * Sh::kQBytes;
+                    ok = __all_sync(~0u, bar_wait(&sh.q_full[qb], (phase / Sh::kQBufs) & 1, abort));
                     for (int32_t t = s.t0; t < s.t1 && ok; ++t, ++job) {
                         const uint32_t stage = job % Sh::kStages, sb = job & 1;
                         ok = __all_sync(~0u, bar_wait(&sh.full[stage], (job / Sh::kStages) & 1, abort));
@@ -268,7 +259,7 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
                         }
                         __syncwarp();
                     }
-                    if (ok && lead) tc_commit(&sh.q_empty[phase & 1]);
+                    if (ok && lead) tc_commit(&sh.q_empty[qb]);
                     __syncwarp();
                 }
             }
@@ -278,6 +269,43 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
                 const long long t0 = clock64();
                 while (!bar_try(&sh.drain, 0) && clock64() - t0 < kWaitCycles) {
                 }
+            }
+        }
+        else {
+            // -------------------------------------------- slots of the tiles to come, three warps in turn
+            const int turn = warp - kMmaWarp - 1;
+            uint32_t job = 0;
+            while (ok && spans.next(&s)) {
+                uint64_t seen = ~0ull;   // drafted tokens that an accepted row sees
+                if (a.tree_mask && s.t1 * KT > s.ctx) {
+                    seen = 0;
+                    for (int j = lane; j < a.next_n; j += 32)
+                        if ((s.took >> j) & 1) seen |= static_cast<uint64_t>(fetch(a.tree_mask + static_cast<int64_t>(s.b) * a.next_n + j));
+                    seen = static_cast<uint64_t>(__reduce_or_sync(~0u, static_cast<uint32_t>(seen >> 32))) << 32 |
+                           __reduce_or_sync(~0u, static_cast<uint32_t>(seen));
+                }
+                for (int32_t ph = 0; ph < s.phases && ok; ++ph)
+                    for (int32_t t = s.t0; t < s.t1; ++t, ++job) {
+                        if (job % 3 != static_cast<uint32_t>(turn)) continue;
+                        const uint32_t r = job % kMaskRing;
+                        Paging::Place at[KT / 32];
+#pragma unroll
+                        for (int k = 0; k < KT / 32; ++k) {
+                            const int32_t pos = t * KT + k * 32 + lane;
+                            at[k] = a.pages.place(s.b, pos, pos < s.n && pos < p.width && (pos < s.ctx || ((seen >> (pos - s.ctx)) & 1)));
+                        }
+                        if (job >= kMaskRing) ok = __all_sync(~0u, bar_wait(&sh.slots_empty[r], (job / kMaskRing - 1) & 1, abort));
+                        if (!ok) break;
+#pragma unroll
+                        for (int k = 0; k < KT / 32; ++k) {
+                            const int32_t slot = static_cast<int32_t>(a.pages.slot(at[k]));
+                            const uint32_t valid = __ballot_sync(~0u, slot >= 0);
+                            sh.slots[r][k * 32 + lane] = slot;
+                            if (lane == 0) sh.mask[r][k] = valid;
+                        }
+                        __syncwarp();
+                        if (lane == 0) bar_arrive(&sh.slots_full[r]);
+                    }
             }
         }
         __syncwarp();
@@ -304,11 +332,12 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
             for (int32_t ph = 0; ph < s.phases && ok; ++ph, ++phase) {
                 const int32_t r0 = (ph % s.groups) * NQ;
                 const int32_t rows = s.rows - r0 < NQ ? s.rows - r0 : NQ, padded = (rows + 15) / 16 * 16;
-                const float *lse2 = sh.lse2[phase & 1];
-                ok = __all_sync(~0u, bar_wait(&sh.q_full[phase & 1], (phase / 2) & 1, abort));
+                const uint32_t qb = phase % Sh::kQBufs;
+                const float *lse2 = sh.lse2 + qb * NQ;
+                ok = __all_sync(~0u, bar_wait(&sh.q_full[qb], (phase / Sh::kQBufs) & 1, abort));
                 for (int32_t t = s.t0; t < s.t1 && ok; ++t, ++job) {
                     if ((job & 1) != static_cast<uint32_t>(wg)) continue;
-                    ok = __all_sync(~0u, bar_wait(&sh.mask_full[job % kMaskRing], (job / kMaskRing) & 1, abort) &&
+                    ok = __all_sync(~0u, bar_wait(&sh.slots_full[job % kMaskRing], (job / kMaskRing) & 1, abort) &&
                                              bar_wait(&sh.s_full[wg], (job / 2) & 1, abort));
                     if (!ok) break;
                     tc_fence_after();
@@ -337,11 +366,14 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
                     if (valid) mine[(t - s.t0) * KT] += add;
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) bar_arrive(&sh.s_empty[wg]);
+                    if (lane == 0) {
+                        bar_arrive(&sh.s_empty[wg]);
+                        bar_arrive(&sh.slots_empty[job % kMaskRing]);
+                    }
                 }
                 if (!ok) break;
                 __syncwarp();
-                if (lane == 0) bar_arrive(&sh.q_empty[phase & 1]);
+                if (lane == 0) bar_arrive(&sh.q_empty[qb]);
             }
             // the two warpgroups' sums, in order; all leave together when one gave up
             ok = !sums_barrier_or(!ok);
@@ -362,19 +394,22 @@ __global__ void __launch_bounds__(Shape<DP>::kThreads, 1) weights_kernel(const _
     if (threadIdx.x == 0 && sh.abort) atomicOr(a.status, kStatusCopyLost);
 }
 
-template <bool BF16, int DP>
+template <bool BF16, int DP, int NQ>
 cudaError_t launch_shape(const WeightParams &p, int sms, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
-    const cudaError_t e = allow_smem(weights_kernel<BF16, DP>, Shape<DP>::kSmem, allowed);
+    const cudaError_t e = allow_smem(weights_kernel<BF16, DP, NQ>, Shape<DP, NQ>::kSmem, allowed);
     if (e != cudaSuccess) return e;
-    return launch_pdl(weights_kernel<BF16, DP>, dim3(static_cast<unsigned>(sms)), Shape<DP>::kThreads, Shape<DP>::kSmem, stream, 1, p);
+    return launch_pdl(weights_kernel<BF16, DP, NQ>, dim3(static_cast<unsigned>(sms)), Shape<DP, NQ>::kThreads, Shape<DP, NQ>::kSmem,
+                      stream, 1, p);
 }
 
+// By the rows of a head, all accepted (how many are is not known here).
 template <bool BF16>
 cudaError_t launch_weights(const WeightParams &p, int sms, cudaStream_t s) {
-    if (p.a.dim <= 64) return launch_shape<BF16, 64>(p, sms, s);
-    if (p.a.dim <= 128) return launch_shape<BF16, 128>(p, sms, s);
-    return launch_shape<BF16, 256>(p, sms, s);
+    const bool few = p.a.next_n * p.a.group <= 32;
+    if (p.a.dim <= 64) return few ? launch_shape<BF16, 64, 32>(p, sms, s) : launch_shape<BF16, 64, 128>(p, sms, s);
+    if (p.a.dim <= 128) return few ? launch_shape<BF16, 128, 32>(p, sms, s) : launch_shape<BF16, 128, 128>(p, sms, s);
+    return few ? launch_shape<BF16, 256, 32>(p, sms, s) : launch_shape<BF16, 256, 64>(p, sms, s);
 }
 
 }  // namespace
