@@ -62,7 +62,7 @@ struct SelectShared {
 };
 
 __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(const __grid_constant__ EvictParams p) {
-    extern __shared__ uint32_t keys[];
+    extern __shared__ __align__(16) uint32_t keys[];
     __shared__ SelectShared sh;
     cg::cluster_group cluster = cg::this_cluster();
     const int size = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -99,7 +99,15 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(const _
     if (size > 1) cluster.sync();
     else __syncthreads();
     auto pos = [&](int32_t s) { return s < a ? s : sh.draft[s - a]; };
-    auto key = [&](int32_t s) { return p.staged ? keys[s - s0] : weight_key(w[pos(s)]); };
+    // keys of the slice's survivors o .. o + 3, o a multiple of 4; those from
+    // `end` on hold anything
+    auto keys_at = [&](int32_t o, int32_t end) {
+        if (p.staged) return o < end ? *reinterpret_cast<const uint4 *>(keys + o) : make_uint4(0, 0, 0, 0);
+        uint32_t k[4] = {};
+        for (int j = 0; j < 4; ++j)
+            if (o + j < end) k[j] = weight_key(w[pos(s0 + o + j)]);
+        return make_uint4(k[0], k[1], k[2], k[3]);
+    };
     if (p.staged) {   // eight loads in flight a thread
         constexpr int kUnroll = 8;
         for (int32_t b = s0 + tid; b < s1; b += kSelectThreads * kUnroll) {
@@ -122,18 +130,22 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(const _
         const uint32_t digit = round < 2 ? kBins11 - 1 : kBins11 / 2 - 1;
         for (int b = tid; b < kBins11; b += kSelectThreads) sh.hist[b] = 0;
         __syncthreads();
-        for (int32_t s = s0 + tid; s - tid < c1; s += kSelectThreads) {
-            uint32_t b = kBins11;
-            if (s < c1) {
-                const uint32_t k = key(s);
-                if (((k ^ t) & ~(digit | ((1u << shift) - 1) | (digit << shift))) == 0) b = (k >> shift) & digit;
-            }
+        const uint32_t above_digit = ~(digit | ((1u << shift) - 1) | (digit << shift));
+        for (int32_t o = tid * 4; o - tid * 4 < c1 - s0; o += kSelectThreads * 4) {
+            const uint4 v = keys_at(o, c1 - s0);
+            const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+            uint32_t bin[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                bin[j] = o + j < c1 - s0 && ((k[j] ^ t) & above_digit) == 0 ? (k[j] >> shift) & digit : kBins11;
             // a warp of equal keys adds once
-            const uint32_t lead = __shfl_sync(~0u, b, 0);
-            if (__all_sync(~0u, b == lead)) {
-                if (lane == 0 && b < kBins11) atomicAdd(&sh.hist[b], 32u);
-            } else if (b < kBins11) {
-                atomicAdd(&sh.hist[b], 1u);
+            const uint32_t lead = __shfl_sync(~0u, bin[0], 0);
+            if (__all_sync(~0u, bin[0] == lead && bin[1] == lead && bin[2] == lead && bin[3] == lead)) {
+                if (lane == 0 && lead < kBins11) atomicAdd(&sh.hist[lead], 128u);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (bin[j] < kBins11) atomicAdd(&sh.hist[bin[j]], 1u);
             }
         }
         if (size > 1) cluster.sync();
@@ -183,25 +195,33 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(const _
         whole = need == sh.count;
     }
     const bool compete = cut > 0 && p.budget > recent;
-    // ordered pass: each warp a segment of the slice
-    const int32_t seg = ((s1 - s0 + kSelectWarps - 1) / kSelectWarps + 31) / 32 * 32;
-    const int32_t b0 = s0 + warp * seg < s1 ? s0 + warp * seg : s1, b1 = b0 + seg < s1 ? b0 + seg : s1;
-    auto classify = [&](int32_t s, bool *eq) {
-        *eq = false;
-        if (s >= b1) return false;
-        if (s >= cut) return true;
-        if (!compete) return false;
-        const uint32_t k = key(s);
-        *eq = !whole && k == t;
-        return whole ? k >= t : k > t;
+    // ordered pass: each warp a segment of the slice, four survivors a lane
+    const int32_t held = s1 - s0;
+    const int32_t seg = ((held + kSelectWarps - 1) / kSelectWarps + 127) / 128 * 128;
+    const int32_t b0 = warp * seg < held ? warp * seg : held, b1 = b0 + seg < held ? b0 + seg : held;
+    // bits of the four from offset o on: kept for sure, equal to the key
+    auto classify = [&](int32_t o, uint32_t *equal) {
+        const uint4 v = keys_at(o, b1);
+        const uint32_t k[4] = {v.x, v.y, v.z, v.w};
+        uint32_t g = 0, e = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            if (o + j >= b1) continue;
+            const bool late = s0 + o + j >= cut;
+            g |= static_cast<uint32_t>(late || (compete && (whole ? k[j] >= t : k[j] > t))) << j;
+            e |= static_cast<uint32_t>(!late && compete && !whole && k[j] == t) << j;
+        }
+        *equal = e;
+        return g;
     };
     uint32_t gt = 0, eq = 0;
-    for (int32_t s = b0; s < b1; s += 32) {
-        bool e;
-        const bool g = classify(s + lane, &e);
-        gt += __popc(__ballot_sync(~0u, g));
-        eq += __popc(__ballot_sync(~0u, e));
+    for (int32_t o = b0 + lane * 4; o < b1; o += 128) {
+        uint32_t e;
+        gt += __popc(classify(o, &e));
+        eq += __popc(e);
     }
+    gt = __reduce_add_sync(~0u, gt);
+    eq = __reduce_add_sync(~0u, eq);
     if (lane == 0) {
         sh.gt[warp] = gt;
         sh.eq[warp] = eq;
@@ -234,20 +254,28 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(const _
         gt += sh.all_gt[r];
         eq += sh.all_eq[r];
     }
-    const uint32_t below = (1u << lane) - 1;
-    for (int32_t s = b0; s < b1; s += 32) {
-        bool e;
-        const bool g = classify(s + lane, &e);
-        const uint32_t gm = __ballot_sync(~0u, g), em = __ballot_sync(~0u, e);
-        const uint32_t eb = eq + __popc(em & below);   // equal keys before this one
-        if (g || (e && eb < need)) {
-            const uint32_t at = gt + __popc(gm & below) + (eb < need ? eb : need);
-            const int32_t q = pos(s + lane);
-            kept[at] = q;
-            out_w[at] = p.staged ? key_weight(keys[s + lane - s0]) : w[q];
+    for (int32_t o0 = b0; o0 < b1; o0 += 128) {
+        const int32_t o = o0 + lane * 4;
+        uint32_t e;
+        const uint32_t g = classify(o, &e), mine = __popc(g) | __popc(e) << 16;
+        uint32_t inc = mine;
+        for (int i = 1; i < 32; i <<= 1) {
+            const uint32_t x = __shfl_up_sync(~0u, inc, i);
+            if (lane >= i) inc += x;
         }
-        gt += __popc(gm);
-        eq += __popc(em);
+        const uint32_t all = __shfl_sync(~0u, inc, 31), before = inc - mine;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t low = (1u << j) - 1, eb = eq + (before >> 16) + __popc(e & low);   // equal keys before this one
+            if (((g >> j) & 1) || (((e >> j) & 1) && eb < need)) {
+                const uint32_t at = gt + (before & 0xffff) + __popc(g & low) + (eb < need ? eb : need);
+                const int32_t q = pos(s0 + o + j);
+                kept[at] = q;
+                out_w[at] = p.staged ? key_weight(keys[o + j]) : w[q];
+            }
+        }
+        gt += all & 0xffff;
+        eq += all >> 16;
     }
     for (int64_t j = m + rank * kSelectThreads + tid; j < p.budget; j += size * kSelectThreads) kept[j] = -1;
     for (int64_t j = m + rank * kSelectThreads + tid; j < p.width; j += size * kSelectThreads) out_w[j] = 0.f;
@@ -387,7 +415,7 @@ extern "C" int gbtopk_cache_evict(const float *weights, int64_t num_requests, in
     const int cluster = select_cluster(rows, width);
     const int64_t slice = (width + cluster - 1) / cluster;
     p.staged = slice <= kStagedKeys;
-    const size_t smem = p.staged ? static_cast<size_t>(slice) * 4 : 0;
+    const size_t smem = p.staged ? static_cast<size_t>((slice + 3) / 4) * 16 : 0;
     // 32 KB of keys and values a block, at most 64 positions
     const int64_t bytes = 2ll * head_dim * es * (weight_heads == 1 ? kv_heads : 1);
     p.move_rows = static_cast<int32_t>(bytes >= 32768 ? 1 : 32768 / bytes > 64 ? 64 : 32768 / bytes);

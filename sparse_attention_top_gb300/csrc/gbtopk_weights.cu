@@ -317,6 +317,15 @@ __global__ void __launch_bounds__(Shape<DP, NQ>::kThreads, 1) weights_kernel(con
         uint32_t phase = 0, job = 0;
         while (ok && spans.next(&s)) {
             for (int i = 0; i < s.t1 - s.t0; ++i) mine[i * KT] = 0.f;
+            // the span's weights, loaded while its products run
+            float *w = p.weights + (static_cast<int64_t>(s.b) * p.weight_heads + s.w) * p.width;
+            constexpr int kHeld = kSpan * KT / 256;
+            float held[kHeld];
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                const int64_t pos = static_cast<int64_t>(s.t0) * KT + i * 256 + threadIdx.x;
+                if (i * 256 + static_cast<int>(threadIdx.x) < (s.t1 - s.t0) * KT && pos < s.n && pos < p.width) held[i] = w[pos];
+            }
             // trees of the accepted tokens, where the span reaches the drafts
             const bool drafts = s.t1 * KT > s.ctx;
             if (drafts) {
@@ -377,12 +386,12 @@ __global__ void __launch_bounds__(Shape<DP, NQ>::kThreads, 1) weights_kernel(con
             }
             // the two warpgroups' sums, in order; all leave together when one gave up
             ok = !sums_barrier_or(!ok);
-            if (ok) {
-                float *w = p.weights + (static_cast<int64_t>(s.b) * p.weight_heads + s.w) * p.width;
-                for (int x = threadIdx.x; x < (s.t1 - s.t0) * KT; x += 256) {
-                    const int64_t pos = static_cast<int64_t>(s.t0) * KT + x;
-                    if (pos < s.n && pos < p.width) w[pos] += sums[x] + sums[kSpan * KT + x];
-                }
+            if (!ok) break;
+#pragma unroll
+            for (int i = 0; i < kHeld; ++i) {
+                const int x = i * 256 + static_cast<int>(threadIdx.x);
+                const int64_t pos = static_cast<int64_t>(s.t0) * KT + x;
+                if (x < (s.t1 - s.t0) * KT && pos < s.n && pos < p.width) w[pos] = held[i] + (sums[x] + sums[kSpan * KT + x]);
             }
             sums_barrier_or(false);
         }
