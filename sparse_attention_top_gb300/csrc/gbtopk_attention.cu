@@ -53,8 +53,9 @@ struct Shape {
     static constexpr int kStageBytes = KT * DP * 2;
     static constexpr int kQBytes = kRows * DP * 2;
     static constexpr int kQBufs = ROWS == 32 ? 2 : 1;       // units whose queries are held
-    static constexpr int kJoin = kSplit ? (ROWS * 33 * 4 + 127) / 128 * 128 : 0;   // 32 columns of the second O
-    static constexpr int kFixed = 6144;                     // barriers, slots and masks, scan scratch
+    static constexpr int kJoinCols = ROWS == 32 ? 32 : 16;  // columns of O that the warpgroups exchange at a time
+    static constexpr int kJoin = kSplit ? (2 * ROWS * (kJoinCols + 1) * 4 + 127) / 128 * 128 : 0;
+    static constexpr int kFixed = 7168;                     // barriers, slots and masks, scan scratch
     static constexpr int kFit = (static_cast<int>(kMaxSmemBytes) - 1024 - kFixed - kJoin - kQBufs * kQBytes) / kStageBytes;
     static constexpr int kStages = kFit < 12 ? kFit : 12;
     static constexpr size_t kSmem = 1024 + kFixed + kJoin + kQBufs * kQBytes + static_cast<size_t>(kStages) * kStageBytes;
@@ -74,12 +75,12 @@ struct Shared {
     uint64_t drain;
     int32_t slots[kMaskRing][128];  // cache slot of each position, -1 where there is none
     uint32_t mask[kMaskRing][4];    // positions with a slot, as bits
-    float2 ml[128];                 // (m, l) of the second warpgroup's rows
+    float2 ml[2][128];              // (m, l) of the two warpgroups' rows
     ScanScratch scan;
     uint32_t tmem;
     uint32_t abort;
 };
-static_assert(sizeof(Shared) <= 6144, "shared block");
+static_assert(sizeof(Shared) <= 7168, "shared block");
 
 // Barrier of the two softmax warps that share rows; true for both when `v`
 // is for one.
@@ -101,7 +102,7 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
     constexpr int KT = Sh::KT;
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
-    float *join = reinterpret_cast<float *>(smem + Sh::kQBufs * Sh::kQBytes + Sh::kStages * Sh::kStageBytes);   // [128][33]
+    float *join = reinterpret_cast<float *>(smem + Sh::kQBufs * Sh::kQBytes + Sh::kStages * Sh::kStageBytes);   // [2][kRows][kJoinCols + 1]
     Shared &sh = *reinterpret_cast<Shared *>(reinterpret_cast<uint8_t *>(join) + Sh::kJoin);
     // stage 0, the queries, the other stages (the products of kShift read
     // around the queries)
@@ -460,19 +461,18 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                 continue;
             }
             const int pair = 1 + row0 / 32;   // barrier of the two warps that have these rows
-            float f0 = 1.f, f1 = 0.f;         // SPLIT: factors of the two O
+            float f_own = 1.f, f_other = 0.f;   // SPLIT: factors of the two O
             if constexpr (SPLIT) {
-                if (wg == 1) sh.ml[row] = make_float2(m, l);
+                sh.ml[wg][row] = make_float2(m, l);
                 ok = !pair_barrier_or(pair, !ok);   // both leave when one gave up
                 if (!ok) break;
-                if (wg == 0) {
-                    const float2 other = sh.ml[row];
-                    const float top = fmaxf(m, other.x);
-                    f0 = m == -INFINITY ? 0.f : exp2_fast(m - top);
-                    f1 = other.x == -INFINITY ? 0.f : exp2_fast(other.x - top);
-                    l = l * f0 + other.y * f1;
-                    m = top;
-                }
+                const float2 other = sh.ml[1 - wg][row];
+                const float top = fmaxf(m, other.x);
+                // (an O without a job holds what an earlier unit left there)
+                f_own = m == -INFINITY ? 0.f : exp2_fast(m - top);
+                f_other = other.x == -INFINITY ? 0.f : exp2_fast(other.x - top);
+                l = l * f_own + other.y * f_other;
+                m = top;
             }
             tc_fence_after();
             const bool whole = u.t0 == 0 && u.t1 == u.tiles;
@@ -480,33 +480,12 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
             const int32_t part_row = row_wg + row;
             const float inv = l > 0.f ? 1.f / l : 0.f;
             const int64_t q_at = r * p.q_heads + h * p.group + gq;
-            for (int c0 = 0; c0 < DP; c0 += 32) {
-                if (c0 >= p.dim) break;
-                __syncwarp();
-                uint32_t o[32];
-                tmem_load32(t_o + c0, o);
-                tc_wait_ld();
-                if constexpr (SPLIT) {   // the second warpgroup's columns through shared memory
-                    if (wg == 1) {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) join[row * 33 + c] = __uint_as_float(o[c]);
-                    }
-                    pair_barrier_or(pair, false);
-                    if (wg == 0) {
-#pragma unroll
-                        for (int c = 0; c < 32; ++c) {
-                            // an O without a job holds what an earlier unit left there
-                            const float a = f0 > 0.f ? __uint_as_float(o[c]) * f0 : 0.f, b = f1 > 0.f ? join[row * 33 + c] * f1 : 0.f;
-                            o[c] = __float_as_uint(a + b);
-                        }
-                    }
-                    pair_barrier_or(pair, false);
-                }
-                if (!mine || (SPLIT && wg == 1)) continue;
+            auto put = [&](int c0, auto &o) {   // columns of the row, eight or more
+                constexpr int N = sizeof(o) / 4;
                 if (whole) {
                     uint8_t *dst = static_cast<uint8_t *>(p.out) + 2 * (q_at * p.dim + c0);
 #pragma unroll
-                    for (int c = 0; c < 32; c += 8) {
+                    for (int c = 0; c < N; c += 8) {
                         if (c0 + c >= p.dim) break;
                         uint32_t y[4];
 #pragma unroll
@@ -518,10 +497,46 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                     // column by column: a warp's rows are 128 consecutive bytes
                     float *dst = p.part_o + (part * DP + c0) * Sh::kRows + part_row;
 #pragma unroll
-                    for (int c = 0; c < 32; ++c) dst[c * Sh::kRows] = __uint_as_float(o[c]);
+                    for (int c = 0; c < N; ++c) dst[c * Sh::kRows] = __uint_as_float(o[c]);
+                }
+            };
+            if constexpr (SPLIT) {
+                // Each warpgroup puts half of the columns out, the other's part
+                // of them through shared memory, a piece at a time.
+                constexpr int N = Sh::kJoinCols, kStride = N + 1;
+                float *give = join + (wg * Sh::kRows + row) * kStride;
+                const float *take = join + ((1 - wg) * Sh::kRows + row) * kStride;
+                auto load = [&](int c0, uint32_t *o) {
+                    if constexpr (N == 32) tmem_load32(t_o + c0, o);
+                    else tmem_load16(t_o + c0, o);
+                    tc_wait_ld();
+                };
+                for (int c0 = 0; c0 < DP / 2; c0 += N) {
+                    const int mine0 = wg * (DP / 2) + c0, other0 = (1 - wg) * (DP / 2) + c0;
+                    uint32_t o[N];
+                    load(other0, o);
+#pragma unroll
+                    for (int c = 0; c < N; ++c) give[c] = __uint_as_float(o[c]);
+                    load(mine0, o);
+                    pair_barrier_or(pair, false);
+#pragma unroll
+                    for (int c = 0; c < N; ++c) {
+                        const float x = f_own > 0.f ? __uint_as_float(o[c]) * f_own : 0.f, y = f_other > 0.f ? take[c] * f_other : 0.f;
+                        o[c] = __float_as_uint(x + y);
+                    }
+                    pair_barrier_or(pair, false);
+                    if (mine && mine0 < p.dim) put(mine0, o);
+                    __syncwarp();
+                }
+            } else {
+                for (int c0 = 0; c0 < p.dim; c0 += 32) {
+                    uint32_t o[32];
+                    tmem_load32(t_o + c0, o);
+                    tc_wait_ld();
+                    if (mine) put(c0, o);
+                    __syncwarp();
                 }
             }
-            if constexpr (SPLIT) pair_barrier_or(pair, false);   // ml is read
             if (mine && !(SPLIT && wg == 1)) {
                 if (!whole) p.part_ml[part * Sh::kRows + part_row] = make_float2(m, l);
                 else if (p.lse) p.lse[q_at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
