@@ -320,9 +320,9 @@ int gbtopk_varlen_static_ws(const void *logits, int dtype, int64_t num_rows, int
  *     s(r,h,p) = scale * <q[r,h], k[slot(i,p), h / group]>  over visible p,
  *     lse[r,h] = log sum_p exp s,   out[r,h] = sum_p exp(s - lse) v[slot(i,p)].
  * A row that sees nothing gives zeros and lse = -infinity.  Keys and values
- * of positions that no row of the request sees are not used, whatever they
- * hold; those of a drafted token that some rows see and others do not have
- * to be finite.
+ * of positions that no row of the request sees are not read, whatever they
+ * hold.  The values of a drafted token that some of the request's rows see
+ * must be finite, or the rows that do not see it become NaN too.
  *
  *  q            device [num_rows, q_heads, head_dim], inner stride 1, row and
  *               head strides multiples of 8, 16-byte aligned.
@@ -335,7 +335,8 @@ int gbtopk_varlen_static_ws(const void *logits, int dtype, int64_t num_rows, int
  *  lse          device fp32 [num_rows, q_heads] or NULL.
  *  workspace    as for gbtopk_varlen, gbtopk_attention_workspace_bytes(...)
  *               bytes; its status word reports bounded waits that gave up
- *               (bit 1: outputs not reliable).
+ *               (bit 1: outputs not reliable; GBTOPK_WAIT_POLLS, which lowers
+ *               the waits' limit, makes them).  At most 2^31 - 1 slots.
  */
 int gbtopk_tree_attention(const void *q, int dtype, int64_t num_rows, int64_t q_row_stride,
                           int64_t q_head_stride, int32_t q_heads, int32_t kv_heads,

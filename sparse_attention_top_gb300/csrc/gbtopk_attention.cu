@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
     pdl_release();
 
     const Share share = block_share<KT, Sh::kThreads>(p, &sh.scan);
-    volatile uint32_t *abort = &sh.abort;
+    const Waits abort{&sh.abort, p.wait_cycles};
     const uint32_t tmem = sh.tmem;
     Walk<KT> walk(p, share);
     const int32_t rows = p.next_n * p.group;   // of a (request, kv head)
@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
 
 int dim_class(int32_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
 
-size_t partial_rows() { return static_cast<size_t>(2 * kMaxGrid) * 256; }
+size_t partial_rows(int32_t dim) { return static_cast<size_t>(2 * kMaxGrid) * (dim > 128 ? 128 : 256); }
 size_t unit_bytes(int64_t num_rows, int32_t q_heads) {   // a unit has a row or more
     return (static_cast<size_t>(num_rows) * q_heads * 8 + 255) / 256 * 256;
 }
@@ -629,7 +629,7 @@ cudaError_t launch_shape(AttnParams p, uint8_t *ws, int sms, cudaStream_t stream
     p.request_units = p.kv_heads * p.row_tiles;
     p.unit_ends = reinterpret_cast<int32_t *>(ws + kWsHeaderBytes);
     p.part_ml = reinterpret_cast<float2 *>(ws + kWsHeaderBytes + unit_bytes(static_cast<int64_t>(p.requests) * p.next_n, p.q_heads));
-    p.part_o = reinterpret_cast<float *>(p.part_ml + partial_rows());
+    p.part_o = reinterpret_cast<float *>(p.part_ml + partial_rows(p.dim));
     static std::atomic<uint64_t> allowed{0};
     cudaError_t e = allow_smem(attention_kernel<BF16, DP, W, ROWS>, Sh::kSmem, allowed);
     if (e != cudaSuccess) return e;
@@ -713,6 +713,7 @@ int attend(AttnParams &p, int dtype, const void *q, int64_t num_rows, int64_t q_
     p.out = out;
     p.lse = lse;
     p.status = static_cast<uint32_t *>(workspace);
+    p.wait_cycles = wait_cycles();
     p.pages.spare = static_cast<const int32_t *>(workspace);
     const int sms = device_sms();
     if (sms == 0) return GBTOPK_ECUDA;
@@ -730,7 +731,7 @@ extern "C" {
 
 size_t gbtopk_attention_workspace_bytes(int64_t num_rows, int32_t q_heads, int32_t kv_heads, int32_t head_dim) {
     if (check_heads(GBTOPK_BF16, num_rows, q_heads, kv_heads, head_dim) != GBTOPK_OK) return 0;
-    return kWsHeaderBytes + unit_bytes(num_rows, q_heads) + partial_rows() * (8 + 4 * static_cast<size_t>(dim_class(head_dim)));
+    return kWsHeaderBytes + unit_bytes(num_rows, q_heads) + partial_rows(head_dim) * (8 + 4 * static_cast<size_t>(dim_class(head_dim)));
 }
 
 int gbtopk_tree_attention(const void *q, int dtype, int64_t num_rows, int64_t q_row_stride, int64_t q_head_stride,

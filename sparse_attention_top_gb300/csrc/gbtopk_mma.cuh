@@ -43,15 +43,22 @@ __device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
 // of it, so a wait that reaches it has lost its partner.
 constexpr long long kWaitCycles = 2000000000ll;
 
+// A block's waits: `given_up` is set by the first that runs out, after `limit`
+// cycles.
+struct Waits {
+    volatile uint32_t *given_up;
+    long long limit;
+};
+
 // Waits for the phase of `parity` to complete.  False when the wait gave up
-// or another one of the block did (*abort set): the caller leaves its loop.
-__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, volatile uint32_t *abort) {
+// or another one of the block did: the caller leaves its loop.
+__device__ __forceinline__ bool bar_wait(uint64_t *bar, uint32_t parity, const Waits &w) {
     if (bar_try(bar, parity)) return true;
     const long long t0 = clock64();
     while (!bar_try(bar, parity)) {
-        if (*abort) return false;
-        if (clock64() - t0 > kWaitCycles) {
-            *abort = 1;
+        if (*w.given_up) return false;
+        if (clock64() - t0 > w.limit) {
+            *w.given_up = 1;
             return false;
         }
     }

@@ -3,10 +3,24 @@
 // tiles over the blocks, and the copies of cached rows.  Not part of the ABI.
 #pragma once
 
+#include <cstdlib>
+
 #include "gbtopk_decode.cuh"
 #include "gbtopk_mma.cuh"
 
 namespace gbtopk {
+
+// Limit of the kernels' waits in cycles: kWaitCycles, or the positive value
+// of GBTOPK_WAIT_POLLS (read once a process), which lets a test run them out.
+inline int64_t wait_cycles() {
+    static const int64_t cycles = [] {
+        const char *v = std::getenv("GBTOPK_WAIT_POLLS");
+        char *end = nullptr;
+        const unsigned long x = v && *v ? std::strtoul(v, &end, 10) : 0;
+        return x > 0 && *end == '\0' && x < kWaitCycles ? static_cast<int64_t>(x) : static_cast<int64_t>(kWaitCycles);
+    }();
+    return cycles;
+}
 
 struct AttnParams {
     const void *q, *k, *v;
@@ -26,6 +40,7 @@ struct AttnParams {
     void *out;
     float *lse;
     uint32_t *status;
+    int64_t wait_cycles;         // limit of each wait
     int32_t *unit_ends;          // first and last block of each unit
     float *part_o;               // [2 grid][rows of a tile][DP]
     float2 *part_ml;             // [2 grid][rows of a tile]

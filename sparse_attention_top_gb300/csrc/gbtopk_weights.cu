@@ -167,7 +167,7 @@ __global__ void __launch_bounds__(Shape<DP, NQ>::kThreads, 1) weights_kernel(con
     pdl_wait();
     pdl_release();
     const Share share = block_share<KT, Sh::kThreads>(a, &sh.scan);
-    volatile uint32_t *abort = &sh.abort;
+    const Waits abort{&sh.abort, a.wait_cycles};
     const uint32_t tmem = sh.tmem;
     Spans<NQ> spans(p, share);
     const int32_t per = a.kv_heads / p.weight_heads;   // kv heads of a weight head
@@ -467,6 +467,7 @@ extern "C" int gbtopk_cache_weights(const void *q, int dtype, int64_t num_rows, 
     a.c = fmaxf(fabsf(scale) * kLog2e, FLT_MIN);
     a.negative = scale < 0.f;
     a.status = static_cast<uint32_t *>(workspace);
+    a.wait_cycles = wait_cycles();
     a.pages.spare = static_cast<const int32_t *>(workspace);
     p.accept_mask = accept_mask;
     p.lse = lse;
