@@ -91,14 +91,32 @@ __device__ __forceinline__ void unpack(const uint4 &v, float *x) {
 }
 
 struct StatScratch {
-    float top[kThreads / 32], sum[kThreads / 32];
-    int32_t first[kThreads / 32];
+    RowStat warp[kThreads / 32];
 };
 
-// The stat of logits [e0, e1) of a row, by the block; thread 0 has it.
-template <int DT>
+// The parts' stats as one: the largest logit first, then every sum scaled to
+// it, so that the exponentials do not wait for one another.
+template <int N>
+__device__ __forceinline__ RowStat join_all(const RowStat *part, bool greedy, float c) {
+    RowStat st = part[0];
+    if (greedy) {
+#pragma unroll
+        for (int k = 1; k < N; ++k) better(st.top, st.first, part[k].top, part[k].first);
+        return st;
+    }
+#pragma unroll
+    for (int k = 1; k < N; ++k) st.top = fmaxf(st.top, part[k].top);
+    const float base = st.top == -INFINITY ? 0.f : st.top;
+    st.sum = 0.f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) st.sum += part[k].sum * exp2f((part[k].top - base) * c);
+    return st;
+}
+
+// The stat of logits [e0, e1) of a row, by the block (every thread has it).
+template <int DT, int UNROLL>
 __device__ RowStat block_stat(const uint8_t *row, int64_t e0, int64_t e1, bool greedy, float c, StatScratch &sh) {
-    constexpr int kBytes = DT == GBTOPK_F32 ? 4 : 2, kVec = 16 / kBytes, kUnroll = 4;
+    constexpr int kBytes = DT == GBTOPK_F32 ? 4 : 2, kVec = 16 / kBytes, kUnroll = UNROLL;
     const int32_t n = static_cast<int32_t>(e1 - e0), tid = static_cast<int32_t>(threadIdx.x);
     const uint8_t *base = row + e0 * kBytes;
     // whole 16-byte vectors from `skip` logits on
@@ -151,24 +169,18 @@ __device__ RowStat block_stat(const uint8_t *row, int64_t e0, int64_t e1, bool g
             sum += part;
         }
     }
-    for (int o = 16; o; o >>= 1) {
-        const float t2 = __shfl_xor_sync(~0u, top, o), s2 = __shfl_xor_sync(~0u, sum, o);
-        const int32_t f2 = __shfl_xor_sync(~0u, first, o);
-        if (greedy) better(top, first, t2, f2);
-        else join(top, sum, t2, s2, c);
+    if (greedy) {
+        for (int o = 16; o; o >>= 1) better(top, first, __shfl_xor_sync(~0u, top, o), __shfl_xor_sync(~0u, first, o));
+    } else {
+        float most = top;
+        for (int o = 16; o; o >>= 1) most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+        sum *= exp2f((top - (most == -INFINITY ? 0.f : most)) * c);
+        top = most;
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
     }
-    if ((tid & 31) == 0) {
-        sh.top[tid >> 5] = top;
-        sh.sum[tid >> 5] = sum;
-        sh.first[tid >> 5] = first;
-    }
+    if ((tid & 31) == 0) sh.warp[tid >> 5] = RowStat{top, sum, first};
     __syncthreads();
-    if (tid == 0)
-        for (int w = 1; w < kThreads / 32; ++w) {
-            if (greedy) better(top, first, sh.top[w], sh.first[w]);
-            else join(top, sum, sh.top[w], sh.sum[w], c);
-        }
-    return RowStat{top, sum, first};
+    return join_all<kThreads / 32>(sh.warp, greedy, c);
 }
 
 // grid: pieces of row 0, of row 1, ...
@@ -181,7 +193,7 @@ __global__ void __launch_bounds__(kThreads) verify_stat_kernel(const __grid_cons
     const int32_t piece = static_cast<int32_t>(blockIdx.x % p.pieces);
     const float t = p.temperature ? fetch(p.temperature + r / p.next_n) : 1.f;
     const int64_t e0 = piece * p.piece, e1 = e0 + p.piece < p.vocab ? e0 + p.piece : p.vocab;
-    const RowStat st = block_stat<DT>(static_cast<const uint8_t *>(p.logits) + r * p.row_stride * (DT == GBTOPK_F32 ? 4 : 2), e0, e1,
+    const RowStat st = block_stat<DT, 4>(static_cast<const uint8_t *>(p.logits) + r * p.row_stride * (DT == GBTOPK_F32 ? 4 : 2), e0, e1,
                                       t <= 0.f, t <= 0.f ? 0.f : kLog2e / t, sh);
     if (threadIdx.x == 0) p.stats[r * p.pieces + piece] = st;
 }
@@ -277,16 +289,10 @@ __global__ void __launch_bounds__(kThreads, 4) verify_path_kernel(const __grid_c
             const bool child = parent == cur && known;
             const float x = child ? logit<DT>(row, x_tok) : 0.f;
             const float q = child && p.draft_probs ? fetch(p.draft_probs + (r0 + cur) * p.vocab + x_tok) : 1.f;
-            const RowStat mine = block_stat<DT>(row, v0, v1, greedy, c, sh.scratch);
-            if (tid == 0)
-                for (int k = 0; k < kCluster; ++k) cluster.map_shared_rank(&sh, k)->part[step & 1][rank] = mine;
+            const RowStat mine = block_stat<DT, 8>(row, v0, v1, greedy, c, sh.scratch);
+            if (tid < kCluster) cluster.map_shared_rank(&sh, tid)->part[step & 1][rank] = mine;
             cluster.sync();
-            RowStat st = sh.part[step & 1][0];
-            for (int k = 1; k < kCluster; ++k) {
-                const RowStat o = sh.part[step & 1][k];
-                if (greedy) better(st.top, st.first, o.top, o.first);
-                else join(st.top, st.sum, o.top, o.sum, c);
-            }
+            RowStat st = join_all<kCluster>(sh.part[step & 1], greedy, c);
             st.sum = st.sum > 0.f ? 1.f / st.sum : 0.f;
             if (tid == 0) sh.stat[cur] = st;
             if (parent == cur) {
