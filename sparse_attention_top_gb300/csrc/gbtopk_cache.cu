@@ -8,6 +8,12 @@
 // handful of bins, whose atomics serialised: 30 us for 17000 weights), and one ordered pass (warp segments, ballots) writes the kept
 // positions in place.  evict_move_kernel then copies the kept rows, blocks of
 // about 32 KB of keys and values.
+//
+// The copies are bound by their bytes: 32 requests x 8 heads of 128, 4096 kept
+// positions each, 150 us = 7.1 TB/s read and written.  The selection of those
+// 256 rows of up to 32768 weights takes 50 us, bound by the instructions of its
+// five passes over the keys in shared memory; one row of 5001 weights, both
+// kernels, 15 us.
 #include <cooperative_groups.h>
 
 #include "gbtopk_decode.cuh"

