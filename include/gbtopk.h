@@ -321,8 +321,8 @@ int gbtopk_varlen_static_ws(const void *logits, int dtype, int64_t num_rows, int
  *     lse[r,h] = log sum_p exp s,   out[r,h] = sum_p exp(s - lse) v[slot(i,p)].
  * A row that sees nothing gives zeros and lse = -infinity.  Keys and values
  * of positions that no row of the request sees are not read, whatever they
- * hold.  The values of a drafted token that some of the request's rows see
- * must be finite, or the rows that do not see it become NaN too.
+ * hold; an infinity or NaN of a drafted token reaches the rows that see it
+ * and no others.
  *
  *  q            device [num_rows, q_heads, head_dim], inner stride 1, row and
  *               head strides multiples of 8, 16-byte aligned.

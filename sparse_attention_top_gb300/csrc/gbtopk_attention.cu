@@ -87,6 +87,7 @@ struct Shared {
     uint64_t drain;
     int32_t slots[kMaskRing][128];  // cache slot of each position, -1 where there is none
     uint32_t mask[kMaskRing][4];    // positions with a slot, as bits
+    uint64_t odd[kMaskRing];        // a tile's drafts left out of the value product (see clean_values)
     float2 ml[2][128];              // (m, l) of the two warpgroups' rows
     ScanScratch scan;
     uint32_t tmem;
@@ -107,7 +108,59 @@ __device__ __forceinline__ bool pair_barrier_or(int id, bool v) {
     return any != 0;
 }
 
-template <bool BF16, int DP, int W, int ROWS>
+// Drafted tokens whose values hold an infinity or a NaN: the product P V
+// would carry 0 x inf into the rows that do not see them.  Their rows of the
+// tile (drafts are `first` up to `end`) are set to zero and marked as bits, and the
+// softmax warps add them at the unit's end to the rows that do.  By the warp
+// that issues the products, in a call of its own: 2 % of the time of a batch of
+// four drafts a request, 3 % of trees of 64 (inlined there 25 %, in the softmax
+// warps, whose registers are all in use, 7 to 12 %, where the slots are looked
+// up 10 %).  Only kernels for several tokens a request have it.
+template <bool BF16, int DP, int KT>
+__device__ __noinline__ void clean_values(uint8_t *tile, int32_t first, int32_t end, int32_t dim, uint64_t *marks) {
+    constexpr int kLanes = DP / 8;   // of a row
+    constexpr uint32_t kExp = BF16 ? 0x7f80u : 0x7c00u;
+    const int lane = threadIdx.x & 31, c = lane % kLanes;
+    const int32_t from = first < 0 ? 0 : first, to = end < KT ? end : KT;
+    uint64_t odd = 0;
+#pragma unroll 4
+    for (int32_t r = from + lane / kLanes; r < to; r += 32 / kLanes) {
+        if (c >= dim / 8) continue;
+        const uint4 x = *reinterpret_cast<const uint4 *>(tile + tile_offset(KT, r, c));
+        const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if ((w[i] & kExp) == kExp || (w[i] >> 16 & kExp) == kExp) odd |= 1ull << (r - from);
+    }
+    odd = static_cast<uint64_t>(__reduce_or_sync(~0u, static_cast<uint32_t>(odd >> 32))) << 32 |
+          __reduce_or_sync(~0u, static_cast<uint32_t>(odd));
+    for (uint64_t left = odd; left; left &= left - 1) {
+        const int32_t r = from + __ffsll(static_cast<long long>(left)) - 1;
+        if (lane < kLanes) *reinterpret_cast<uint4 *>(tile + tile_offset(KT, r, lane)) = make_uint4(0, 0, 0, 0);
+    }
+    fence_async_reads();
+    if (lane == 0) *marks = odd << (from - first);
+    __threadfence_block();
+    __syncwarp();
+}
+
+// 2^(c q.k - m) of one row and one position.
+template <bool BF16>
+__device__ __forceinline__ float row_prob(const AttnParams &p, const uint4 *q, const uint4 *k, float m) {
+    float s = 0.f;
+#pragma unroll 1
+    for (int c = 0; c < p.dim / 8; ++c) {
+        const uint4 a = fetch(q + c), b = fetch(k + c);
+        const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = Half2<BF16>::up(x[i]), g = Half2<BF16>::up(y[i]);
+            s = fmaf(f.x, g.x, fmaf(f.y, g.y, s));
+        }
+    }
+    return exp2f((p.negative ? -s : s) * p.c - m);
+}
+
+template <bool BF16, int DP, int W, int ROWS, bool DRAFTS>
 __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_kernel(const __grid_constant__ AttnParams p) {
     using Sh = Shape<DP, W, ROWS>;
     constexpr bool SPLIT = Sh::kSplit;
@@ -219,6 +272,9 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
             for (; __any_sync(~0u, walk.more()) && ok; walk.next()) {
                 if (__any_sync(~0u, walk.u.span.n == 0)) continue;
                 const uint32_t nt = __shfl_sync(~0u, static_cast<uint32_t>(walk.u.t1 - walk.u.t0), 0), jobs = nt * Sh::kJobs;
+                // the first job that reaches the drafts
+                const int32_t before = walk.u.span.ctx / KT - walk.u.t0;
+                const uint32_t drafts = __shfl_sync(~0u, before > 0 && walk.u.span.ctx > 0 ? static_cast<uint32_t>(before) * Sh::kJobs : 0u, 0);
                 const uint32_t qb = unit % Sh::kQBufs;
                 ok = __all_sync(~0u, bar_wait(&sh.q_full[qb], (unit / Sh::kQBufs) & 1, abort));
                 if (!ok) break;
@@ -246,7 +302,16 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                 for (uint32_t j = 0; j < jobs && ok; ++j) {
                     const uint32_t job = job0 + j, sb = job & 1;
                     const uint32_t item = 2 * (gi + j / Sh::kJobs) + 1, s = item % Sh::kStages;
-                    ok = wait_item(item) && __all_sync(~0u, bar_wait(&sh.p_full[sb], (job >> 1) & 1, abort));
+                    ok = wait_item(item);
+                    if (!ok) break;
+                    if constexpr (DRAFTS) {
+                        if (j >= drafts && (Sh::kJobs == 1 || !(j & 1))) {
+                            const int32_t at = (walk.u.t0 + static_cast<int32_t>(j / Sh::kJobs)) * KT;
+                            clean_values<BF16, DP, KT>(smem + (stage_at(s) - ring), walk.u.span.ctx - at, walk.u.span.n - at, p.dim,
+                                                       &sh.odd[(gi + j / Sh::kJobs) % kMaskRing]);
+                        }
+                    }
+                    ok = __all_sync(~0u, bar_wait(&sh.p_full[sb], (job >> 1) & 1, abort));
                     if (!ok) break;
                     fence_async_reads();
                     tc_fence_after();
@@ -472,6 +537,46 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                 if (!ok) break;
                 continue;
             }
+            if (DRAFTS && ok && u.t1 * KT > u.span.ctx) {
+                // Odd drafts of this warpgroup's tiles (they are in the last
+                // two), the same for the warp's rows: added where a row sees them.
+                uint64_t odd = 0;
+                for (uint32_t back = 1; back <= 2; ++back)
+                    if (u.t1 - u.t0 >= static_cast<int32_t>(back) && (u.t1 - static_cast<int32_t>(back) + 1) * KT > u.span.ctx &&
+                        !(SPLIT && ((tile - back) & 1) != static_cast<uint32_t>(wg)))
+                        odd |= reinterpret_cast<volatile uint64_t *>(sh.odd)[(tile - back) % kMaskRing];
+                if (odd != 0) tc_fence_after();
+#pragma unroll 1
+                for (; odd; odd &= odd - 1) {
+                    const int j = __ffsll(static_cast<long long>(odd)) - 1;
+                    const int64_t slot = p.pages.slot(u.b, u.span.ctx + j);
+                    const uint8_t *k = static_cast<const uint8_t *>(p.k) + 2 * (slot * p.k_slot + h * p.k_head);
+                    const uint8_t *q = static_cast<const uint8_t *>(p.q) + 2 * (r * p.q_row + (h * p.group + gq) * p.q_head);
+                    const uint4 *v = reinterpret_cast<const uint4 *>(static_cast<const uint8_t *>(p.v) + 2 * (slot * p.v_slot + h * p.v_head));
+                    const bool sees = mine && ((tree >> j) & 1);
+                    const float pr = sees ? row_prob<BF16>(p, reinterpret_cast<const uint4 *>(q), reinterpret_cast<const uint4 *>(k), m) : 0.f;
+                    __syncwarp();
+#pragma unroll 1
+                    for (int c = 0; c < p.dim; c += 16) {
+                        uint32_t o[16];
+                        tmem_load16(t_o + c, o);
+                        tc_wait_ld();
+                        const uint4 x = fetch(v + c / 8), y = c + 8 < p.dim ? fetch(v + c / 8 + 1) : x;
+                        const uint32_t w[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
+#pragma unroll
+                        for (int d = 0; d < 8; ++d) {
+                            const float2 f = Half2<BF16>::up(w[d]);
+                            if (sees) {
+                                o[2 * d] = __float_as_uint(fmaf(pr, f.x, __uint_as_float(o[2 * d])));
+                                o[2 * d + 1] = __float_as_uint(fmaf(pr, f.y, __uint_as_float(o[2 * d + 1])));
+                            }
+                        }
+                        __syncwarp();
+                        tmem_store16(t_o + c, o);
+                        tc_wait_st();
+                    }
+                }
+            }
             const int pair = 1 + row0 / 32;   // barrier of the two warps that have these rows
             float f_own = 1.f, f_other = 0.f;   // SPLIT: factors of the two O
             if constexpr (SPLIT) {
@@ -481,8 +586,8 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                 const float2 other = sh.ml[1 - wg][row];
                 const float top = fmaxf(m, other.x);
                 // (an O without a job holds what an earlier unit left there)
-                f_own = m == -INFINITY ? 0.f : exp2_fast(m - top);
-                f_other = other.x == -INFINITY ? 0.f : exp2_fast(other.x - top);
+                f_own = l == 0.f ? 0.f : exp2_fast(m - top);   // (a NaN score leaves l NaN)
+                f_other = other.y == 0.f ? 0.f : exp2_fast(other.x - top);
                 l = l * f_own + other.y * f_other;
                 m = top;
             }
@@ -490,7 +595,7 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
             const bool whole = u.t0 == 0 && u.t1 == u.tiles;
             const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (u.t0 > 0 ? 0 : 1);
             const int32_t part_row = row_wg + row;
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             const int64_t q_at = r * p.q_heads + h * p.group + gq;
             auto put = [&](int c0, auto &o) {   // columns of the row, eight or more
                 constexpr int N = sizeof(o) / 4;
@@ -551,7 +656,7 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
             }
             if (mine && !(SPLIT && wg == 1)) {
                 if (!whole) p.part_ml[part * Sh::kRows + part_row] = make_float2(m, l);
-                else if (p.lse) p.lse[q_at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                else if (p.lse) p.lse[q_at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             }
         }
     }
@@ -599,15 +704,14 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
         float top = m;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);
-        if (top == -INFINITY) continue;
-        const float f = exp2_fast(m - top);
+        const float f = l == 0.f ? 0.f : exp2_fast(m - top);
         m = top;
         l *= f;
 #pragma unroll
         for (int d = 0; d < kCols; ++d) acc[d] *= f;
 #pragma unroll
         for (int k = 0; k < kBatch; ++k) {
-            if (ml[k].x == -INFINITY) continue;
+            if (ml[k].y == 0.f) continue;   // (a NaN score leaves it NaN)
             const float fk = exp2_fast(ml[k].x - top);
             l += ml[k].y * fk;
 #pragma unroll
@@ -616,14 +720,14 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
     }
     const int32_t t = (r0 + row) / p.group, gq = r0 + row - t * p.group;
     const int64_t q_at = (static_cast<int64_t>(b) * p.next_n + t) * p.q_heads + h * p.group + gq;
-    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
     for (int d = 0; d < kCols; d += 4) {
         if (col + d >= p.dim) break;
         *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) + 2 * (q_at * p.dim + col + d)) =
             make_uint2(Half2<BF16>::down(acc[d] * inv, acc[d + 1] * inv), Half2<BF16>::down(acc[d + 2] * inv, acc[d + 3] * inv));
     }
-    if (p.lse && col == 0) p.lse[q_at] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (p.lse && col == 0) p.lse[q_at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 int dim_class(int32_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
@@ -642,11 +746,15 @@ cudaError_t launch_shape(AttnParams p, uint8_t *ws, int sms, cudaStream_t stream
     p.unit_ends = reinterpret_cast<int32_t *>(ws + kWsHeaderBytes);
     p.part_ml = reinterpret_cast<float2 *>(ws + kWsHeaderBytes + unit_bytes(static_cast<int64_t>(p.requests) * p.next_n, p.q_heads));
     p.part_o = reinterpret_cast<float *>(p.part_ml + partial_rows(p.dim));
-    static std::atomic<uint64_t> allowed{0};
-    cudaError_t e = allow_smem(attention_kernel<BF16, DP, W, ROWS>, Sh::kSmem, allowed);
-    if (e != cudaSuccess) return e;
+    // (a single token is seen by all of its request's rows)
     const int grid = sms < kMaxGrid ? sms : kMaxGrid;
-    e = launch_pdl(attention_kernel<BF16, DP, W, ROWS>, dim3(static_cast<unsigned>(grid)), Sh::kThreads, Sh::kSmem, stream, 1, p);
+    auto launch = [&](auto kernel, std::atomic<uint64_t> &allowed) {
+        const cudaError_t e = allow_smem(kernel, Sh::kSmem, allowed);
+        return e != cudaSuccess ? e : launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), Sh::kThreads, Sh::kSmem, stream, 1, p);
+    };
+    static std::atomic<uint64_t> allowed[2];
+    const cudaError_t e = p.next_n > 1 ? launch(attention_kernel<BF16, DP, W, ROWS, true>, allowed[1])
+                                       : launch(attention_kernel<BF16, DP, W, ROWS, false>, allowed[0]);
     if (e != cudaSuccess) return e;
     const int64_t units = static_cast<int64_t>(p.requests) * p.request_units;
     // no unit spans blocks where none has more than one tile

@@ -127,7 +127,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(const _
         }
         __syncthreads();
     }
-    // the key t at the budget: keys above it are kept, and the first `ties`
+    // the key t at the budget: keys above it are kept, and the first `need`
     // equal to it (with `whole` every key of at least t)
     uint32_t t = 0;
     bool whole = false;

@@ -370,8 +370,16 @@ __global__ void __launch_bounds__(Shape<DP, NQ>::kThreads, 1) weights_kernel(con
 #pragma unroll
                             for (int c = 0; c < 16; ++c) {
                                 const int32_t k = (r0 + c0 + c) / a.group;
-                                if (j > 63 || r0 + c0 + c >= s.rows || !((sh.tree[k] >> j) & 1)) e[c] = INFINITY;
+                                if (j > 63 || r0 + c0 + c >= s.rows || !((sh.tree[k] >> j) & 1)) {
+                                    e[c] = INFINITY;
+                                    x[c] = 0;   // whatever the key holds
+                                }
                             }
+                        }
+                        if (c0 + 16 > rows) {   // rows of zeros behind the last: 0 x inf
+#pragma unroll
+                            for (int c = 0; c < 16; ++c)
+                                if (c0 + c >= rows) x[c] = 0;
                         }
                         float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
