@@ -16,8 +16,8 @@
 // list whatever the lengths are, and a unit (request, head, row tile) that
 // spans blocks leaves partial O, m, l in the workspace for combine_kernel.
 //
-// A block: W warpgroups of softmax (one row a thread), a warpgroup whose first
-// warp issues the matrix products and whose others look up the cache slots of
+// A block: W warpgroups of softmax (one row a thread), a warpgroup one warp of
+// which issues the matrix products and whose others look up the cache slots of
 // the tiles to come, a warpgroup that copies keys and values from those slots
 // (cp.async, 16 bytes a lane, any page size and stride) into a ring of tiles.
 // Copies run ahead of the products by the whole ring.
@@ -25,11 +25,11 @@
 // Bound by the cache's bytes up to some 100 rows a head, by the softmax and
 // the products' turn-taking above.  Measured on one GB300 (copy rate 6.78
 // TB/s, bf16 products 1884 TFLOP/s): 64 requests x 4 drafts over 1..8192
-// positions, 8 heads of 128, 163 us = 6.63 TB/s; 2 requests x 8 over 163840
-// positions in pages of one, 8 heads of 64, 135 us = 4.97 TB/s (128-byte rows
-// at random); 16 requests x 64 drafts, 512 rows a head, 103 us = 995 TFLOP/s;
+// positions, 8 heads of 128, 167 us = 6.44 TB/s; 2 requests x 8 over 163840
+// positions in pages of one, 8 heads of 64, 135 us = 4.96 TB/s (128-byte rows
+// at random); 16 requests x 64 drafts, 512 rows a head, 106 us = 961 TFLOP/s;
 // 64 rows x 2048 selected entries of two heads, 29 us = 4.5 TB/s; one request
-// of 1027 positions, 13 us.
+// of 1027 positions, 11.7 us.
 #include <cfloat>
 #include <cmath>
 
@@ -668,14 +668,25 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
 }
 
 // Joins the partial results of units that span blocks: blocks of 32 rows (a
-// lane each) and sixteen warps, each DP / 16 columns; grid (units, row
-// groups).  A batch of BATCH parts is loaded at once: more for few blocks,
-// where a batch's latency counts (one request of 1027 positions: 15.7 us a
-// call with 4, 14.1 with 8), fewer for many, where registers bound the blocks
-// an SM holds (16 wide trees: 102.9 us with 4, 107.1 with 8).
+// lane each) and sixteen warps, of COLS columns each, in GROUPS groups that
+// take batches of BATCH parts in turn and are joined in order at the end; grid
+// (units, row groups, column groups).  A batch is loaded at once: its latency
+// bounds a join of many parts, which few units have.  So the shapes with more
+// blocks and more parts in flight are taken as long as their blocks all run at
+// once, one an SM by their registers:
+//     four columns, four groups of sixteen parts (1 request x 4 drafts, 16
+//     heads over one of 128, 65536 positions, 152 parts: 20.1 us a call; one
+//     request of 1027 positions over eight heads, 9 tiles: 11.7);
+//     four columns, sixteen parts (34.4; 12.2. 1 request x 64 drafts, 32 heads
+//     over four, 8192 positions: 26.8);
+//     eight columns, eight parts at dimension 128 (44.7; 13.2; 29.0. 4 requests
+//     x 32 drafts, 32 heads over four, 8192 positions: 33.9, against 36.6 with
+//     the next);
+//     all columns, four parts otherwise (8 requests x 32 drafts, 16 heads over
+//     two of 256, 4096 positions: 39.7, with four and sixteen 44).
 constexpr int kCombineRows = 32, kCombineThreads = 512;
 
-template <bool BF16, int DP, int BATCH>
+template <bool BF16, int DP, int COLS, int BATCH, int GROUPS>
 __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_constant__ AttnParams p, int32_t unit_rows) {
     pdl_wait();
     pdl_release();
@@ -684,40 +695,69 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
     if (c0 == c1 || c0 < 0 || c1 < c0 || c1 >= kMaxGrid) return;   // whole, or not written by a block that gave up
     const int32_t b = static_cast<int32_t>(blockIdx.x / p.request_units), hm = static_cast<int32_t>(blockIdx.x % p.request_units);
     const int32_t h = hm / p.row_tiles, r0 = (hm - h * p.row_tiles) * unit_rows;
-    const int32_t row = static_cast<int32_t>(blockIdx.y) * kCombineRows + static_cast<int32_t>(threadIdx.x & 31);
-    if (row >= unit_rows || r0 + row >= p.next_n * p.group) return;
-    constexpr int kCols = DP / 16, kBatch = BATCH;
-    const int32_t col = static_cast<int32_t>(threadIdx.x >> 5) * kCols;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int32_t row = static_cast<int32_t>(blockIdx.y) * kCombineRows + lane;
+    const bool mine = row < unit_rows && r0 + row < p.next_n * p.group;
+    constexpr int kCols = COLS, kBatch = BATCH, kWarps = kCombineThreads / 32 / GROUPS;   // warps of a group
+    const int32_t col = static_cast<int32_t>(blockIdx.z * kWarps + warp % kWarps) * kCols;
     float m = -INFINITY, l = 0.f, acc[kCols] = {};
-    for (int32_t g0 = c0; g0 <= c1; g0 += kBatch) {
-        float2 ml[kBatch];
-        float o[kBatch][kCols];
-#pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            ml[k] = make_float2(-INFINITY, 0.f);
-            if (g0 + k > c1) continue;
-            const int64_t part = 2ll * (g0 + k) + (g0 + k == c0 ? 1 : 0);
-            ml[k] = p.part_ml[part * unit_rows + row];
-#pragma unroll
-            for (int d = 0; d < kCols; ++d) o[k][d] = p.part_o[(part * DP + col + d) * unit_rows + row];
-        }
+    // the parts (x: m, y: l) and o of a batch, joined to m, l, acc
+    auto join = [&](const float2 *ml, const float (*o)[kCols], int n) {
         float top = m;
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) top = fmaxf(top, ml[k].x);
+        for (int k = 0; k < n; ++k) top = fmaxf(top, ml[k].x);
         const float f = l == 0.f ? 0.f : exp2_fast(m - top);
         m = top;
         l *= f;
 #pragma unroll
         for (int d = 0; d < kCols; ++d) acc[d] *= f;
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
+        for (int k = 0; k < n; ++k) {
             if (ml[k].y == 0.f) continue;   // (a NaN score leaves it NaN)
             const float fk = exp2_fast(ml[k].x - top);
             l += ml[k].y * fk;
 #pragma unroll
             for (int d = 0; d < kCols; ++d) acc[d] += fk * o[k][d];
         }
+    };
+    if (mine) {
+        for (int32_t g0 = c0 + warp / kWarps * kBatch; g0 <= c1; g0 += GROUPS * kBatch) {
+            float2 ml[kBatch];
+            float o[kBatch][kCols];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                ml[k] = make_float2(-INFINITY, 0.f);
+                if (g0 + k > c1) continue;
+                const int64_t part = 2ll * (g0 + k) + (g0 + k == c0 ? 1 : 0);
+                ml[k] = p.part_ml[part * unit_rows + row];
+#pragma unroll
+                for (int d = 0; d < kCols; ++d) o[k][d] = p.part_o[(part * DP + col + d) * unit_rows + row];
+            }
+            join(ml, o, kBatch);
+        }
     }
+    if constexpr (GROUPS > 1) {   // the groups' results, in order
+        __shared__ float2 group_ml[GROUPS - 1][kWarps][32];
+        __shared__ float group_o[GROUPS - 1][kWarps][kCols][32];
+        const int g = warp / kWarps - 1, w = warp % kWarps;
+        if (g >= 0) {
+            group_ml[g][w][lane] = make_float2(m, l);
+#pragma unroll
+            for (int d = 0; d < kCols; ++d) group_o[g][w][d][lane] = acc[d];
+        }
+        __syncthreads();
+        if (g >= 0) return;
+        float2 ml[GROUPS - 1];
+        float o[GROUPS - 1][kCols];
+#pragma unroll
+        for (int k = 0; k < GROUPS - 1; ++k) {
+            ml[k] = group_ml[k][w][lane];
+#pragma unroll
+            for (int d = 0; d < kCols; ++d) o[k][d] = group_o[k][w][d][lane];
+        }
+        join(ml, o, GROUPS - 1);
+    }
+    if (!mine) return;
     const int32_t t = (r0 + row) / p.group, gq = r0 + row - t * p.group;
     const int64_t q_at = (static_cast<int64_t>(b) * p.next_n + t) * p.q_heads + h * p.group + gq;
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -761,10 +801,17 @@ cudaError_t launch_shape(AttnParams p, uint8_t *ws, int sms, cudaStream_t stream
     const int64_t longest = p.seq_lens ? p.pages.cols * p.pages.page.d : p.top_k;
     if (longest <= Sh::KT) return cudaSuccess;
     const int64_t each = rows < Sh::kRows ? rows : Sh::kRows;
-    const dim3 blocks(static_cast<unsigned>(units), static_cast<unsigned>((each + kCombineRows - 1) / kCombineRows));
-    const bool few = units * blocks.y <= sms && DP <= 128;
-    return few ? launch_pdl(combine_kernel<BF16, DP, DP <= 128 ? 8 : 4>, blocks, kCombineThreads, 0, stream, 1, p, Sh::kRows)
-               : launch_pdl(combine_kernel<BF16, DP, 4>, blocks, kCombineThreads, 0, stream, 1, p, Sh::kRows);
+    dim3 blocks(static_cast<unsigned>(units), static_cast<unsigned>((each + kCombineRows - 1) / kCombineRows));
+    blocks.z = DP / 16;
+    if (units * blocks.y * blocks.z <= sms)
+        return launch_pdl(combine_kernel<BF16, DP, 4, 16, 4>, blocks, kCombineThreads, 0, stream, 1, p, Sh::kRows);
+    blocks.z = DP / 64;
+    if (units * blocks.y * blocks.z <= sms)
+        return launch_pdl(combine_kernel<BF16, DP, 4, 16, 1>, blocks, kCombineThreads, 0, stream, 1, p, Sh::kRows);
+    blocks.z = 1;
+    if (DP == 128 && units * blocks.y <= sms)
+        return launch_pdl(combine_kernel<BF16, DP, DP / 16, DP == 128 ? 8 : 4, 1>, blocks, kCombineThreads, 0, stream, 1, p, Sh::kRows);
+    return launch_pdl(combine_kernel<BF16, DP, DP / 16, 4, 1>, blocks, kCombineThreads, 0, stream, 1, p, Sh::kRows);
 }
 
 // By the rows of a head: up to 32, up to 128 (both warpgroups on them), more
