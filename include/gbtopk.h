@@ -420,7 +420,7 @@ int gbtopk_cache_weights(const void *q, int dtype, int64_t num_rows, int64_t q_r
  *               positions, padded with -1.
  *  new_lens     device int32 [num_requests]: positions kept.
  *  out_weights  device fp32 like weights, not overlapping it: the kept
- *               positions' weights, zeros behind them.
+ *               positions' weights (-0 as +0), zeros behind them.
  */
 int gbtopk_cache_evict(const float *weights, int64_t num_requests, int32_t weight_heads,
                        int64_t width, const int32_t *seq_lens, int32_t next_n,

@@ -439,7 +439,7 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                         bits[c] = reinterpret_cast<volatile uint32_t *>(sh.mask[tile % kMaskRing])[c];
                         whole &= bits[c] == ~0u;
                     }
-                    if (i * KT + KT > u.span.ctx) {
+                    if (i * KT > u.span.ctx - KT) {   // (KT more could pass 31 bits)
                         whole = false;
 #pragma unroll
                         for (int c = 0; c < KT / 32; ++c) {
@@ -537,12 +537,12 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                 if (!ok) break;
                 continue;
             }
-            if (DRAFTS && ok && u.t1 * KT > u.span.ctx) {
+            if (DRAFTS && ok && (u.t1 - 1) * KT > u.span.ctx - KT) {
                 // Odd drafts of this warpgroup's tiles (they are in the last
                 // two), the same for the warp's rows: added where a row sees them.
                 uint64_t odd = 0;
                 for (uint32_t back = 1; back <= 2; ++back)
-                    if (u.t1 - u.t0 >= static_cast<int32_t>(back) && (u.t1 - static_cast<int32_t>(back) + 1) * KT > u.span.ctx &&
+                    if (u.t1 - u.t0 >= static_cast<int32_t>(back) && (u.t1 - static_cast<int32_t>(back)) * KT > u.span.ctx - KT &&
                         !(SPLIT && ((tile - back) & 1) != static_cast<uint32_t>(wg)))
                         odd |= reinterpret_cast<volatile uint64_t *>(sh.odd)[(tile - back) % kMaskRing];
                 if (odd != 0) tc_fence_after();

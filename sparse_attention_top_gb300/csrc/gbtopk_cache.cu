@@ -5,9 +5,10 @@
 // survivors in shared memory, three rounds of 11-bit radix histograms (summed
 // over the cluster through distributed shared memory) give the key at the
 // budget (8-bit rounds put all weights of one sign and a few binades into a
-// handful of bins, whose atomics serialised: 30 us for 17000 weights), and one ordered pass (warp segments, ballots) writes the kept
-// positions in place.  evict_move_kernel then copies the kept rows, blocks of
-// about 32 KB of keys and values.
+// handful of bins, whose atomics serialised: 30 us for 17000 weights), and one
+// ordered pass (warp segments, prefix sums) writes the kept positions in place.
+// evict_move_kernel then copies the kept rows, blocks of about 32 KB of keys
+// and values.
 //
 // The copies are bound by their bytes: 32 requests x 8 heads of 128, 4096 kept
 // positions each, 150 us = 7.1 TB/s read and written.  The selection of those
@@ -277,7 +278,7 @@ __global__ void __launch_bounds__(kSelectThreads, 2) evict_select_kernel(const _
                 const uint32_t at = gt + (before & 0xffff) + __popc(g & low) + (eb < need ? eb : need);
                 const int32_t q = pos(s0 + o + j);
                 kept[at] = q;
-                out_w[at] = p.staged ? key_weight(keys[o + j]) : w[q];
+                out_w[at] = key_weight(p.staged ? keys[o + j] : weight_key(w[q]));
             }
         }
         gt += all & 0xffff;

@@ -2,6 +2,8 @@
 // (gbtopk_verify_drafts).
 #include <cooperative_groups.h>
 
+#include <cfloat>
+
 #include "gbtopk_decode.cuh"
 #include "gbtopk_mma.cuh"
 
@@ -63,6 +65,10 @@ __device__ __forceinline__ float logit(const void *x, int64_t at) {
     if constexpr (DT == GBTOPK_BF16) return __bfloat162float(static_cast<const __nv_bfloat16 *>(x)[at]);
     return __half2float(static_cast<const __half *>(x)[at]);
 }
+
+// log2 e / temperature, neither 0 (its product with -infinity) nor infinite
+// (with 0) at the ends of the temperature's range.
+__device__ __forceinline__ float exponent_of(float t) { return fminf(fmaxf(kLog2e / t, FLT_MIN), FLT_MAX); }
 
 __device__ __forceinline__ void better(float &v, int32_t &i, float v2, int32_t i2) {
     if (v2 > v || (v2 == v && i2 < i)) {
@@ -199,7 +205,7 @@ __global__ void __launch_bounds__(kThreads) verify_stat_kernel(const __grid_cons
     const float t = p.temperature ? fetch(p.temperature + r / p.next_n) : 1.f;
     const int64_t e0 = piece * p.piece, e1 = e0 + p.piece < p.vocab ? e0 + p.piece : p.vocab;
     const RowStat st = block_stat<DT, 4>(static_cast<const uint8_t *>(p.logits) + r * p.row_stride * (DT == GBTOPK_F32 ? 4 : 2), e0, e1,
-                                      t <= 0.f, t <= 0.f ? 0.f : kLog2e / t, sh);
+                                      t <= 0.f, t <= 0.f ? 0.f : exponent_of(t), sh);
     if (threadIdx.x == 0) p.stats[r * p.pieces + piece] = st;
 }
 
@@ -230,7 +236,7 @@ __global__ void __launch_bounds__(kThreads, 4) verify_path_kernel(const __grid_c
     pdl_release();
     const float t = p.temperature ? fetch(p.temperature + i) : 1.f;
     const bool greedy = t <= 0.f;
-    const float c = greedy ? 0.f : kLog2e / t;
+    const float c = greedy ? 0.f : exponent_of(t);
     const int32_t part = static_cast<int32_t>((p.vocab + kCluster - 1) / kCluster);
     const int32_t v0 = rank * part < p.vocab ? rank * part : static_cast<int32_t>(p.vocab);
     const int32_t v1 = v0 + part < p.vocab ? v0 + part : static_cast<int32_t>(p.vocab);

@@ -283,7 +283,7 @@ __global__ void __launch_bounds__(Shape<DP, NQ>::kThreads, 1) weights_kernel(con
             uint32_t job = 0;
             while (ok && spans.next(&s)) {
                 uint64_t seen = ~0ull;   // drafted tokens that an accepted row sees
-                if (a.tree_mask && s.t1 * KT > s.ctx) {
+                if (a.tree_mask && (s.t1 - 1) * KT > s.ctx - KT) {   // (KT more could pass 31 bits)
                     seen = 0;
                     for (int j = lane; j < a.next_n; j += 32)
                         if ((s.took >> j) & 1) seen |= static_cast<uint64_t>(fetch(a.tree_mask + static_cast<int64_t>(s.b) * a.next_n + j));
@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(Shape<DP, NQ>::kThreads, 1) weights_kernel(con
                 if (i * 256 + static_cast<int>(threadIdx.x) < (s.t1 - s.t0) * KT && pos < s.n && pos < p.width) held[i] = w[pos];
             }
             // trees of the accepted tokens, where the span reaches the drafts
-            const bool drafts = s.t1 * KT > s.ctx;
+            const bool drafts = (s.t1 - 1) * KT > s.ctx - KT;
             if (drafts) {
                 sums_barrier_or(false);
                 const int k = threadIdx.x;
@@ -366,7 +366,7 @@ __global__ void __launch_bounds__(Shape<DP, NQ>::kThreads, 1) weights_kernel(con
 #pragma unroll
                         for (int c = 0; c < 16; c += 4) *reinterpret_cast<float4 *>(e + c) = *reinterpret_cast<const float4 *>(lse2 + c0 + c);
                         tc_wait_ld();
-                        if (t * KT + KT > s.ctx && j >= 0) {
+                        if (t * KT > s.ctx - KT && j >= 0) {
 #pragma unroll
                             for (int c = 0; c < 16; ++c) {
                                 const int32_t k = (r0 + c0 + c) / a.group;
