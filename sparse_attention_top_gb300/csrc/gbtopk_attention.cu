@@ -5,12 +5,14 @@
 // group - are the rows of one matrix tile, so each cached key and value is
 // read once for all of them.  Per tile of KT cached positions:
 //     S = Q K^T (tensor core, 32-bit accumulator in tensor memory),
-//     P = 2^(c S - m), the running maximum m and sum l in registers,
+//     P = 2^(c S - m), the reference m (about the running maximum) and the
+//         sum l in registers,
 //     O += P V (P from tensor memory, O stays there),
-// O being rescaled only when m rises by more than 8 (base 2): P then stays
-// below 2^8, which both 16-bit types hold.  P is rounded to the inputs' type
-// for the product (its error is that of one rounding of the output, and the
-// sum l is of the unrounded values); S, m, l and O are 32 bits.  The work of a
+// O being rescaled only when a tile's maximum rises more than 8 (base 2) over
+// m: P then stays below 2^8, in fp16 kernels below 2^15 (see kLift), which the
+// type holds.  P is rounded to the inputs' type for the product (each
+// probability is off by up to 2^-8 of itself in bf16 and 2^-11 in fp16, as the
+// output is by its own rounding; the sum l is of the unrounded values); S, m, l and O are 32 bits.  The work of a
 // call is the list of all (request, kv head, row tile, position tile); block
 // c of a grid of one block per SM takes the c-th share of equal cost of that
 // list whatever the lengths are, and a unit (request, head, row tile) that
@@ -40,7 +42,36 @@ namespace {
 
 constexpr int kMaxGrid = 160;       // blocks of the attention kernel (workspace bound)
 constexpr int kMaskRing = 8;        // tiles whose slots and validity bits are looked up ahead
-constexpr float kRescale = 8.f;     // rise of the running maximum (base 2) that rescales O
+constexpr float kRescale = 8.f;     // rise of a tile's maximum over the reference m (base 2) that rescales O
+
+// fp16 holds 2^-14 .. 2^15 with all its digits and nothing below 2^-25, so
+// with m the maximum a key 17 nats above the others (an attention sink) left
+// nothing of their P.  There the reference is 2^7 below a tile's maximum (P is
+// at most 2^15 before O is rescaled), and it also falls, by a whole power of
+// two that scales O and l up, where a tile's maximum is more than 2^8 below
+// the one that set it: every tile's P then reaches 2^-1 or more, and what its
+// elements below 2^-14 lose is 2^-24 of the tile's largest each.  l stays at or
+// below 2^80 (O below 2^127 for any values and lengths); what lies further down
+// than that is below the smallest fp16 output.  bf16 has the range of the sums.
+template <bool BF16>
+constexpr float kLift = BF16 ? 0.f : 7.f;
+constexpr float kMostSum = 0x1p80f;
+
+// 2^x of a whole number, exactly (0 below 2^-126).
+__device__ __forceinline__ float exp2_whole(float x) {
+    return __int_as_float((static_cast<int>(fminf(fmaxf(x, -127.f), 128.f)) + 127) << 23);
+}
+
+// Log-sum-exp of a row from its reference and sum.  fp16's may be a high sum
+// over a low reference, both powers of two apart from the digits of the sum.
+template <bool BF16>
+__device__ __forceinline__ float row_lse(float m, float l) {
+    if (l == 0.f) return -INFINITY;
+    if constexpr (BF16) return (m + log2f(l)) * kLn2;
+    int e;
+    const float digits = frexpf(l, &e);
+    return (m + static_cast<float>(e) + log2f(digits)) * kLn2;
+}
 
 // DP: head dimension rounded up to 64, 128 or 256.  W: softmax warpgroups.
 // ROWS: query rows of a unit.  With two warpgroups and up to 128 rows both
@@ -471,12 +502,23 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                     load_half(0);
                     max_half();
                     const float best = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * p.c;
-                    const bool rise = best > m + kRescale;   // also from -inf
-                    if (__any_sync(~0u, rise)) {
-                        const float f = rise && l > 0.f ? exp2_fast(m - best) : 1.f;
-                        if (rise) {
-                            l *= f;
-                            m = best;
+                    bool move = best > m + (kRescale + kLift<BF16>);   // also from -inf
+                    if constexpr (!BF16) move |= best < m + (kLift<BF16> - kRescale) && best >= -FLT_MAX;
+                    if (__any_sync(~0u, move)) {
+                        float f = 1.f;
+                        if constexpr (BF16) {
+                            if (move) {
+                                f = l > 0.f ? exp2_fast(m - best) : 1.f;
+                                l *= f;
+                                m = best;
+                            }
+                        } else if (move) {
+                            const float to = rintf(best) - kLift<BF16>, g = l > 0.f ? exp2_whole(m - to) : 1.f;
+                            if (g <= 1.f || l * g <= kMostSum) {
+                                f = g;
+                                l *= f;
+                                m = to;
+                            }
                         }
                         if (__any_sync(~0u, f != 1.f)) {
                             // O is complete up to the row's last job
@@ -656,7 +698,7 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
             }
             if (mine && !(SPLIT && wg == 1)) {
                 if (!whole) p.part_ml[part * Sh::kRows + part_row] = make_float2(m, l);
-                else if (p.lse) p.lse[q_at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+                else if (p.lse) p.lse[q_at] = row_lse<BF16>(m, l);
             }
         }
     }
@@ -767,7 +809,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
         *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(p.out) + 2 * (q_at * p.dim + col + d)) =
             make_uint2(Half2<BF16>::down(acc[d] * inv, acc[d + 1] * inv), Half2<BF16>::down(acc[d + 2] * inv, acc[d + 3] * inv));
     }
-    if (p.lse && col == 0) p.lse[q_at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    if (p.lse && col == 0) p.lse[q_at] = row_lse<BF16>(m, l);
 }
 
 int dim_class(int32_t dim) { return dim <= 64 ? 64 : dim <= 128 ? 128 : 256; }
