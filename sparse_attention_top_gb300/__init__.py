@@ -236,8 +236,14 @@ def gbtopk_page_table_transform_cu_seqlens(scores: torch.Tensor, lengths: torch.
 # One workspace per (device, stream), grown on demand.  Apart from its
 # status word the library writes every workspace byte before reading it, so
 # one workspace serves every call on a stream.  Create it (by one eager
-# call) before capturing a CUDA graph on that stream.
+# call) before capturing a CUDA graph on that stream.  A captured graph keeps
+# the addresses it was captured with, so an outgrown workspace is never freed;
+# each is at least twice the one before, so those kept are together smaller
+# than the one in use.  Graphs captured on one stream share its workspace with
+# each other and with that stream's own calls: none of them may overlap
+# (a caller's own `workspace` lifts that).
 _WS = {}
+_OUTGROWN = []
 
 
 def _workspace(device: torch.device, nbytes: int) -> torch.Tensor:
@@ -247,7 +253,11 @@ def _workspace(device: torch.device, nbytes: int) -> torch.Tensor:
         if torch.cuda.is_current_stream_capturing():
             raise RuntimeError("gbtopk: no workspace for this stream yet; run one eager call "
                                "on the capturing stream before graph capture")
-        ws = torch.zeros(max(nbytes, 256), dtype=torch.uint8, device=device)
+        size = max(nbytes, 256)
+        if ws is not None:
+            _OUTGROWN.append(ws)
+            size = max(size, 2 * ws.numel())
+        ws = torch.zeros(size, dtype=torch.uint8, device=device)
         _WS[key] = ws
     return ws
 
