@@ -125,8 +125,15 @@ def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
 
 
+try:   # the handle alone, without a Stream object
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
+
 def _stream_handle(device: torch.device):
-    return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(device.index)
 
 
 def gbtopk_workspace_bytes(num_rows: int, width: int, top_k: int, dtype: torch.dtype) -> int:
@@ -262,6 +269,22 @@ def _workspace(device: torch.device, nbytes: int) -> torch.Tensor:
     return ws
 
 
+# A call's kernels hand partial results to one another in the workspace, so
+# from its look-up to the last launch no other host thread may enqueue a call
+# on the stream (the C calls run without the interpreter's lock).
+class _Locks(dict):
+    def __missing__(self, key):
+        return self.setdefault(key, threading.RLock())
+
+
+_LOCKS = _Locks()
+
+
+def _turn(device: torch.device):
+    """The lock of the device's current stream."""
+    return _LOCKS[device.index, _stream_handle(device)]
+
+
 def _require_cuda(t: torch.Tensor, name: str):
     if not isinstance(t, torch.Tensor) or t.device.type != "cuda":
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
@@ -320,10 +343,11 @@ def top_k_varlen(logits: torch.Tensor, seq_lens: torch.Tensor, top_k: int,
         else:
             warnings.warn("pre_idx is malformed and was discarded; running hint-free",
                           RuntimeWarning, stacklevel=2)
-    ws = workspace if workspace is not None else _workspace(
-        logits.device, gbtopk_workspace_bytes(R, W, top_k, logits.dtype))
-    st = gbtopk_varlen(logits, seq_lens, top_k, hint, next_n, compress_ratio, idx, val,
-                       flags, ws)
+    with _turn(logits.device):
+        ws = workspace if workspace is not None else _workspace(
+            logits.device, gbtopk_workspace_bytes(R, W, top_k, logits.dtype))
+        st = gbtopk_varlen(logits, seq_lens, top_k, hint, next_n, compress_ratio, idx, val,
+                           flags, ws)
     if st == HINT_DISCARDED:
         warnings.warn("pre_idx is not 16-byte aligned and was discarded; running hint-free",
                       RuntimeWarning, stacklevel=2)
@@ -366,10 +390,11 @@ def top_k_page_table_transform(scores: torch.Tensor, lengths: torch.Tensor,
     raw = None
     if out_raw_indices is not None:
         raw = _out_view(out_raw_indices, R, top_k, torch.int32, scores.device, "out_raw_indices")
-    ws = workspace if workspace is not None else _workspace(
-        scores.device, gbtopk_workspace_bytes(R, W, top_k, scores.dtype))
-    gbtopk_page_table_transform(scores, lengths, row_starts, page_table, page_table_row_starts,
-                                page_size, top_k, o, raw, flags, ws)
+    with _turn(scores.device):
+        ws = workspace if workspace is not None else _workspace(
+            scores.device, gbtopk_workspace_bytes(R, W, top_k, scores.dtype))
+        gbtopk_page_table_transform(scores, lengths, row_starts, page_table, page_table_row_starts,
+                                    page_size, top_k, o, raw, flags, ws)
     return (o, raw) if raw is not None else o
 
 
@@ -401,10 +426,11 @@ def top_k_ragged_transform(scores: torch.Tensor, lengths: torch.Tensor,
             or not topk_indices_offset.is_contiguous()):
         raise ValueError("topk_indices_offset must be a contiguous int32 tensor of num_rows")
     o = _out_view(out, R, top_k, torch.int32, scores.device, "out")
-    ws = workspace if workspace is not None else _workspace(
-        scores.device, gbtopk_workspace_bytes(R, W, top_k, scores.dtype))
-    gbtopk_ragged_transform(scores, lengths, row_starts, topk_indices_offset, top_k, o,
-                            flags, ws)
+    with _turn(scores.device):
+        ws = workspace if workspace is not None else _workspace(
+            scores.device, gbtopk_workspace_bytes(R, W, top_k, scores.dtype))
+        gbtopk_ragged_transform(scores, lengths, row_starts, topk_indices_offset, top_k, o,
+                                flags, ws)
     return o
 
 
@@ -429,10 +455,11 @@ def top_k_page_table_transform_cu_seqlens(scores: torch.Tensor, lengths: torch.T
             or cu_seqlens_q.numel() != page_table.shape[0] + 1 or not cu_seqlens_q.is_contiguous()):
         raise ValueError("cu_seqlens_q must be a contiguous int32 tensor of num_reqs + 1")
     o = _out_view(out, R, top_k, torch.int32, scores.device, "out")
-    ws = workspace if workspace is not None else _workspace(
-        scores.device, gbtopk_workspace_bytes(R, W, top_k, scores.dtype))
-    gbtopk_page_table_transform_cu_seqlens(scores, lengths, row_starts, page_table, cu_seqlens_q,
-                                           top_k, o, flags, ws)
+    with _turn(scores.device):
+        ws = workspace if workspace is not None else _workspace(
+            scores.device, gbtopk_workspace_bytes(R, W, top_k, scores.dtype))
+        gbtopk_page_table_transform_cu_seqlens(scores, lengths, row_starts, page_table, cu_seqlens_q,
+                                               top_k, o, flags, ws)
     return o
 
 

@@ -143,18 +143,13 @@ def _outputs(q, shape, dev, out, lse, return_lse: bool):
     return out, lse
 
 
-try:   # the handle alone, without a Stream object
-    _raw_stream = torch._C._cuda_getCurrentRawStream
-except AttributeError:
-    def _raw_stream(index):
-        return torch.cuda.current_stream(index).cuda_stream
-
 _attention_bytes = functools.lru_cache(maxsize=None)(gbtopk_attention_workspace_bytes)
 _verify_bytes = functools.lru_cache(maxsize=None)(gbtopk_verify_workspace_bytes)
 
 
 def _scratch(workspace, dev, stream, nbytes: int):
-    """Address and size of the caller's workspace, or of the stream's."""
+    """Address and size of the caller's workspace, or of the stream's (under
+    the stream's lock)."""
     if workspace is None:
         workspace = _gb._WS.get((dev.index, stream))
         if workspace is None or workspace.numel() < nbytes:
@@ -194,14 +189,15 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
                 (False, "tree_mask must be contiguous int64 [num_rows]"))
     out, lse = _outputs(q, shape, dev, out, lse, return_lse)
     lib = _calls or _lib()
-    stream = _raw_stream(dev.index)
-    ws, ws_bytes = _scratch(workspace, dev, stream, _attention_bytes(rows, heads, kv, dim))
-    status = lib.gbtopk_tree_attention(
-        q.data_ptr(), _gb._DTYPES[q.dtype], rows, qs[0], qs[1], heads, kv, dim, k_cache.data_ptr(), ks[0], ks[1],
-        v_cache.data_ptr(), vs[0], vs[1], slots, page_table.data_ptr(), page_table.shape[1], page_table.stride(0),
-        page_size, seq_lens.data_ptr(), next_n, None if tree_mask is None else tree_mask.data_ptr(),
-        dim ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(), ws, ws_bytes,
-        stream)
+    stream = _gb._stream_handle(dev)
+    with _gb._LOCKS[dev.index, stream]:
+        ws, ws_bytes = _scratch(workspace, dev, stream, _attention_bytes(rows, heads, kv, dim))
+        status = lib.gbtopk_tree_attention(
+            q.data_ptr(), _gb._DTYPES[q.dtype], rows, qs[0], qs[1], heads, kv, dim, k_cache.data_ptr(), ks[0], ks[1],
+            v_cache.data_ptr(), vs[0], vs[1], slots, page_table.data_ptr(), page_table.shape[1], page_table.stride(0),
+            page_size, seq_lens.data_ptr(), next_n, None if tree_mask is None else tree_mask.data_ptr(),
+            dim ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(), ws,
+            ws_bytes, stream)
     if status < 0:
         _gb._check(status)
     return out if lse is None else (out, lse)
@@ -225,13 +221,14 @@ def selected_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Te
                 (False, "indices must be int32 [num_rows, top_k], inner stride 1"))
     out, lse = _outputs(q, shape, dev, out, lse, return_lse)
     lib = _calls or _lib()
-    stream = _raw_stream(dev.index)
-    ws, ws_bytes = _scratch(workspace, dev, stream, _attention_bytes(rows, heads, kv, dim))
-    status = lib.gbtopk_selected_attention(
-        q.data_ptr(), _gb._DTYPES[q.dtype], rows, qs[0], qs[1], heads, kv, dim, k_cache.data_ptr(), ks[0], ks[1],
-        v_cache.data_ptr(), vs[0], vs[1], slots, indices.data_ptr(), indices.shape[1], indices.stride(0),
-        dim ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(), ws, ws_bytes,
-        stream)
+    stream = _gb._stream_handle(dev)
+    with _gb._LOCKS[dev.index, stream]:
+        ws, ws_bytes = _scratch(workspace, dev, stream, _attention_bytes(rows, heads, kv, dim))
+        status = lib.gbtopk_selected_attention(
+            q.data_ptr(), _gb._DTYPES[q.dtype], rows, qs[0], qs[1], heads, kv, dim, k_cache.data_ptr(), ks[0], ks[1],
+            v_cache.data_ptr(), vs[0], vs[1], slots, indices.data_ptr(), indices.shape[1], indices.stride(0),
+            dim ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(), ws,
+            ws_bytes, stream)
     if status < 0:
         _gb._check(status)
     return out if lse is None else (out, lse)
@@ -265,14 +262,15 @@ def accumulate_cache_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.
                 (_maybe(tree_mask, dev, _I64, (rows,)), "tree_mask must be contiguous int64 [num_rows]"),
                 (False, "accept_mask must be contiguous int64 [num_requests]"))
     lib = _calls or _lib()
-    stream = _raw_stream(dev.index)
-    ws, ws_bytes = _scratch(workspace, dev, stream, _attention_bytes(rows, heads, kv, dim))
-    status = lib.gbtopk_cache_weights(
-        q.data_ptr(), _gb._DTYPES[q.dtype], rows, qs[0], qs[1], heads, kv, dim, k_cache.data_ptr(), ks[0], ks[1], slots,
-        lse.data_ptr(), page_table.data_ptr(), page_table.shape[1], page_table.stride(0), page_size, seq_lens.data_ptr(),
-        next_n, None if tree_mask is None else tree_mask.data_ptr(),
-        None if accept_mask is None else accept_mask.data_ptr(), dim ** -0.5 if scale is None else scale,
-        weights.data_ptr(), wshape[1], wshape[2], ws, ws_bytes, stream)
+    stream = _gb._stream_handle(dev)
+    with _gb._LOCKS[dev.index, stream]:
+        ws, ws_bytes = _scratch(workspace, dev, stream, _attention_bytes(rows, heads, kv, dim))
+        status = lib.gbtopk_cache_weights(
+            q.data_ptr(), _gb._DTYPES[q.dtype], rows, qs[0], qs[1], heads, kv, dim, k_cache.data_ptr(), ks[0], ks[1], slots,
+            lse.data_ptr(), page_table.data_ptr(), page_table.shape[1], page_table.stride(0), page_size,
+            seq_lens.data_ptr(), next_n, None if tree_mask is None else tree_mask.data_ptr(),
+            None if accept_mask is None else accept_mask.data_ptr(), dim ** -0.5 if scale is None else scale,
+            weights.data_ptr(), wshape[1], wshape[2], ws, ws_bytes, stream)
     if status < 0:
         _gb._check(status)
     return weights
@@ -335,7 +333,7 @@ def evict_cache(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
         v_cache.data_ptr(), vs[0], vs[1], slots, kv, dim, k_cache.element_size(), page_table.data_ptr(),
         page_table.shape[1], page_table.stride(0), out_page_table.data_ptr(), out_page_table.shape[1],
         out_page_table.stride(0), page_size, kept.data_ptr(), new_lens.data_ptr(), out_weights.data_ptr(),
-        _raw_stream(dev.index))
+        _gb._stream_handle(dev))
     if status < 0:
         _gb._check(status)
     return Evicted(kept, new_lens, out_weights)
@@ -386,13 +384,15 @@ def verify_drafts(logits: torch.Tensor, tokens: torch.Tensor, uniforms: torch.Te
     next_token = torch.empty((requests,), dtype=_I32, device=dev)
     accept_mask = torch.empty((requests,), dtype=_I64, device=dev)
     lib = _calls or _lib()
-    stream = _raw_stream(dev.index)
-    ws, ws_bytes = _scratch(workspace, dev, stream, _verify_bytes(rows, vocab, next_n))
-    status = lib.gbtopk_verify_drafts(
-        logits.data_ptr(), _gb._DTYPES[logits.dtype], rows, vocab, logits.stride(0), tokens.data_ptr(),
-        uniforms.data_ptr(), noise.data_ptr(), next_n, None if tree_mask is None else tree_mask.data_ptr(),
-        None if temperature is None else temperature.data_ptr(), None if draft_probs is None else draft_probs.data_ptr(),
-        accepted.data_ptr(), path.data_ptr(), next_token.data_ptr(), accept_mask.data_ptr(), ws, ws_bytes, stream)
+    stream = _gb._stream_handle(dev)
+    with _gb._LOCKS[dev.index, stream]:
+        ws, ws_bytes = _scratch(workspace, dev, stream, _verify_bytes(rows, vocab, next_n))
+        status = lib.gbtopk_verify_drafts(
+            logits.data_ptr(), _gb._DTYPES[logits.dtype], rows, vocab, logits.stride(0), tokens.data_ptr(),
+            uniforms.data_ptr(), noise.data_ptr(), next_n, None if tree_mask is None else tree_mask.data_ptr(),
+            None if temperature is None else temperature.data_ptr(),
+            None if draft_probs is None else draft_probs.data_ptr(),
+            accepted.data_ptr(), path.data_ptr(), next_token.data_ptr(), accept_mask.data_ptr(), ws, ws_bytes, stream)
     if status < 0:
         _gb._check(status)
     return Verified(accepted, path, next_token, accept_mask)

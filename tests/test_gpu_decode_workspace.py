@@ -1,5 +1,7 @@
 """The workspaces that the Python calls keep, on the GPU (see also
 test_workspace_host)."""
+import threading
+
 import pytest
 import torch
 
@@ -42,3 +44,35 @@ def test_a_captured_call_outlives_its_workspace(dev):
     torch.cuda.synchronize(dev)
     assert all(torch.equal(x, y) for x, y in zip(got, want))
     assert all(bool((x == 85).all()) for x in new)
+
+
+def test_two_host_threads_on_one_stream(dev):
+    """Calls whose parts are joined by a second kernel, from two threads, one
+    with batches that grow: every output is the same call's alone, to the bit."""
+    batches = [[make(dev, [9000 + 50 * i], 2, 8, 1, 128, 16, BF, i) for i in range(3)],
+               [make(dev, [5000] * (i + 1), 4, 16, 2, 128, 16, BF, 10 + i) for i in range(6)]]
+    tokens = [2, 4]
+
+    def call(which, a):
+        return gb.tree_attention(*a, page_size=16, next_n=tokens[which], return_lse=True)
+    want = [[[x.clone() for x in call(w, a)] for a in b] for w, b in enumerate(batches)]
+    torch.cuda.synchronize(dev)
+    gb._WS.pop((dev.index, gb._stream_handle(dev)))     # start from a small one again
+    wrong, failed = [], []
+
+    def job(which):
+        try:
+            torch.cuda.set_device(dev)
+            for turn in range(40):
+                got = [call(which, a) for a in batches[which]]
+                torch.cuda.synchronize(dev)
+                wrong.extend((which, turn, i) for i, (g, w) in enumerate(zip(got, want[which]))
+                             if not all(torch.equal(x, y) for x, y in zip(g, w)))
+        except BaseException as e:      # noqa: B902
+            failed.append(e)
+    threads = [threading.Thread(target=job, args=(w,)) for w in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(120)
+    assert not failed and not wrong, (failed, wrong[:5])

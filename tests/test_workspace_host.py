@@ -52,3 +52,134 @@ def test_a_capture_needs_a_workspace_that_is_there(made, monkeypatch):
     monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
     with pytest.raises(RuntimeError):
         gb._workspace(GPU, 1000)
+
+
+# ------------------------------------------------------ two host threads
+
+BF, I32, I64 = torch.bfloat16, torch.int32, torch.int64
+
+
+class Library:
+    """Stands in for the C calls: `hold(name, address)` runs inside each."""
+
+    def __init__(self, hold):
+        self.hold = hold
+
+    def __getattr__(self, name):
+        def call(*args):
+            self.hold(name, args[-3])     # workspace, its bytes, stream
+            return 0
+        return call
+
+
+def attention(rows):
+    q, cache = fake(rows, 4, 64, dtype=BF), fake(32, 2, 64, dtype=BF)
+    return q, cache, fake(rows, 1, dtype=I32), fake(rows, dtype=I32), fake(rows, 4)
+
+
+def tree(rows):
+    q, cache, table, lens, lse = attention(rows)
+    gb.tree_attention(q, cache, cache, table, lens, page_size=32, out=fake(rows, 4, 64, dtype=BF), lse=lse)
+
+
+def selected(rows):
+    q, cache, table, _, lse = attention(rows)
+    gb.selected_attention(q, cache, cache, table, out=fake(rows, 4, 64, dtype=BF), lse=lse)
+
+
+def weights(rows):
+    q, cache, table, lens, lse = attention(rows)
+    gb.accumulate_cache_weights(q, cache, lse, table, lens, fake(rows, 2, 32), page_size=32)
+
+
+def verify(rows):
+    gb.verify_drafts(fake(rows, 9), fake(rows, dtype=I32), fake(rows), fake(rows, 9))
+
+
+def top_k(rows):
+    gb.top_k_varlen(fake(rows, 40), fake(rows, dtype=I32), 4, out_indices=fake(rows, 4, dtype=I32))
+
+
+def pages(rows):
+    gb.top_k_page_table_transform(fake(rows, 40), fake(rows, dtype=I32), fake(rows, 40, dtype=I32), 4,
+                                  out=fake(rows, 4, dtype=I32))
+
+
+CALLS = [tree, selected, weights, verify, top_k, pages]
+
+
+@pytest.fixture
+def library(made, monkeypatch):
+    """install(hold): the C calls are hold's, the workspaces grow with the rows."""
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: empty(*a, **k))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    for at, name in ((gb.decode, "_attention_bytes"), (gb.decode, "_verify_bytes"), (gb, "gbtopk_workspace_bytes")):
+        monkeypatch.setattr(at, name, lambda rows, *a: 1000 * rows)
+
+    def install(hold):
+        lib = Library(hold)
+        monkeypatch.setattr(gb.decode, "_calls", lib)
+        monkeypatch.setattr(gb, "load_library", lambda: lib)
+    return install
+
+
+def run(*jobs):
+    failed = []
+
+    def go(job):
+        try:
+            job()
+        except BaseException as e:      # noqa: B902
+            failed.append(e)
+    threads = [threading.Thread(target=go, args=(j,)) for j in jobs]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join(60)
+    assert not failed, failed
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_workspace_is_one_calls_until_it_is_enqueued(library, made, call):
+    """Two threads on one stream, one of them with growing calls: the tensor
+    stays and no other call comes between, while the first is in the library."""
+    inside, gate, seen = [], threading.Event(), []
+
+    def hold(name, address):
+        inside.append(address)
+        seen.append((len(inside), made[address]() is not None))
+        gate.wait(0.1 if len(seen) < 3 else 0.001)     # long enough for the other thread to come in
+        seen.append((len(inside), made[address]() is not None))
+        inside.remove(address)
+    library(hold)
+    run(lambda: [call(1) for _ in range(4)], lambda: [call(n) for n in (2, 20, 200)])
+    assert len(seen) == 14 and all(s == (1, True) for s in seen), seen
+
+
+def test_calls_on_two_streams_do_not_wait_for_one_another(library, made, monkeypatch):
+    stream = threading.local()
+    monkeypatch.setattr(gb, "_stream_handle", lambda device: stream.handle)
+    both = threading.Barrier(2)
+    library(lambda name, address: both.wait(30))
+
+    def job(handle):
+        stream.handle = handle
+        tree(1)
+    run(lambda: job(3), lambda: job(4))
+
+
+def test_a_call_that_fails_gives_its_workspace_back(library, made, monkeypatch):
+    library(lambda name, address: None)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: True)
+    with pytest.raises(RuntimeError):
+        tree(1)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+
+    def fails(name, address):
+        raise OSError
+    library(fails)
+    with pytest.raises(OSError):
+        tree(1)
+    library(lambda name, address: None)
+    run(lambda: tree(1))
