@@ -3,7 +3,8 @@
 Thin ctypes binding over the C ABI of ``libgbtopk.so`` (``include/gbtopk.h``).
 PyTorch is used only for device memory, streams and pointers: every step of
 the selection runs in the library's CUDA kernels.  There is no CPU path; if
-the library has not been built the calls raise ``RuntimeError``.
+the library has not been built the calls raise ``RuntimeError``.  A call's tensors
+have to be on the current device (``ValueError`` otherwise).
 
 Low-level entry points keep the C names (``gbtopk_varlen``,
 ``gbtopk_page_table_transform``, ``gbtopk_workspace_bytes``,
@@ -131,9 +132,22 @@ except AttributeError:
     def _raw_stream(index):
         return torch.cuda.current_stream(index).cuda_stream
 
+# (with a tensor on a GPU there is nothing left to initialise)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
 
 def _stream_handle(device: torch.device):
+    """The current stream of ``device``, which has to be the current device:
+    the library launches there, and the default stream's handle names no device."""
+    if device.index != _current_device():
+        raise ValueError(f"the tensors are on {device}, but the current device is "
+                         f"cuda:{_current_device()}; call under torch.cuda.device({device.index})")
     return _raw_stream(device.index)
+
+
+def _launch_stream(device: torch.device, stream):
+    current = _stream_handle(device)
+    return current if stream is None else stream
 
 
 def gbtopk_workspace_bytes(num_rows: int, width: int, top_k: int, dtype: torch.dtype) -> int:
@@ -167,7 +181,7 @@ def gbtopk_varlen(logits: torch.Tensor, seq_lens: torch.Tensor, top_k: int,
     """Direct call of the C entry point on tensors (no checks beyond the library's)."""
     R, W = logits.shape
     stride = logits.stride(0) if R > 1 else W
-    s = _stream_handle(logits.device) if stream is None else stream
+    s = _launch_stream(logits.device, stream)
     return _check(load_library().gbtopk_varlen(
         _ptr(logits), _DTYPES[logits.dtype], R, W, stride, _ptr(seq_lens), next_n,
         compress_ratio, top_k, _ptr(pre_idx), _ptr(out_indices), _ptr(out_values),
@@ -183,7 +197,7 @@ def gbtopk_varlen_static_ws(logits: torch.Tensor, seq_lens: torch.Tensor, top_k:
     per GPU, shared by every call: serialise calls that could overlap)."""
     R, W = logits.shape
     stride = logits.stride(0) if R > 1 else W
-    s = _stream_handle(logits.device) if stream is None else stream
+    s = _launch_stream(logits.device, stream)
     return _check(load_library().gbtopk_varlen_static_ws(
         _ptr(logits), _DTYPES[logits.dtype], R, W, stride, _ptr(seq_lens), next_n,
         compress_ratio, top_k, _ptr(pre_idx), _ptr(out_indices), _ptr(out_values),
@@ -200,7 +214,7 @@ def gbtopk_page_table_transform(scores: torch.Tensor, lengths: torch.Tensor,
     stride = scores.stride(0) if R > 1 else W
     P = page_table.shape[1]
     pstride = page_table.stride(0) if page_table.shape[0] > 1 else P
-    s = _stream_handle(scores.device) if stream is None else stream
+    s = _launch_stream(scores.device, stream)
     return _check(load_library().gbtopk_page_table_transform(
         _ptr(scores), _DTYPES[scores.dtype], R, W, stride, _ptr(lengths), _ptr(row_starts),
         _ptr(page_table), P, pstride, _ptr(page_table_row_starts), page_size, top_k, _ptr(out),
@@ -215,7 +229,7 @@ def gbtopk_ragged_transform(scores: torch.Tensor, lengths: torch.Tensor,
     """Direct call of the C entry point on tensors."""
     R, W = scores.shape
     stride = scores.stride(0) if R > 1 else W
-    s = _stream_handle(scores.device) if stream is None else stream
+    s = _launch_stream(scores.device, stream)
     return _check(load_library().gbtopk_ragged_transform(
         _ptr(scores), _DTYPES[scores.dtype], R, W, stride, _ptr(lengths), _ptr(row_starts),
         _ptr(topk_indices_offset), top_k, _ptr(out), int(deterministic), _ptr(workspace),
@@ -232,7 +246,7 @@ def gbtopk_page_table_transform_cu_seqlens(scores: torch.Tensor, lengths: torch.
     stride = scores.stride(0) if R > 1 else W
     P = page_table.shape[1]
     pstride = page_table.stride(0) if page_table.shape[0] > 1 else P
-    s = _stream_handle(scores.device) if stream is None else stream
+    s = _launch_stream(scores.device, stream)
     return _check(load_library().gbtopk_page_table_transform_cu_seqlens(
         _ptr(scores), _DTYPES[scores.dtype], R, W, stride, _ptr(lengths), _ptr(row_starts),
         _ptr(page_table), P, pstride, _ptr(cu_seqlens_q), cu_seqlens_q.numel() - 1, top_k,

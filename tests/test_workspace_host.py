@@ -113,7 +113,6 @@ def library(made, monkeypatch):
     """install(hold): the C calls are hold's, the workspaces grow with the rows."""
     empty = torch.empty
     monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: empty(*a, **k))
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
     for at, name in ((gb.decode, "_attention_bytes"), (gb.decode, "_verify_bytes"), (gb, "gbtopk_workspace_bytes")):
         monkeypatch.setattr(at, name, lambda rows, *a: 1000 * rows)
 
@@ -183,3 +182,49 @@ def test_a_call_that_fails_gives_its_workspace_back(library, made, monkeypatch):
         tree(1)
     library(lambda name, address: None)
     run(lambda: tree(1))
+
+
+# ------------------------------------------------------ another device's tensors
+
+class Other(Fake):
+    device = property(lambda self: torch.device("cuda:1"))
+
+
+def evict(rows):
+    cache, table = fake(64, 2, 64, dtype=BF), fake(rows, 1, dtype=I32)
+    gb.evict_cache(fake(rows, 2, 32), cache, cache, table, fake(rows, dtype=I32), table, 8, page_size=32,
+                   out_weights=fake(rows, 2, 32))
+
+
+def direct(rows):
+    gb.gbtopk_varlen(fake(rows, 40), fake(rows, dtype=I32), 4, None, 1, 1, fake(rows, 4, dtype=I32), None, 0,
+                     fake(1000, dtype=torch.uint8))
+
+
+def direct_on_a_stream(rows):
+    gb.gbtopk_varlen(fake(rows, 40), fake(rows, dtype=I32), 4, None, 1, 1, fake(rows, 4, dtype=I32), None, 0,
+                     fake(1000, dtype=torch.uint8), stream=5)
+
+
+@pytest.mark.parametrize("call", CALLS + [evict, direct, direct_on_a_stream])
+def test_tensors_of_a_device_that_is_not_current_are_refused(made, monkeypatch, call):
+    """The library launches on the current device."""
+    monkeypatch.undo()
+    calls, empty, zeros = [], torch.empty, torch.zeros
+    lib = Library(lambda name, address: calls.append(name))
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: empty(*a, **k))
+    monkeypatch.setattr(torch, "zeros", lambda *a, device=None, **k: zeros(*a, **k))
+    monkeypatch.setattr(gb, "_current_device", lambda: 0, raising=False)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: False)
+    monkeypatch.setattr(gb, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(gb, "_WS", {})
+    for at, name in ((gb.decode, "_attention_bytes"), (gb.decode, "_verify_bytes"), (gb, "gbtopk_workspace_bytes")):
+        monkeypatch.setattr(at, name, lambda rows, *a: 1000 * rows)
+    monkeypatch.setattr(gb.decode, "_calls", lib)
+    monkeypatch.setattr(gb, "load_library", lambda: lib)
+    call(1)                                     # on the current device it goes through
+    assert len(calls) == 1
+    monkeypatch.setattr("test_workspace_host.Fake", Other)
+    with pytest.raises(ValueError, match="current device"):
+        call(1)
+    assert len(calls) == 1
