@@ -2381,7 +2381,13 @@ __global__ void __launch_bounds__(kThreads, 3) chunk_kernel(const __grid_constan
     int64_t n, col0;
     row_window(p, row, n, col0);
     const int64_t nch = split_chunks(p, n);
-    if (ch >= nch) return;
+    if (ch >= nch) {
+        // Where every row is short no block has a chunk, and this grid could
+        // complete before the row kernel, whose outputs the stream's next
+        // kernel waits for through this grid alone: one block waits for it.
+        if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     const int64_t CH = p.plan.chunk;
     const int64_t c0 = ch * CH;
     const int len = static_cast<int>((n - c0) < CH ? (n - c0) : CH);
