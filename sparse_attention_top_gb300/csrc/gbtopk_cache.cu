@@ -338,10 +338,11 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const __grid_c
 
 // Blocks of a selection's cluster: enough for two blocks an SM to stage their
 // slices (256 rows of 32768 weights, one block each of 1024 threads: 56 us),
-// and for few rows as many as leave each block 4096 weights.
-int select_cluster(int64_t rows, int64_t width) {
+// and for rows that leave half of the SMs idle as many as leave each block 4096
+// weights.
+int select_cluster(int64_t rows, int64_t width, int sms) {
     int c = 1;
-    while (c < kMaxCluster && ((width + c - 1) / c > 24576 || (rows * c * 2 <= 152 && width / c > 4096))) c *= 2;
+    while (c < kMaxCluster && ((width + c - 1) / c > 24576 || (rows * c * 2 <= sms && width / c > 4096))) c *= 2;
     return c;
 }
 
@@ -419,7 +420,9 @@ extern "C" int gbtopk_cache_evict(const float *weights, int64_t num_requests, in
     p.out_weights = out_weights;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t rows = num_requests * weight_heads;
-    const int cluster = select_cluster(rows, width);
+    const int sms = device_sms();
+    if (sms == 0) return GBTOPK_ECUDA;
+    const int cluster = select_cluster(rows, width, sms);
     const int64_t slice = (width + cluster - 1) / cluster;
     p.staged = slice <= kStagedKeys;
     const size_t smem = p.staged ? static_cast<size_t>((slice + 3) / 4) * 16 : 0;

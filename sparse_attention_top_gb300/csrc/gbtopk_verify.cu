@@ -421,10 +421,10 @@ int elem_bytes(int dtype) { return dtype == GBTOPK_F32 ? 4 : 2; }
 
 // Logits of a piece: kPieceBytes of them, more where a row would have over
 // kMaxPieces pieces, fewer where a call would have fewer blocks than SMs.
-int64_t piece_of(int64_t num_rows, int64_t vocab, int es) {
+int64_t piece_of(int64_t num_rows, int64_t vocab, int es, int sms) {
     int64_t piece = kPieceBytes / es;
     while (piece * kMaxPieces < vocab) piece *= 2;
-    while (piece > 4096 / es * 2 && num_rows * ((vocab + piece - 1) / piece) < 152 && piece / 2 * kMaxPieces >= vocab) piece /= 2;
+    while (piece > 4096 / es * 2 && num_rows * ((vocab + piece - 1) / piece) < sms && piece / 2 * kMaxPieces >= vocab) piece /= 2;
     return piece;
 }
 
@@ -473,7 +473,9 @@ int gbtopk_verify_drafts(const void *logits, int dtype, int64_t num_rows, int64_
     VerifyParams p{logits, num_rows, vocab, row_stride, tokens, uniforms, noise, next_n, tree_mask, temperature,
                    draft_probs, accepted, path, next_token, accept_mask,
                    reinterpret_cast<RowStat *>(static_cast<uint8_t *>(workspace) + kWsHeaderBytes), 0, 0};
-    p.piece = piece_of(num_rows, vocab, elem_bytes(dtype));
+    const int sms = device_sms();
+    if (sms == 0) return GBTOPK_ECUDA;
+    p.piece = piece_of(num_rows, vocab, elem_bytes(dtype), sms);
     p.pieces = static_cast<int32_t>((vocab + p.piece - 1) / p.piece);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const cudaError_t e = dtype == GBTOPK_F32    ? launch_verify<GBTOPK_F32>(p, s)
