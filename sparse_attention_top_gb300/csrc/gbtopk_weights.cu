@@ -67,12 +67,13 @@ struct Shared {
     int32_t slots[kMaskRing][KT];   // cache slot of each position, -1 where there is none
     alignas(16) float lse2[256];    // base-2 lse of the phases' rows; +inf: adds nothing
     uint64_t tree[GBTOPK_MAX_NEXT_N];
+    alignas(16) uint32_t without[8][4];         // a phase has rows without an lse, by copying warp
     ScanScratch scan;
     uint32_t tmem;
     uint32_t abort;
 };
 static_assert(sizeof(Shared) <= 8192, "shared block");
-static_assert(offsetof(Shared, lse2) % 16 == 0, "vector loads of the rows' lse");
+static_assert(offsetof(Shared, lse2) % 16 == 0 && offsetof(Shared, without) % 16 == 0, "vector loads");
 
 // One span of a share: tiles t0 .. t1 - 1 of a (request, weight head), and
 // its phases.
@@ -203,17 +204,22 @@ __global__ void __launch_bounds__(Shape<DP, NQ>::kThreads, 1) weights_kernel(con
                     copy16(q_smem + qb * Sh::kQBytes + tile_offset(NQ, r, c), src, have ? 16u : 0u);
                 }
                 bar_arrive_copies(&sh.q_full[qb]);
+                bool none = false;
                 for (int r = w * 32 + lane; r < padded; r += 128) {
                     float v = INFINITY;
                     if (r < rows) {
                         const int32_t k = (r0 + r) / a.group, gq = r0 + r - k * a.group;
                         const float lse = fetch(p.lse + (static_cast<int64_t>(s.b) * a.next_n + nth_bit(s.took, k)) * a.q_heads + h * a.group + gq);
                         v = lse == -INFINITY ? INFINITY : lse * kLog2e;
+                        none |= lse == -INFINITY;
                     }
                     sh.lse2[qb * NQ + r] = v;
                 }
-                __syncwarp();
-                if (lane == 0) bar_arrive(&sh.q_full[qb]);
+                none = __any_sync(~0u, none);
+                if (lane == 0) {
+                    sh.without[qb][w] = none;
+                    bar_arrive(&sh.q_full[qb]);
+                }
                 for (int32_t t = s.t0; t < s.t1; ++t, ++job) {
                     ok = __all_sync(~0u, bar_wait(&sh.slots_full[job % kMaskRing], (job / kMaskRing) & 1, abort));
                     if (!ok) break;
@@ -350,6 +356,8 @@ __global__ void __launch_bounds__(Shape<DP, NQ>::kThreads, 1) weights_kernel(con
                 const uint32_t qb = phase % Sh::kQBufs;
                 const float *lse2 = sh.lse2 + qb * NQ;
                 ok = __all_sync(~0u, bar_wait(&sh.q_full[qb], (phase / Sh::kQBufs) & 1, abort));
+                const uint4 wo = *reinterpret_cast<const uint4 *>(sh.without[qb]);
+                const bool without = (wo.x | wo.y | wo.z | wo.w) != 0;
                 for (int32_t t = s.t0; t < s.t1 && ok; ++t, ++job) {
                     if ((job & 1) != static_cast<uint32_t>(wg)) continue;
                     ok = __all_sync(~0u, bar_wait(&sh.slots_full[job % kMaskRing], (job / kMaskRing) & 1, abort) &&
@@ -376,10 +384,12 @@ __global__ void __launch_bounds__(Shape<DP, NQ>::kThreads, 1) weights_kernel(con
                                 }
                             }
                         }
-                        if (c0 + 16 > rows) {   // rows of zeros behind the last: 0 x inf
+                        // rows that add nothing, behind the last or without an lse:
+                        // infinite keys would make their scores NaN
+                        if (c0 + 16 > rows || without) {
 #pragma unroll
                             for (int c = 0; c < 16; ++c)
-                                if (c0 + c >= rows) x[c] = 0;
+                                if (e[c] == INFINITY) x[c] = 0;
                         }
                         float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll

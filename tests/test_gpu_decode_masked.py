@@ -138,3 +138,35 @@ def test_weights_of_keys_that_are_not_finite(dev):
     rest[3] = False
     off = np.abs(got.double().numpy() - want)
     assert np.all((off <= tol)[:, :, rest]), np.max((off - tol)[:, :, rest])
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("next_n,q_heads,kv_heads,dim,shared", [(2, 4, 2, 64, False), (20, 4, 2, 128, True), (64, 6, 2, 256, False)])
+def test_weights_of_rows_without_a_sum(dev, dtype, next_n, q_heads, kv_heads, dim, shared):
+    """A row whose lse is -infinity adds nothing, whatever the keys hold."""
+    b = Batch([300, 170], next_n, q_heads, kv_heads, dim, 16, dtype, seed=next_n)
+    for i in range(2):
+        for p, x in ((10, math.nan), (20, math.inf), (131, -math.inf)):
+            b.kv[0, int(b.table[i, p // 16]) * 16 + p % 16] = x
+    k, _ = b.caches(dev)
+    w = torch.rand((2, 1 if shared else kv_heads, 300), generator=torch.Generator().manual_seed(2))
+    lse = torch.full((2 * next_n, q_heads), -math.inf)
+    for accept in (None, torch.tensor([1, 3])):
+        got = gb.accumulate_cache_weights(b.q.to(dev), k, lse.to(dev), b.table.to(dev), b.lens.to(dev), w.to(dev), page_size=16,
+                                          next_n=next_n, accept_mask=None if accept is None else accept.to(dev))
+        assert torch.equal(got.cpu(), w)
+    # beside rows that have one: request 1 alone keeps its lse, over finite keys
+    for p in (10, 20, 131):
+        b.kv[0, int(b.table[1, p // 16]) * 16 + p % 16] = 0.5
+    k, v = b.caches(dev)
+    full = gb.tree_attention(b.q.to(dev), k, v, b.table.to(dev), b.lens.to(dev), page_size=16, next_n=next_n, return_lse=True)[1]
+    lse[next_n:] = full[next_n:].cpu()
+    lse[next_n, 0] = -math.inf
+    got = gb.accumulate_cache_weights(b.q.to(dev), k, lse.to(dev), b.table.to(dev), b.lens.to(dev), w.to(dev), page_size=16,
+                                      next_n=next_n).cpu()
+    assert torch.equal(got[0], w[0])
+    q, kk, _ = b.wide()
+    want, tol = ref.weights(q[next_n:], kk, lse.numpy()[next_n:], w.numpy()[1:], b.table.numpy()[1:], 16, k.shape[0],
+                            b.lens.numpy()[1:], next_n, None, None, b.group, b.scale)
+    off = np.abs(got[1:].double().numpy() - want)
+    assert np.all(off <= tol), np.max(off - tol)
