@@ -418,7 +418,8 @@ int gbtopk_cache_weights(const void *q, int dtype, int64_t num_rows, int64_t q_r
  *               page_size >= budget.
  *  kept         device int32 [num_requests, weight_heads, budget]: the kept
  *               positions, padded with -1.
- *  new_lens     device int32 [num_requests]: positions kept.
+ *  new_lens     device int32 [num_requests]: positions kept.  Not overlapping
+ *               seq_lens.
  *  out_weights  device fp32 like weights, not overlapping it: the kept
  *               positions' weights (-0 as +0), zeros behind them.
  */

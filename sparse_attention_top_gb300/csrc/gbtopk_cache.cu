@@ -387,6 +387,9 @@ extern "C" int gbtopk_cache_evict(const float *weights, int64_t num_requests, in
         return GBTOPK_EALIGN;
     const size_t wbytes = static_cast<size_t>(num_requests) * weight_heads * width * 4;
     if (width > 0 && overlap(weights, wbytes, out_weights, wbytes)) return GBTOPK_EOVERLAP;
+    // (a request's heads are separate blocks: one would read what another wrote)
+    const size_t lbytes = static_cast<size_t>(num_requests) * 4;
+    if (overlap(seq_lens, lbytes, new_lens, lbytes)) return GBTOPK_EOVERLAP;
     EvictParams p{};
     p.weights = weights;
     p.seq_lens = seq_lens;

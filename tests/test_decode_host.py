@@ -141,3 +141,9 @@ def test_python_checks():
         gb.tree_attention(q, q, q, torch.zeros((2, 1), dtype=torch.int32), torch.ones(2, dtype=torch.int32))
     with pytest.raises(ValueError):
         gb.verify_drafts(torch.zeros((2, 9)), torch.zeros(2, dtype=torch.int32), torch.zeros(2), torch.zeros((2, 9)))
+
+
+@pytest.mark.parametrize("new_lens,status", [(A, gb.EOVERLAP), (A + 4, gb.EOVERLAP), (A - 4, gb.EOVERLAP)])
+def test_cache_evict_refuses_lengths_in_place(new_lens, status):
+    """A request's heads read its length at different times."""
+    assert evict(lens=A, new_lens=new_lens) == status
