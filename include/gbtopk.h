@@ -304,7 +304,8 @@ int gbtopk_varlen_static_ws(const void *logits, int dtype, int64_t num_rows, int
  *
  * The cache holds one key and one value row of head_dim elements for each
  * (slot, kv head), with any slot and head strides (in elements) that are
- * multiples of 8; bases 16-byte aligned (GBTOPK_EALIGN).  Query head h reads
+ * multiples of 8; bases, and fp32 weights, 16-byte aligned, every other array
+ * on its element's boundary (GBTOPK_EALIGN).  Query head h reads
  * kv head h / (q_heads / kv_heads).  dtype is GBTOPK_BF16 or GBTOPK_F16 for
  * queries, cache and output alike; head_dim is a multiple of 8, 8 .. 256;
  * next_n is 1 .. 64; q_heads is a multiple of kv_heads (others:

@@ -959,6 +959,7 @@ int gbtopk_tree_attention(const void *q, int dtype, int64_t num_rows, int64_t q_
         return rc;
     if (num_rows == 0) return GBTOPK_OK;
     if (!seq_lens) return GBTOPK_EINVAL;
+    if (!aligned_to(seq_lens, 4) || !aligned_to(tree_mask, 8)) return GBTOPK_EALIGN;
     p.seq_lens = seq_lens;
     p.next_n = next_n;
     p.tree_mask = tree_mask;
@@ -978,6 +979,7 @@ int gbtopk_selected_attention(const void *q, int dtype, int64_t num_rows, int64_
     if (top_k > INT32_MAX / 2) return GBTOPK_EUNSUPPORTED;
     if (num_rows == 0) return GBTOPK_OK;
     if (top_k > 0 && !indices) return GBTOPK_EINVAL;
+    if (!aligned_to(indices, 4)) return GBTOPK_EALIGN;
     AttnParams p{};
     p.pages.num_slots = num_slots;
     p.pages.page.init(1);

@@ -383,7 +383,8 @@ extern "C" int gbtopk_cache_evict(const float *weights, int64_t num_requests, in
     if (!aligned_to(k_cache, 16) || !aligned_to(v_cache, 16) || !multiple_of(k_slot_stride * es, 16) ||
         !multiple_of(k_head_stride * es, 16) || !multiple_of(v_slot_stride * es, 16) ||
         !multiple_of(v_head_stride * es, 16) || !multiple_of(static_cast<int64_t>(head_dim) * es, 16) ||
-        !aligned_to(weights, 16) || !aligned_to(out_weights, 16) || !aligned_to(kept, 16) || !aligned_to(new_lens, 4))
+        !aligned_to(weights, 16) || !aligned_to(out_weights, 16) || !aligned_to(kept, 16) || !aligned_to(new_lens, 4) ||
+        !aligned_to(seq_lens, 4) || !aligned_to(accept_mask, 8) || !aligned_to(page_table, 4) || !aligned_to(out_page_table, 4))
         return GBTOPK_EALIGN;
     const size_t wbytes = static_cast<size_t>(num_requests) * weight_heads * width * 4;
     if (width > 0 && overlap(weights, wbytes, out_weights, wbytes)) return GBTOPK_EOVERLAP;

@@ -180,6 +180,7 @@ inline int check_pages(const int32_t *table, int64_t cols, int64_t stride, int32
                 int64_t requests, Paging *out) {
     if (page < 1 || page > (1 << 30) || cols < 0 || num_slots < 0 || (requests > 1 && stride < cols)) return GBTOPK_EINVAL;
     if (requests > 0 && cols > 0 && !table) return GBTOPK_EINVAL;
+    if (!aligned_to(table, 4)) return GBTOPK_EALIGN;
     if (cols > INT32_MAX / page) cols = INT32_MAX / page;  // positions are 31-bit numbers
     out->table = table;
     out->cols = cols;

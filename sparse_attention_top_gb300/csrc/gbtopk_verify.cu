@@ -467,7 +467,8 @@ int gbtopk_verify_drafts(const void *logits, int dtype, int64_t num_rows, int64_
     if (!logits || !tokens || !uniforms || !noise || !accepted || !path || !next_token || !accept_mask)
         return GBTOPK_EINVAL;
     if (!aligned_to(logits, dtype == GBTOPK_F32 ? 4 : 2) || !aligned_to(noise, 4) || !aligned_to(draft_probs, 4) ||
-        !aligned_to(accepted, 4) || !aligned_to(path, 4) || !aligned_to(next_token, 4) || !aligned_to(accept_mask, 8))
+        !aligned_to(accepted, 4) || !aligned_to(path, 4) || !aligned_to(next_token, 4) || !aligned_to(accept_mask, 8) ||
+        !aligned_to(tokens, 4) || !aligned_to(uniforms, 4) || !aligned_to(tree_mask, 8) || !aligned_to(temperature, 4))
         return GBTOPK_EALIGN;
     if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < need) return GBTOPK_EWORKSPACE;
     VerifyParams p{logits, num_rows, vocab, row_stride, tokens, uniforms, noise, next_n, tree_mask, temperature,

@@ -470,7 +470,9 @@ extern "C" int gbtopk_cache_weights(const void *q, int dtype, int64_t num_rows, 
     if (!seq_lens || !lse || !weights) return GBTOPK_EINVAL;
     if ((rc = check_rows(q, q_row_stride, q_head_stride, true)) != GBTOPK_OK) return rc;
     if ((rc = check_rows(k_cache, k_slot_stride, k_head_stride, num_slots > 0)) != GBTOPK_OK) return rc;
-    if (!aligned_to(lse, 4) || !aligned_to(weights, 16)) return GBTOPK_EALIGN;
+    if (!aligned_to(lse, 4) || !aligned_to(weights, 16) || !aligned_to(seq_lens, 4) || !aligned_to(tree_mask, 8) ||
+        !aligned_to(accept_mask, 8))
+        return GBTOPK_EALIGN;
     if (!workspace || !aligned_to(workspace, 256) || workspace_bytes < kWsHeaderBytes) return GBTOPK_EWORKSPACE;
     a.q = q;
     a.q_row = q_row_stride;

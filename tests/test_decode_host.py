@@ -147,3 +147,17 @@ def test_python_checks():
 def test_cache_evict_refuses_lengths_in_place(new_lens, status):
     """A request's heads read its length at different times."""
     assert evict(lens=A, new_lens=new_lens) == status
+
+
+@pytest.mark.parametrize("call,kw", [
+    (tree, dict(table=A + 2)), (tree, dict(lens=A + 1)), (tree, dict(tree=A + 4)),
+    (selected, dict(idx=A + 2)),
+    (weights, dict(table=A + 2)), (weights, dict(lens=A + 2)), (weights, dict(tree=A + 4)), (weights, dict(accept=A + 4)),
+    (weights, dict(lse=A + 2)),
+    (evict, dict(lens=A + 18)), (evict, dict(accept=A + 4)), (evict, dict(table=A + 2)), (evict, dict(new_table=A + 2)),
+    (evict, dict(new_lens=A + 18)),
+    (verify, dict(tokens=A + 2)), (verify, dict(uniforms=A + 2)), (verify, dict(tree=A + 4)), (verify, dict(temperature=A + 2)),
+    (verify, dict(draft=A + 2)), (verify, dict(path=A + 2)),
+])
+def test_arrays_off_their_types_boundary_are_refused(call, kw):
+    assert call(**kw) == gb.EALIGN
