@@ -304,6 +304,13 @@ def _require_cuda(t: torch.Tensor, name: str):
         raise ValueError(f"{name} must be a CUDA tensor (there is no CPU path)")
 
 
+def _check_workspace(workspace: Optional[torch.Tensor], device: torch.device):
+    """A caller's workspace: its bytes have to be its own, on ``device``."""
+    if workspace is not None and not (isinstance(workspace, torch.Tensor) and workspace.device == device
+                                      and workspace.is_contiguous()):
+        raise ValueError(f"workspace must be a contiguous tensor on {device}")
+
+
 def _out_view(buf: Optional[torch.Tensor], R: int, k: int, dtype, device, name: str):
     if buf is None:
         return torch.empty((R, k), dtype=dtype, device=device)
@@ -357,6 +364,7 @@ def top_k_varlen(logits: torch.Tensor, seq_lens: torch.Tensor, top_k: int,
         else:
             warnings.warn("pre_idx is malformed and was discarded; running hint-free",
                           RuntimeWarning, stacklevel=2)
+    _check_workspace(workspace, logits.device)
     with _turn(logits.device):
         ws = workspace if workspace is not None else _workspace(
             logits.device, gbtopk_workspace_bytes(R, W, top_k, logits.dtype))
@@ -404,6 +412,7 @@ def top_k_page_table_transform(scores: torch.Tensor, lengths: torch.Tensor,
     raw = None
     if out_raw_indices is not None:
         raw = _out_view(out_raw_indices, R, top_k, torch.int32, scores.device, "out_raw_indices")
+    _check_workspace(workspace, scores.device)
     with _turn(scores.device):
         ws = workspace if workspace is not None else _workspace(
             scores.device, gbtopk_workspace_bytes(R, W, top_k, scores.dtype))
@@ -440,6 +449,7 @@ def top_k_ragged_transform(scores: torch.Tensor, lengths: torch.Tensor,
             or not topk_indices_offset.is_contiguous()):
         raise ValueError("topk_indices_offset must be a contiguous int32 tensor of num_rows")
     o = _out_view(out, R, top_k, torch.int32, scores.device, "out")
+    _check_workspace(workspace, scores.device)
     with _turn(scores.device):
         ws = workspace if workspace is not None else _workspace(
             scores.device, gbtopk_workspace_bytes(R, W, top_k, scores.dtype))
@@ -469,6 +479,7 @@ def top_k_page_table_transform_cu_seqlens(scores: torch.Tensor, lengths: torch.T
             or cu_seqlens_q.numel() != page_table.shape[0] + 1 or not cu_seqlens_q.is_contiguous()):
         raise ValueError("cu_seqlens_q must be a contiguous int32 tensor of num_reqs + 1")
     o = _out_view(out, R, top_k, torch.int32, scores.device, "out")
+    _check_workspace(workspace, scores.device)
     with _turn(scores.device):
         ws = workspace if workspace is not None else _workspace(
             scores.device, gbtopk_workspace_bytes(R, W, top_k, scores.dtype))

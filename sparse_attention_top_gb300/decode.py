@@ -155,7 +155,7 @@ def _scratch(workspace, dev, stream, nbytes: int):
         if workspace is None or workspace.numel() < nbytes:
             workspace = _gb._workspace(dev, nbytes)
         return workspace.data_ptr(), workspace.numel()
-    _gb._require_cuda(workspace, "workspace")
+    _gb._check_workspace(workspace, dev)
     return workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 

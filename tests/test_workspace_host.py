@@ -228,3 +228,33 @@ def test_tensors_of_a_device_that_is_not_current_are_refused(made, monkeypatch, 
     with pytest.raises(ValueError, match="current device"):
         call(1)
     assert len(calls) == 1
+
+
+# ------------------------------------------------------ a caller's workspace
+
+def given(call, workspace, monkeypatch):
+    """The call with that workspace: its kernels' address, or None if refused."""
+    seen = []
+    lib = Library(lambda name, address: seen.append(address))
+    monkeypatch.setattr(gb.decode, "_calls", lib)
+    monkeypatch.setattr(gb, "load_library", lambda: lib)
+    for at, name in ((gb, "top_k_varlen"), (gb, "top_k_page_table_transform"), (gb, "tree_attention"),
+                     (gb, "selected_attention"), (gb, "accumulate_cache_weights"), (gb, "verify_drafts")):
+        real = getattr(at, name)
+        monkeypatch.setattr(at, name, lambda *a, real=real, **k: real(*a, workspace=workspace, **k))
+    try:
+        call(1)
+    except ValueError:
+        return None
+    return seen[0]
+
+
+@pytest.mark.parametrize("call", CALLS)
+def test_a_callers_workspace_has_to_own_its_bytes(library, monkeypatch, call):
+    monkeypatch.setattr(gb, "_current_device", lambda: 0)
+    good = fake(4096, dtype=torch.uint8)
+    for ok, ws in ((True, good), (False, good[:1].expand(4096)), (False, good[::2]), (False, torch.zeros(4096, dtype=torch.uint8)),
+                   (False, torch.Tensor._make_subclass(Other, torch.empty(4096, dtype=torch.uint8)))):
+        with monkeypatch.context() as m:
+            assert given(call, ws, m) == (ws.data_ptr() if ok else None)
+    assert not gb._WS
