@@ -28,6 +28,7 @@ __all__ = [
 
 MAX_NEXT_N = 64
 MAX_HEAD_DIM = 256
+MAX_PAGE_SIZE = 1 << 30
 
 _i32, _i64, _vp, _sz, _f = (ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_size_t,
                             ctypes.c_float)
@@ -124,6 +125,10 @@ def _cache(t, q, dev, dim):
     return slots, heads, strides
 
 
+# (numbers beyond the C types would reach the library cut off)
+_PAGE_RULE = f"page_size must be in [1, {MAX_PAGE_SIZE}]"
+
+
 def _requests(rows: int, next_n: int) -> int:
     if next_n < 1 or next_n > MAX_NEXT_N or rows % next_n != 0:
         raise ValueError(f"num_rows must be a multiple of next_n, next_n in [1, {MAX_NEXT_N}]")
@@ -181,9 +186,10 @@ def tree_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor
     requests = _requests(rows, next_n)
     slots, kv, ks = _cache(k_cache, q, dev, dim)
     vslots, vkv, vs = _cache(v_cache, q, dev, dim)
-    if not (slots == vslots and kv == vkv and _table(page_table, dev, requests)
+    if not (slots == vslots and kv == vkv and 1 <= page_size <= MAX_PAGE_SIZE and _table(page_table, dev, requests)
             and _dense(seq_lens, dev, _I32, (requests,)) and _maybe(tree_mask, dev, _I64, (rows,))):
         _refuse((slots == vslots and kv == vkv, "k_cache and v_cache must have one shape"),
+                (1 <= page_size <= MAX_PAGE_SIZE, _PAGE_RULE),
                 (_table(page_table, dev, requests), "page_table must be int32 [num_requests, pt_cols], inner stride 1"),
                 (_dense(seq_lens, dev, _I32, (requests,)), "seq_lens must be contiguous int32 [num_requests]"),
                 (False, "tree_mask must be contiguous int64 [num_rows]"))
@@ -252,10 +258,11 @@ def accumulate_cache_weights(q: torch.Tensor, k_cache: torch.Tensor, lse: torch.
     slots, kv, ks = _cache(k_cache, q, dev, dim)
     wshape = weights.shape if isinstance(weights, torch.Tensor) and weights.dim() == 3 else (-1, -1, -1)
     fits = wshape[0] == requests and wshape[1] in (1, kv) and _dense(weights, dev, _F32, wshape)
-    if not (fits and _table(page_table, dev, requests) and _dense(seq_lens, dev, _I32, (requests,))
-            and _dense(lse, dev, _F32, shape[:2]) and _maybe(tree_mask, dev, _I64, (rows,))
-            and _maybe(accept_mask, dev, _I64, (requests,))):
+    if not (fits and 1 <= page_size <= MAX_PAGE_SIZE and _table(page_table, dev, requests)
+            and _dense(seq_lens, dev, _I32, (requests,)) and _dense(lse, dev, _F32, shape[:2])
+            and _maybe(tree_mask, dev, _I64, (rows,)) and _maybe(accept_mask, dev, _I64, (requests,))):
         _refuse((fits, "weights must be contiguous fp32 [num_requests, 1 or kv_heads, width]"),
+                (1 <= page_size <= MAX_PAGE_SIZE, _PAGE_RULE),
                 (_table(page_table, dev, requests), "page_table must be int32 [num_requests, pt_cols], inner stride 1"),
                 (_dense(seq_lens, dev, _I32, (requests,)), "seq_lens must be contiguous int32 [num_requests]"),
                 (_dense(lse, dev, _F32, shape[:2]), "lse must be contiguous fp32 [num_rows, q_heads]"),
@@ -312,7 +319,8 @@ def evict_cache(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
     one = k_cache.shape == v_cache.shape and k_cache.dtype is v_cache.dtype
     if not (one and wheads in (1, kv) and _table(page_table, dev, requests) and _table(out_page_table, dev, requests)
             and _dense(seq_lens, dev, _I32, (requests,)) and _maybe(accept_mask, dev, _I64, (requests,))
-            and budget >= 1 and recent >= 0 and page_size >= 1 and out_page_table.shape[1] * page_size >= budget
+            and 1 <= budget < 1 << 31 and 0 <= recent < 1 << 31 and 1 <= page_size <= MAX_PAGE_SIZE
+            and 1 <= next_n <= MAX_NEXT_N and out_page_table.shape[1] * page_size >= budget
             and _maybe(out_weights, dev, _F32, wshape)):
         _refuse((one, "k_cache and v_cache must have one shape and type"),
                 (wheads in (1, kv), "weights must be [num_requests, 1 or kv_heads, width]"),
@@ -321,7 +329,10 @@ def evict_cache(weights: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Ten
                 (_dense(seq_lens, dev, _I32, (requests,)), "seq_lens must be contiguous int32 [num_requests]"),
                 (_maybe(accept_mask, dev, _I64, (requests,)), "accept_mask must be contiguous int64 [num_requests]"),
                 (_maybe(out_weights, dev, _F32, wshape), "out_weights must be contiguous fp32 like weights"),
-                (False, "budget >= 1, recent >= 0 and room for budget positions in out_page_table are required"))
+                (1 <= page_size <= MAX_PAGE_SIZE, _PAGE_RULE),
+                (1 <= next_n <= MAX_NEXT_N, f"next_n must be in [1, {MAX_NEXT_N}]"),
+                (False, "budget in [1, 2**31), recent in [0, 2**31) and room for budget positions in out_page_table are "
+                        "required"))
     if out_weights is None:
         out_weights = torch.empty(wshape, dtype=_F32, device=dev)
     kept = torch.empty((requests, wheads, budget), dtype=_I32, device=dev)

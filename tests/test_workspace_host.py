@@ -258,3 +258,38 @@ def test_a_callers_workspace_has_to_own_its_bytes(library, monkeypatch, call):
         with monkeypatch.context() as m:
             assert given(call, ws, m) == (ws.data_ptr() if ok else None)
     assert not gb._WS
+
+
+# ------------------------------------------------------ numbers beyond the C types
+
+def evicted(page_size=32, next_n=1, budget=8, recent=0, cols=1):
+    cache, table = fake(64, 2, 64, dtype=BF), fake(1, cols, dtype=I32)
+    gb.evict_cache(fake(1, 2, 32), cache, cache, table, fake(1, dtype=I32), table, budget, recent=recent, page_size=page_size,
+                   next_n=next_n, out_weights=fake(1, 2, 32))
+
+
+def paged(page_size):
+    q, cache, table, lens, lse = attention(1)
+    gb.tree_attention(q, cache, cache, table, lens, page_size=page_size, out=fake(1, 4, 64, dtype=BF), lse=lse)
+
+
+def weighed(page_size):
+    q, cache, table, lens, lse = attention(1)
+    gb.accumulate_cache_weights(q, cache, lse, table, lens, fake(1, 2, 32), page_size=page_size)
+
+
+@pytest.mark.parametrize("call,good,bad", [
+    (paged, 32, 2 ** 32 + 32), (paged, 2 ** 30, 2 ** 30 + 1), (paged, 1, 0), (weighed, 32, 2 ** 32 + 32), (weighed, 1, -1),
+    (lambda n: evicted(page_size=n), 32, 2 ** 32 + 32), (lambda n: evicted(next_n=n), 64, 2 ** 32 + 1),
+    (lambda n: evicted(budget=n, page_size=2 ** 30, cols=5), 100, 2 ** 32 + 8),
+    (lambda n: evicted(recent=n), 2 ** 31 - 1, 2 ** 32),
+])
+def test_numbers_that_the_library_cannot_hold_are_refused(library, monkeypatch, call, good, bad):
+    monkeypatch.setattr(gb, "_current_device", lambda: 0)
+    seen = []
+    library(lambda name, address: seen.append(name))
+    call(good)
+    assert len(seen) == 1
+    with pytest.raises(ValueError):
+        call(bad)
+    assert len(seen) == 1
