@@ -32,8 +32,8 @@ extern "C" {
 #define GBTOPK_OK 0
 #define GBTOPK_HINT_DISCARDED 1 /* warning: pre_idx unusable, ran hint-free (result still exact) */
 #define GBTOPK_EINVAL (-1)       /* shape, dtype, grouping or null-pointer error */
-#define GBTOPK_EALIGN (-2)       /* an output (or the score base) is misaligned */
-#define GBTOPK_EOVERLAP (-3)     /* two output buffers overlap */
+#define GBTOPK_EALIGN (-2)       /* an output, the score base or a decode-step array is misaligned */
+#define GBTOPK_EOVERLAP (-3)     /* two output buffers, or an output and what it may not lie over, overlap */
 #define GBTOPK_EUNSUPPORTED (-4) /* outside the supported envelope (e.g. top_k too large) */
 #define GBTOPK_ECUDA (-5)        /* the CUDA runtime refused the launch */
 #define GBTOPK_EWORKSPACE (-6)   /* workspace missing, misaligned or too small */
@@ -325,6 +325,15 @@ int gbtopk_varlen_static_ws(const void *logits, int dtype, int64_t num_rows, int
  * hold; an infinity or NaN of a drafted token reaches the rows that see it
  * and no others.
  *
+ * Arithmetic: scores, sums and the output until it is stored are 32 bits; the
+ * products are the tensor core's.  Each probability is rounded to dtype for
+ * its product with the value (by up to 2^-8 of itself in bf16, 2^-11 in fp16;
+ * the sum it is divided by is of the unrounded ones), and the output once
+ * more, so the output's error is 1.2 to 1.4 times that of its own rounding.
+ * In fp16 the positions of a tile (128 consecutive ones, 64 above dimension
+ * 128) have one scale: probabilities below 2^-13 of the tile's largest (2^-20
+ * where that is the row's largest) are off by up to 2^-24 (2^-31) of it.
+ *
  *  q            device [num_rows, q_heads, head_dim], inner stride 1, row and
  *               head strides multiples of 8, 16-byte aligned.
  *  page_table   device int32 [num_rows / next_n, pt_cols], row stride
@@ -457,6 +466,12 @@ int gbtopk_cache_evict(const float *weights, int64_t num_requests, int32_t weigh
  * when noise is standard exponential: rest is p without the refused tokens,
  * or max(p - q, 0) after a refusal under draft_probs, or p.  -1 where rest
  * is zero everywhere.  A token outside [0, vocab) is never accepted.
+ * (A request with fewer drafts than next_n: such a token in the places left
+ * over, and under draft_probs a row of zeros for the node before them.)
+ * Probabilities are 32-bit numbers; the exponentials of the sums and of the
+ * draw, and the draw's division by the noise, are the fast ones (relative
+ * errors of about 2^-20), so of two words whose races are that close either
+ * may be drawn.
  *
  *  logits       device [num_rows, vocab] of dtype (any of the three), row
  *               stride row_stride.  Logits of -infinity have p = 0.

@@ -3,7 +3,8 @@
 //
 // The rows that share a cached head - next_n tokens x the query heads of the
 // group - are the rows of one matrix tile, so each cached key and value is
-// read once for all of them.  Per tile of KT cached positions:
+// copied once for all of them; above 256 rows (128 above dimension 128) once
+// for each row tile of as many.  Per tile of KT cached positions:
 //     S = Q K^T (tensor core, 32-bit accumulator in tensor memory),
 //     P = 2^(c S - m), the reference m (about the running maximum) and the
 //         sum l in registers,
@@ -12,11 +13,12 @@
 // m: P then stays below 2^8, in fp16 kernels below 2^15 (see kLift), which the
 // type holds.  P is rounded to the inputs' type for the product (each
 // probability is off by up to 2^-8 of itself in bf16 and 2^-11 in fp16, as the
-// output is by its own rounding; the sum l is of the unrounded values); S, m, l and O are 32 bits.  The work of a
-// call is the list of all (request, kv head, row tile, position tile); block
-// c of a grid of one block per SM takes the c-th share of equal cost of that
-// list whatever the lengths are, and a unit (request, head, row tile) that
-// spans blocks leaves partial O, m, l in the workspace for combine_kernel.
+// output is by its own rounding; the sum l is of the unrounded values); S, m, l
+// and O are 32 bits.  The work of a call is the list of all (request, kv head,
+// row tile, position tile); block c of a grid of one block per SM takes the
+// c-th share of equal cost of that list whatever the lengths are, and a unit
+// (request, head, row tile) that spans blocks leaves partial O, m, l in the
+// workspace for combine_kernel.
 //
 // A block: W warpgroups of softmax (one row a thread), a warpgroup one warp of
 // which issues the matrix products and whose others look up the cache slots of
@@ -24,14 +26,17 @@
 // (cp.async, 16 bytes a lane, any page size and stride) into a ring of tiles.
 // Copies run ahead of the products by the whole ring.
 //
-// Bound by the cache's bytes up to some 100 rows a head, by the softmax and
-// the products' turn-taking above.  Measured on one GB300 (copy rate 6.78
-// TB/s, bf16 products 1884 TFLOP/s): 64 requests x 4 drafts over 1..8192
-// positions, 8 heads of 128, 167 us = 6.44 TB/s; 2 requests x 8 over 163840
-// positions in pages of one, 8 heads of 64, 135 us = 4.96 TB/s (128-byte rows
-// at random); 16 requests x 64 drafts, 512 rows a head, 106 us = 961 TFLOP/s;
-// 64 rows x 2048 selected entries of two heads, 29 us = 4.5 TB/s; one request
-// of 1027 positions, 11.7 us.
+// Bound by the cache's bytes up to some 100 rows a head, above by the softmax
+// and the products, which wait for one another: a tile's value product for all
+// of its P, the key product after next for that.  Measured on one GB300 (copy
+// rate 6.78 TB/s, bf16 products 1884 TFLOP/s), the kernels alone: 64 requests x
+// 4 drafts over 1..8192 positions, 8 heads of 128, fp16, 170 us = 6.34 TB/s; of
+// 256, 331 us = 6.51 TB/s; 2 requests x 8 over 163840 positions in pages of
+// one, 8 heads of 64, 135 us = 4.96 TB/s (128-byte rows at random), of 256,
+// 426 us = 6.30 TB/s; 16 requests x 64 drafts, 512 rows a head of 128, 105 us =
+// 972 TFLOP/s (14 us of it the join), of 256, 276 us = 742 TFLOP/s (four row
+// tiles, each of which copies the cache); 64 rows x 2048 selected entries of two
+// heads, 29 us = 4.5 TB/s; one request of 1027 positions, 11.6 us.
 #include <cfloat>
 #include <cmath>
 

@@ -18,23 +18,37 @@ namespace {
 // exponentials per thread, joined over the cluster through distributed shared
 // memory), decides its children in order, and goes on from the accepted one;
 // the last node's row is then drawn from.  Rows that the path does not reach
-// are not read.  A step costs about 3 us of latency, so where all rows of the
-// call are read sooner than its steps would take (kLazyBytes),
-// verify_stat_kernel reads them all first, blocks of (row, piece of the
-// vocabulary), and the path kernel only joins the pieces.
+// are not read.  For small calls (kLazyBytes) verify_stat_kernel reads all rows
+// first, blocks of (row, piece of the vocabulary), and the path kernel only
+// joins the pieces.
 //
-// Measured on one GB300: 64 requests x 16 nodes over 131073 bf16 words, 47 us
-// (48 MB of the 268 MB of logits are read; bound by the steps of the longest
-// path, not by bytes; reading all rows first took 123 us); one request x 4
-// nodes over 32000 fp32 words with draft probabilities, 8 us.
+// Measured on one GB300, 64 requests x 16 nodes over 131073 bf16 words.  Greedy,
+// nothing accepted: 9.7 us (one step).  Sampled: 32 us, since the draw reads the
+// 34 MB of noise and the last row again, in eight rounds of loads a thread; each
+// further step adds 5.5 to 6.5 us (15 accepted: 117), and each child refused
+// before the draw 2.4 us (15 of them: 69), because every word that leads its
+// thread's race is compared with all of them.  Trees of 16 with a third of a
+// draft accepted a request: 42 to 47 us, most of it the draw.  One request
+// x 4 nodes over 32000 fp32 words with draft probabilities: 8 us.
 constexpr int kThreads = 256;
 constexpr int kCluster = 8;
 constexpr int kMaxPieces = 32;
 // A piece: 64 KB of a row, fewer for few rows (see piece_of).
 constexpr int kPieceBytes = 65536;
-// One row of logits of every request: above this many bytes the walk reads
-// rows as it reaches them.  (Half of next_n steps of 3 us at 6.5 TB/s against
-// next_n rows of all requests.)
+// Bytes of one row of logits of every request, above which the walk reads rows
+// as it reaches them.  How far walks go is not known here, and neither order
+// is the faster one for all; as (nothing, a quarter, all accepted), walking
+// against reading all rows first, us, bf16:
+//     64 requests x 16 nodes x 131073 words (16.8 MB a row): 35, 59, 117 / 88
+//     64 x  4 x 131073 (16.8 MB):                            35, 41, 51 / 53
+//     32 x 16 x 131073 (8.4 MB):                             27, 50, 94 / 65
+//     16 x 16 x 131073 (4.2 MB):                             23, 45, 91 / 47
+//      8 x 16 x 131073 (2.1 MB):                             23, 36, 89 / 41
+//     64 x  8 x  32000 (4.1 MB):                             11, 18, 36 / 25
+//    128 x  8 x  32000 fp32 (16.4 MB):                       21, 37, 70 / 39
+//      1 x  4 x  32000 fp32 (0.1 MB):                         7,  9, 13 / 8
+// Above the bound a walk to the end costs 1.0 to 1.8 times the other order and
+// a short one saves up to 60 %; below it a walk to the end costs up to 2.2 times.
 constexpr int64_t kLazyBytes = 10 << 20;
 
 // Of a row, or a piece of one: the largest logit, its lowest index (greedy
