@@ -58,6 +58,9 @@ constexpr float kRescale = 8.f;     // rise of a tile's maximum over the referen
 // elements below 2^-14 lose is 2^-24 of the tile's largest each.  l stays at or
 // below 2^80 (O below 2^127 for any values and lengths); what lies further down
 // than that is below the smallest fp16 output.  bf16 has the range of the sums.
+// 32 requests x 4 drafts over 6000 positions: 129.4 -> 130.6 us; 8 x 64 drafts
+// whose tiles' maxima jump by 10 nats at random, so that some row's reference
+// moves at nearly every tile: 64.1 -> 69.0, without jumps 63.1 -> 63.2.
 template <bool BF16>
 constexpr float kLift = BF16 ? 0.f : 7.f;
 constexpr float kMostSum = 0x1p80f;
