@@ -52,12 +52,16 @@ constexpr float kRescale = 8.f;     // rise of a tile's maximum over the referen
 // fp16 holds 2^-14 .. 2^15 with all its digits and nothing below 2^-25, so
 // with m the maximum a key 17 nats above the others (an attention sink) left
 // nothing of their P.  There the reference is 2^7 below a tile's maximum (P is
-// at most 2^15 before O is rescaled), and it also falls, by a whole power of
-// two that scales O and l up, where a tile's maximum is more than 2^8 below
-// the one that set it: every tile's P then reaches 2^-1 or more, and what its
-// elements below 2^-14 lose is 2^-24 of the tile's largest each.  l stays at or
-// below 2^80 (O below 2^127 for any values and lengths); what lies further down
-// than that is below the smallest fp16 output.  bf16 has the range of the sums.
+// at most 2^15 before O is rescaled), and it also falls, scaling O and l up,
+// where a tile's maximum is more than 2^8 below the one that set it: every
+// tile's P then reaches 2^-1 or more, and what its elements below 2^-14 lose is
+// 2^-24 of the tile's largest each.  l stays at or below 2^80 (O below 2^127 for
+// any values and lengths); what lies further down than that is below the
+// smallest fp16 output.  The first reference gives the first tile's largest
+// element a P of 2^7, which needs no rounding (with whole numbers as references
+// short rows' error was 1.16 times as large); from there it moves by whole
+// numbers, so that the many moves of a row add no error of their own to a sum
+// that each of them may scale as a whole.  bf16 has the range of the sums.
 // 32 requests x 4 drafts over 6000 positions: 129.4 -> 130.6 us; 8 x 64 drafts
 // whose tiles' maxima jump by 10 nats at random, so that some row's reference
 // moves at nearly every tile: 64.1 -> 69.0, without jumps 63.1 -> 63.2.
@@ -70,8 +74,20 @@ __device__ __forceinline__ float exp2_whole(float x) {
     return __int_as_float((static_cast<int>(fminf(fmaxf(x, -127.f), 128.f)) + 127) << 23);
 }
 
-// Log-sum-exp of a row from its reference and sum.  fp16's may be a high sum
-// over a low reference, both powers of two apart from the digits of the sum.
+// 2^(a - b) of two references.  In fp16 kernels the part that it scales down may
+// be the larger one all the same (a high sum over a low reference), so what the
+// subtraction of the two rounds off counts (Knuth, "The Art of Computer
+// Programming", volume 2, 4.2.2, theorem B).
+template <bool BF16>
+__device__ __forceinline__ float exp2_between(float a, float b) {
+    const float d = a - b, e = exp2_fast(d);
+    if constexpr (BF16) return e;
+    const float bv = __fsub_rn(d, a), rest = __fadd_rn(__fsub_rn(a, __fsub_rn(d, bv)), __fsub_rn(-b, bv));
+    return e == 0.f ? 0.f : fmaf(e, rest * kLn2, e);
+}
+
+// Log-sum-exp of a row from its reference and sum (fp16: a high sum over a low
+// reference, whose large parts cancel before the rest is added).
 template <bool BF16>
 __device__ __forceinline__ float row_lse(float m, float l) {
     if (l == 0.f) return -INFINITY;
@@ -520,9 +536,13 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                                 l *= f;
                                 m = best;
                             }
+                        } else if (move && !(l > 0.f)) {
+                            m = best - kLift<BF16>;
                         } else if (move) {
-                            const float to = rintf(best) - kLift<BF16>, g = l > 0.f ? exp2_whole(m - to) : 1.f;
-                            if (g <= 1.f || l * g <= kMostSum) {
+                            // a whole number k lower; m - k is rounded where it is the larger
+                            const float k = rintf(m + kLift<BF16> - best), to = m - k;
+                            const float g = exp2_whole(k) * exp2_fast(m - (to + k));
+                            if (k < 0.f || l * g <= kMostSum) {
                                 f = g;
                                 l *= f;
                                 m = to;
@@ -636,8 +656,8 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                 const float2 other = sh.ml[1 - wg][row];
                 const float top = fmaxf(m, other.x);
                 // (an O without a job holds what an earlier unit left there)
-                f_own = l == 0.f ? 0.f : exp2_fast(m - top);   // (a NaN score leaves l NaN)
-                f_other = other.y == 0.f ? 0.f : exp2_fast(other.x - top);
+                f_own = l == 0.f ? 0.f : exp2_between<BF16>(m, top);   // (a NaN score leaves l NaN)
+                f_other = other.y == 0.f ? 0.f : exp2_between<BF16>(other.x, top);
                 l = l * f_own + other.y * f_other;
                 m = top;
             }
@@ -756,7 +776,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
         float top = m;
 #pragma unroll
         for (int k = 0; k < n; ++k) top = fmaxf(top, ml[k].x);
-        const float f = l == 0.f ? 0.f : exp2_fast(m - top);
+        const float f = l == 0.f ? 0.f : exp2_between<BF16>(m, top);
         m = top;
         l *= f;
 #pragma unroll
@@ -764,7 +784,7 @@ __global__ void __launch_bounds__(kCombineThreads) combine_kernel(const __grid_c
 #pragma unroll
         for (int k = 0; k < n; ++k) {
             if (ml[k].y == 0.f) continue;   // (a NaN score leaves it NaN)
-            const float fk = exp2_fast(ml[k].x - top);
+            const float fk = exp2_between<BF16>(ml[k].x, top);
             l += ml[k].y * fk;
 #pragma unroll
             for (int d = 0; d < kCols; ++d) acc[d] += fk * o[k][d];

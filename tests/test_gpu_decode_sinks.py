@@ -114,3 +114,51 @@ def test_selected_attention_with_a_sink(dev, dtype, kind, gap):
     torch.cuda.synchronize(dev)
     for r in range(2):
         check(out[r], lse[r], q[r], k[:, 0], v[:, 0], dtype)
+
+
+@pytest.mark.parametrize("dtype", [HF, BF])
+@pytest.mark.parametrize("next_n,dim", [(1, 64), (1, 128), (40, 128), (40, 256), (1, 256)])
+def test_a_row_that_sees_one_token_is_its_value(dev, dtype, next_n, dim):
+    """To the bit: its probability is one, whatever its score."""
+    g = torch.Generator(device=dev).manual_seed(dim)
+    n, heads = 30, 8
+    q = torch.randn((n * next_n, heads, dim), generator=g, device=dev).to(dtype)
+    k, v = torch.randn((2, n * next_n, 2, dim), generator=g, device=dev).to(dtype)
+    table = torch.arange(n, dtype=torch.int32, device=dev).unsqueeze(1)
+    lens = torch.full((n,), next_n, dtype=torch.int32, device=dev)
+    alone = (1 << torch.arange(next_n, device=dev)).repeat(n)          # each token sees itself
+    out = gb.tree_attention(q, k, v, table, lens, page_size=next_n, next_n=next_n, tree_mask=alone)
+    assert torch.equal(out, v.repeat_interleave(heads // 2, 1))
+    idx = torch.arange(n * next_n, dtype=torch.int32, device=dev).unsqueeze(1)
+    assert torch.equal(gb.selected_attention(q, k, v, idx), v.repeat_interleave(heads // 2, 1))
+
+
+@pytest.mark.parametrize("dtype", [HF, BF])
+@pytest.mark.parametrize("next_n,q_heads,kv_heads,dim,n", [(1, 8, 2, 128, 20011), (9, 16, 2, 128, 9000), (17, 32, 2, 64, 5000),
+                                                          (5, 12, 2, 256, 9000)])
+@pytest.mark.parametrize("kind,gap,value", [("first", 24, 64), ("many", 20, 4), ("many", 44, 64)])
+def test_tree_attention_with_a_sink_whose_score_is_zero(dev, dtype, next_n, q_heads, kv_heads, dim, n, kind, gap, value):
+    """The others far below zero: the log-sum-exp is small, the references are
+    not; and scores that are no whole powers of two."""
+    g = torch.Generator(device=dev).manual_seed(gap + dim)
+    at, zero = levels(kind, gap, n - next_n, g, dev)
+    k = torch.zeros((n, kv_heads, dim), device=dev)
+    k[:, :, 3] = -gap / 8
+    k[:n - next_n, :, 3] += at.unsqueeze(1) / 8
+    k[:, :, 5] = 0.01 * torch.randn((n, kv_heads), generator=g, device=dev)
+    v = value * (1 + 0.25 * torch.randn(k.shape, generator=g, device=dev))
+    v[:n - next_n][zero] = 0
+    q = torch.zeros((next_n, q_heads, dim), device=dev)
+    q[:, :, 3] = 8
+    q[:, 1::2, 3] = 7
+    q[:, :, 5] = torch.randn((next_n, q_heads), generator=g, device=dev)
+    q, k, v = q.to(dtype), k.to(dtype), v.to(dtype)
+    table = torch.arange(n, dtype=torch.int32, device=dev).unsqueeze(0)
+    out, lse = gb.tree_attention(q, k, v, table, torch.tensor([n], dtype=torch.int32, device=dev), next_n=next_n, scale=1.0,
+                                 return_lse=True)
+    group = q_heads // kv_heads
+    for t in range(next_n):
+        seen = n - next_n + t + 1
+        for h in range(kv_heads):
+            heads = slice(h * group, h * group + group)
+            check(out[t, heads], lse[t, heads], q[t, heads], k[:seen, h], v[:seen, h], dtype)
