@@ -531,8 +531,8 @@ __global__ void __launch_bounds__(Shape<DP, W, ROWS>::kThreads, 1) attention_ker
                     if (__any_sync(~0u, move)) {
                         float f = 1.f;
                         if constexpr (BF16) {
+                            f = move && l > 0.f ? exp2_fast(m - best) : 1.f;
                             if (move) {
-                                f = l > 0.f ? exp2_fast(m - best) : 1.f;
                                 l *= f;
                                 m = best;
                             }
