@@ -498,6 +498,109 @@ int gbtopk_verify_drafts(const void *logits, int dtype, int64_t num_rows, int64_
 /* Scratch of gbtopk_verify_drafts (a pure function; 0 for invalid sizes). */
 size_t gbtopk_verify_workspace_bytes(int64_t num_rows, int64_t vocab, int32_t next_n);
 
+/* ------------------------------------------------------------------------
+ * From the prompt to the cache: norms and rotation of queries and keys with
+ * the cache write in the same pass, caches held in 4 bits, and attention over
+ * packed prompts.
+ *
+ * A 4-bit cache holds one row of gbtopk_int4_row_bytes(head_dim) bytes for
+ * each (slot, kv head), keys and values together: with C = 16 ceil(head_dim /
+ * 32) and S = 8 (16 above head_dim 128),
+ *     C bytes  codes of the key,        C bytes  codes of the value,
+ *     S bytes  scales of the key,       S bytes  scales of the value;
+ * head_dim is a multiple of 16, the rows' strides (in bytes) and the base are
+ * multiples of 16.  A scale belongs to a block of 16 elements: the low seven
+ * bits of a byte, four of exponent (bias 7) and three of mantissa, subnormals
+ * included (2^-9 .. 480; the top bit is ignored, and no byte is a NaN).  A
+ * code is a sign and a magnitude of three bits.  Eight codes are one
+ * little-endian 32-bit word: for j = 0 .. 3 element 2j has its magnitude in
+ * bits 4j .. 4j+2 and its sign in bit (4j + 15) mod 32, element 2j + 1 has
+ * them in bits 4j+16 .. 4j+18 and (4j + 31) mod 32.  The element is
+ *     code * scale * unit,
+ * unit the call's k_scale or v_scale: one power of two for the whole cache
+ * (2^-60 .. 2^60; GBTOPK_EINVAL for other numbers), which is 1 unless the
+ * scales' own range does not do.
+ *
+ * Writing takes, for a block with largest magnitude a, scale = a / (7 unit)
+ * rounded to the nearest of its numbers (ties to even, at most 448) and code =
+ * x / (scale unit) rounded to the nearest whole number (ties to even) and
+ * clamped to -7 .. 7, all of the formula's real numbers: each element is off by
+ * at most half of scale * unit where a is in 7 unit * [2^-6, 448].  A block
+ * whose scale rounds to 0 is zeros, an infinity the largest code, a NaN 0.
+ */
+
+/* Bytes of a row of a 4-bit cache (0 for a head_dim it cannot have). */
+int64_t gbtopk_int4_row_bytes(int32_t head_dim);
+
+/*
+ * gbtopk_rotate_and_cache — per token and head,
+ *     y = x / sqrt(mean(x^2) + eps) * weight      (q and k; weight NULL: y = x)
+ * and a rotation of the first 2 num_freqs elements of q and k by the angles
+ * positions[token] * inv_freq[i]: of elements i and i + num_freqs, or with
+ * `interleaved` of 2i and 2i + 1,
+ *     (a, b) -> (a cos - b sin, b cos + a sin).
+ * The queries go to q_out, keys and values (the latter as they are) to the
+ * caches at slots[token]; a token whose slot is < 0 or >= num_slots writes no
+ * key and value.  Slots of one call differ from one another: where a slot is
+ * listed twice its contents are some mixture of the two tokens'.  Sums and
+ * products are 32 bits, the angles' turns are reduced in 64, and each element
+ * is rounded once.
+ *
+ *  q, k, v      device [num_tokens, q_heads or kv_heads, head_dim] of dtype
+ *               (bf16 or fp16), inner stride 1, the other strides multiples of
+ *               8, 16-byte aligned.  q_heads a multiple of kv_heads, head_dim a
+ *               multiple of 8 up to 256.
+ *  positions    device int32 [num_tokens] (any number).
+ *  inv_freq     device fp32 [num_freqs]: radians a position; num_freqs a
+ *               multiple of 8 up to head_dim / 2, 0: no rotation (both may be
+ *               NULL then).
+ *  q_weight, k_weight  device [head_dim] of weight_dtype (dtype or
+ *               GBTOPK_F32), 16-byte aligned, or NULL.
+ *  q_out        like q; q itself with q's strides is allowed, other overlaps
+ *               are not.
+ *  k_cache, v_cache  as for gbtopk_tree_attention.
+ */
+int gbtopk_rotate_and_cache(const void *q, int dtype, int64_t num_tokens, int64_t q_row_stride,
+                            int64_t q_head_stride, const void *k, int64_t k_row_stride,
+                            int64_t k_head_stride, const void *v, int64_t v_row_stride,
+                            int64_t v_head_stride, int32_t q_heads, int32_t kv_heads,
+                            int32_t head_dim, const int32_t *positions, const float *inv_freq,
+                            int32_t num_freqs, int interleaved, const void *q_weight,
+                            const void *k_weight, int weight_dtype, float eps, void *q_out,
+                            int64_t q_out_row_stride, int64_t q_out_head_stride,
+                            const int32_t *slots, void *k_cache, int64_t k_slot_stride,
+                            int64_t k_cache_head_stride, void *v_cache, int64_t v_slot_stride,
+                            int64_t v_cache_head_stride, int64_t num_slots, void *stream);
+
+/*
+ * gbtopk_rotate_and_cache_int4 — the same into a 4-bit cache (head_dim a
+ * multiple of 16; strides in bytes).  The codes are those of the unrounded
+ * keys: where 32-bit arithmetic cannot tell on which side of a border an
+ * element lies, the row is computed again in 64 bits.
+ */
+int gbtopk_rotate_and_cache_int4(const void *q, int dtype, int64_t num_tokens, int64_t q_row_stride,
+                                 int64_t q_head_stride, const void *k, int64_t k_row_stride,
+                                 int64_t k_head_stride, const void *v, int64_t v_row_stride,
+                                 int64_t v_head_stride, int32_t q_heads, int32_t kv_heads,
+                                 int32_t head_dim, const int32_t *positions, const float *inv_freq,
+                                 int32_t num_freqs, int interleaved, const void *q_weight,
+                                 const void *k_weight, int weight_dtype, float eps, void *q_out,
+                                 int64_t q_out_row_stride, int64_t q_out_head_stride,
+                                 const int32_t *slots, void *cache, int64_t slot_stride,
+                                 int64_t head_stride, int64_t num_slots, float k_scale,
+                                 float v_scale, void *stream);
+
+/*
+ * gbtopk_cache_read_int4 — keys and values of listed slots of a 4-bit cache:
+ * k_out and v_out, device [n, kv_heads, head_dim] of dtype (bf16 or fp16),
+ * contiguous and 16-byte aligned, the exact element rounded once; zeros for a
+ * slot < 0 or >= num_slots.  slots device int32 [n].
+ */
+int gbtopk_cache_read_int4(const void *cache, int64_t slot_stride, int64_t head_stride,
+                           int64_t num_slots, int32_t kv_heads, int32_t head_dim,
+                           const int32_t *slots, int64_t n, float k_scale, float v_scale, int dtype,
+                           void *k_out, void *v_out, void *stream);
+
 /* Human-readable name of a status code (static string).  The pages define no
  * such call; the codes follow the error cases of the FlashInfer
  * `top_k_varlen` page ("Raises") and the status convention above. */

@@ -15,8 +15,10 @@ page-table API quoted on the SGLang PR #33237 page.
 
 ``decode`` holds the rest of a speculative decode step over the same paged
 cache (``tree_attention``, ``selected_attention``,
-``accumulate_cache_weights``, ``evict_cache``, ``verify_drafts``); its names
-are exported here too.
+``accumulate_cache_weights``, ``evict_cache``, ``verify_drafts``); ``prefill`` holds what
+fills that cache, and caches held in 4 bits (``rotate_and_cache``,
+``rotate_and_cache_int4``, ``read_cache_int4``).  The names of both are
+exported here too.
 """
 from __future__ import annotations
 
@@ -491,4 +493,7 @@ def top_k_page_table_transform_cu_seqlens(scores: torch.Tensor, lengths: torch.T
 from . import decode  # noqa: E402
 from .decode import *  # noqa: E402,F401,F403
 
-__all__ += ["decode", *decode.__all__]
+from . import prefill  # noqa: E402
+from .prefill import *  # noqa: E402,F401,F403
+
+__all__ += ["decode", *decode.__all__, "prefill", *prefill.__all__]

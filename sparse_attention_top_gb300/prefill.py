@@ -1,0 +1,188 @@
+"""From the prompt to the cache: norms and rotation of queries and keys with the
+cache write in the same pass, and caches held in 4 bits.
+
+Bindings of ``gbtopk_rotate_and_cache``, ``gbtopk_rotate_and_cache_int4`` and
+``gbtopk_cache_read_int4`` (``include/gbtopk.h``, which states the formulas and
+the rows of a 4-bit cache).  Slots are those of the decode step's calls.  A
+4-bit cache is a uint8 tensor [num_slots, kv_heads, int4_row_bytes(head_dim)]
+whose slot and head strides are multiples of 16 bytes.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple, Optional
+
+import torch
+
+import sparse_attention_top_gb300 as _gb
+
+from .decode import (_F32, _HALF, _I32, _dense, _f, _i32, _i64, _refuse, _vp)
+
+__all__ = ["rotate_and_cache", "rotate_and_cache_int4", "read_cache_int4", "CachedRows", "int4_row_bytes"]
+
+_TOKENS = [_vp, ctypes.c_int, _i64, _i64, _i64] + [_vp, _i64, _i64] * 2 + [_i32] * 3 + [_vp, _vp, _i32, ctypes.c_int] \
+    + [_vp, _vp, ctypes.c_int, _f] + [_vp, _i64, _i64] + [_vp]
+_SIGNATURES = {
+    "gbtopk_rotate_and_cache": _TOKENS + [_vp, _i64, _i64] * 2 + [_i64, _vp],
+    "gbtopk_rotate_and_cache_int4": _TOKENS + [_vp, _i64, _i64, _i64, _f, _f, _vp],
+    "gbtopk_cache_read_int4": [_vp, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _f, _f, ctypes.c_int, _vp, _vp, _vp],
+}
+_calls = None
+
+
+def _lib():
+    global _calls
+    if _calls is None:
+        lib = _gb.load_library()
+        for name, args in _SIGNATURES.items():
+            getattr(lib, name).restype = ctypes.c_int
+            getattr(lib, name).argtypes = args
+        lib.gbtopk_int4_row_bytes.restype = _i64
+        lib.gbtopk_int4_row_bytes.argtypes = [_i32]
+        _calls = lib
+    return _calls
+
+
+def int4_row_bytes(head_dim: int) -> int:
+    """Bytes of a row of a 4-bit cache: a head's key and value in one slot."""
+    n = int(_lib().gbtopk_int4_row_bytes(head_dim)) if 0 < head_dim < 1 << 31 else 0
+    if n == 0:
+        raise ValueError("head_dim of a 4-bit cache must be a multiple of 16 up to 256")
+    return n
+
+
+def _inner(t) -> bool:
+    return t.stride(-1) == 1 or t.shape[-1] < 2
+
+
+def _heads(q, k, v, same_rows: bool):
+    """[rows, heads, dim] queries with keys and values of one shape."""
+    if not (isinstance(q, torch.Tensor) and q.is_cuda and q.dim() == 3 and q.dtype in _HALF and _inner(q)):
+        _gb._require_cuda(q, "q")
+        raise ValueError("q must be a 3-D bf16/fp16 tensor [rows, q_heads, head_dim], inner stride 1")
+    for t, name in ((k, "k"), (v, "v")):
+        if not (isinstance(t, torch.Tensor) and t.dtype is q.dtype and t.device == q.device and t.dim() == 3 and _inner(t)):
+            raise ValueError(f"{name} must be a 3-D {q.dtype} tensor on {q.device}, inner stride 1")
+    rows, heads, dim = q.shape
+    if not (k.shape == v.shape and k.shape[2] == dim and k.shape[1] >= 1 and heads % k.shape[1] == 0
+            and (k.shape[0] == rows or not same_rows)):
+        raise ValueError("k and v must be [rows, kv_heads, head_dim] of one shape, q_heads a multiple of kv_heads")
+    return rows, heads, k.shape[1], dim
+
+
+def _tokens(q, k, v, positions, slots, inv_freq, q_weight, k_weight, eps, interleaved, q_out):
+    """The arguments that both writes share, up to `slots`, and q_out."""
+    rows, heads, kv, dim = _heads(q, k, v, True)
+    dev = q.device
+    freqs = 0 if inv_freq is None else inv_freq.numel() if isinstance(inv_freq, torch.Tensor) else -1
+    weights = [w for w in (q_weight, k_weight) if w is not None]
+    wtype = weights[0].dtype if weights and isinstance(weights[0], torch.Tensor) else q.dtype
+    if q_out is None:
+        q_out = torch.empty((rows, heads, dim), dtype=q.dtype, device=dev)
+    if not ((freqs == 0 or (_dense(inv_freq, dev, _F32, (freqs,)) and _dense(positions, dev, _I32, (rows,))))
+            and freqs % 8 == 0 and 0 <= 2 * freqs <= dim and _dense(slots, dev, _I32, (rows,)) and wtype in (_F32, q.dtype)
+            and all(_dense(w, dev, wtype, (dim,)) for w in weights) and eps >= 0
+            and isinstance(q_out, torch.Tensor) and q_out.shape == q.shape and q_out.dtype is q.dtype and q_out.device == dev
+            and _inner(q_out)):
+        _refuse((freqs == 0 or _dense(inv_freq, dev, _F32, (freqs,)), "inv_freq must be contiguous fp32 [num_freqs]"),
+                (freqs == 0 or _dense(positions, dev, _I32, (rows,)), "positions must be contiguous int32 [rows]"),
+                (freqs % 8 == 0 and 0 <= 2 * freqs <= dim, "inv_freq must have a multiple of 8 entries, at most head_dim / 2"),
+                (_dense(slots, dev, _I32, (rows,)), "slots must be contiguous int32 [rows]"),
+                (wtype in (_F32, q.dtype) and all(_dense(w, dev, wtype, (dim,)) for w in weights),
+                 "the norm weights must be contiguous [head_dim], both fp32 or both of q's type"),
+                (eps >= 0, "eps must not be negative"),
+                (False, "q_out must be a tensor like q, inner stride 1"))
+    qs, ks, vs, os = q.stride(), k.stride(), v.stride(), q_out.stride()
+    return (q.data_ptr(), _gb._DTYPES[q.dtype], rows, qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+            heads, kv, dim, None if positions is None else positions.data_ptr(), None if freqs == 0 else inv_freq.data_ptr(),
+            freqs, int(bool(interleaved)), _gb._ptr(q_weight), _gb._ptr(k_weight), _gb._DTYPES[wtype], eps, q_out.data_ptr(),
+            os[0], os[1], slots.data_ptr()), q_out, kv, dim
+
+
+def rotate_and_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: Optional[torch.Tensor],
+                     slots: torch.Tensor, inv_freq: Optional[torch.Tensor], k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, q_weight: Optional[torch.Tensor] = None,
+                     k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                     q_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Norms and rotates queries and keys and writes keys and values into the
+    caches, in one pass; returns the queries.
+
+    ``q`` [tokens, q_heads, head_dim], ``k`` / ``v`` [tokens, kv_heads,
+    head_dim] bf16/fp16 with any strides that are multiples of 8 elements (the
+    parts of one projection's output will do); ``positions`` and ``slots``
+    int32 [tokens], a token with slot < 0 writes no key and value, the other
+    slots all differ; ``inv_freq`` fp32, radians a position of each rotated
+    pair (elements i and i + len(inv_freq), or neighbours with
+    ``interleaved``), None for no rotation; ``q_weight`` / ``k_weight``
+    [head_dim] of ``q``'s type or fp32, None for no norm; caches as for
+    ``tree_attention``.  ``q_out`` may be ``q``."""
+    args, q_out, kv, dim = _tokens(q, k, v, positions, slots, inv_freq, q_weight, k_weight, eps, interleaved, q_out)
+    dev = q.device
+    for t in (k_cache, v_cache):
+        if not (isinstance(t, torch.Tensor) and t.dtype is q.dtype and t.device == dev and t.dim() == 3
+                and t.shape[1:] == (kv, dim) and t.shape[0] == k_cache.shape[0] and _inner(t)):
+            raise ValueError("the caches must be [num_slots, kv_heads, head_dim] of q's type and one shape, inner stride 1")
+    ks, vs = k_cache.stride(), v_cache.stride()
+    status = (_calls or _lib()).gbtopk_rotate_and_cache(
+        *args, k_cache.data_ptr(), ks[0], ks[1], v_cache.data_ptr(), vs[0], vs[1], k_cache.shape[0], _gb._stream_handle(dev))
+    if status < 0:
+        _gb._check(status)
+    return q_out
+
+
+def _int4(cache, dev, kv: Optional[int], dim: int):
+    """Slots, heads and strides (bytes) of a 4-bit cache."""
+    if not (isinstance(cache, torch.Tensor) and cache.dtype is torch.uint8 and cache.device == dev and cache.dim() == 3
+            and cache.shape[2] == int4_row_bytes(dim) and cache.stride(2) == 1
+            and (kv is None or cache.shape[1] == kv) and cache.shape[1] >= 1):
+        raise ValueError(f"cache must be a uint8 tensor [num_slots, kv_heads, int4_row_bytes({dim})] on {dev}, inner stride 1")
+    return cache.shape[0], cache.shape[1], cache.stride()
+
+
+def rotate_and_cache_int4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: Optional[torch.Tensor],
+                          slots: torch.Tensor, inv_freq: Optional[torch.Tensor], cache: torch.Tensor,
+                          q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                          eps: float = 1e-6, interleaved: bool = False, k_scale: float = 1.0, v_scale: float = 1.0,
+                          q_out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``rotate_and_cache`` into a 4-bit cache (``head_dim`` a multiple of 16).
+    ``k_scale`` / ``v_scale``: powers of two, the unit of the cache's scales
+    (whose own range, 2^-9 to 448, as a rule needs no other than 1)."""
+    args, q_out, kv, dim = _tokens(q, k, v, positions, slots, inv_freq, q_weight, k_weight, eps, interleaved, q_out)
+    n, _, cs = _int4(cache, q.device, kv, dim)
+    status = (_calls or _lib()).gbtopk_rotate_and_cache_int4(
+        *args, cache.data_ptr(), cs[0], cs[1], n, k_scale, v_scale, _gb._stream_handle(q.device))
+    if status < 0:
+        _gb._check(status)
+    return q_out
+
+
+class CachedRows(NamedTuple):
+    k: torch.Tensor   # [n, kv_heads, head_dim]
+    v: torch.Tensor
+
+
+def read_cache_int4(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, dtype: torch.dtype = torch.bfloat16,
+                    k_scale: float = 1.0, v_scale: float = 1.0, k_out: Optional[torch.Tensor] = None,
+                    v_out: Optional[torch.Tensor] = None) -> CachedRows:
+    """Keys and values of the listed slots (int32 [n]) of a 4-bit cache, zeros
+    for slots that do not exist."""
+    _gb._require_cuda(cache, "cache")
+    dev = cache.device
+    n, kv, cs = _int4(cache, dev, None, head_dim)
+    listed = slots.numel() if isinstance(slots, torch.Tensor) else -1
+    shape = (listed, kv, head_dim)
+    if not (_dense(slots, dev, _I32, (listed,)) and dtype in _HALF and (k_out is None or _dense(k_out, dev, dtype, shape))
+            and (v_out is None or _dense(v_out, dev, dtype, shape))):
+        _refuse((_dense(slots, dev, _I32, (listed,)), "slots must be contiguous int32 [n]"),
+                (dtype in _HALF, "dtype must be bf16 or fp16"),
+                (False, "k_out and v_out must be contiguous [n, kv_heads, head_dim] of dtype"))
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=dev)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=dtype, device=dev)
+    status = (_calls or _lib()).gbtopk_cache_read_int4(
+        cache.data_ptr(), cs[0], cs[1], n, kv, head_dim, slots.data_ptr(), listed, k_scale, v_scale, _gb._DTYPES[dtype],
+        k_out.data_ptr(), v_out.data_ptr(), _gb._stream_handle(dev))
+    if status < 0:
+        _gb._check(status)
+    return CachedRows(k_out, v_out)

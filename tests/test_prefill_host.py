@@ -1,0 +1,92 @@
+"""Refusals of the prompt's entry points: decided on the host, before anything
+is enqueued (the addresses here are never dereferenced)."""
+import math
+
+import pytest
+
+import sparse_attention_top_gb300 as gb
+
+A = 0x10000000
+
+
+def call(name, order, defaults, **kw):
+    a = dict(defaults)
+    a.update(kw)
+    assert set(a) == set(order)
+    return getattr(gb.prefill._lib(), name)(*[a[k] for k in order])
+
+
+TOKENS = ("q dtype rows q_row q_head k k_row k_head v v_row v_head q_heads kv_heads dim positions freq freqs pairs wq wk wtype eps "
+          "q_out qo_row qo_head slots").split()
+TOKENS_DEFAULTS = dict(q=A, dtype=1, rows=4, q_row=768, q_head=64, k=A, k_row=768, k_head=64, v=A, v_row=768, v_head=64, q_heads=8,
+                       kv_heads=2, dim=64, positions=A, freq=A, freqs=32, pairs=0, wq=A, wk=A, wtype=1, eps=1e-6, q_out=A,
+                       qo_row=512, qo_head=64, slots=A)
+
+
+def rotate(**kw):
+    return call("gbtopk_rotate_and_cache", TOKENS + "kc k_slot kc_head vc v_slot vc_head n stream".split(),
+                {**TOKENS_DEFAULTS, "kc": A, "k_slot": 128, "kc_head": 64, "vc": A, "v_slot": 128, "vc_head": 64, "n": 50,
+                 "stream": None}, **kw)
+
+
+def rotate4(**kw):
+    return call("gbtopk_rotate_and_cache_int4", TOKENS + "cache slot head n ks vs stream".split(),
+                {**TOKENS_DEFAULTS, "cache": A, "slot": 160, "head": 80, "n": 50, "ks": 1.0, "vs": 1.0, "stream": None}, **kw)
+
+
+def read(**kw):
+    return call("gbtopk_cache_read_int4", "cache slot head n kv_heads dim slots listed ks vs dtype k v stream".split(),
+                dict(cache=A, slot=160, head=80, n=50, kv_heads=2, dim=64, slots=A, listed=7, ks=1.0, vs=1.0, dtype=1, k=A, v=A,
+                     stream=None), **kw)
+
+
+SHARED = [
+    (dict(dtype=7), gb.EINVAL), (dict(dtype=0), gb.EUNSUPPORTED), (dict(rows=-1), gb.EINVAL), (dict(q_heads=0), gb.EINVAL),
+    (dict(kv_heads=3), gb.EINVAL), (dict(dim=0), gb.EINVAL), (dict(dim=60), gb.EUNSUPPORTED), (dict(dim=272), gb.EUNSUPPORTED),
+    (dict(q=None), gb.EINVAL), (dict(k=None), gb.EINVAL), (dict(v=None), gb.EINVAL), (dict(q_out=None), gb.EINVAL),
+    (dict(q=A + 8), gb.EALIGN), (dict(v_row=770), gb.EALIGN), (dict(qo_head=4), gb.EALIGN), (dict(k_head=-8), gb.EINVAL),
+    (dict(positions=None), gb.EINVAL), (dict(freq=None), gb.EINVAL), (dict(freqs=40), gb.EINVAL), (dict(freqs=-8), gb.EINVAL),
+    (dict(freqs=12), gb.EUNSUPPORTED), (dict(wtype=2), gb.EUNSUPPORTED), (dict(wq=A + 4), gb.EALIGN), (dict(eps=-1.0), gb.EINVAL),
+    (dict(eps=math.nan), gb.EINVAL), (dict(slots=None), gb.EINVAL), (dict(slots=A + 2), gb.EALIGN), (dict(n=-1), gb.EINVAL),
+    (dict(n=1 << 31), gb.EUNSUPPORTED), (dict(rows=1 << 31), gb.EUNSUPPORTED), (dict(positions=A + 1), gb.EALIGN),
+]
+
+
+@pytest.mark.parametrize("kw,status", SHARED + [
+    (dict(kc=None), gb.EINVAL), (dict(vc=A + 2), gb.EALIGN), (dict(k_slot=132), gb.EALIGN), (dict(vc_head=-64), gb.EINVAL)])
+def test_rotate_and_cache_refuses(kw, status):
+    assert rotate(**kw) == status
+
+
+UNITS = [(dict(ks=0.0), gb.EINVAL), (dict(ks=3.0), gb.EINVAL), (dict(vs=-2.0), gb.EINVAL), (dict(vs=math.inf), gb.EINVAL),
+         (dict(vs=math.nan), gb.EINVAL), (dict(ks=2.0 ** 61), gb.EINVAL), (dict(ks=2.0 ** -61), gb.EINVAL)]
+
+
+@pytest.mark.parametrize("kw,status", SHARED + UNITS + [
+    (dict(cache=None), gb.EINVAL), (dict(cache=A + 8), gb.EALIGN), (dict(slot=168), gb.EALIGN), (dict(head=-80), gb.EINVAL),
+    (dict(dim=72, freqs=0), gb.EUNSUPPORTED)])
+def test_rotate_and_cache_int4_refuses(kw, status):
+    assert rotate4(**kw) == status
+
+
+@pytest.mark.parametrize("kw,status", UNITS + [
+    (dict(dtype=0), gb.EUNSUPPORTED), (dict(dtype=5), gb.EINVAL), (dict(dim=72), gb.EUNSUPPORTED), (dict(kv_heads=0), gb.EINVAL),
+    (dict(cache=None), gb.EINVAL), (dict(cache=A + 4), gb.EALIGN), (dict(slot=72), gb.EALIGN), (dict(listed=-1), gb.EINVAL),
+    (dict(listed=1 << 31), gb.EUNSUPPORTED), (dict(slots=None), gb.EINVAL), (dict(k=None), gb.EINVAL), (dict(v=None), gb.EINVAL),
+    (dict(slots=A + 1), gb.EALIGN), (dict(v=A + 8), gb.EALIGN), (dict(n=-1), gb.EINVAL)])
+def test_cache_read_int4_refuses(kw, status):
+    assert read(**kw) == status
+
+
+def test_nothing_to_do():
+    assert rotate(rows=0, q=None, k=None, v=None, q_out=None, slots=None, positions=None) == gb.OK
+    assert rotate4(rows=0, q=None, k=None, v=None, q_out=None, slots=None, positions=None) == gb.OK
+    assert read(listed=0, slots=None, k=None, v=None) == gb.OK
+
+
+@pytest.mark.parametrize("dim,n", [(16, 48), (64, 80), (80, 112), (96, 112), (128, 144), (144, 192), (256, 288)])
+def test_int4_row_bytes(dim, n):
+    assert gb.int4_row_bytes(dim) == n
+    for bad in (0, -16, dim + 8, 272):
+        with pytest.raises(ValueError):
+            gb.int4_row_bytes(bad)
