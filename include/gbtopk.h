@@ -601,6 +601,31 @@ int gbtopk_cache_read_int4(const void *cache, int64_t slot_stride, int64_t head_
                            const int32_t *slots, int64_t n, float k_scale, float v_scale, int dtype,
                            void *k_out, void *v_out, void *stream);
 
+/*
+ * gbtopk_tree_attention_int4, gbtopk_selected_attention_int4 — the two
+ * attention calls over a 4-bit cache: the same rows, masks, lists, outputs and
+ * workspace (gbtopk_attention_workspace_bytes), with cache, strides (in bytes)
+ * and units as above and head_dim a multiple of 16.  Keys and values are the
+ * exact elements.  Arithmetic as there, but fp16 probabilities keep 16 bits and
+ * have no scale to share.
+ */
+int gbtopk_tree_attention_int4(const void *q, int dtype, int64_t num_rows, int64_t q_row_stride,
+                               int64_t q_head_stride, int32_t q_heads, int32_t kv_heads,
+                               int32_t head_dim, const void *cache, int64_t slot_stride,
+                               int64_t head_stride, int64_t num_slots, float k_scale, float v_scale,
+                               const int32_t *page_table, int64_t pt_cols, int64_t pt_row_stride,
+                               int32_t page_size, const int32_t *seq_lens, int32_t next_n,
+                               const int64_t *tree_mask, float scale, void *out, float *lse,
+                               void *workspace, size_t workspace_bytes, void *stream);
+
+int gbtopk_selected_attention_int4(const void *q, int dtype, int64_t num_rows, int64_t q_row_stride,
+                                   int64_t q_head_stride, int32_t q_heads, int32_t kv_heads,
+                                   int32_t head_dim, const void *cache, int64_t slot_stride,
+                                   int64_t head_stride, int64_t num_slots, float k_scale,
+                                   float v_scale, const int32_t *indices, int64_t top_k,
+                                   int64_t idx_row_stride, float scale, void *out, float *lse,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+
 /* Human-readable name of a status code (static string).  The pages define no
  * such call; the codes follow the error cases of the FlashInfer
  * `top_k_varlen` page ("Raises") and the status convention above. */

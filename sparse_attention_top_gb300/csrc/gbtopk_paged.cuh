@@ -79,7 +79,7 @@ struct Unit {
 };
 
 struct ScanScratch {
-    int64_t warps[16], low[16];
+    int64_t warps[20], low[20];   // of a block of up to 640 threads
     int64_t off;
     int32_t b;
 };
@@ -133,6 +133,7 @@ struct Walk {
 // the block.
 template <int KT, int THREADS>
 __device__ int64_t sum_cost(const AttnParams &p, int32_t b, int64_t *before, ScanScratch *scratch) {
+    static_assert(THREADS / 32 <= 20, "scratch");
     if (!p.seq_lens) {
         const int64_t each = static_cast<int64_t>(tiles_of<KT>(span_of(p, 0)) + kUnitCost) * p.request_units;
         *before = b * each;

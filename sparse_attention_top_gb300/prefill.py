@@ -1,8 +1,9 @@
 """From the prompt to the cache: norms and rotation of queries and keys with the
-cache write in the same pass, and caches held in 4 bits.
+cache write in the same pass, and caches held in 4 bits with attention over them.
 
-Bindings of ``gbtopk_rotate_and_cache``, ``gbtopk_rotate_and_cache_int4`` and
-``gbtopk_cache_read_int4`` (``include/gbtopk.h``, which states the formulas and
+Bindings of ``gbtopk_rotate_and_cache``, ``gbtopk_rotate_and_cache_int4``,
+``gbtopk_cache_read_int4``, ``gbtopk_tree_attention_int4`` and
+``gbtopk_selected_attention_int4`` (``include/gbtopk.h``, which states the formulas and
 the rows of a 4-bit cache).  Slots are those of the decode step's calls.  A
 4-bit cache is a uint8 tensor [num_slots, kv_heads, int4_row_bytes(head_dim)]
 whose slot and head strides are multiples of 16 bytes.
@@ -16,15 +17,20 @@ import torch
 
 import sparse_attention_top_gb300 as _gb
 
-from .decode import (_F32, _HALF, _I32, _dense, _f, _i32, _i64, _refuse, _vp)
+from .decode import (_F32, _HALF, _I32, _I64, _PAGE_RULE, _PAGES, _QUERY, MAX_PAGE_SIZE, _attention_bytes, _dense, _f, _i32,
+                     _i64, _maybe, _outputs, _query, _refuse, _requests, _scratch, _sz, _table, _vp)
 
-__all__ = ["rotate_and_cache", "rotate_and_cache_int4", "read_cache_int4", "CachedRows", "int4_row_bytes"]
+__all__ = ["rotate_and_cache", "rotate_and_cache_int4", "read_cache_int4", "CachedRows", "int4_row_bytes",
+           "tree_attention_int4", "selected_attention_int4"]
 
 _TOKENS = [_vp, ctypes.c_int, _i64, _i64, _i64] + [_vp, _i64, _i64] * 2 + [_i32] * 3 + [_vp, _vp, _i32, ctypes.c_int] \
     + [_vp, _vp, ctypes.c_int, _f] + [_vp, _i64, _i64] + [_vp]
 _SIGNATURES = {
     "gbtopk_rotate_and_cache": _TOKENS + [_vp, _i64, _i64] * 2 + [_i64, _vp],
     "gbtopk_rotate_and_cache_int4": _TOKENS + [_vp, _i64, _i64, _i64, _f, _f, _vp],
+    "gbtopk_tree_attention_int4": _QUERY + [_vp, _i64, _i64, _i64, _f, _f] + _PAGES + [_f, _vp, _vp, _vp, _sz, _vp],
+    "gbtopk_selected_attention_int4": _QUERY + [_vp, _i64, _i64, _i64, _f, _f] + [_vp, _i64, _i64]
+    + [_f, _vp, _vp, _vp, _sz, _vp],
     "gbtopk_cache_read_int4": [_vp, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _f, _f, ctypes.c_int, _vp, _vp, _vp],
 }
 _calls = None
@@ -186,3 +192,63 @@ def read_cache_int4(cache: torch.Tensor, slots: torch.Tensor, head_dim: int, dty
     if status < 0:
         _gb._check(status)
     return CachedRows(k_out, v_out)
+
+
+def tree_attention_int4(q: torch.Tensor, cache: torch.Tensor, page_table: torch.Tensor, seq_lens: torch.Tensor,
+                        page_size: int = 1, next_n: int = 1, tree_mask: Optional[torch.Tensor] = None,
+                        scale: Optional[float] = None, k_scale: float = 1.0, v_scale: float = 1.0,
+                        out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                        return_lse: bool = False, workspace: Optional[torch.Tensor] = None):
+    """``tree_attention`` over a 4-bit cache; ``k_scale`` / ``v_scale`` as it
+    was written with, everything else as there."""
+    shape, dev, qs = _query(q)
+    rows, heads, dim = shape
+    requests = _requests(rows, next_n)
+    slots, kv, cs = _int4(cache, dev, None, dim)
+    if not (heads % kv == 0 and 1 <= page_size <= MAX_PAGE_SIZE and _table(page_table, dev, requests)
+            and _dense(seq_lens, dev, _I32, (requests,)) and _maybe(tree_mask, dev, _I64, (rows,))):
+        _refuse((heads % kv == 0, "q_heads must be a multiple of kv_heads"),
+                (1 <= page_size <= MAX_PAGE_SIZE, _PAGE_RULE),
+                (_table(page_table, dev, requests), "page_table must be int32 [num_requests, pt_cols], inner stride 1"),
+                (_dense(seq_lens, dev, _I32, (requests,)), "seq_lens must be contiguous int32 [num_requests]"),
+                (False, "tree_mask must be contiguous int64 [num_rows]"))
+    out, lse = _outputs(q, shape, dev, out, lse, return_lse)
+    lib = _calls or _lib()
+    stream = _gb._stream_handle(dev)
+    with _gb._LOCKS[dev.index, stream]:
+        ws, ws_bytes = _scratch(workspace, dev, stream, _attention_bytes(rows, heads, kv, dim))
+        status = lib.gbtopk_tree_attention_int4(
+            q.data_ptr(), _gb._DTYPES[q.dtype], rows, qs[0], qs[1], heads, kv, dim, cache.data_ptr(), cs[0], cs[1], slots,
+            k_scale, v_scale, page_table.data_ptr(), page_table.shape[1], page_table.stride(0), page_size,
+            seq_lens.data_ptr(), next_n, None if tree_mask is None else tree_mask.data_ptr(),
+            dim ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(), ws,
+            ws_bytes, stream)
+    if status < 0:
+        _gb._check(status)
+    return out if lse is None else (out, lse)
+
+
+def selected_attention_int4(q: torch.Tensor, cache: torch.Tensor, indices: torch.Tensor, scale: Optional[float] = None,
+                            k_scale: float = 1.0, v_scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                            lse: Optional[torch.Tensor] = None, return_lse: bool = False,
+                            workspace: Optional[torch.Tensor] = None):
+    """``selected_attention`` over a 4-bit cache."""
+    shape, dev, qs = _query(q)
+    rows, heads, dim = shape
+    slots, kv, cs = _int4(cache, dev, None, dim)
+    if not (heads % kv == 0 and _table(indices, dev, rows)):
+        _refuse((heads % kv == 0, "q_heads must be a multiple of kv_heads"),
+                (False, "indices must be int32 [num_rows, top_k], inner stride 1"))
+    out, lse = _outputs(q, shape, dev, out, lse, return_lse)
+    lib = _calls or _lib()
+    stream = _gb._stream_handle(dev)
+    with _gb._LOCKS[dev.index, stream]:
+        ws, ws_bytes = _scratch(workspace, dev, stream, _attention_bytes(rows, heads, kv, dim))
+        status = lib.gbtopk_selected_attention_int4(
+            q.data_ptr(), _gb._DTYPES[q.dtype], rows, qs[0], qs[1], heads, kv, dim, cache.data_ptr(), cs[0], cs[1], slots,
+            k_scale, v_scale, indices.data_ptr(), indices.shape[1], indices.stride(0),
+            dim ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(), ws,
+            ws_bytes, stream)
+    if status < 0:
+        _gb._check(status)
+    return out if lse is None else (out, lse)

@@ -90,3 +90,45 @@ def test_int4_row_bytes(dim, n):
     for bad in (0, -16, dim + 8, 272):
         with pytest.raises(ValueError):
             gb.int4_row_bytes(bad)
+
+
+QUERY = "q dtype rows q_row q_head q_heads kv_heads dim cache slot head n ks vs".split()
+QUERY_DEFAULTS = dict(q=A, dtype=1, rows=4, q_row=512, q_head=64, q_heads=8, kv_heads=2, dim=64, cache=A, slot=160, head=80, n=50,
+                      ks=1.0, vs=1.0)
+TAIL = "scale out lse ws ws_bytes stream".split()
+TAIL_DEFAULTS = dict(scale=1.0, out=A, lse=None, ws=A, ws_bytes=1 << 30, stream=None)
+
+
+def tree4(**kw):
+    return call("gbtopk_tree_attention_int4", QUERY + "table cols pt_stride page lens next_n tree".split() + TAIL,
+                {**QUERY_DEFAULTS, "table": A, "cols": 7, "pt_stride": 7, "page": 16, "lens": A, "next_n": 2, "tree": None,
+                 **TAIL_DEFAULTS}, **kw)
+
+
+def selected4(**kw):
+    return call("gbtopk_selected_attention_int4", QUERY + "idx top_k idx_stride".split() + TAIL,
+                {**QUERY_DEFAULTS, "idx": A, "top_k": 8, "idx_stride": 8, **TAIL_DEFAULTS}, **kw)
+
+
+ATTENTION = UNITS + [
+    (dict(dtype=7), gb.EINVAL), (dict(dtype=0), gb.EUNSUPPORTED), (dict(rows=-2), gb.EINVAL), (dict(q_heads=0), gb.EINVAL),
+    (dict(kv_heads=3), gb.EINVAL), (dict(dim=72), gb.EUNSUPPORTED), (dict(dim=272), gb.EUNSUPPORTED), (dict(q=None), gb.EINVAL),
+    (dict(cache=None), gb.EINVAL), (dict(q=A + 8), gb.EALIGN), (dict(cache=A + 8), gb.EALIGN), (dict(slot=168), gb.EALIGN),
+    (dict(head=-80), gb.EINVAL), (dict(n=-1), gb.EINVAL), (dict(n=1 << 31), gb.EUNSUPPORTED), (dict(out=None), gb.EINVAL),
+    (dict(out=A + 2), gb.EALIGN), (dict(lse=A + 2), gb.EALIGN), (dict(ws=None), gb.EWORKSPACE), (dict(ws=A + 16), gb.EWORKSPACE),
+    (dict(ws_bytes=16), gb.EWORKSPACE)]
+
+
+@pytest.mark.parametrize("kw,status", ATTENTION + [
+    (dict(next_n=0), gb.EINVAL), (dict(next_n=3), gb.EINVAL), (dict(rows=130, next_n=65), gb.EUNSUPPORTED), (dict(page=0), gb.EINVAL),
+    (dict(cols=-1), gb.EINVAL), (dict(pt_stride=6), gb.EINVAL), (dict(table=None), gb.EINVAL), (dict(lens=None), gb.EINVAL),
+    (dict(tree=A + 4), gb.EALIGN)])
+def test_tree_attention_int4_refuses(kw, status):
+    assert tree4(**kw) == status
+
+
+@pytest.mark.parametrize("kw,status", ATTENTION + [
+    (dict(idx=None), gb.EINVAL), (dict(top_k=-1), gb.EINVAL), (dict(idx_stride=7), gb.EINVAL),
+    (dict(top_k=1 << 31, idx_stride=1 << 31), gb.EUNSUPPORTED)])
+def test_selected_attention_int4_refuses(kw, status):
+    assert selected4(**kw) == status
