@@ -24,28 +24,33 @@
 //
 // A block, one an SM: four warps of softmax and output, four that turn the codes
 // of keys into tensor memory, four that turn those of values into a
-// shared-memory tile, four that copy the cached rows (cp.async, 16 bytes a
-// lane) into a ring, one that issues products, three that look up slots and
-// fetch queries.  Shares, units and the join are those of gbtopk_attention.cu.
+// shared-memory tile, seven that look up slots and have the rows copied into a
+// ring (each a tile in turn; a lane gathers four rows by a tensor map), one that
+// issues products.  Shares, units and the join are
+// those of gbtopk_attention.cu.
 #include <cfloat>
 #include <cmath>
+#include <numeric>
 
 #include "gbtopk_int4.cuh"
 #include "gbtopk_join.cuh"
+#include "gbtopk_tma.cuh"
 
 namespace gbtopk {
 namespace {
 
 constexpr int kTile = 128;          // positions a tile
 constexpr int kThreads4 = 640;
-constexpr int kSlotRing = 8;        // tiles whose slots are looked up ahead
 constexpr int kMaxStages = 12;
+constexpr int kMasks = 16;          // tiles whose validity bits are kept: the ring's and the two that are decoded
 constexpr float kRise = 8.f;        // rise of a score over its row's reference (base 2) that moves it
-constexpr int kKeyWarp = 4, kValueWarp = 8, kCopyWarp = 12, kIssueWarp = 16;
+constexpr float kFar = 0x1p100f;
+constexpr int kKeyWarp = 4, kValueWarp = 8, kCopyWarp = 12, kCopyWarps = 7, kIssueWarp = 19;
 
 struct Int4Params {
-    AttnParams a;                   // k, k_slot, k_head: the rows, strides in bytes
-    int32_t codes, row, stride;     // bytes of a row's codes, of a row, of a row in shared memory
+    CUtensorMap rows;               // the cache: a line of `row` bytes every pitch
+    AttnParams a;                   // k_slot, k_head: strides in pitches
+    int32_t codes, row, four;       // bytes of a row's codes, of a row, of four rows in shared memory
     int32_t stages, q_bufs;
     uint32_t q_off, p_off, ring_off, stage_bytes, shared_off;   // shared memory
     float k_mul, v_mul;             // c and the values' unit, times 2^15
@@ -53,19 +58,64 @@ struct Int4Params {
 
 struct Shared4 {
     uint64_t full[kMaxStages], empty[kMaxStages];
-    uint64_t slots_full[kSlotRing], slots_empty[kSlotRing];
     uint64_t q_full[2], q_empty[2];
     uint64_t key_full[2], s_full[2], p_full[2], v_full[2], v_free[2], pv_done[2];
     uint64_t drain;
-    int32_t slots[kSlotRing][kTile];
-    uint64_t tree[64];              // tree masks of the unit's rows
-    int64_t row_at[64];             // (row, head) of the output, -1: none
-    float m[64], scale[64];         // references; factors of a move, of the output
-    float part[4][64];              // a warp's maxima or sums
+    uint32_t mask[kMasks][4];       // positions of a tile with a slot: bit b of word w is position 4 b + w
+    uint64_t tree[32];              // tree masks of the unit's rows
+    int64_t row_at[32];             // (row, head) of the output, -1: none
+    float4 less_m[8];               // rows' references, negated; kFar: none yet
+    float4 scale[8];                // factors of a move, of the output
+    float part[4][32];              // a warp's maxima or sums
     ScanScratch scan;
     uint32_t tmem;
     uint32_t abort;
 };
+
+__device__ __forceinline__ void tmem_load8(uint32_t addr, uint32_t *v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(addr)
+                 : "memory");
+}
+
+// A wait of the whole warp.  Between two looks at the clock nothing but tries,
+// because the six roles' loops share the instruction cache, which all of their
+// code together only just fits: whatever is in a loop costs every role.
+__device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, const Waits &w) {
+    bool got = bar_try(bar, parity);
+    if (!got) {
+        const long long t0 = clock64();
+        uint32_t tries = 0;
+        while (!(got = bar_try(bar, parity))) {
+            if (++tries & 255) continue;
+            if (*w.given_up) break;
+            if (clock64() - t0 > w.limit) {
+                *w.given_up = 1;
+                break;
+            }
+        }
+    }
+    return __all_sync(~0u, got);
+}
+
+// Products as in gbtopk_mma.cuh, issued by the lane with `lead` of a converged
+// warp: a predicate, where a branch would move every descriptor to uniform
+// registers again.
+__device__ __forceinline__ void mma_ss_if(bool lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(static_cast<uint32_t>(lead))
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(bool lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(static_cast<uint32_t>(lead))
+        : "memory");
+}
 
 // Barrier of the softmax warps.
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
@@ -88,46 +138,52 @@ __device__ __forceinline__ float of_order(int32_t b) {
     return b == INT32_MIN ? -INFINITY : __int_as_float(b ^ ((b >> 31) & 0x7fffffff));
 }
 
-// The block of sixteen elements whose codes are c0, c1 and whose scale (times
-// 2^118, twice) is s, times 2^-15.
-__device__ __forceinline__ void decode16(uint32_t c0, uint32_t c1, uint32_t s, uint32_t *out) {
-    out[0] = mul_bf16x2(int4_pair<0>(c0), s);
-    out[1] = mul_bf16x2(int4_pair<1>(c0), s);
-    out[2] = mul_bf16x2(int4_pair<2>(c0), s);
-    out[3] = mul_bf16x2(int4_pair<3>(c0), s);
-    out[4] = mul_bf16x2(int4_pair<0>(c1), s);
-    out[5] = mul_bf16x2(int4_pair<1>(c1), s);
-    out[6] = mul_bf16x2(int4_pair<2>(c1), s);
-    out[7] = mul_bf16x2(int4_pair<3>(c1), s);
+// 32 elements (two blocks, their scales the bytes of `two`) times 2^-15, as bf16.
+__device__ __forceinline__ void decode32(const uint4 &c, uint32_t two, uint32_t *out) {
+    const uint32_t s = int4_scales2(__byte_perm(two, 0, 0x4140)), s0 = __byte_perm(s, 0, 0x1010), s1 = __byte_perm(s, 0, 0x3232);
+    const uint32_t word[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+        out[4 * w] = mul_bf16x2(int4_pair<0>(word[w]), w < 2 ? s0 : s1);
+        out[4 * w + 1] = mul_bf16x2(int4_pair<1>(word[w]), w < 2 ? s0 : s1);
+        out[4 * w + 2] = mul_bf16x2(int4_pair<2>(word[w]), w < 2 ? s0 : s1);
+        out[4 * w + 3] = mul_bf16x2(int4_pair<3>(word[w]), w < 2 ? s0 : s1);
+    }
 }
+
+__device__ __forceinline__ void put16(uint32_t addr, const uint32_t *v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]) : "memory");
+}
+
+// Columns of a product: R rows, two each with fp16; 16 at least.
+template <bool F16, int R>
+constexpr int kCols = F16 ? 2 * R : R < 16 ? 16 : R;
 
 // R: query rows of a unit.  WIDE: head dimensions above 128.
 template <bool F16, int R, bool WIDE>
 __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __grid_constant__ Int4Params pp) {
     const AttnParams &p = pp.a;
-    constexpr int N = F16 ? 2 * R : R;              // columns of a product
+    constexpr int N = kCols<F16, R>;
+    constexpr int CH = R < 16 ? 8 : 16;             // rows at a time
     constexpr int kBlocks = WIDE ? 2 : 1;           // blocks of 128 of the head dimension
     constexpr uint32_t kKeyCols = WIDE ? 128 : 64;  // tensor memory columns of a tile's keys
     constexpr uint32_t kS = 0, kK = 2 * N, kO = kK + 2 * kKeyCols;
-    constexpr uint32_t kValueBytes = kTile * 256, kProbBytes = kTile * 128 * (N > 64 ? 2 : 1);
-    static_assert(kO + kBlocks * N <= 512, "tensor memory");
+    constexpr uint32_t kValueBytes = kTile * 256, kProbBytes = kTile * 128;
+    static_assert(kO + kBlocks * N <= 512 && N <= 64, "tensor memory, one panel of probabilities");
     extern __shared__ uint8_t raw[];
     uint8_t *smem = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     Shared4 &sh = *reinterpret_cast<Shared4 *>(smem + pp.shared_off);
+    float *less_m = reinterpret_cast<float *>(sh.less_m), *scale = reinterpret_cast<float *>(sh.scale);
     const uint32_t base = smem_addr(smem), v_smem = base;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     if (threadIdx.x == 0) {
         for (int i = 0; i < pp.stages; ++i) {
-            bar_init(&sh.full[i], 128);
+            bar_init(&sh.full[i], 1);
             bar_init(&sh.empty[i], 8);
         }
-        for (int i = 0; i < kSlotRing; ++i) {
-            bar_init(&sh.slots_full[i], 1);
-            bar_init(&sh.slots_empty[i], 4);
-        }
         for (int i = 0; i < 2; ++i) {
-            bar_init(&sh.q_full[i], 3);
+            bar_init(&sh.q_full[i], kCopyWarps);
             bar_init(&sh.q_empty[i], 1);
             bar_init(&sh.key_full[i], 4);
             bar_init(&sh.s_full[i], 1);
@@ -154,6 +210,11 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
     const int32_t rows = p.next_n * p.group;   // of a (request, kv head)
     bool ok = true;
 
+    // The softmax warps hold sums and scores of 32 rows: 152 registers a thread
+    // for them and 80 for the other four warpgroups are 472 of the launch's 480.
+    if (warp < kKeyWarp) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+
     if (warp < kKeyWarp) {
         // ------------------------------------------------ softmax, output
         const int at = warp * 32 + lane;                               // position of the tile, and lane of O
@@ -169,7 +230,7 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
                 const int64_t r = static_cast<int64_t>(u.b) * p.next_n + t;
                 sh.row_at[at] = at < here ? r * p.q_heads + h * p.group + gq : -1;
                 sh.tree[at] = at >= here || !p.seq_lens ? 0 : p.tree_mask ? static_cast<uint64_t>(fetch(p.tree_mask + r)) : ~0ull >> (63 - t);
-                sh.m[at] = -INFINITY;
+                less_m[at] = at < here ? kFar : 0.f;
             }
             if (at == 0) {   // the blocks that share the unit
                 int32_t *ends = p.unit_ends + 2 * (static_cast<int64_t>(u.b) * p.request_units + u.hm);
@@ -189,145 +250,138 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
             const uint32_t job0 = job;
             for (int32_t i = u.t0; i < u.t1; ++i, ++job) {
                 const uint32_t sb = job & 1, ph = (job >> 1) & 1;
-                ok = __all_sync(~0u, bar_wait(&sh.slots_full[job % kSlotRing], (job / kSlotRing) & 1, abort) &&
-                                         bar_wait(&sh.s_full[sb], ph, abort));
-                // (the warps leave together: they meet at barriers)
-                if (softmax_any(!ok)) {
-                    ok = false;
-                    break;
-                }
+                ok = wait(&sh.s_full[sb], ph, abort);
                 tc_fence_after();
                 const uint32_t t_s = tmem + lanes + kS + sb * N;
-                const bool is = reinterpret_cast<volatile int32_t *>(sh.slots[job % kSlotRing])[at] >= 0;
-                const bool drafts = i * kTile > u.span.ctx - kTile;          // the tile has drafted tokens
-                const int32_t draft = i * kTile + at - u.span.ctx;
-                // 16 rows' scores of the thread's position, base 2
-                auto scores = [&](int c, float *t) {
-                    uint32_t x[16];
-                    tmem_load16(t_s + c, x);
-                    if constexpr (F16) {
-                        uint32_t y[16];
-                        tmem_load16(t_s + R + c, y);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) t[k] = (__uint_as_float(x[k]) + __uint_as_float(y[k])) * pp.k_mul;
-                    } else {
-                        tc_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) t[k] = __uint_as_float(x[k]) * pp.k_mul;
-                    }
-                    if (!is) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) t[k] = -INFINITY;
-                    } else if (drafts && draft >= 0) {
-#pragma unroll
-                        for (int k = 0; k < 16; ++k)
-                            if (draft > 63 || !((sh.tree[c + k] >> draft) & 1)) t[k] = -INFINITY;
-                    }
-                };
-                float over = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < R; c += 16) {
-                    if (c >= here) break;
-                    float t[16];
-                    scores(c, t);
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float rise = t[k] - sh.m[c + k];
-                        if (c + k < here) over = fmaxf(over, rise);   // (a NaN is no maximum)
+                const bool is = (reinterpret_cast<volatile uint32_t *>(sh.mask[job % kMasks])[at & 3] >> (at >> 2)) & 1;
+                uint32_t sees = is ? ~0u : 0;     // rows that see the thread's position
+                if (i * kTile > u.span.ctx - kTile) {
+                    const int32_t draft = i * kTile + at - u.span.ctx;
+                    if (is && draft >= 0) {
+                        sees = 0;
+#pragma unroll 1
+                        for (int r = 0; r < here; ++r) sees |= (draft < 64 ? static_cast<uint32_t>(sh.tree[r] >> draft) & 1 : 0) << r;
                     }
                 }
-                if (softmax_any(over > kRise)) {
-                    // ---- some row's reference moves
+                const bool all = __all_sync(~0u, sees == ~0u);
+                // scores of the thread's position less their rows' references, base 2
+                float d[R];
+                auto scores = [&]() {
 #pragma unroll
-                    for (int c = 0; c < R; c += 16) {
+                    for (int c = 0; c < R; c += CH) {
                         if (c >= here) break;
-                        float t[16];
-                        scores(c, t);
+                        uint32_t x[16], y[16];
+                        if constexpr (!F16 && CH == 8) tmem_load8(t_s, x);
+                        else tmem_load16(t_s + c, x);      // (eight rows of fp16: both halves)
+                        if constexpr (F16 && CH == 16) tmem_load16(t_s + R + c, y);
+                        tc_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            const int32_t best = __reduce_max_sync(~0u, order_of(t[k]));
-                            if (lane == 0) sh.part[warp][c + k] = of_order(best);
+                        for (int k = 0; k < CH; k += 4) {
+                            const float4 m = sh.less_m[(c + k) / 4];
+                            const float mm[4] = {m.x, m.y, m.z, m.w};
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                float v = __uint_as_float(x[k + j]);
+                                if constexpr (F16) v += __uint_as_float(CH == 8 ? x[(k + j + 8) & 15] : y[k + j]);
+                                d[c + k + j] = fmaf(v, pp.k_mul, mm[j]);
+                            }
+                        }
+                        if (!all) {
+#pragma unroll
+                            for (int k = 0; k < CH; ++k)
+                                if (!((sees >> (c + k)) & 1)) d[c + k] = -INFINITY;
+                        }
+                    }
+                };
+                scores();
+                float over = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < R; c += CH) {
+                    if (c >= here) break;
+#pragma unroll
+                    for (int k = 0; k < CH; ++k) over = fmaxf(over, d[c + k]);   // (a NaN is no maximum)
+                }
+                if (softmax_any(over > kRise || !ok)) {
+                    // ---- some row's reference moves, or a wait ran out
+                    if (*reinterpret_cast<volatile uint32_t *>(&sh.abort)) ok = false;
+                    // O is complete up to the last job
+                    if (ok && job != job0) ok = wait(&sh.pv_done[(job - 1) & 1], ((job - 1) >> 1) & 1, abort);
+                    if (softmax_any(!ok)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const float before = at < R ? less_m[at] : 0.f;
+                    if (at < R && before == kFar) less_m[at] = 0.f;
+                    softmax_sync();
+                    scores();
+#pragma unroll
+                    for (int c = 0; c < R; c += CH) {
+                        if (c >= here) break;
+#pragma unroll
+                        for (int k = 0; k < CH; ++k) {
+                            const float best = of_order(__reduce_max_sync(~0u, order_of(d[c + k])));
+                            if (lane == 0) sh.part[warp][c + k] = best;
                         }
                     }
                     softmax_sync();
                     if (at < R) {
                         float f = 1.f;
                         if (at < here) {
-                            const float best = fmaxf(fmaxf(sh.part[0][at], sh.part[1][at]), fmaxf(sh.part[2][at], sh.part[3][at]));
-                            const float m = sh.m[at];
-                            if (best - m > kRise) {
-                                f = m == -INFINITY ? 0.f : exp2_fast(m - best);
-                                sh.m[at] = best;
+                            const float rise = fmaxf(fmaxf(sh.part[0][at], sh.part[1][at]), fmaxf(sh.part[2][at], sh.part[3][at]));
+                            if (before == kFar) {
+                                less_m[at] = rise > -INFINITY ? -rise : kFar;
+                            } else if (rise > kRise) {
+                                less_m[at] = before - rise;
+                                f = exp2_fast((before - rise) - before);
                             }
                         }
-                        sh.scale[at] = f;
+                        scale[at] = f;
                     }
                     softmax_sync();
 #pragma unroll
-                    for (int r = 0; r < R; ++r) l[r] *= sh.scale[r];
+                    for (int r = 0; r < R; ++r) l[r] *= scale[r];
                     if (job != job0) {
-                        // O is complete up to the last job
-                        ok = __all_sync(~0u, bar_wait(&sh.pv_done[(job - 1) & 1], ((job - 1) >> 1) & 1, abort));
-                        if (softmax_any(!ok)) {
-                            ok = false;
-                            break;
-                        }
-                        tc_fence_after();
 #pragma unroll 1
                         for (int c = 0; c < kBlocks * N; c += 16) {
                             uint32_t o[16];
                             tmem_load16(tmem + lanes + kO + c, o);
                             tc_wait_ld();
 #pragma unroll
-                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * sh.scale[(c + k) % R]);
+                            for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * scale[(c + k) % R]);
                             tmem_store16(tmem + lanes + kO + c, o);
                         }
                         tc_wait_st();
                     }
+                    scores();
                 }
                 // P^T of the tile before last has been read
-                if (job >= 2) ok = __all_sync(~0u, bar_wait(&sh.pv_done[sb], ph ^ 1, abort));
-                const uint32_t p_tile = pp.p_off + sb * kProbBytes;
+                if (job >= 2) ok = wait(&sh.pv_done[sb], ph ^ 1, abort);
+                const uint32_t p_row = base + pp.p_off + sb * kProbBytes + at * 128, swizzle = (at & 7) << 4;
 #pragma unroll
-                for (int c = 0; c < R; c += 16) {
+                for (int c = 0; c < R; c += 8) {
                     if (c >= here) break;
-                    float t[16];
-                    scores(c, t);
-                    uint32_t hi[8], lo[8];
+                    uint32_t hi[4], lo[4];
 #pragma unroll
-                    for (int k = 0; k < 16; k += 2) {
-                        float e[2];
-#pragma unroll
-                        for (int j = 0; j < 2; ++j) {
-                            const float m = sh.m[c + k + j];
-                            e[j] = exp2_fast(t[k + j] - (m == -INFINITY ? 0.f : m));
-                            l[c + k + j] += e[j];
-                        }
-                        hi[k / 2] = Half2<true>::down(e[0], e[1]);
+                    for (int k = 0; k < 8; k += 2) {
+                        const float a = exp2_fast(d[c + k]), b = exp2_fast(d[c + k + 1]);
+                        l[c + k] += a;
+                        l[c + k + 1] += b;
+                        hi[k / 2] = Half2<true>::down(a, b);
                         if constexpr (F16) {
                             const float2 f = Half2<true>::up(hi[k / 2]);
-                            lo[k / 2] = Half2<true>::down(e[0] - f.x, e[1] - f.y);
+                            lo[k / 2] = Half2<true>::down(a - f.x, b - f.y);
                         }
                     }
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        *reinterpret_cast<uint4 *>(smem + p_tile + tile_offset(kTile, at, c / 8 + k)) =
-                            make_uint4(hi[4 * k], hi[4 * k + 1], hi[4 * k + 2], hi[4 * k + 3]);
-                        if constexpr (F16)
-                            *reinterpret_cast<uint4 *>(smem + p_tile + tile_offset(kTile, at, (R + c) / 8 + k)) =
-                                make_uint4(lo[4 * k], lo[4 * k + 1], lo[4 * k + 2], lo[4 * k + 3]);
-                    }
+                    put16(p_row + ((c * 2) ^ swizzle), hi);
+                    if constexpr (F16) put16(p_row + (((R + c) * 2) ^ swizzle), lo);
                 }
                 fence_async_reads();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) {
-                    bar_arrive(&sh.p_full[sb]);
-                    bar_arrive(&sh.slots_empty[job % kSlotRing]);
-                }
+                if (lane == 0) bar_arrive(&sh.p_full[sb]);
             }
-            if (ok && job != job0) ok = __all_sync(~0u, bar_wait(&sh.pv_done[(job - 1) & 1], ((job - 1) >> 1) & 1, abort));
+            if (ok) ok = wait(&sh.pv_done[(job - 1) & 1], ((job - 1) >> 1) & 1, abort);
             if (softmax_any(!ok)) {
                 ok = false;
                 break;
@@ -344,46 +398,39 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
             const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (u.t0 > 0 ? 0 : 1);
             if (at < R) {
                 const float s = (sh.part[0][at] + sh.part[1][at]) + (sh.part[2][at] + sh.part[3][at]);
-                sh.scale[at] = whole ? (s == 0.f ? 0.f : pp.v_mul / s) : pp.v_mul;
+                const float m = less_m[at] == kFar ? -INFINITY : -less_m[at];
+                scale[at] = whole ? (s == 0.f ? 0.f : pp.v_mul / s) : pp.v_mul;
                 if (at < here) {
-                    if (!whole) p.part_ml[part * R + at] = make_float2(sh.m[at], s);
-                    else if (p.lse) p.lse[sh.row_at[at]] = row_lse<true>(sh.m[at], s);
+                    if (!whole) p.part_ml[part * R + at] = make_float2(m, s);
+                    else if (p.lse) p.lse[sh.row_at[at]] = row_lse<true>(m, s);
                 }
             }
             softmax_sync();
             tc_fence_after();
+            const int dp = WIDE ? 256 : p.dim <= 64 ? 64 : 128;
 #pragma unroll 1
             for (int b = 0; b < kBlocks; ++b) {
                 const int d = b * 128 + at;
 #pragma unroll 1
-                for (int c = 0; c < here; c += 16) {
-                    uint32_t o[16];
-                    float x[16];
-                    tmem_load16(tmem + lanes + kO + b * N + c, o);
-                    if constexpr (F16) {
-                        uint32_t y[16];
-                        tmem_load16(tmem + lanes + kO + b * N + R + c, y);
-                        tc_wait_ld();
+                for (int c = 0; c < here; c += 8) {
+                    uint32_t o[8], y[8];
+                    float x[8];
+                    tmem_load8(tmem + lanes + kO + b * N + c, o);
+                    if constexpr (F16) tmem_load8(tmem + lanes + kO + b * N + R + c, y);
+                    tc_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) x[k] = (__uint_as_float(o[k]) + __uint_as_float(y[k])) * sh.scale[c + k];
-                    } else {
-                        tc_wait_ld();
-#pragma unroll
-                        for (int k = 0; k < 16; ++k) x[k] = __uint_as_float(o[k]) * sh.scale[c + k];
-                    }
+                    for (int k = 0; k < 8; ++k) x[k] = (__uint_as_float(o[k]) + (F16 ? __uint_as_float(y[k]) : 0.f)) * scale[c + k];
                     if (whole) {
                         if (d < p.dim) {
 #pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                if (c + k < here) {
-                                    const uint32_t y = Half2<!F16>::down(x[k], 0.f);
-                                    static_cast<uint16_t *>(p.out)[sh.row_at[c + k] * p.dim + d] = static_cast<uint16_t>(y);
-                                }
+                            for (int k = 0; k < 8; ++k)
+                                if (c + k < here)
+                                    static_cast<uint16_t *>(p.out)[sh.row_at[c + k] * p.dim + d] = static_cast<uint16_t>(Half2<!F16>::down(x[k], 0.f));
                         }
-                    } else if (d < (WIDE ? 256 : p.dim <= 64 ? 64 : 128)) {
-                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + (part * (WIDE ? 256 : p.dim <= 64 ? 64 : 128) + d) * R + c);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) dst[k] = make_float4(x[4 * k], x[4 * k + 1], x[4 * k + 2], x[4 * k + 3]);
+                    } else if (d < dp) {
+                        float4 *dst = reinterpret_cast<float4 *>(p.part_o + (part * dp + d) * R + c);
+                        dst[0] = make_float4(x[0], x[1], x[2], x[3]);
+                        dst[1] = make_float4(x[4], x[5], x[6], x[7]);
                     }
                     __syncwarp();
                 }
@@ -399,31 +446,23 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
         for (; walk.more() && ok; walk.next()) {
             if (walk.u.span.n == 0) continue;
             for (int32_t i = walk.u.t0; i < walk.u.t1; ++i, ++job) {
-                ok = __all_sync(~0u, bar_wait(&sh.full[stage], lap & 1, abort));
-                if (!ok) break;
-                const uint8_t *row = smem + pp.ring_off + stage * pp.stage_bytes + at * pp.stride;
-                const uint4 s0 = *reinterpret_cast<const uint4 *>(row + 2 * pp.codes);
-                uint32_t s[8];   // scales of blocks 0, 2 | 1, 3 | 4, 6 | 5, 7 | ...
-                int4_scales4(s0.x, s);
-                int4_scales4(s0.y, s + 2);
-                if constexpr (WIDE) {
-                    int4_scales4(s0.z, s + 4);
-                    int4_scales4(s0.w, s + 6);
-                }
-                // the tile before last has been multiplied
-                if (job >= 2) ok = __all_sync(~0u, bar_wait(&sh.s_full[job & 1], ((job >> 1) & 1) ^ 1, abort));
+                // (the tile before last has been multiplied)
+                ok = wait(&sh.full[stage], lap & 1, abort) && (job < 2 || wait(&sh.s_full[job & 1], ((job >> 1) & 1) ^ 1, abort));
                 if (!ok) break;
                 tc_fence_after();
+                const uint8_t *row = smem + pp.ring_off + stage * pp.stage_bytes + (at >> 2) * pp.four + (at & 3) * pp.row;
                 const uint32_t dst = tmem + lanes + kK + (job & 1) * kKeyCols;
-#pragma unroll
-                for (int b = 0; b < (WIDE ? 16 : 8); b += 2) {
-                    if (b * 16 >= p.dim) break;
-                    const uint4 c = *reinterpret_cast<const uint4 *>(row + b * 8);
+                // (the next codes are loaded before the store, which holds later loads back)
+                const uint8_t *scales = row + 2 * pp.codes;
+                uint4 c = *reinterpret_cast<const uint4 *>(row);
+                uint32_t two = *reinterpret_cast<const uint16_t *>(scales);
+#pragma unroll 1
+                for (int b = 0; b * 32 < p.dim; ++b) {
                     uint32_t y[16];
-                    const int sel = b & 2 ? 0x3232 : 0x1010, q = b / 4 * 2;
-                    decode16(c.x, c.y, __byte_perm(s[q], 0, sel), y);
-                    decode16(c.z, c.w, __byte_perm(s[q + 1], 0, sel), y + 8);
-                    tmem_store16(dst + b * 8, y);
+                    decode32(c, two, y);
+                    c = *reinterpret_cast<const uint4 *>(row + b * 16 + 16);   // (behind the last: the row's other bytes)
+                    two = *reinterpret_cast<const uint16_t *>(scales + b * 2 + 2);
+                    tmem_store16(dst + b * 16, y);
                 }
                 tc_wait_st();
                 tc_fence_before();
@@ -444,38 +483,35 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
         uint32_t item = 0, stage = 0, lap = 0;
         for (; walk.more() && ok; walk.next()) {
             if (walk.u.span.n == 0) continue;
-            for (int32_t i = walk.u.t0; i < walk.u.t1 && ok; ++i) {
-                ok = __all_sync(~0u, bar_wait(&sh.full[stage], lap & 1, abort));
+            for (int32_t i = walk.u.t0; i < walk.u.t1; ++i) {
+                ok = wait(&sh.full[stage], lap & 1, abort);
                 if (!ok) break;
-                const uint8_t *row = smem + pp.ring_off + stage * pp.stage_bytes + at * pp.stride;
-                const uint8_t *from = row + 2 * pp.codes + (WIDE ? 16 : 8);
-                for (int mb = 0; mb < kBlocks; ++mb, ++item) {
-                    uint32_t s[4];
-                    const uint2 s0 = *reinterpret_cast<const uint2 *>(from + mb * 8);
-                    int4_scales4(s0.x, s);
-                    int4_scales4(s0.y, s + 2);
-                    if (item >= 2) ok = __all_sync(~0u, bar_wait(&sh.v_free[item & 1], ((item >> 1) & 1) ^ 1, abort));
+                const uint8_t *row = smem + pp.ring_off + stage * pp.stage_bytes + (at >> 2) * pp.four + (at & 3) * pp.row;
+                const uint8_t *scales = row + 2 * pp.codes + (WIDE ? 16 : 8);
+                row += pp.codes;
+                uint4 c = *reinterpret_cast<const uint4 *>(row);
+                uint32_t two = *reinterpret_cast<const uint16_t *>(scales);
+                for (int b = 0; b * 32 < p.dim; ++item) {   // items of 128 dimensions
+                    if (item >= 2) ok = wait(&sh.v_free[item & 1], ((item >> 1) & 1) ^ 1, abort);
                     if (!ok) break;
-                    uint8_t *dst = smem + (item & 1) * kValueBytes;
-#pragma unroll
-                    for (int b = 0; b < 8; b += 2) {
-                        if (mb * 128 + b * 16 >= p.dim) break;
-                        const uint4 c = *reinterpret_cast<const uint4 *>(row + pp.codes + mb * 64 + b * 8);
+                    uint32_t to = v_smem + (item & 1) * kValueBytes + at * 128, turn = (at & 7) << 4;
+                    const int end = b + 4;
+#pragma unroll 1
+                    for (; b < end && b * 32 < p.dim; ++b) {
                         uint32_t y[16];
-                        const int sel = b & 2 ? 0x3232 : 0x1010, q = b / 4 * 2;
-                        decode16(c.x, c.y, __byte_perm(s[q], 0, sel), y);
-                        decode16(c.z, c.w, __byte_perm(s[q + 1], 0, sel), y + 8);
+                        decode32(c, two, y);
+                        c = *reinterpret_cast<const uint4 *>(row + b * 16 + 16);   // (behind the last: the row's scales)
+                        two = *reinterpret_cast<const uint16_t *>(scales + b * 2 + 2);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            *reinterpret_cast<uint4 *>(dst + tile_offset(kTile, at, 2 * b + k)) =
-                                make_uint4(y[4 * k], y[4 * k + 1], y[4 * k + 2], y[4 * k + 3]);
+                        for (int k = 0; k < 4; ++k) put16(to + (turn ^ (k * 16)), y + 4 * k);
+                        turn ^= 64;
+                        to += b & 1 ? kTile * 128 : 0;
                     }
                     fence_async_reads();
                     __syncwarp();
                     if (lane == 0) bar_arrive(&sh.v_full[item & 1]);
                 }
                 if (!ok) break;
-                __syncwarp();
                 if (lane == 0) bar_arrive(&sh.empty[stage]);
                 if (++stage == static_cast<uint32_t>(pp.stages)) {
                     stage = 0;
@@ -483,112 +519,16 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
                 }
             }
         }
-    } else if (warp < kIssueWarp) {
-        // ------------------------------------------------ copies
-        const int tid = (warp - kCopyWarp) * 32 + lane;
-        const uint8_t *cache = static_cast<const uint8_t *>(p.k);
-        const int32_t chunks = pp.row / 16;
-        uint32_t stage = 0, lap = 0, tile = 0;
-        for (; walk.more() && ok; walk.next()) {
-            if (walk.u.span.n == 0) continue;
-            const int32_t h = walk.u.hm / p.row_tiles;
-            const uint8_t *head = cache + h * p.k_head;
-            for (int32_t i = walk.u.t0; i < walk.u.t1; ++i, ++tile) {
-                ok = __all_sync(~0u, bar_wait(&sh.slots_full[tile % kSlotRing], (tile / kSlotRing) & 1, abort));
-                if (ok && lap) ok = __all_sync(~0u, bar_wait(&sh.empty[stage], (lap - 1) & 1, abort));
-                if (!ok) break;
-                const volatile int32_t *slots = sh.slots[tile % kSlotRing];
-                const uint32_t dst = base + pp.ring_off + stage * pp.stage_bytes;
-                // lane groups walk a row's chunks: (row, chunk) of tid, then 128 chunks on
-                int32_t r = tid / chunks, c = tid - r * chunks;
-                const int32_t dr = 128 / chunks, dc = 128 - dr * chunks;
-#pragma unroll 4
-                for (int k = 0; k < chunks; ++k) {
-                    const int32_t slot = slots[r];
-                    copy16(dst + r * pp.stride + c * 16, head + static_cast<int64_t>(slot < 0 ? 0 : slot) * p.k_slot + c * 16, slot < 0 ? 0u : 16u);
-                    r += dr;
-                    c += dc;
-                    if (c >= chunks) {
-                        c -= chunks;
-                        ++r;
-                    }
-                }
-                bar_arrive_copies(&sh.full[stage]);
-                if (++stage == static_cast<uint32_t>(pp.stages)) {
-                    stage = 0;
-                    ++lap;
-                }
-            }
-        }
-        copies_land();
-    } else if (warp == kIssueWarp) {
-        // ------------------------------------------------ matrix products (all lanes alike, see elect_lane)
-        const bool lead = elect_lane();
-        const uint32_t s_desc = mma_desc(true, 128, N, false, p.negative != 0);
-        const uint32_t o_desc = mma_desc(true, 128, N, true, false) | 1u << 15;   // A transposed too
-        const int ksteps = p.dim / 16;
-        const uint32_t q_bytes = N * (WIDE ? 512 : 256);
-        uint32_t unit = 0, job0 = 0, item = 0;
-        for (; __any_sync(~0u, walk.more()) && ok; walk.next()) {
-            if (__any_sync(~0u, walk.u.span.n == 0)) continue;
-            const uint32_t jobs = __shfl_sync(~0u, static_cast<uint32_t>(walk.u.t1 - walk.u.t0), 0);
-            const uint32_t qb = pp.q_bufs == 2 ? unit & 1 : 0, qph = pp.q_bufs == 2 ? unit >> 1 : unit;
-            ok = __all_sync(~0u, bar_wait(&sh.q_full[qb], qph & 1, abort));
-            if (!ok) break;
-            auto issue_s = [&](uint32_t j) {
-                const uint32_t job = job0 + j, sb = job & 1;
-                if (!__all_sync(~0u, bar_wait(&sh.key_full[sb], (job >> 1) & 1, abort))) return false;
-                tc_fence_after();
-                const uint32_t qa = base + pp.q_off + qb * q_bytes, ka = tmem + kK + sb * kKeyCols;
-                if (lead) {
-#pragma unroll
-                    for (int kk = 0; kk < (WIDE ? 16 : 8); ++kk)
-                        if (kk < ksteps)
-                            mma_ts(tmem + kS + sb * N, ka + kk * 8, smem_desc(qa + (kk >> 2) * (N * 128) + (kk & 3) * 32, 16, 1024), s_desc, kk > 0);
-                    tc_commit(&sh.s_full[sb]);
-                    if (j + 1 == jobs) tc_commit(&sh.q_empty[qb]);
-                }
-                __syncwarp();
-                return true;
-            };
-            for (uint32_t j = 0; j < 2 && j < jobs && ok; ++j) ok = issue_s(j);
-            for (uint32_t j = 0; j < jobs && ok; ++j) {
-                const uint32_t job = job0 + j, sb = job & 1;
-                for (int mb = 0; mb < kBlocks; ++mb, ++item) {
-                    ok = __all_sync(~0u, bar_wait(&sh.v_full[item & 1], (item >> 1) & 1, abort) &&
-                                             bar_wait(&sh.p_full[sb], (job >> 1) & 1, abort));
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t va = v_smem + (item & 1) * kValueBytes, pa = base + pp.p_off + sb * kProbBytes;
-                    if (lead) {
-#pragma unroll
-                        for (int kk = 0; kk < kTile / 16; ++kk)
-                            mma_ss(tmem + kO + mb * N, smem_desc(va + kk * 2048, kTile * 128, 1024),
-                                   smem_desc(pa + kk * 2048, kTile * 128, 1024), o_desc, j > 0 || kk > 0);
-                        tc_commit(&sh.v_free[item & 1]);
-                        if (mb + 1 == kBlocks) tc_commit(&sh.pv_done[sb]);
-                    }
-                    __syncwarp();
-                }
-                if (ok && j + 2 < jobs) ok = issue_s(j + 2);
-            }
-            job0 += jobs;
-            ++unit;
-        }
-        // every product is done before the block gives its memory up
-        if (lead) tc_commit(&sh.drain);
-        __syncwarp();
-        if (!bar_wait(&sh.drain, 0, abort)) {
-            const long long t0 = clock64();
-            while (!bar_try(&sh.drain, 0) && clock64() - t0 < kWaitCycles) {
-            }
-        }
-    } else {
-        // ------------------------------------------------ queries, slots of the tiles to come
-        const int turn = warp - kIssueWarp - 1, tid = turn * 32 + lane;
+    } else if (warp != kIssueWarp) {
+        // ------------------------------------------------ slots and copies, the warps in turn; queries
+        // As many warps take tiles as there are stages, at most: a warp that waits
+        // for a stage to be empty has then seen the tile before its last one there
+        // emptied, so that the parity it waits for is of this lap and not of the
+        // one before.
+        const uint32_t turn = warp - kCopyWarp, turns = pp.stages < kCopyWarps ? pp.stages : kCopyWarps;
         int32_t last_b = -1;
         uint64_t seen = ~0ull;   // drafted tokens that some row of the request sees
-        uint32_t tile = 0, unit = 0;
+        uint32_t stage = 0, lap = 0, tile = 0, unit = 0, flying = 0, odd_lap = 0;   // stages that the warp has copied to, their parity
         for (; walk.more() && ok; walk.next()) {
             const Unit u = walk.u;
             if (u.span.n == 0) continue;
@@ -600,62 +540,150 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
                        __reduce_or_sync(~0u, static_cast<uint32_t>(m));
             }
             last_b = u.b;
-            auto look_up = [&](int32_t t) {
-                const uint32_t r = tile % kSlotRing;
-                Paging::Place place[4];
+            const int64_t head = (u.hm / p.row_tiles) * p.k_head;
+            // a tile a warp before the unit's queries, so that copies start (no more:
+            // their stages are the last unit's, whose queries are there)
+            const int32_t q_at = u.t1 - u.t0 < static_cast<int32_t>(turns) ? u.t1 : u.t0 + static_cast<int32_t>(turns);
+            for (int32_t t = u.t0; ok; ++t) {
+                if (t == q_at) {
+                    const int32_t h = u.hm / p.row_tiles, r0 = (u.hm - h * p.row_tiles) * R;
+                    const int32_t here = rows - r0 < R ? rows - r0 : R, padded = (here + CH - 1) / CH * CH, lanes8 = p.dim / 8;
+                    const uint32_t qb = pp.q_bufs == 2 ? unit & 1 : 0, qph = pp.q_bufs == 2 ? unit >> 1 : unit;
+                    if (qph > 0) ok = wait(&sh.q_empty[qb], (qph - 1) & 1, abort);
+                    if (!ok) break;
+                    const uint32_t q_tile = base + pp.q_off + qb * (N * (WIDE ? 512 : 256));
+#pragma unroll 2
+                    for (int32_t k = turn * 32 + lane; k < padded * lanes8; k += kCopyWarps * 32) {
+                        const int32_t r = k / lanes8, c = k - r * lanes8, tok = (r0 + r) / p.group, gq = r0 + r - tok * p.group;
+                        const uint8_t *src = static_cast<const uint8_t *>(p.q) +
+                                             2 * ((static_cast<int64_t>(u.b) * p.next_n + tok) * p.q_row + (h * p.group + gq) * p.q_head);
+                        const uint4 v = r < here ? fetch(reinterpret_cast<const uint4 *>(src) + c) : make_uint4(0, 0, 0, 0);
+                        const uint32_t x[4] = {v.x, v.y, v.z, v.w};
+                        if constexpr (F16) {
+                            uint32_t hi[4], lo[4];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const int32_t pos = t * kTile + k * 32 + lane;
-                    const bool is = pos < u.span.n && (pos < u.span.ctx || ((seen >> (pos - u.span.ctx)) & 1));
-                    place[k] = p.seq_lens ? p.pages.place(u.b, pos, is) : p.pages.listed(p.indices + u.b * p.idx_row + pos, is);
-                }
-                if (tile >= kSlotRing && !__all_sync(~0u, bar_wait(&sh.slots_empty[r], (tile / kSlotRing - 1) & 1, abort))) return false;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) sh.slots[r][k * 32 + lane] = static_cast<int32_t>(p.pages.slot(place[k]));
-                __syncwarp();
-                if (lane == 0) bar_arrive(&sh.slots_full[r]);
-                return true;
-            };
-            // the warp's first tile of the unit goes before the queries, so that copies start
-            int32_t t = u.t0;
-            for (; t < u.t1 && t < u.t0 + 3 && ok; ++t, ++tile)
-                if (tile % 3 == static_cast<uint32_t>(turn)) ok = look_up(t);
-            if (!ok) break;
-            const int32_t h = u.hm / p.row_tiles, r0 = (u.hm - h * p.row_tiles) * R;
-            const int32_t here = rows - r0 < R ? rows - r0 : R, lanes8 = p.dim / 8;
-            const uint32_t qb = pp.q_bufs == 2 ? unit & 1 : 0, qph = pp.q_bufs == 2 ? unit >> 1 : unit;
-            if (qph > 0) ok = __all_sync(~0u, bar_wait(&sh.q_empty[qb], (qph - 1) & 1, abort));
-            if (!ok) break;
-            uint8_t *q_tile = smem + pp.q_off + qb * (N * (WIDE ? 512 : 256));
-#pragma unroll 4
-            for (int32_t k = tid; k < here * lanes8; k += 96) {
-                const int32_t r = k / lanes8, c = k - r * lanes8, tok = (r0 + r) / p.group, gq = r0 + r - tok * p.group;
-                const uint8_t *src = static_cast<const uint8_t *>(p.q) +
-                                     2 * ((static_cast<int64_t>(u.b) * p.next_n + tok) * p.q_row + (h * p.group + gq) * p.q_head);
-                const uint4 v = fetch(reinterpret_cast<const uint4 *>(src) + c);
-                if constexpr (F16) {
-                    const uint32_t x[4] = {v.x, v.y, v.z, v.w};
-                    uint32_t hi[4], lo[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float2 f = Half2<false>::up(x[j]);
-                        hi[j] = Half2<true>::down(f.x, f.y);
-                        const float2 g = Half2<true>::up(hi[j]);
-                        // (an infinity is whole)
-                        lo[j] = Half2<true>::down(isinf(f.x) ? 0.f : f.x - g.x, isinf(f.y) ? 0.f : f.y - g.y);
+                            for (int j = 0; j < 4; ++j) {
+                                const float2 f = Half2<false>::up(x[j]);
+                                hi[j] = Half2<true>::down(f.x, f.y);
+                                const float2 g = Half2<true>::up(hi[j]);
+                                // (an infinity is whole)
+                                lo[j] = Half2<true>::down(isinf(f.x) ? 0.f : f.x - g.x, isinf(f.y) ? 0.f : f.y - g.y);
+                            }
+                            put16(q_tile + tile_offset(N, r, c), hi);
+                            put16(q_tile + tile_offset(N, R + r, c), lo);
+                        } else {
+                            put16(q_tile + tile_offset(N, r, c), x);
+                        }
                     }
-                    *reinterpret_cast<uint4 *>(q_tile + tile_offset(N, r, c)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    *reinterpret_cast<uint4 *>(q_tile + tile_offset(N, R + r, c)) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                } else {
-                    *reinterpret_cast<uint4 *>(q_tile + tile_offset(N, r, c)) = v;
+                    fence_async_reads();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&sh.q_full[qb]);
+                    ++unit;
+                }
+                if (t >= u.t1) break;
+                const uint32_t n = tile++;
+                if (n % turns == turn) {
+                    Paging::Place place[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int32_t pos = t * kTile + lane * 4 + k;
+                        const bool is = pos < u.span.n && (pos < u.span.ctx || ((seen >> (pos - u.span.ctx)) & 1));
+                        place[k] = p.seq_lens ? p.pages.place(u.b, pos, is) : p.pages.listed(p.indices + u.b * p.idx_row + pos, is);
+                    }
+                    if (lap > 0) ok = wait(&sh.empty[stage], (lap - 1) & 1, abort);
+                    if (!ok) break;
+                    int32_t row[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const int64_t slot = p.pages.slot(place[k]);
+                        const uint32_t bits = __ballot_sync(~0u, slot >= 0);
+                        if (lane == 0) sh.mask[n % kMasks][k] = bits;
+                        // (a position without a slot gets the first one's row: its probability is 0)
+                        row[k] = static_cast<int32_t>((slot < 0 ? 0 : slot) * p.k_slot + head);
+                    }
+                    if (lane == 0) bar_expect(&sh.full[stage], kTile * pp.row);
+                    __syncwarp();
+                    gather_rows4(base + pp.ring_off + stage * pp.stage_bytes + lane * pp.four, &pp.rows, make_int4(row[0], row[1], row[2], row[3]),
+                                 &sh.full[stage]);
+                    flying |= 1u << stage;
+                    if (lap & 1) odd_lap |= 1u << stage;
+                    else odd_lap &= ~(1u << stage);
+                }
+                if (++stage == static_cast<uint32_t>(pp.stages)) {
+                    stage = 0;
+                    ++lap;
                 }
             }
-            fence_async_reads();
-            __syncwarp();
-            if (lane == 0) bar_arrive(&sh.q_full[qb]);
+        }
+        // the block does not end before its copies have
+        const long long t0 = clock64();
+        for (int i = 0; i < pp.stages; ++i)
+            while (((flying >> i) & 1) && !bar_try(&sh.full[i], (odd_lap >> i) & 1) && clock64() - t0 < kWaitCycles) {
+            }
+    } else {
+        // ------------------------------------------------ matrix products (all lanes alike, see elect_lane)
+        const bool lead = elect_lane();
+        const uint32_t s_desc = mma_desc(true, 128, N, false, p.negative != 0);
+        const uint32_t o_desc = mma_desc(true, 128, N, true, false) | 1u << 15;   // A transposed too
+        const int ksteps = p.dim / 16;
+        const uint32_t q_bytes = N * (WIDE ? 512 : 256);
+        // (broadcasts: values known to be warp-uniform)
+        const uint32_t t_issue = __shfl_sync(~0u, tmem, 0), base_u = __shfl_sync(~0u, base, 0);
+        uint32_t unit = 0, job0 = 0, item = 0;
+        for (; __any_sync(~0u, walk.more()) && ok; walk.next()) {
+            if (__any_sync(~0u, walk.u.span.n == 0)) continue;
+            const uint32_t jobs = __shfl_sync(~0u, static_cast<uint32_t>(walk.u.t1 - walk.u.t0), 0);
+            const uint32_t qb = pp.q_bufs == 2 ? unit & 1 : 0, qph = pp.q_bufs == 2 ? unit >> 1 : unit;
+            ok = wait(&sh.q_full[qb], qph & 1, abort);
+            // scores run two jobs ahead of outputs
+            for (uint32_t ahead = 0; ahead < jobs + 2 && ok; ++ahead) {
+                if (ahead >= 2) {
+                    const uint32_t j = ahead - 2, job = job0 + j, sb = job & 1;
+#pragma unroll 1
+                    for (int mb = 0; mb < kBlocks; ++mb, ++item) {
+                        ok = wait(&sh.v_full[item & 1], (item >> 1) & 1, abort) && wait(&sh.p_full[sb], (job >> 1) & 1, abort);
+                        if (!ok) break;
+                        tc_fence_after();
+                        const uint64_t va = smem_desc(base_u + (item & 1) * kValueBytes, kTile * 128, 1024);
+                        const uint64_t pa = smem_desc(base_u + pp.p_off + sb * kProbBytes, kTile * 128, 1024);
+#pragma unroll 2
+                        for (int kk = 0; kk < kTile / 16; ++kk)
+                            mma_ss_if(lead, t_issue + kO + mb * N, va + kk * 128, pa + kk * 128, o_desc, j > 0 || kk > 0);
+                        if (lead) {
+                            tc_commit(&sh.v_free[item & 1]);
+                            if (mb + 1 == kBlocks) tc_commit(&sh.pv_done[sb]);
+                        }
+                        __syncwarp();
+                    }
+                    if (!ok) break;
+                }
+                if (ahead < jobs) {
+                    const uint32_t job = job0 + ahead, sb = job & 1;
+                    ok = wait(&sh.key_full[sb], (job >> 1) & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t qa = smem_desc(base_u + pp.q_off + qb * q_bytes, 16, 1024);
+                    const uint32_t ka = t_issue + kK + sb * kKeyCols;
+#pragma unroll 2
+                    for (int kk = 0; kk < ksteps; ++kk)
+                        mma_ts_if(lead, t_issue + kS + sb * N, ka + kk * 8, qa + (kk >> 2) * (N * 8) + (kk & 3) * 2, s_desc, kk > 0);
+                    if (lead) {
+                        tc_commit(&sh.s_full[sb]);
+                        if (ahead + 1 == jobs) tc_commit(&sh.q_empty[qb]);
+                    }
+                    __syncwarp();
+                }
+            }
+            job0 += jobs;
             ++unit;
-            for (; t < u.t1 && ok; ++t, ++tile)
-                if (tile % 3 == static_cast<uint32_t>(turn)) ok = look_up(t);
+        }
+        // every product is done before the block gives its memory up
+        if (lead) tc_commit(&sh.drain);
+        __syncwarp();
+        if (!bar_wait(&sh.drain, 0, abort)) {
+            const long long t0 = clock64();
+            while (!bar_try(&sh.drain, 0) && clock64() - t0 < kWaitCycles) {
+            }
         }
     }
     __syncwarp();
@@ -669,25 +697,23 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
 template <bool F16, int R, bool WIDE>
 cudaError_t launch_rows(Int4Params pp, uint8_t *ws, int sms, cudaStream_t stream) {
     AttnParams &p = pp.a;
-    constexpr int N = F16 ? 2 * R : R;
     const int64_t rows = static_cast<int64_t>(p.next_n) * p.group;
     p.row_tiles = static_cast<int32_t>((rows + R - 1) / R);
     p.request_units = p.kv_heads * p.row_tiles;
     place_parts(p, ws);
     pp.codes = int4_codes(p.dim);
     pp.row = int4_row(p.dim);
-    pp.stride = pp.row | 16;       // an odd number of 16-byte pieces: neighbouring rows in other banks
+    pp.four = (4 * pp.row + 127) / 128 * 128;
     // values (two tiles of 128 x 128), probabilities, queries, the ring
-    constexpr uint32_t kQ = N * (WIDE ? 512 : 256);
-    const uint32_t most = kMaxSmemBytes - 1024 - (sizeof(Shared4) + 15) / 16 * 16;
+    constexpr uint32_t kQ = kCols<F16, R> * (WIDE ? 512 : 256);
+    constexpr uint32_t most = kMaxSmemBytes - 1024 - (sizeof(Shared4) + 15) / 16 * 16;
     pp.p_off = 2 * kTile * 256;
-    pp.q_off = pp.p_off + 2 * kTile * 128 * (N > 64 ? 2 : 1);
+    pp.q_off = pp.p_off + 2 * kTile * 128;
     pp.q_bufs = kQ > 16384 ? 1 : 2;
     pp.ring_off = pp.q_off + pp.q_bufs * kQ;
-    pp.stage_bytes = kTile * pp.stride;
+    pp.stage_bytes = kTile / 4 * pp.four;
     const uint32_t fit = (most - pp.ring_off) / pp.stage_bytes;
     pp.stages = static_cast<int32_t>(fit < kMaxStages ? fit : kMaxStages);
-    if (pp.stages > kSlotRing - 1) pp.stages = kSlotRing - 1;   // (copies wait for a stage, never for slots behind it)
     if (pp.stages < 1) return cudaErrorInvalidValue;
     pp.shared_off = pp.ring_off + pp.stages * pp.stage_bytes;
     const size_t bytes = 1024 + pp.shared_off + sizeof(Shared4);
@@ -702,15 +728,14 @@ cudaError_t launch_rows(Int4Params pp, uint8_t *ws, int sms, cudaStream_t stream
     else return p.dim <= 64 ? launch_join<!F16, 64>(p, R, kTile, sms, stream) : launch_join<!F16, 128>(p, R, kTile, sms, stream);
 }
 
-// By the rows of a head: 16, 32, 64 (above dimension 128 tensor memory has room
-// for 32).  More rows are more units, each of which decodes the cache.
+// By the rows of a head: 8, 16, 32.  More rows are more units, each of which
+// decodes the cache.
 template <bool F16>
 cudaError_t launch_int4(const Int4Params &pp, uint8_t *ws, int sms, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(pp.a.next_n) * pp.a.group;
     if (pp.a.dim > 128) return rows <= 16 ? launch_rows<F16, 16, true>(pp, ws, sms, s) : launch_rows<F16, 32, true>(pp, ws, sms, s);
-    if (rows <= 16) return launch_rows<F16, 16, false>(pp, ws, sms, s);
-    if (rows <= 32) return launch_rows<F16, 32, false>(pp, ws, sms, s);
-    return launch_rows<F16, 64, false>(pp, ws, sms, s);
+    if (rows <= 8) return launch_rows<F16, 8, false>(pp, ws, sms, s);
+    return rows <= 16 ? launch_rows<F16, 16, false>(pp, ws, sms, s) : launch_rows<F16, 32, false>(pp, ws, sms, s);
 }
 
 int attend_int4(Int4Params &pp, int dtype, const void *q, int64_t num_rows, int64_t q_row_stride, int64_t q_head_stride,
@@ -730,9 +755,20 @@ int attend_int4(Int4Params &pp, int dtype, const void *q, int64_t num_rows, int6
     p.q = q;
     p.q_row = q_row_stride;
     p.q_head = q_head_stride;
-    p.k = cache;
-    p.k_slot = slot_stride;
-    p.k_head = head_stride;
+    // A map of lines at one pitch that holds every row: the strides' greatest
+    // common divisor (an empty cache: one line of the workspace, never read as a row).
+    const int64_t slots = p.pages.num_slots, row = int4_row(head_dim);
+    const int64_t heads_at = kv_heads > 1 ? head_stride : 0, slots_at = slots > 1 ? slot_stride : 0;
+    int64_t pitch = std::gcd(heads_at, slots_at);
+    if (pitch == 0) pitch = row;
+    if (pitch < row) return GBTOPK_EUNSUPPORTED;
+    const int64_t lines = slots > 0 ? ((slots - 1) * slots_at + (kv_heads - 1) * heads_at) / pitch + 1 : 1;
+    if (lines > INT32_MAX || pitch >= 1ll << 40) return GBTOPK_EUNSUPPORTED;
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row / 2), static_cast<cuuint64_t>(lines)}, strides[1] = {static_cast<cuuint64_t>(pitch)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(row / 2), 1};
+    if (!tensor_map(&pp.rows, slots > 0 ? cache : workspace, 2, dims, strides, box, CU_TENSOR_MAP_SWIZZLE_NONE)) return GBTOPK_ECUDA;
+    p.k_slot = slots_at / pitch;
+    p.k_head = slots > 0 ? heads_at / pitch : 0;
     p.requests = static_cast<int32_t>(num_rows / p.next_n);
     p.q_heads = q_heads;
     p.kv_heads = kv_heads;

@@ -33,14 +33,12 @@ __device__ __forceinline__ uint32_t int4_pair(uint32_t word) {
     return (J ? __funnelshift_r(word, word, 4 * J) : word) & 0x80078007u;
 }
 
-// Four scale bytes times 2^118 as bf16: s[0] has those of bytes 0 and 2, s[1]
-// those of bytes 1 and 3.  A byte's low seven bits, moved to bf16's exponent
-// and mantissa, are the scale times 2^-120 (its subnormals are bf16's); 2^238
-// is more than one factor holds.
-__device__ __forceinline__ void int4_scales4(uint32_t bytes, uint32_t *s) {
+// Two scales, the bytes 0 and 2 of `bytes`, times 2^118 as bf16.  A byte's low
+// seven bits, moved to bf16's exponent and mantissa, are the scale times 2^-120
+// (its subnormals are bf16's); 2^238 is more than one factor holds.
+__device__ __forceinline__ uint32_t int4_scales2(uint32_t bytes) {
     constexpr uint32_t k119 = (119u + 127u) << 7, kTwice = k119 << 16 | k119;
-    s[0] = mul_bf16x2(mul_bf16x2((bytes & 0x007f007fu) << 4, kTwice), kTwice);
-    s[1] = mul_bf16x2(mul_bf16x2((bytes & 0x7f007f00u) >> 4, kTwice), kTwice);
+    return mul_bf16x2(mul_bf16x2((bytes & 0x007f007fu) << 4, kTwice), kTwice);
 }
 
 // (a power of two: codes times scales stay exact)

@@ -378,9 +378,7 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
     for (int u = 0; u < kEach; ++u) {
         const int64_t i = base + u * kRowThreads;
         if (i >= total) continue;
-        uint32_t s[2];
-        int4_scales4(byte[u], s);
-        const uint32_t scale = __byte_perm(s[0], s[0], 0x1010);
+        const uint32_t scale = __byte_perm(int4_scales2(byte[u]), 0, 0x1010);
         const uint32_t pair[4] = {int4_pair<0>(word[u]), int4_pair<1>(word[u]), int4_pair<2>(word[u]), int4_pair<3>(word[u])};
         uint32_t out[4];
 #pragma unroll
