@@ -626,6 +626,46 @@ int gbtopk_selected_attention_int4(const void *q, int dtype, int64_t num_rows, i
                                    int64_t idx_row_stride, float scale, void *out, float *lse,
                                    void *workspace, size_t workspace_bytes, void *stream);
 
+/*
+ * gbtopk_prompt_attention — causal attention over packed sequences:
+ * sequence i has the query rows cu_seqlens_q[i] .. cu_seqlens_q[i+1] - 1 and
+ * the keys cu_seqlens_k[i] .. cu_seqlens_k[i+1] - 1 (NULL: the same offsets).
+ * With n query rows and m keys its row t sees the keys 0 .. m - n + t, so that
+ * the last row sees all: keys before the queries' own are an earlier context
+ * (a chunk of a prompt), and where m < n the first rows see nothing and give
+ * zeros and lse = -infinity.  Query head h reads kv head h / (q_heads /
+ * kv_heads).
+ *
+ * Keys and values that a row does not see do not reach it, whatever they hold:
+ * infinities and NaN of later tokens and of other sequences are left out.
+ * Offsets are clamped to 0 .. num_rows (num_keys) and to ascending order.  Rows
+ * of out and lse that no sequence has are left as they were.  Arithmetic as for
+ * gbtopk_tree_attention (in fp16 the tiles are 128 consecutive keys, 64 above
+ * head_dim 128).
+ *
+ *  q, k, v      device [num_rows or num_keys, q_heads or kv_heads, head_dim] of
+ *               dtype (bf16 or fp16), inner stride 1, the other strides
+ *               multiples of 8 (0 only for a single row or head:
+ *               GBTOPK_EUNSUPPORTED), 16-byte aligned.
+ *  cu_seqlens_q, cu_seqlens_k  device int32 [num_seqs + 1].
+ *  out          device [num_rows, q_heads, head_dim], contiguous, 16-byte
+ *               aligned.
+ *  lse          device fp32 [num_rows, q_heads] or NULL.
+ *  workspace    gbtopk_prompt_workspace_bytes(...) bytes, as for gbtopk_varlen;
+ *               its status word as for gbtopk_tree_attention.
+ */
+int gbtopk_prompt_attention(const void *q, int dtype, int64_t num_rows, int64_t q_row_stride,
+                            int64_t q_head_stride, int32_t q_heads, int32_t kv_heads,
+                            int32_t head_dim, const void *k, int64_t k_row_stride,
+                            int64_t k_head_stride, const void *v, int64_t v_row_stride,
+                            int64_t v_head_stride, int64_t num_keys, const int32_t *cu_seqlens_q,
+                            const int32_t *cu_seqlens_k, int32_t num_seqs, float scale, void *out,
+                            float *lse, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Scratch of gbtopk_prompt_attention (a pure function; 0 for invalid sizes). */
+size_t gbtopk_prompt_workspace_bytes(int64_t num_rows, int32_t num_seqs, int32_t q_heads,
+                                     int32_t kv_heads, int32_t head_dim);
+
 /* Human-readable name of a status code (static string).  The pages define no
  * such call; the codes follow the error cases of the FlashInfer
  * `top_k_varlen` page ("Raises") and the status convention above. */

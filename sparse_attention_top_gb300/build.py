@@ -18,7 +18,7 @@ INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(PKG, "libgbtopk.so")
 SOURCES = ["gbtopk_api.cu", "gbtopk_kernels.cu", "gbtopk_static_ws.cu", "gbtopk_attention.cu",
            "gbtopk_weights.cu", "gbtopk_cache.cu", "gbtopk_verify.cu", "gbtopk_rotate.cu",
-           "gbtopk_attention_int4.cu"]
+           "gbtopk_attention_int4.cu", "gbtopk_prompt.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

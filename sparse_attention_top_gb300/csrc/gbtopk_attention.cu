@@ -46,32 +46,6 @@ namespace gbtopk {
 namespace {
 
 constexpr int kMaskRing = 8;        // tiles whose slots and validity bits are looked up ahead
-constexpr float kRescale = 8.f;     // rise of a tile's maximum over the reference m (base 2) that rescales O
-
-// fp16 holds 2^-14 .. 2^15 with all its digits and nothing below 2^-25, so
-// with m the maximum a key 17 nats above the others (an attention sink) left
-// nothing of their P.  There the reference is 2^7 below a tile's maximum (P is
-// at most 2^15 before O is rescaled), and it also falls, scaling O and l up,
-// where a tile's maximum is more than 2^8 below the one that set it: every
-// tile's P then reaches 2^-1 or more, and what its elements below 2^-14 lose is
-// 2^-24 of the tile's largest each.  l stays at or below 2^80 (O below 2^127 for
-// any values and lengths); what lies further down than that is below the
-// smallest fp16 output.  The first reference gives the first tile's largest
-// element a P of 2^7, which needs no rounding (with whole numbers as references
-// short rows' error was 1.16 times as large); from there it moves by whole
-// numbers, so that the many moves of a row add no error of their own to a sum
-// that each of them may scale as a whole.  bf16 has the range of the sums.
-// 32 requests x 4 drafts over 6000 positions: 129.4 -> 130.6 us; 8 x 64 drafts
-// whose tiles' maxima jump by 10 nats at random, so that some row's reference
-// moves at nearly every tile: 64.1 -> 69.0, without jumps 63.1 -> 63.2.
-template <bool BF16>
-constexpr float kLift = BF16 ? 0.f : 7.f;
-constexpr float kMostSum = 0x1p80f;
-
-// 2^x of a whole number, exactly (0 below 2^-126).
-__device__ __forceinline__ float exp2_whole(float x) {
-    return __int_as_float((static_cast<int>(fminf(fmaxf(x, -127.f), 128.f)) + 127) << 23);
-}
 
 // DP: head dimension rounded up to 64, 128 or 256.  W: softmax warpgroups.
 // ROWS: query rows of a unit.  With two warpgroups and up to 128 rows both

@@ -1,9 +1,10 @@
 """From the prompt to the cache: norms and rotation of queries and keys with the
-cache write in the same pass, and caches held in 4 bits with attention over them.
+cache write in the same pass, attention over packed prompts, and caches held in 4
+bits with attention over them.
 
 Bindings of ``gbtopk_rotate_and_cache``, ``gbtopk_rotate_and_cache_int4``,
-``gbtopk_cache_read_int4``, ``gbtopk_tree_attention_int4`` and
-``gbtopk_selected_attention_int4`` (``include/gbtopk.h``, which states the formulas and
+``gbtopk_cache_read_int4``, ``gbtopk_tree_attention_int4``,
+``gbtopk_selected_attention_int4`` and ``gbtopk_prompt_attention`` (``include/gbtopk.h``, which states the formulas and
 the rows of a 4-bit cache).  Slots are those of the decode step's calls.  A
 4-bit cache is a uint8 tensor [num_slots, kv_heads, int4_row_bytes(head_dim)]
 whose slot and head strides are multiples of 16 bytes.
@@ -11,6 +12,7 @@ whose slot and head strides are multiples of 16 bytes.
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -21,7 +23,7 @@ from .decode import (_F32, _HALF, _I32, _I64, _PAGE_RULE, _PAGES, _QUERY, MAX_PA
                      _i64, _maybe, _outputs, _query, _refuse, _requests, _scratch, _sz, _table, _vp)
 
 __all__ = ["rotate_and_cache", "rotate_and_cache_int4", "read_cache_int4", "CachedRows", "int4_row_bytes",
-           "tree_attention_int4", "selected_attention_int4"]
+           "tree_attention_int4", "selected_attention_int4", "prompt_attention", "gbtopk_prompt_workspace_bytes"]
 
 _TOKENS = [_vp, ctypes.c_int, _i64, _i64, _i64] + [_vp, _i64, _i64] * 2 + [_i32] * 3 + [_vp, _vp, _i32, ctypes.c_int] \
     + [_vp, _vp, ctypes.c_int, _f] + [_vp, _i64, _i64] + [_vp]
@@ -31,6 +33,7 @@ _SIGNATURES = {
     "gbtopk_tree_attention_int4": _QUERY + [_vp, _i64, _i64, _i64, _f, _f] + _PAGES + [_f, _vp, _vp, _vp, _sz, _vp],
     "gbtopk_selected_attention_int4": _QUERY + [_vp, _i64, _i64, _i64, _f, _f] + [_vp, _i64, _i64]
     + [_f, _vp, _vp, _vp, _sz, _vp],
+    "gbtopk_prompt_attention": _QUERY + [_vp, _i64, _i64] * 2 + [_i64, _vp, _vp, _i32, _f, _vp, _vp, _vp, _sz, _vp],
     "gbtopk_cache_read_int4": [_vp, _i64, _i64, _i64, _i32, _i32, _vp, _i64, _f, _f, ctypes.c_int, _vp, _vp, _vp],
 }
 _calls = None
@@ -45,6 +48,8 @@ def _lib():
             getattr(lib, name).argtypes = args
         lib.gbtopk_int4_row_bytes.restype = _i64
         lib.gbtopk_int4_row_bytes.argtypes = [_i32]
+        lib.gbtopk_prompt_workspace_bytes.restype = _sz
+        lib.gbtopk_prompt_workspace_bytes.argtypes = [_i64, _i32, _i32, _i32, _i32]
         _calls = lib
     return _calls
 
@@ -249,6 +254,47 @@ def selected_attention_int4(q: torch.Tensor, cache: torch.Tensor, indices: torch
             k_scale, v_scale, indices.data_ptr(), indices.shape[1], indices.stride(0),
             dim ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(), ws,
             ws_bytes, stream)
+    if status < 0:
+        _gb._check(status)
+    return out if lse is None else (out, lse)
+
+
+def gbtopk_prompt_workspace_bytes(num_rows: int, num_seqs: int, q_heads: int, kv_heads: int, head_dim: int) -> int:
+    return int(_lib().gbtopk_prompt_workspace_bytes(num_rows, num_seqs, q_heads, kv_heads, head_dim))
+
+
+_prompt_bytes = functools.lru_cache(maxsize=None)(gbtopk_prompt_workspace_bytes)
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
+                     cu_seqlens_k: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                     out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                     return_lse: bool = False, workspace: Optional[torch.Tensor] = None):
+    """Causal attention over packed sequences: rows ``cu_seqlens[i] ..
+    cu_seqlens[i + 1]`` of ``q`` [rows, q_heads, head_dim] over the keys and
+    values of the same offsets, or of ``cu_seqlens_k``, aligned at their ends
+    (a chunk of a prompt behind its earlier context; rows that see nothing are
+    zero with ``lse`` -inf).  int32 offsets, on the device: a captured call
+    follows them.  Rows behind the last sequence are left as they were in
+    ``out`` and ``lse`` (undefined where those are made here).  Everything else
+    as for ``tree_attention``."""
+    rows, heads, kv, dim = _heads(q, k, v, False)
+    dev, shape = q.device, q.shape
+    n = cu_seqlens.numel() if isinstance(cu_seqlens, torch.Tensor) else 0
+    if not (n >= 1 and _dense(cu_seqlens, dev, _I32, (n,)) and _maybe(cu_seqlens_k, dev, _I32, (n,))):
+        _refuse((n >= 1 and _dense(cu_seqlens, dev, _I32, (n,)), "cu_seqlens must be contiguous int32 [num_seqs + 1]"),
+                (False, "cu_seqlens_k must be contiguous int32 [num_seqs + 1]"))
+    out, lse = _outputs(q, shape, dev, out, lse, return_lse)
+    lib = _calls or _lib()
+    qs, ks, vs = q.stride(), k.stride(), v.stride()
+    stream = _gb._stream_handle(dev)
+    with _gb._LOCKS[dev.index, stream]:
+        ws, ws_bytes = _scratch(workspace, dev, stream, _prompt_bytes(rows, n - 1, heads, kv, dim))
+        status = lib.gbtopk_prompt_attention(
+            q.data_ptr(), _gb._DTYPES[q.dtype], rows, qs[0], qs[1], heads, kv, dim, k.data_ptr(), ks[0], ks[1], v.data_ptr(),
+            vs[0], vs[1], k.shape[0], cu_seqlens.data_ptr(), None if cu_seqlens_k is None else cu_seqlens_k.data_ptr(), n - 1,
+            dim ** -0.5 if scale is None else scale, out.data_ptr(), None if lse is None else lse.data_ptr(), ws, ws_bytes,
+            stream)
     if status < 0:
         _gb._check(status)
     return out if lse is None else (out, lse)

@@ -132,3 +132,28 @@ def test_tree_attention_int4_refuses(kw, status):
     (dict(top_k=1 << 31, idx_stride=1 << 31), gb.EUNSUPPORTED)])
 def test_selected_attention_int4_refuses(kw, status):
     assert selected4(**kw) == status
+
+
+def prompt(**kw):
+    return call("gbtopk_prompt_attention",
+                "q dtype rows q_row q_head q_heads kv_heads dim k k_row k_head v v_row v_head keys cu cu_k seqs".split() + TAIL,
+                dict(q=A, dtype=1, rows=100, q_row=512, q_head=64, q_heads=8, kv_heads=2, dim=64, k=A, k_row=128, k_head=64, v=A,
+                     v_row=128, v_head=64, keys=100, cu=A, cu_k=None, seqs=3, **TAIL_DEFAULTS), **kw)
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dtype=7), gb.EINVAL), (dict(dtype=0), gb.EUNSUPPORTED), (dict(rows=-2), gb.EINVAL), (dict(keys=-1), gb.EINVAL),
+    (dict(seqs=-1), gb.EINVAL), (dict(kv_heads=3), gb.EINVAL), (dict(dim=60), gb.EUNSUPPORTED), (dict(dim=264), gb.EUNSUPPORTED),
+    (dict(q=None), gb.EINVAL), (dict(k=None), gb.EINVAL), (dict(v=None), gb.EINVAL), (dict(q=A + 8), gb.EALIGN), (dict(k_row=132), gb.EALIGN),
+    (dict(v_head=-64), gb.EINVAL), (dict(k_head=0), gb.EUNSUPPORTED), (dict(q_row=0), gb.EUNSUPPORTED), (dict(cu=None), gb.EINVAL),
+    (dict(cu=A + 2), gb.EALIGN), (dict(cu_k=A + 1), gb.EALIGN), (dict(out=None), gb.EINVAL), (dict(out=A + 8), gb.EALIGN),
+    (dict(lse=A + 2), gb.EALIGN), (dict(ws=None), gb.EWORKSPACE), (dict(ws=A + 16), gb.EWORKSPACE), (dict(ws_bytes=512), gb.EWORKSPACE),
+    (dict(rows=(1 << 31) - 1), gb.EUNSUPPORTED), (dict(keys=1 << 31), gb.EUNSUPPORTED)])
+def test_prompt_attention_refuses(kw, status):
+    assert prompt(**kw) == status
+
+
+def test_prompt_workspace():
+    f = gb.gbtopk_prompt_workspace_bytes
+    assert f(1000, 3, 8, 2, 64) >= 512 + 8 * (1000 // 64 + 3) and f(1000, 3, 8, 3, 64) == 0 and f(-1, 3, 8, 2, 64) == 0
+    assert prompt(rows=0, q=None) == gb.OK and prompt(seqs=0) == gb.OK
