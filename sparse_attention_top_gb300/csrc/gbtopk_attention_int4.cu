@@ -99,24 +99,6 @@ __device__ __forceinline__ bool wait(uint64_t *bar, uint32_t parity, const Waits
     return __all_sync(~0u, got);
 }
 
-// Products as in gbtopk_mma.cuh, issued by the lane with `lead` of a converged
-// warp: a predicate, where a branch would move every descriptor to uniform
-// registers again.
-__device__ __forceinline__ void mma_ss_if(bool lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(static_cast<uint32_t>(lead))
-        : "memory");
-}
-__device__ __forceinline__ void mma_ts_if(bool lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
-        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(static_cast<uint32_t>(lead))
-        : "memory");
-}
-
 // Barrier of the softmax warps.
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 __device__ __forceinline__ bool softmax_any(bool v) {

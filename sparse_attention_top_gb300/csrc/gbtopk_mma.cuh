@@ -150,6 +150,24 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         : "memory");
 }
 
+// The same issued by the lane with `lead` of a converged warp: a predicate in
+// place of a branch, in which every descriptor is moved to uniform registers
+// again (a long prompt's attention 640 -> 598 us).
+__device__ __forceinline__ void mma_ss_if(bool lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(static_cast<uint32_t>(lead))
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts_if(bool lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.u32 p, %4, 0;\n setp.ne.u32 q, %5, 0;\n"
+        " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(static_cast<uint32_t>(add)), "r"(static_cast<uint32_t>(lead))
+        : "memory");
+}
+
 // 32 columns of the warp's 32 lanes, one lane a thread.  The values are there
 // after tc_wait_ld.
 __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t *v) {
@@ -180,6 +198,21 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t *v) {
         "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
         "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
         : "memory");
+}
+
+// Two products and sums, two sums, as one instruction.
+__device__ __forceinline__ float2 fma2(float x, float y, float k, float n) {   // k x + n, k y + n
+    float2 r;
+    asm("{\n .reg .b64 v, k, n;\n mov.b64 v, {%2, %3};\n mov.b64 k, {%4, %4};\n mov.b64 n, {%5, %5};\n"
+        " fma.rn.f32x2 v, v, k, n;\n mov.b64 {%0, %1}, v;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x), "f"(y), "f"(k), "f"(n));
+    return r;
+}
+__device__ __forceinline__ void add2(float2 &s, float x, float y) {
+    asm("{\n .reg .b64 v, s;\n mov.b64 v, {%2, %3};\n mov.b64 s, {%0, %1};\n add.rn.f32x2 s, s, v;\n mov.b64 {%0, %1}, s;\n}"
+        : "+f"(s.x), "+f"(s.y)
+        : "f"(x), "f"(y));
 }
 
 __device__ __forceinline__ float exp2_fast(float x) {

@@ -276,141 +276,143 @@ __global__ void __launch_bounds__(Prompt<DP>::kThreads, 1) prompt_kernel(const _
     Deal<DP> deal(p);
     bool ok = true;
 
-    if (warp == kCopy) {
-        // ------------------------------------------------ copies
-        const bool lead = elect_lane();
-        uint32_t unit = 0, stage = 0, lap = 0;
-        for (; deal.here && ok; deal.next()) {
-            if (deal.tiles == 0) continue;
-            if (unit > 0) ok = warp_wait(&sh.q_empty, (unit - 1) & 1, abort);
-            if (!ok) break;
-            if (lead) {
-                bar_expect(&sh.q_full, Sh::kQBytes);
-                for (int w = 0; w < W; ++w)
-                    for (int n = 0; n < Sh::kPanels; ++n)
-                        copy_box(q_smem + (w * Sh::kPanels + n) * 128 * 128, &p.q_map, n * 64, deal.head,
-                                 deal.s.q0 + deal.token + w * (128 >> p.shift), &sh.q_full);
-            }
-            ++unit;
-            for (int32_t t = 0; t < deal.tiles && ok; ++t) {
-                for (int kv = 0; kv < 2; ++kv) {
-                    if (lap > 0) ok = warp_wait(&sh.empty[stage], (lap - 1) & 1, abort);
-                    if (!ok) break;
-                    if (lead) {
-                        bar_expect(&sh.full[stage], Sh::kStageBytes);
+    if (warp >= kIssue) {
+        if (warp == kCopy) {
+            // ------------------------------------------------ copies
+            const bool lead = elect_lane();
+            uint32_t unit = 0, stage = 0, lap = 0;
+            for (; deal.here && ok; deal.next()) {
+                if (deal.tiles == 0) continue;
+                if (unit > 0) ok = warp_wait(&sh.q_empty, (unit - 1) & 1, abort);
+                if (!ok) break;
+                if (lead) {
+                    bar_expect(&sh.q_full, Sh::kQBytes);
+                    for (int w = 0; w < W; ++w)
                         for (int n = 0; n < Sh::kPanels; ++n)
-                            copy_box(ring + stage * Sh::kStageBytes + n * KT * 128, kv ? &p.v_map : &p.k_map, n * 64, deal.kv,
-                                     deal.s.k0 + t * KT, &sh.full[stage]);
-                    }
-                    __syncwarp();
-                    if (++stage == Sh::kStages) {
-                        stage = 0;
-                        ++lap;
+                            copy_box(q_smem + (w * Sh::kPanels + n) * 128 * 128, &p.q_map, n * 64, deal.head,
+                                     deal.s.q0 + deal.token + w * (128 >> p.shift), &sh.q_full);
+                }
+                ++unit;
+                for (int32_t t = 0; t < deal.tiles && ok; ++t) {
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (lap > 0) ok = warp_wait(&sh.empty[stage], (lap - 1) & 1, abort);
+                        if (!ok) break;
+                        if (lead) {
+                            bar_expect(&sh.full[stage], Sh::kStageBytes);
+                            for (int n = 0; n < Sh::kPanels; ++n)
+                                copy_box(ring + stage * Sh::kStageBytes + n * KT * 128, kv ? &p.v_map : &p.k_map, n * 64, deal.kv,
+                                         deal.s.k0 + t * KT, &sh.full[stage]);
+                        }
+                        __syncwarp();
+                        if (++stage == Sh::kStages) {
+                            stage = 0;
+                            ++lap;
+                        }
                     }
                 }
             }
-        }
-        // the block does not end before its copies have
-        const long long t0 = clock64();
-        const uint32_t n = lap * Sh::kStages + stage;     // items begun
-        for (uint32_t i = n > Sh::kStages ? n - Sh::kStages : 0; i < n; ++i)
-            while (!bar_try(&sh.full[i % Sh::kStages], (i / Sh::kStages) & 1) && clock64() - t0 < kWaitCycles) {
+            // the block does not end before its copies have
+            const long long t0 = clock64();
+            const uint32_t n = lap * Sh::kStages + stage;     // items begun
+            for (uint32_t i = n > Sh::kStages ? n - Sh::kStages : 0; i < n; ++i)
+                while (!bar_try(&sh.full[i % Sh::kStages], (i / Sh::kStages) & 1) && clock64() - t0 < kWaitCycles) {
+                }
+            while (unit > 0 && !bar_try(&sh.q_full, (unit - 1) & 1) && clock64() - t0 < kWaitCycles) {
             }
-        while (unit > 0 && !bar_try(&sh.q_full, (unit - 1) & 1) && clock64() - t0 < kWaitCycles) {
-        }
-        __syncwarp();
-    } else if (warp == kIssue) {
-        // ------------------------------------------------ matrix products (all lanes alike, see elect_lane)
-        const bool lead = elect_lane();
-        const uint32_t qk_desc = mma_desc(BF16, 128, KT, false, p.negative != 0);
-        const uint32_t pv_desc = mma_desc(BF16, 128, (p.dim + 15) / 16 * 16, true, false);
-        const int ksteps = (p.dim + 15) / 16;
-        uint32_t unit = 0, job0 = 0, gi = 0, cleaned = 0;   // gi: the unit's first tile since the start; parities of the stages' cleaning
-        auto wait_item = [&](uint32_t i) { return warp_wait(&sh.full[i % Sh::kStages], (i / Sh::kStages) & 1, abort); };
-        for (; __any_sync(~0u, deal.here) && ok; deal.next()) {
-            const uint32_t nt = __shfl_sync(~0u, static_cast<uint32_t>(deal.tiles), 0), jobs = nt * W;
-            const uint32_t whole = __shfl_sync(~0u, static_cast<uint32_t>(deal.whole), 0);
-            if (nt == 0) continue;
-            ok = warp_wait(&sh.q_full, unit & 1, abort);
-            if (!ok) break;
-            auto issue_qk = [&](uint32_t j) {
-                const uint32_t item = 2 * (gi + j / W), s = item % Sh::kStages, sb = (job0 + j) & 1;
-                if (!wait_item(item)) return false;
-                tc_fence_after();
-                const uint64_t qa = smem_desc(q_smem + (W == 2 ? sb * 128 * DP * 2 : 0), 16, 1024), ka = smem_desc(ring + s * Sh::kStageBytes, 16, 1024);
-                if (lead) {
+            __syncwarp();
+        } else if (warp == kIssue) {
+            // ------------------------------------------------ matrix products (all lanes alike, see elect_lane)
+            const bool lead = elect_lane();
+            const uint32_t qk_desc = mma_desc(BF16, 128, KT, false, p.negative != 0);
+            const uint32_t pv_desc = mma_desc(BF16, 128, (p.dim + 15) / 16 * 16, true, false);
+            const int ksteps = (p.dim + 15) / 16;
+            uint32_t unit = 0, job0 = 0, gi = 0, cleaned = 0;   // gi: the unit's first tile since the start; parities of the stages' cleaning
+            auto wait_item = [&](uint32_t i) { return warp_wait(&sh.full[i % Sh::kStages], (i / Sh::kStages) & 1, abort); };
+            for (; __any_sync(~0u, deal.here) && ok; deal.next()) {
+                const uint32_t nt = __shfl_sync(~0u, static_cast<uint32_t>(deal.tiles), 0), jobs = nt * W;
+                const uint32_t whole = __shfl_sync(~0u, static_cast<uint32_t>(deal.whole), 0);
+                if (nt == 0) continue;
+                ok = warp_wait(&sh.q_full, unit & 1, abort);
+                if (!ok) break;
+                auto issue_qk = [&](uint32_t j) {
+                    const uint32_t item = 2 * (gi + j / W), s = item % Sh::kStages, sb = (job0 + j) & 1;
+                    if (!wait_item(item)) return false;
+                    tc_fence_after();
+                    const uint64_t qa = smem_desc(q_smem + (W == 2 ? sb * 128 * DP * 2 : 0), 16, 1024), ka = smem_desc(ring + s * Sh::kStageBytes, 16, 1024);
 #pragma unroll
                     for (int kk = 0; kk < DP / 16; ++kk)
                         if (kk < ksteps)
-                            mma_ss(tmem + Sh::kS + sb * KT, qa + (kk >> 2) * 1024 + (kk & 3) * 2, ka + (kk >> 2) * (KT * 8) + (kk & 3) * 2, qk_desc, kk > 0);
-                    tc_commit(&sh.s_full[sb]);
-                    if (W == 1 || (j & 1)) tc_commit(&sh.empty[s]);
-                    if (j + 1 == jobs) tc_commit(&sh.q_empty);
-                }
-                __syncwarp();
-                return true;
-            };
-            for (uint32_t j = 0; j < 2 && j < jobs && ok; ++j) ok = issue_qk(j);
-            for (uint32_t j = 0; j < jobs && ok; ++j) {
-                const uint32_t job = job0 + j, sb = job & 1, item = 2 * (gi + j / W) + 1, s = item % Sh::kStages;
-                ok = wait_item(item);
-                if (ok && j / W >= whole && (W == 1 || !(j & 1))) {
-                    ok = warp_wait(&sh.clean[s], (cleaned >> s) & 1, abort);
-                    cleaned ^= 1u << s;
-                }
-                ok = ok && warp_wait(&sh.p_full[sb], (job >> 1) & 1, abort);
-                if (!ok) break;
-                tc_fence_after();
-                const uint64_t va = smem_desc(ring + s * Sh::kStageBytes, KT * 128, 1024);
-                if (lead) {
+                            mma_ss_if(lead, tmem + Sh::kS + sb * KT, qa + (kk >> 2) * 1024 + (kk & 3) * 2, ka + (kk >> 2) * (KT * 8) + (kk & 3) * 2, qk_desc, kk > 0);
+                    if (lead) {
+                        tc_commit(&sh.s_full[sb]);
+                        if (W == 1 || (j & 1)) tc_commit(&sh.empty[s]);
+                        if (j + 1 == jobs) tc_commit(&sh.q_empty);
+                    }
+                    __syncwarp();
+                    return true;
+                };
+                for (uint32_t j = 0; j < 2 && j < jobs && ok; ++j) ok = issue_qk(j);
+                for (uint32_t j = 0; j < jobs && ok; ++j) {
+                    const uint32_t job = job0 + j, sb = job & 1, item = 2 * (gi + j / W) + 1, s = item % Sh::kStages;
+                    ok = wait_item(item);
+                    if (ok && j / W >= whole && (W == 1 || !(j & 1))) {
+                        ok = warp_wait(&sh.clean[s], (cleaned >> s) & 1, abort);
+                        cleaned ^= 1u << s;
+                    }
+                    ok = ok && warp_wait(&sh.p_full[sb], (job >> 1) & 1, abort);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint64_t va = smem_desc(ring + s * Sh::kStageBytes, KT * 128, 1024);
 #pragma unroll
                     for (int kk = 0; kk < KT / 16; ++kk)
-                        mma_ts(tmem + Sh::kO + (W == 2 ? sb * DP : 0), tmem + Sh::kS + sb * KT + kk * 8, va + kk * 128, pv_desc, j >= W || kk > 0);
-                    tc_commit(&sh.pv_done[sb]);
-                    if (W == 1 || (j & 1)) tc_commit(&sh.empty[s]);
+                        mma_ts_if(lead, tmem + Sh::kO + (W == 2 ? sb * DP : 0), tmem + Sh::kS + sb * KT + kk * 8, va + kk * 128, pv_desc, j >= W || kk > 0);
+                    if (lead) {
+                        tc_commit(&sh.pv_done[sb]);
+                        if (W == 1 || (j & 1)) tc_commit(&sh.empty[s]);
+                    }
+                    __syncwarp();
+                    if (j + 2 < jobs) ok = issue_qk(j + 2);
                 }
-                __syncwarp();
-                if (j + 2 < jobs) ok = issue_qk(j + 2);
+                job0 += jobs;
+                gi += nt;
+                ++unit;
             }
-            job0 += jobs;
-            gi += nt;
-            ++unit;
-        }
-        // every product is done before the block gives its memory up
-        if (lead) tc_commit(&sh.drain);
-        __syncwarp();
-        if (!bar_wait(&sh.drain, 0, abort)) {
-            const long long t0 = clock64();
-            while (!bar_try(&sh.drain, 0) && clock64() - t0 < kWaitCycles) {
+            // every product is done before the block gives its memory up
+            if (lead) tc_commit(&sh.drain);
+            __syncwarp();
+            if (!bar_wait(&sh.drain, 0, abort)) {
+                const long long t0 = clock64();
+                while (!bar_try(&sh.drain, 0) && clock64() - t0 < kWaitCycles) {
+                }
             }
-        }
-        __syncwarp();
-    } else if (warp == kClean) {
-        // ------------------------------------------------ value tiles that are not whole
-        uint32_t unit = 0, gi = 0;
-        for (; deal.here && ok; deal.next()) {
-            if (deal.tiles == 0) continue;
-            const uint32_t u = unit % kOddUnits;
-            bool any = false;
-            // (every item is waited for in turn: a parity tells two laps of a stage apart)
-            for (int32_t t = 0; t < deal.tiles; ++t) {
-                const uint32_t item = 2 * (gi + t) + 1, s = item % Sh::kStages;
-                ok = warp_wait(&sh.full[(item - 1) % Sh::kStages], ((item - 1) / Sh::kStages) & 1, abort) &&
-                     warp_wait(&sh.full[s], (item / Sh::kStages) & 1, abort);
-                if (!ok) break;
-                if (t < deal.whole) continue;
-                const int32_t first = deal.s.keys - deal.s.rows + deal.token + 1 - t * KT;    // the first that not every row sees
-                any |= clean_tile<BF16, DP, KT>(smem + Sh::kQBytes + s * Sh::kStageBytes, first, deal.s.keys - t * KT, p.dim, sh.odd[u][t - deal.whole]);
-                if (lane == 0) reinterpret_cast<volatile uint32_t *>(sh.any_odd)[u] = any;
-                fence_async_reads();
-                __syncwarp();
-                if (lane == 0) bar_arrive(&sh.clean[s]);
+            __syncwarp();
+        } else if (warp == kClean) {
+            // ------------------------------------------------ value tiles that are not whole
+            uint32_t unit = 0, gi = 0;
+            for (; deal.here && ok; deal.next()) {
+                if (deal.tiles == 0) continue;
+                const uint32_t u = unit % kOddUnits;
+                bool any = false;
+                // (every item is waited for in turn: a parity tells two laps of a stage apart)
+                for (int32_t t = 0; t < deal.tiles; ++t) {
+                    const uint32_t item = 2 * (gi + t) + 1, s = item % Sh::kStages;
+                    ok = warp_wait(&sh.full[(item - 1) % Sh::kStages], ((item - 1) / Sh::kStages) & 1, abort) &&
+                         warp_wait(&sh.full[s], (item / Sh::kStages) & 1, abort);
+                    if (!ok) break;
+                    if (t < deal.whole) continue;
+                    const int32_t first = deal.s.keys - deal.s.rows + deal.token + 1 - t * KT;    // the first that not every row sees
+                    any |= clean_tile<BF16, DP, KT>(smem + Sh::kQBytes + s * Sh::kStageBytes, first, deal.s.keys - t * KT, p.dim, sh.odd[u][t - deal.whole]);
+                    if (lane == 0) reinterpret_cast<volatile uint32_t *>(sh.any_odd)[u] = any;
+                    fence_async_reads();
+                    __syncwarp();
+                    if (lane == 0) bar_arrive(&sh.clean[s]);
+                }
+                gi += deal.tiles;
+                ++unit;
             }
-            gi += deal.tiles;
-            ++unit;
+            __syncwarp();
         }
-        __syncwarp();
-    } else if (warp < kIssue) {
+    } else {
         // ------------------------------------------------ softmax, output
         const int wg = warp >> 2, row = (warp & 3) * 32 + lane;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;   // the warp's tensor memory lanes
@@ -490,21 +492,20 @@ __global__ void __launch_bounds__(Prompt<DP>::kThreads, 1) prompt_kernel(const _
                     }
                 }
                 const float mm = m == -INFINITY ? 0.f : m;
-                float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                float2 sum[2] = {};
 #pragma unroll
                 for (int c0 = 0; c0 < KT; c0 += 32) {
                     uint32_t y[16];
 #pragma unroll
                     for (int c = 0; c < 32; c += 2) {
-                        const float a = exp2_fast(fmaf(__uint_as_float(x[c0 + c]), p.c, -mm));
-                        const float b = exp2_fast(fmaf(__uint_as_float(x[c0 + c + 1]), p.c, -mm));
-                        sum[c & 2] += a;
-                        sum[(c & 2) + 1] += b;
+                        const float2 e = fma2(__uint_as_float(x[c0 + c]), __uint_as_float(x[c0 + c + 1]), p.c, -mm);
+                        const float a = exp2_fast(e.x), b = exp2_fast(e.y);
+                        add2(sum[c / 2 & 1], a, b);
                         y[c / 2] = Half2<BF16>::down(a, b);
                     }
                     tmem_store16(t_s + c0 / 2, y);
                 }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tc_wait_st();
                 tc_fence_before();
                 before = job;
