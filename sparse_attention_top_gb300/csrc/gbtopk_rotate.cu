@@ -27,7 +27,7 @@ namespace gbtopk {
 namespace {
 
 constexpr int kRowThreads = 256;
-constexpr int kInFlight = 3;   // head rows that a lane group has in flight
+constexpr int kMostTokens = 8;   // of a block
 
 struct RotateParams {
     const void *x[3];                 // q, k, v
@@ -39,8 +39,10 @@ struct RotateParams {
     int64_t qo_row, qo_head, k_slot, k_head, v_slot, v_head;   // elements (4-bit rows: bytes)
     int64_t num_slots;
     int32_t q_heads, kv_heads, dim, half;   // half: rotated pairs
-    int32_t steps;                    // row groups of a block
-    float eps, inv_unit[2];
+    int64_t num_tokens;
+    int32_t tokens, groups;           // of a block
+    FastDiv by_half;
+    float eps, inv_dim, unit[2], inv_unit[2];
 };
 
 template <bool BF16>
@@ -81,10 +83,11 @@ __device__ __forceinline__ uint32_t scale_byte(float s) {   // of a number that 
     return (__float_as_uint(s) >> 20) - (120u << 3);
 }
 
-__device__ __forceinline__ uint32_t put_code(int i, int code) {   // element i of a word of eight
-    const int j = i / 2;
-    const uint32_t mag = static_cast<uint32_t>(code < 0 ? -code : code), sign = code < 0;
-    return i & 1 ? mag << (4 * j + 16) | sign << ((4 * j + 31) & 31) : mag << (4 * j) | sign << (4 * j + 15);
+// Element i of a word of eight: a whole number of at most 7 in magnitude.
+__device__ __forceinline__ uint32_t put_code(int i, float code) {
+    const int j = i / 2, m = i & 1 ? 4 * j + 16 : 4 * j, s = i & 1 ? (4 * j + 31) & 31 : 4 * j + 15;
+    const uint32_t mag = __float_as_uint(fabsf(code) + 0x1p23f) & 7u, sign = __float_as_uint(code + 0.f) >> 31;   // (-0 is 0)
+    return mag << m | sign << s;
 }
 
 struct Row {
@@ -93,243 +96,316 @@ struct Row {
     bool there;            // the lane has elements
 };
 
-// The lane's eight elements of the normalised and rotated row in 64 bits, one
-// row a group of LP lanes; every lane of the warp takes part.
+// Sine and cosine of 2 pi x for |x| <= 1/2, off by less than 1e-13: the quarter
+// turn nearest to x by its symmetries, the rest, at most pi / 4, by its Taylor
+// series up to the 15th power.
+__device__ __forceinline__ void turn_wide(double x, double *sine, double *cosine) {
+    const double quarter = rint(4 * x), r = (x - 0.25 * quarter) * 6.283185307179586477, z = r * r;
+    double s = -1.0 / 1307674368000.0, c = -1.0 / 87178291200.0;
+    s = fma(s, z, 1.0 / 6227020800.0);
+    c = fma(c, z, 1.0 / 479001600.0);
+    s = fma(s, z, -1.0 / 39916800.0);
+    c = fma(c, z, -1.0 / 3628800.0);
+    s = fma(s, z, 1.0 / 362880.0);
+    c = fma(c, z, 1.0 / 40320.0);
+    s = fma(s, z, -1.0 / 5040.0);
+    c = fma(c, z, -1.0 / 720.0);
+    s = fma(s, z, 1.0 / 120.0);
+    c = fma(c, z, 1.0 / 24.0);
+    s = fma(s, z, -1.0 / 6.0);
+    c = fma(c, z, -0.5);
+    s = fma(s * z, r, r);
+    c = fma(c, z, 1.0);
+    const int q = static_cast<int>(quarter) & 3;
+    *sine = q == 0 ? s : q == 1 ? c : q == 2 ? -s : -c;
+    *cosine = q == 0 ? c : q == 1 ? -s : q == 2 ? -c : s;
+}
+
+// Codes and scale of the lane's eight elements from the normalised and rotated
+// row in 64 bits, one row a group of LP lanes; every lane of the warp takes part.
+// Rare (some 2 in 100,000 elements) and by one warp alone, whose time is mostly
+// that of its instructions' way to the SM: loops that are not unrolled, no
+// division.
 template <bool BF16, int LP, bool PAIRS>
-__device__ __noinline__ void turned_wide(const RotateParams &p, const Row &row, const void *w, bool w_wide, double position, double *y) {
+__device__ __noinline__ uint32_t encode_again(const RotateParams &p, const Row &row, const void *w, bool w_wide, double position,
+                                              double inv_unit, uint32_t *byte) {
     const int lane = threadIdx.x & (LP - 1);
-    double sum = 0;
-    float x[8], f[8];
+    double sum = 0, y[8];
+    float f[8];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 t = Half2<BF16>::up(row.raw[i]);
-        x[2 * i] = t.x;
-        x[2 * i + 1] = t.y;
-        sum += static_cast<double>(t.x) * t.x + static_cast<double>(t.y) * t.y;
+        y[2 * i] = t.x;
+        y[2 * i + 1] = t.y;
     }
-    for (int o = LP / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-    const double r = w ? 1.0 / sqrt(sum / p.dim + static_cast<double>(p.eps)) : 1.0;
-    if (w && row.there) load_weights<BF16>(w, w_wide, row.at, f);
-    for (int i = 0; i < 8; ++i) y[i] = w && row.there ? x[i] * r * f[i] : x[i] * r;
-    auto turn = [&](int32_t k, double *c, double *s) {
-        const double a = position * (static_cast<double>(p.inv_freq[k]) * 0.15915494309189533577);
-        sincospi(2 * (a - rint(a)), s, c);
-    };
-    const int32_t rotary = 2 * p.half;
-    if constexpr (PAIRS) {
-        if (!row.there || row.at >= rotary) return;
-        for (int i = 0; i < 8; i += 2) {
-            double c, s;
-            turn((row.at + i) / 2, &c, &s);
-            const double a = y[i], b = y[i + 1];
-            y[i] = a * c - b * s;
-            y[i + 1] = b * c + a * s;
-        }
-    } else {
-        const bool in = row.there && row.at < rotary, second = row.at >= p.half;
-        const int from = in ? (second ? lane - p.half / 8 : lane + p.half / 8) : lane;
-        for (int i = 0; i < 8; ++i) {
-            const double other = __shfl_sync(~0u, y[i], from, LP);
-            if (!in) continue;
-            double c, s;
-            turn(row.at - (second ? p.half : 0) + i, &c, &s);
-            y[i] = second ? y[i] * c + other * s : y[i] * c - other * s;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) sum = fma(y[i], y[i], sum);
+    if (w) {
+#pragma unroll 1
+        for (int o = LP / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+        const double v = sum / p.dim + static_cast<double>(p.eps);
+        double r = rsqrtf(static_cast<float>(v));      // two steps of Newton's method from 22 bits
+        r = r * fma(-0.5 * v * r, r, 1.5);
+        r = r * fma(-0.5 * v * r, r, 1.5);
+        if (row.there) load_weights<BF16>(w, w_wide, row.at, f);
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) y[i] = row.there ? y[i] * r * f[i] : 0;
+    }
+    const bool in = row.there && row.at < 2 * p.half, second = !PAIRS && row.at >= p.half;
+    const int32_t k0 = !in ? 0 : PAIRS ? row.at / 2 : row.at - (second ? p.half : 0);
+    const int from = in && !PAIRS ? (second ? lane - p.half / 8 : lane + p.half / 8) : lane;
+    double top = 0, s, c;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+        if (p.half && !(PAIRS && (i & 1))) {
+            const double a = position * (static_cast<double>(p.inv_freq[k0 + (PAIRS ? i / 2 : i)]) * 0.15915494309189533577);
+            turn_wide(a - rint(a), &s, &c);
+            const double other = PAIRS ? y[i + 1] : __shfl_sync(~0u, y[i], from, LP), mine = y[i];
+            if (in) {
+                y[i] = second ? mine * c + other * s : mine * c - other * s;
+                if (PAIRS) y[i + 1] = other * c + mine * s;
+            }
         }
     }
-}
-
-// Codes of the lane's elements (a block's other eight are the lane's
-// neighbour's) and the block's scale byte, from numbers in 64 bits.
-__device__ __noinline__ uint32_t encode_wide(const double *y, double inv_unit, uint32_t *byte) {
-    double top = 0;
-    for (int i = 0; i < 8; ++i) top = fmax(top, fabs(y[i] * inv_unit));
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) {
+        y[i] *= inv_unit;
+        top = fmax(top, fabs(y[i]));
+    }
     top = fmax(top, __shfl_xor_sync(~0u, top, 1));
-    double t = top / 7;
-    t = t > 448 ? 448 : t;
-    int e = static_cast<int>(static_cast<unsigned long long>(__double_as_longlong(t)) >> 52) - 1023;
+    // as block_scale
+    top = fmin(top, 4096.0);
+    int e = static_cast<int>(static_cast<unsigned long long>(__double_as_longlong(top * (1.0 / 7.0))) >> 52) - 1023;
     e = e < -6 ? -6 : e;
-    const double step = __longlong_as_double(static_cast<long long>(e - 3 + 1023) << 52);
-    double s = rint(t / step) * step;
-    s = s > 448 ? 448 : s;
-    *byte = scale_byte(static_cast<float>(s));
+    const double step = __longlong_as_double(static_cast<long long>(e - 3 + 1023) << 52), steps = __longlong_as_double(static_cast<long long>(3 - e + 1023) << 52);
+    const double low = floor(top * (1.0 / 7.0) * steps), off = top * steps - 7 * (low + 0.5);
+    const bool up = off > 0 || (off == 0 && (static_cast<int>(low) & 1));
+    const double scale = fmin((low + (up ? 1 : 0)) * step, 448.0);
+    *byte = scale_byte(static_cast<float>(scale));
+    double per = scale > 0 ? 1.f / static_cast<float>(scale) : 0.f;
+    per = per * fma(-scale, per, 2.0);
     uint32_t word = 0;
+#pragma unroll 1
     for (int i = 0; i < 8; ++i) {
-        double c = s > 0 ? rint(y[i] * inv_unit / s) : 0;
-        c = c > 7 ? 7 : c < -7 ? -7 : c == c ? c : 0;
-        word |= put_code(i, static_cast<int>(c));
+        double x = rint(y[i] * per);
+        const double rest = fma(-x, scale, y[i]);
+        if (fabs(rest) == 0.5 * scale) x = 2 * rint(0.5 * (x + copysign(0.5, rest)));
+        x = x > 7 ? 7 : x < -7 ? -7 : x == x ? x : 0;
+        word |= put_code(i, static_cast<float>(x));
     }
     return word;
 }
 
-// The same from 32-bit numbers with errors up to err[i]; *doubt where an error
-// could have changed a code or the scale.
-__device__ __forceinline__ uint32_t encode(const float *y, const float *err, float inv_unit, uint32_t *byte, bool *doubt) {
-    float top = 0.f, off = 0.f;
+// The same from 32-bit numbers, keys with errors of at most err[i]; *doubt where
+// an error could have changed a code or the scale.
+template <bool KEYS>
+__device__ __forceinline__ uint32_t encode(const float *y, const float *err, float unit, float inv_unit, uint32_t *byte, bool *doubt) {
+    float top = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        top = fmaxf(top, fabsf(y[i] * inv_unit));   // (a NaN is no maximum)
-        off = fmaxf(off, err[i] * inv_unit);
-    }
-    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-    off = fmaxf(off, __shfl_xor_sync(~0u, off, 1));
+    for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(y[i]));   // (a NaN is no maximum)
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1)) * inv_unit;
     float near;
-    const float s = block_scale(fminf(top, 4096.f), &near);   // (saturated from 7 * 464 on)
-    bool odd = off > 0.f && near <= off;
-    *byte = scale_byte(s);
-    const float per = s > 0.f ? 1.f / s : 0.f, half = 0.5f * s;
+    const float steps = block_scale(fminf(top, 4096.f), &near);   // (saturated from 7 * 464 on)
+    *byte = scale_byte(steps);
+    const float s = steps * unit, per = s > 0.f ? 1.f / s : 0.f;
+    constexpr float kWhole = 0x1.8p23f;    // a sum with it is rounded to a whole number
+    float border = 1.f, most = 0.f;        // the least of distances from a border less errors, in codes
+    float mag[8];
     uint32_t word = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float x = y[i] * inv_unit;
-        float c = rintf(fminf(fmaxf(x * per, -8.f), 8.f));
-        if (!(x == x)) c = 0.f;
-        const float rest = fmaf(-c, s, x), far = fabsf(rest);   // exact where the nearest code is not beyond 8
-        const bool tie = far == half && (static_cast<int>(c) & 1);
-        if (fabsf(c) < 8.f && s > 0.f && (far > half || tie)) c += rest > 0.f ? 1.f : -1.f;
-        odd |= err[i] > 0.f && fabsf(far - half) <= err[i] * inv_unit;
-        c = fminf(fmaxf(c, -7.f), 7.f);
-        word |= put_code(i, static_cast<int>(c));
+        // The quotient with its one correction is exact on borders (shown for all
+        // scales and codes), and away from them by more than it is off: the
+        // 16-bit types' own numbers have at most 11 bits, keys their err.
+        float t = y[i] * per;
+        t = fmaf(fmaf(-t, s, y[i]), per, t);
+        const float c = (t + kWhole) - kWhole;
+        if constexpr (KEYS) {
+            border = fminf(border, err[i] > 0.f ? fmaf(-err[i], per, fabsf(fabsf(t - c) - 0.5f)) : 1.f);
+            most = fmaxf(most, err[i]);
+        }
+        mag[i] = fminf(fabsf(c), 7.f);
+        const int j = i / 2, at = i & 1 ? (4 * j + 31) & 31 : 4 * j + 15;
+        word |= (__float_as_uint(c) & 0x80000000u) >> (31 - at);
     }
-    *doubt = odd;
-    return word;
+    const float even = fmaf(fmaf(fmaf(mag[6], 16.f, mag[4]), 16.f, mag[2]), 16.f, mag[0]);
+    const float odd = fmaf(fmaf(fmaf(mag[7], 16.f, mag[5]), 16.f, mag[3]), 16.f, mag[1]);
+    word |= __byte_perm(__float_as_uint(even + 0x1p23f), __float_as_uint(odd + 0x1p23f), 0x5410);
+    if constexpr (KEYS) {
+        most = fmaxf(most, __shfl_xor_sync(~0u, most, 1));
+        *doubt = border <= 0.f || (most > 0.f && near <= most * inv_unit);
+    }
+    return s > 0.f ? word : 0u;
 }
 
-// Grid (tokens, chunks of a token's head rows): rows q heads, k heads, v heads.
+// A block has p.tokens tokens, and of each the head-row groups blockIdx.y *
+// p.groups on.  A group is a warp's rows at a time (32 / LP heads of q, of k or
+// of v): a warp has one kind of work, whose addresses and weights it keeps while
+// it goes through the tokens, four rows in flight.  (With the heads inside and
+// the tokens outside, 16,001 tokens of 32 over 8 heads took 94 us, most of it
+// address arithmetic.)
 template <bool BF16, int LP, bool PAIRS, bool INT4>
-__global__ void __launch_bounds__(kRowThreads) rotate_kernel(const __grid_constant__ RotateParams p, int w_wide) {
-    constexpr int kRows = kRowThreads / LP;   // a step
-    __shared__ float2 turn[128];           // cosine and sine of the token's angles
+__global__ void __launch_bounds__(kRowThreads, 4) rotate_kernel(const __grid_constant__ RotateParams p, int w_wide) {
+    constexpr int kRows = 32 / LP;         // of a group
+    constexpr int kAhead = 4;
+    extern __shared__ float2 turns[];      // [tokens][half]: cosine and sine
+    __shared__ int32_t slots[kMostTokens];
     pdl_wait();
     pdl_release();
-    const int64_t token = blockIdx.x;
-    const int lane = threadIdx.x & (LP - 1), group = threadIdx.x / LP;
-    const int32_t rows = p.q_heads + 2 * p.kv_heads;
-    const int32_t first = static_cast<int32_t>(blockIdx.y) * p.steps;
-    const int32_t slot = p.slots[token];
-    const bool kept = slot >= 0 && slot < p.num_slots;
-    const int32_t at = lane * 8;
-    const bool there = at < p.dim;
-    const int32_t position = p.half ? p.positions[token] : 0;
-    bool turned = false;
-    for (int32_t s0 = 0; s0 < p.steps; s0 += kInFlight) {
-        Row row[kInFlight];
-        int32_t head[kInFlight];
-        int kind[kInFlight];                  // q, k, v, or -1
-#pragma unroll
-        for (int u = 0; u < kInFlight; ++u) {
-            int32_t h = s0 + u < p.steps ? (first + s0 + u) * kRows + group : rows;
-            kind[u] = h >= rows ? -1 : h < p.q_heads ? 0 : h < p.q_heads + p.kv_heads ? 1 : 2;
-            if (kind[u] > 0) h -= p.q_heads + (kind[u] - 1) * p.kv_heads;
-            head[u] = h;
-            if (kind[u] > 0 && !kept) kind[u] = -1;
-            row[u].at = at;
-            row[u].there = there && kind[u] >= 0;
-            uint4 v = make_uint4(0, 0, 0, 0);
-            if (row[u].there) {
-                const uint8_t *base = static_cast<const uint8_t *>(kind[u] == 0 ? p.x[0] : kind[u] == 1 ? p.x[1] : p.x[2]);
-                const int64_t sr = kind[u] == 0 ? p.x_row[0] : kind[u] == 1 ? p.x_row[1] : p.x_row[2];
-                const int64_t sh = kind[u] == 0 ? p.x_head[0] : kind[u] == 1 ? p.x_head[1] : p.x_head[2];
-                v = *reinterpret_cast<const uint4 *>(base + 2 * (token * sr + h * sh + at));
-            }
-            row[u].raw[0] = v.x; row[u].raw[1] = v.y; row[u].raw[2] = v.z; row[u].raw[3] = v.w;
+    const int64_t token0 = static_cast<int64_t>(blockIdx.x) * p.tokens;
+    const int32_t tokens = static_cast<int32_t>(p.num_tokens - token0 < p.tokens ? p.num_tokens - token0 : p.tokens);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & (LP - 1), sub = (threadIdx.x & 31) / LP;
+    const int32_t gq = (p.q_heads + kRows - 1) / kRows, gk = (p.kv_heads + kRows - 1) / kRows;
+    const int32_t at = lane * 8, rotary = 2 * p.half;
+    const int32_t end = gq + 2 * gk < (static_cast<int32_t>(blockIdx.y) + 1) * p.groups ? gq + 2 * gk : (static_cast<int32_t>(blockIdx.y) + 1) * p.groups;
+    if (static_cast<int32_t>(threadIdx.x) < tokens) slots[threadIdx.x] = p.slots[token0 + threadIdx.x];
+    for (int k = threadIdx.x; k < tokens * p.half; k += kRowThreads) {
+        const int32_t t = static_cast<int32_t>(p.by_half.div(static_cast<uint32_t>(k)));
+        const double a = static_cast<double>(p.positions[token0 + t]) * (static_cast<double>(p.inv_freq[k - t * p.half]) * 0.15915494309189533577);
+        float s, c;
+        const double rest = a - rint(a);
+        const float near = static_cast<float>(rest), off = static_cast<float>(rest - near) * 6.2831853f;
+        sincospif(2.f * near, &s, &c);
+        turns[k] = make_float2(fmaf(-s, off, c), fmaf(c, off, s));     // (what the 32-bit turns leave out)
+    }
+    __syncthreads();
+    // the lane's partner in the rotation, its angles, the sign of its sine
+    const bool in = at < rotary, second = !PAIRS && at >= p.half;
+    const int from = in ? (second ? lane - p.half / 8 : lane + p.half / 8) : lane;
+    const float2 *mine = turns + (!in ? 0 : PAIRS ? at / 2 : at - (second ? p.half : 0));
+
+    for (int32_t g = static_cast<int32_t>(blockIdx.y) * p.groups + warp; g < end; g += kRowThreads / 32) {
+        const int kind = g < gq ? 0 : g < gq + gk ? 1 : 2;
+        const int32_t head = (g - (kind == 0 ? 0 : gq + (kind - 1) * gk)) * kRows + sub;
+        const bool there = at < p.dim && head < (kind == 0 ? p.q_heads : p.kv_heads);
+        const uint8_t *src = static_cast<const uint8_t *>(p.x[kind]) + 2 * (token0 * p.x_row[kind] + (there ? head * p.x_head[kind] + at : 0));
+        const int64_t step = 2 * p.x_row[kind];
+        // (16-bit caches: rows of k or v; 4-bit ones: bytes of the row)
+        uint8_t *dst;
+        int64_t dst_step;
+        if (kind == 0) {
+            dst = static_cast<uint8_t *>(p.q_out) + 2 * (token0 * p.qo_row + head * p.qo_head + at);
+            dst_step = 2 * p.qo_row;
+        } else if (INT4) {
+            dst = static_cast<uint8_t *>(p.k_cache) + head * p.k_head + (kind - 1) * int4_codes(p.dim) + at / 2;
+            dst_step = p.k_slot;
+        } else {
+            dst = static_cast<uint8_t *>(kind == 1 ? p.k_cache : p.v_cache) + 2 * (head * (kind == 1 ? p.k_head : p.v_head) + at);
+            dst_step = 2 * (kind == 1 ? p.k_slot : p.v_slot);
         }
-        if (!turned && p.half) {           // while the rows are in flight
-            for (int k = threadIdx.x; k < p.half; k += kRowThreads) {
-                const double a = static_cast<double>(position) * (static_cast<double>(p.inv_freq[k]) * 0.15915494309189533577);
-                float s, c;
-                sincospif(2.f * static_cast<float>(a - rint(a)), &s, &c);
-                turn[k] = make_float2(c, s);
-            }
-            __syncthreads();
-            turned = true;
-        }
+        const void *w = kind < 2 ? p.w[kind] : nullptr;
+        float f[8];
+        if (w && there) load_weights<BF16>(w, w_wide != 0, at, f);
+        uint32_t doubts = 0;      // tokens whose codes need 64 bits
+        for (int32_t t0 = 0; t0 < tokens; t0 += kAhead) {
+            uint4 raw[kAhead];
 #pragma unroll
-        for (int u = 0; u < kInFlight; ++u) {
-            if (__all_sync(~0u, kind[u] < 0)) continue;
-            const void *w = kind[u] == 0 ? p.w[0] : kind[u] == 1 ? p.w[1] : nullptr;
-            const bool rotates = kind[u] == 0 || kind[u] == 1;
-            float y[8], err[8];
-            float sum = 0.f;
+            for (int u = 0; u < kAhead; ++u)
+                raw[u] = there && t0 + u < tokens ? *reinterpret_cast<const uint4 *>(src + (t0 + u) * step) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 t = Half2<BF16>::up(row[u].raw[i]);
-                y[2 * i] = t.x;
-                y[2 * i + 1] = t.y;
-                sum = fmaf(t.x, t.x, fmaf(t.y, t.y, sum));
-            }
-            for (int o = LP / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-            const float r = rsqrtf(sum / static_cast<float>(p.dim) + p.eps);
-            if (w && row[u].there) {
-                float f[8];
-                load_weights<BF16>(w, w_wide != 0, at, f);
+            for (int u = 0; u < kAhead; ++u) {
+                const int32_t t = t0 + u;
+                if (t >= tokens) break;
+                const int32_t slot = kind > 0 ? slots[t] : t;
+                if (kind > 0 && (slot < 0 || slot >= p.num_slots)) continue;
+                uint8_t *to = dst + slot * dst_step;
+                if (kind == 2 && !INT4) {      // as they are
+                    if (there) *reinterpret_cast<uint4 *>(to) = raw[u];
+                    continue;
+                }
+                const uint32_t v[4] = {raw[u].x, raw[u].y, raw[u].z, raw[u].w};
+                float y[8], pair[4];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) y[i] *= r * f[i];
-            }
-            // Relative errors, in units of 2^-24: the sum 14, halved by the
-            // root, rsqrtf 4, the products 3; cosine and sine 2 ulp and the
-            // turns' rounding, 2 pi / 2, of 1.  2^-19 of the terms is twice that.
+                for (int j = 0; j < 4; ++j) {
+                    const float2 z = Half2<BF16>::up(v[j]);
+                    y[2 * j] = z.x;
+                    y[2 * j + 1] = z.y;
+                    pair[j] = fmaf(z.x, z.x, z.y * z.y);
+                }
+                float sum = (pair[0] + pair[1]) + (pair[2] + pair[3]);
+                if (w) {
+                    for (int o = LP / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+                    const float mean = fmaf(sum, p.inv_dim, p.eps);
+                    float r = rsqrtf(mean);
+                    if (INT4 && kind == 1) r = fmaf(0.5f * r, fmaf(-mean * r, r, 1.f), r);    // (a step of Newton's method)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) err[i] = w ? fabsf(y[i]) * 0x1p-19f : 0.f;
-            const int32_t rotary = 2 * p.half;
-            if constexpr (PAIRS) {
-                if (rotates && there && at < rotary) {
+                    for (int j = 0; j < 8; ++j) y[j] *= r * f[j];
+                }
+                // Relative errors of a key, in units of 2^-24: the sum 9, its mean 2, both
+                // halved by the root; the refined root 2, the products 2; sine and cosine
+                // 2; the rotation 2.  2^-20 of an element's terms is more than all of it.
+                float err[8];
+                if constexpr (INT4) {
 #pragma unroll
-                    for (int i = 0; i < 8; i += 2) {
-                        const float2 cs = turn[(at + i) / 2];
-                        const float a = y[i], b = y[i + 1];
-                        y[i] = a * cs.x - b * cs.y;
-                        y[i + 1] = b * cs.x + a * cs.y;
-                        if constexpr (INT4) err[i] = err[i + 1] = (fabsf(a) + fabsf(b)) * 0x1p-19f;
+                    for (int j = 0; j < 8; ++j) err[j] = w ? fabsf(y[j]) * 0x1p-20f : 0.f;
+                }
+                if (kind < 2 && rotary) {
+                    const float2 *turn = mine + t * p.half;
+                    if constexpr (PAIRS) {
+                        if (in) {
+#pragma unroll
+                            for (int j = 0; j < 8; j += 2) {
+                                const float2 cs = turn[j / 2];
+                                const float a = y[j], b = y[j + 1];
+                                y[j] = a * cs.x - b * cs.y;
+                                y[j + 1] = b * cs.x + a * cs.y;
+                                if constexpr (INT4) err[j] = err[j + 1] = (fabsf(a) + fabsf(b)) * 0x1p-20f;
+                            }
+                        }
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float other = __shfl_sync(~0u, y[j], from, LP);
+                            const float2 cs = turn[j];
+                            if constexpr (INT4) err[j] = in ? (fabsf(y[j]) + fabsf(other)) * 0x1p-20f : err[j];
+                            y[j] = in ? fmaf(second ? other : -other, cs.y, y[j] * cs.x) : y[j];
+                        }
                     }
                 }
-            } else {
-                const bool in = rotates && there && at < rotary, second = at >= p.half;
-                const int from = in ? (second ? lane - p.half / 8 : lane + p.half / 8) : lane;
-                const int32_t k0 = in ? at - (second ? p.half : 0) : 0;
+                if (!INT4 || kind == 0) {
+                    if (there)
+                        *reinterpret_cast<uint4 *>(to) = make_uint4(Half2<BF16>::down(y[0], y[1]), Half2<BF16>::down(y[2], y[3]),
+                                                                    Half2<BF16>::down(y[4], y[5]), Half2<BF16>::down(y[6], y[7]));
+                } else if constexpr (INT4) {
+                    if (__any_sync(~0u, !(sum < INFINITY))) {      // (a NaN is stored as 0, an infinity as the largest)
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float other = __shfl_sync(~0u, y[i], from, LP);
-                    if (!in) continue;
-                    const float2 cs = turn[k0 + i];
-                    if constexpr (INT4) err[i] = (fabsf(y[i]) + fabsf(other)) * 0x1p-19f;
-                    y[i] = second ? y[i] * cs.x + other * cs.y : y[i] * cs.x - other * cs.y;
+                        for (int j = 0; j < 8; ++j) y[j] = y[j] == y[j] ? fminf(fmaxf(y[j], -FLT_MAX), FLT_MAX) : 0.f;
+                    }
+                    uint32_t byte;
+                    bool doubt = false;
+                    const float unit = p.unit[kind - 1], inv_unit = p.inv_unit[kind - 1];
+                    const uint32_t word = kind == 1 ? encode<true>(y, err, unit, inv_unit, &byte, &doubt) : encode<false>(y, err, unit, inv_unit, &byte, &doubt);
+                    if (there) {
+                        *reinterpret_cast<uint32_t *>(to) = word;
+                        // (the scales lie behind both codes)
+                        if (!(lane & 1))
+                            to[(3 - kind) * int4_codes(p.dim) - at / 2 + (kind - 1) * int4_scales(p.dim) + at / 16] = static_cast<uint8_t>(byte);
+                    }
+                    if (__any_sync(~0u, doubt && there)) doubts |= 1u << t;
                 }
             }
-            if (!INT4 || __any_sync(~0u, kind[u] == 0)) {
-                if (row[u].there && !(INT4 && kind[u] > 0)) {
-                    uint4 v;
-                    v.x = Half2<BF16>::down(y[0], y[1]);
-                    v.y = Half2<BF16>::down(y[2], y[3]);
-                    v.z = Half2<BF16>::down(y[4], y[5]);
-                    v.w = Half2<BF16>::down(y[6], y[7]);
-                    if (kind[u] == 2) v = make_uint4(row[u].raw[0], row[u].raw[1], row[u].raw[2], row[u].raw[3]);
-                    uint8_t *dst = kind[u] == 0 ? static_cast<uint8_t *>(p.q_out) + 2 * (token * p.qo_row + head[u] * p.qo_head)
-                                   : kind[u] == 1 ? static_cast<uint8_t *>(p.k_cache) + 2 * (slot * p.k_slot + head[u] * p.k_head)
-                                                  : static_cast<uint8_t *>(p.v_cache) + 2 * (slot * p.v_slot + head[u] * p.v_head);
-                    *reinterpret_cast<uint4 *>(dst + 2 * at) = v;
-                }
-            }
-            if constexpr (INT4) {
-                if (__all_sync(~0u, kind[u] <= 0)) continue;
-                const float inv_unit = kind[u] == 2 ? p.inv_unit[1] : p.inv_unit[0];
+        }
+        if constexpr (INT4) {
+            // (behind the loop, whose registers it would take)
+#pragma unroll 1
+            for (; doubts; doubts &= doubts - 1) {
+                const int32_t t = __ffs(static_cast<int>(doubts)) - 1;
+                Row row;
+                row.at = at;
+                row.there = there;
+                const uint4 v = there ? *reinterpret_cast<const uint4 *>(src + t * step) : make_uint4(0, 0, 0, 0);
+                row.raw[0] = v.x;
+                row.raw[1] = v.y;
+                row.raw[2] = v.z;
+                row.raw[3] = v.w;
                 uint32_t byte;
-                bool doubt;
-                uint32_t word = encode(y, err, inv_unit, &byte, &doubt);
-                if (__any_sync(~0u, doubt && row[u].there && kind[u] == 1)) {
-                    double wide[8];
-                    turned_wide<BF16, LP, PAIRS>(p, row[u], kind[u] == 1 ? p.w[1] : nullptr, w_wide != 0, position, wide);
-                    uint32_t b;
-                    const uint32_t again = encode_wide(wide, inv_unit, &b);
-                    if (kind[u] == 1) {
-                        word = again;
-                        byte = b;
-                    }
-                }
-                if (row[u].there && kind[u] > 0) {
-                    uint8_t *dst = static_cast<uint8_t *>(p.k_cache) + slot * p.k_slot + head[u] * p.k_head;
-                    const int c = int4_codes(p.dim), part = kind[u] - 1;
-                    *reinterpret_cast<uint32_t *>(dst + part * c + at / 2) = word;
-                    if (!(lane & 1)) dst[2 * c + part * int4_scales(p.dim) + at / 16] = static_cast<uint8_t>(byte);
+                const uint32_t word = encode_again<BF16, LP, PAIRS>(p, row, w, w_wide != 0, p.half ? p.positions[token0 + t] : 0,
+                                                                    p.inv_unit[kind - 1], &byte);
+                uint8_t *to = dst + slots[t] * dst_step;
+                if (there) {
+                    *reinterpret_cast<uint32_t *>(to) = word;
+                    if (!(lane & 1))
+                        to[(3 - kind) * int4_codes(p.dim) - at / 2 + (kind - 1) * int4_scales(p.dim) + at / 16] = static_cast<uint8_t>(byte);
                 }
             }
         }
@@ -392,14 +468,20 @@ __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant
 
 template <bool BF16, int LP, bool PAIRS>
 cudaError_t launch_rotate(RotateParams p, int64_t tokens, bool int4, int w_wide, int sms, cudaStream_t s) {
-    const int32_t rows = p.q_heads + 2 * p.kv_heads, per = kRowThreads / LP, steps = (rows + per - 1) / per;
-    // A block a token; where that leaves SMs idle, a block a step of its rows
-    // (each works the token's angles out again).
-    const int32_t chunks = tokens < 2ll * sms ? steps : 1;
-    p.steps = chunks == 1 ? steps : 1;
-    const dim3 grid(static_cast<unsigned>(tokens), static_cast<unsigned>(chunks));
-    return int4 ? launch_pdl(rotate_kernel<BF16, LP, PAIRS, true>, grid, kRowThreads, 0, s, 1, p, w_wide)
-                : launch_pdl(rotate_kernel<BF16, LP, PAIRS, false>, grid, kRowThreads, 0, s, 1, p, w_wide);
+    const int32_t per = 32 / LP, warps = kRowThreads / 32;
+    const int32_t groups = (p.q_heads + per - 1) / per + 2 * ((p.kv_heads + per - 1) / per);
+    // As many tokens a block as leave every SM four blocks; a token's groups
+    // spread over blocks (each of which works its angles out again) where even a
+    // block a token leaves SMs idle.
+    p.num_tokens = tokens;
+    const int64_t fair = tokens / (4ll * sms);
+    p.tokens = fair >= kMostTokens ? kMostTokens : fair > 1 ? static_cast<int32_t>(fair) : 1;
+    p.groups = tokens < 2ll * sms && groups > warps ? warps : groups;
+    p.by_half.init(static_cast<uint32_t>(p.half > 0 ? p.half : 1));
+    const dim3 grid(static_cast<unsigned>((tokens + p.tokens - 1) / p.tokens), static_cast<unsigned>((groups + p.groups - 1) / p.groups));
+    const size_t bytes = static_cast<size_t>(p.tokens) * p.half * sizeof(float2);
+    return int4 ? launch_pdl(rotate_kernel<BF16, LP, PAIRS, true>, grid, kRowThreads, bytes, s, 1, p, w_wide)
+                : launch_pdl(rotate_kernel<BF16, LP, PAIRS, false>, grid, kRowThreads, bytes, s, 1, p, w_wide);
 }
 
 template <bool BF16, bool PAIRS>
@@ -457,6 +539,7 @@ RotateParams fill(const void *q, int64_t q_row, int64_t q_head, const void *k, i
     p.dim = dim;
     p.half = half;
     p.eps = eps;
+    p.inv_dim = 1.f / static_cast<float>(dim > 0 ? dim : 1);
     return p;
 }
 
@@ -511,6 +594,8 @@ int gbtopk_rotate_and_cache_int4(const void *q, int dtype, int64_t num_tokens, i
     p.k_cache = cache;
     p.k_slot = slot_stride;
     p.k_head = head_stride;
+    p.unit[0] = k_scale;
+    p.unit[1] = v_scale;
     p.inv_unit[0] = 1.f / k_scale;
     p.inv_unit[1] = 1.f / v_scale;
     return rotate(p, dtype, num_tokens, weight_dtype, interleaved, true, stream);
