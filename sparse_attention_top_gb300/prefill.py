@@ -54,6 +54,7 @@ def _lib():
     return _calls
 
 
+@functools.lru_cache(maxsize=None)
 def int4_row_bytes(head_dim: int) -> int:
     """Bytes of a row of a 4-bit cache: a head's key and value in one slot."""
     n = int(_lib().gbtopk_int4_row_bytes(head_dim)) if 0 < head_dim < 1 << 31 else 0
@@ -83,31 +84,54 @@ def _heads(q, k, v, same_rows: bool):
 
 def _tokens(q, k, v, positions, slots, inv_freq, q_weight, k_weight, eps, interleaved, q_out):
     """The arguments that both writes share, up to `slots`, and q_out."""
+    try:
+        shape, kshape, dt, dev = q.shape, k.shape, q.dtype, q.device
+        rows, heads, dim = shape
+        kv = kshape[1]
+        qs, ks, vs = q.stride(), k.stride(), v.stride()
+        if q_out is None:
+            q_out, os = torch.empty(shape, dtype=dt, device=dev), (heads * dim, dim, 1)
+        else:
+            os = q_out.stride()
+        freqs = 0 if inv_freq is None else inv_freq.shape[0]
+        w = k_weight if q_weight is None else q_weight
+        wtype = dt if w is None else w.dtype
+        fine = (dt in _HALF and q.is_cuda and k.dtype is dt and v.dtype is dt and k.device == dev and v.device == dev
+                and kshape == v.shape and kshape[0] == rows and kshape[2] == dim and kv >= 1 and heads % kv == 0
+                and (dim < 2 or qs[2] == ks[2] == vs[2] == os[2] == 1)
+                and q_out.shape == shape and q_out.dtype is dt and q_out.device == dev
+                and (freqs == 0 or (inv_freq.dtype is _F32 and inv_freq.device == dev and inv_freq.dim() == 1 and inv_freq.is_contiguous()
+                                    and positions.dtype is _I32 and positions.device == dev and positions.shape == (rows,)
+                                    and positions.is_contiguous()))
+                and freqs % 8 == 0 and 2 * freqs <= dim
+                and slots.dtype is _I32 and slots.device == dev and slots.shape == (rows,) and slots.is_contiguous()
+                and (w is None or ((wtype is dt or wtype is _F32) and _maybe(q_weight, dev, wtype, (dim,))
+                                   and _maybe(k_weight, dev, wtype, (dim,)))) and eps >= 0)
+    except (AttributeError, IndexError, ValueError, TypeError):
+        fine = False
+    if not fine:
+        _refuse_tokens(q, k, v, positions, slots, inv_freq, q_weight, k_weight, eps, q_out)
+    return (q.data_ptr(), _gb._DTYPES[dt], rows, qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
+            heads, kv, dim, None if freqs == 0 else positions.data_ptr(), None if freqs == 0 else inv_freq.data_ptr(), freqs,
+            1 if interleaved else 0, None if q_weight is None else q_weight.data_ptr(),
+            None if k_weight is None else k_weight.data_ptr(), _gb._DTYPES[wtype], eps, q_out.data_ptr(), os[0], os[1],
+            slots.data_ptr()), q_out, kv, dim
+
+
+def _refuse_tokens(q, k, v, positions, slots, inv_freq, q_weight, k_weight, eps, q_out):
     rows, heads, kv, dim = _heads(q, k, v, True)
     dev = q.device
     freqs = 0 if inv_freq is None else inv_freq.numel() if isinstance(inv_freq, torch.Tensor) else -1
     weights = [w for w in (q_weight, k_weight) if w is not None]
     wtype = weights[0].dtype if weights and isinstance(weights[0], torch.Tensor) else q.dtype
-    if q_out is None:
-        q_out = torch.empty((rows, heads, dim), dtype=q.dtype, device=dev)
-    if not ((freqs == 0 or (_dense(inv_freq, dev, _F32, (freqs,)) and _dense(positions, dev, _I32, (rows,))))
-            and freqs % 8 == 0 and 0 <= 2 * freqs <= dim and _dense(slots, dev, _I32, (rows,)) and wtype in (_F32, q.dtype)
-            and all(_dense(w, dev, wtype, (dim,)) for w in weights) and eps >= 0
-            and isinstance(q_out, torch.Tensor) and q_out.shape == q.shape and q_out.dtype is q.dtype and q_out.device == dev
-            and _inner(q_out)):
-        _refuse((freqs == 0 or _dense(inv_freq, dev, _F32, (freqs,)), "inv_freq must be contiguous fp32 [num_freqs]"),
-                (freqs == 0 or _dense(positions, dev, _I32, (rows,)), "positions must be contiguous int32 [rows]"),
-                (freqs % 8 == 0 and 0 <= 2 * freqs <= dim, "inv_freq must have a multiple of 8 entries, at most head_dim / 2"),
-                (_dense(slots, dev, _I32, (rows,)), "slots must be contiguous int32 [rows]"),
-                (wtype in (_F32, q.dtype) and all(_dense(w, dev, wtype, (dim,)) for w in weights),
-                 "the norm weights must be contiguous [head_dim], both fp32 or both of q's type"),
-                (eps >= 0, "eps must not be negative"),
-                (False, "q_out must be a tensor like q, inner stride 1"))
-    qs, ks, vs, os = q.stride(), k.stride(), v.stride(), q_out.stride()
-    return (q.data_ptr(), _gb._DTYPES[q.dtype], rows, qs[0], qs[1], k.data_ptr(), ks[0], ks[1], v.data_ptr(), vs[0], vs[1],
-            heads, kv, dim, None if positions is None else positions.data_ptr(), None if freqs == 0 else inv_freq.data_ptr(),
-            freqs, int(bool(interleaved)), _gb._ptr(q_weight), _gb._ptr(k_weight), _gb._DTYPES[wtype], eps, q_out.data_ptr(),
-            os[0], os[1], slots.data_ptr()), q_out, kv, dim
+    _refuse((freqs == 0 or _dense(inv_freq, dev, _F32, (freqs,)), "inv_freq must be contiguous fp32 [num_freqs]"),
+            (freqs == 0 or _dense(positions, dev, _I32, (rows,)), "positions must be contiguous int32 [rows]"),
+            (freqs % 8 == 0 and 0 <= 2 * freqs <= dim, "inv_freq must have a multiple of 8 entries, at most head_dim / 2"),
+            (_dense(slots, dev, _I32, (rows,)), "slots must be contiguous int32 [rows]"),
+            (wtype in (_F32, q.dtype) and all(_dense(w, dev, wtype, (dim,)) for w in weights),
+             "the norm weights must be contiguous [head_dim], both fp32 or both of q's type"),
+            (eps >= 0, "eps must not be negative"),
+            (False, "q_out must be a tensor like q, inner stride 1"))
 
 
 def rotate_and_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: Optional[torch.Tensor],
@@ -128,14 +152,18 @@ def rotate_and_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, position
     [head_dim] of ``q``'s type or fp32, None for no norm; caches as for
     ``tree_attention``.  ``q_out`` may be ``q``."""
     args, q_out, kv, dim = _tokens(q, k, v, positions, slots, inv_freq, q_weight, k_weight, eps, interleaved, q_out)
-    dev = q.device
-    for t in (k_cache, v_cache):
-        if not (isinstance(t, torch.Tensor) and t.dtype is q.dtype and t.device == dev and t.dim() == 3
-                and t.shape[1:] == (kv, dim) and t.shape[0] == k_cache.shape[0] and _inner(t)):
-            raise ValueError("the caches must be [num_slots, kv_heads, head_dim] of q's type and one shape, inner stride 1")
-    ks, vs = k_cache.stride(), v_cache.stride()
+    dev, dt = q.device, q.dtype
+    try:
+        n = k_cache.shape[0]
+        ks, vs = k_cache.stride(), v_cache.stride()
+        fine = (k_cache.dtype is dt and v_cache.dtype is dt and k_cache.device == dev and v_cache.device == dev
+                and k_cache.shape == (n, kv, dim) and v_cache.shape == (n, kv, dim) and (dim < 2 or ks[2] == vs[2] == 1))
+    except (AttributeError, IndexError):
+        fine = False
+    if not fine:
+        raise ValueError("the caches must be [num_slots, kv_heads, head_dim] of q's type and one shape, inner stride 1")
     status = (_calls or _lib()).gbtopk_rotate_and_cache(
-        *args, k_cache.data_ptr(), ks[0], ks[1], v_cache.data_ptr(), vs[0], vs[1], k_cache.shape[0], _gb._stream_handle(dev))
+        *args, k_cache.data_ptr(), ks[0], ks[1], v_cache.data_ptr(), vs[0], vs[1], n, _gb._stream_handle(dev))
     if status < 0:
         _gb._check(status)
     return q_out
@@ -143,11 +171,15 @@ def rotate_and_cache(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, position
 
 def _int4(cache, dev, kv: Optional[int], dim: int):
     """Slots, heads and strides (bytes) of a 4-bit cache."""
-    if not (isinstance(cache, torch.Tensor) and cache.dtype is torch.uint8 and cache.device == dev and cache.dim() == 3
-            and cache.shape[2] == int4_row_bytes(dim) and cache.stride(2) == 1
-            and (kv is None or cache.shape[1] == kv) and cache.shape[1] >= 1):
-        raise ValueError(f"cache must be a uint8 tensor [num_slots, kv_heads, int4_row_bytes({dim})] on {dev}, inner stride 1")
-    return cache.shape[0], cache.shape[1], cache.stride()
+    row = int4_row_bytes(dim)
+    try:
+        shape, strides = cache.shape, cache.stride()
+        if cache.dtype is torch.uint8 and cache.device == dev and shape[2] == row and strides[2] == 1 \
+                and len(shape) == 3 and (shape[1] == kv if kv is not None else shape[1] >= 1):
+            return shape[0], shape[1], strides
+    except (AttributeError, IndexError):
+        pass
+    raise ValueError(f"cache must be a uint8 tensor [num_slots, kv_heads, int4_row_bytes({dim})] on {dev}, inner stride 1")
 
 
 def rotate_and_cache_int4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, positions: Optional[torch.Tensor],
