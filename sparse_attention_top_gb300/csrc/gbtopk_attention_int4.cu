@@ -51,6 +51,7 @@ struct Int4Params {
     CUtensorMap rows;               // the cache: a line of `row` bytes every pitch
     AttnParams a;                   // k_slot, k_head: strides in pitches
     int32_t codes, row, four;       // bytes of a row's codes, of a row, of four rows in shared memory
+    int32_t gang, units;            // blocks side by side; units of a request
     int32_t stages, q_bufs;
     uint32_t q_off, p_off, ring_off, stage_bytes, shared_off;   // shared memory
     float k_mul, v_mul;             // c and the values' unit, times 2^15
@@ -185,7 +186,10 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
     pdl_wait();
     pdl_release();
 
-    const Share share = block_share<kTile, kThreads4>(p, &sh.scan);
+    const int gang = static_cast<int>(blockIdx.x) / pp.gang, member = static_cast<int>(blockIdx.x) - gang * pp.gang;
+    const int gangs = static_cast<int>(gridDim.x) / pp.gang;
+    const int block = member * gangs + gang;       // the blocks of a unit one behind another
+    const Share share = block_share<kTile, kThreads4>(p, &sh.scan, gang, gangs);
     const Waits abort{&sh.abort, p.wait_cycles};
     const uint32_t tmem = sh.tmem;
     Walk<kTile> walk(p, share);
@@ -204,7 +208,8 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
         uint32_t job = 0;
         float l[R];
         for (; walk.more() && ok; walk.next()) {
-            const Unit u = walk.u;
+            Unit u = walk.u;
+            u.hm = u.hm * pp.gang + member;
             const int32_t h = u.hm / p.row_tiles, r0 = (u.hm - h * p.row_tiles) * R;
             const int32_t here = rows - r0 < R ? rows - r0 : R;
             if (at < R) {
@@ -215,9 +220,9 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
                 less_m[at] = at < here ? kFar : 0.f;
             }
             if (at == 0) {   // the blocks that share the unit
-                int32_t *ends = p.unit_ends + 2 * (static_cast<int64_t>(u.b) * p.request_units + u.hm);
-                if (u.t0 == 0) ends[0] = static_cast<int32_t>(blockIdx.x);
-                if (u.t1 == u.tiles) ends[1] = static_cast<int32_t>(blockIdx.x);
+                int32_t *ends = p.unit_ends + 2 * (static_cast<int64_t>(u.b) * pp.units + u.hm);
+                if (u.t0 == 0) ends[0] = block;
+                if (u.t1 == u.tiles) ends[1] = block;
             }
             softmax_sync();
             if (u.span.n == 0) {   // nothing to see
@@ -377,7 +382,7 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
             }
             softmax_sync();
             const bool whole = u.t0 == 0 && u.t1 == u.tiles;
-            const int64_t part = 2 * static_cast<int64_t>(blockIdx.x) + (u.t0 > 0 ? 0 : 1);
+            const int64_t part = 2ll * block + (u.t0 > 0 ? 0 : 1);
             if (at < R) {
                 const float s = (sh.part[0][at] + sh.part[1][at]) + (sh.part[2][at] + sh.part[3][at]);
                 const float m = less_m[at] == kFar ? -INFINITY : -less_m[at];
@@ -512,7 +517,8 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
         uint64_t seen = ~0ull;   // drafted tokens that some row of the request sees
         uint32_t stage = 0, lap = 0, tile = 0, unit = 0, flying = 0, odd_lap = 0;   // stages that the warp has copied to, their parity
         for (; walk.more() && ok; walk.next()) {
-            const Unit u = walk.u;
+            Unit u = walk.u;
+            u.hm = u.hm * pp.gang + member;
             if (u.span.n == 0) continue;
             if (u.b != last_b && p.seq_lens && p.tree_mask) {
                 const int64_t *tm = p.tree_mask + static_cast<int64_t>(u.b) * p.next_n;
@@ -681,7 +687,12 @@ cudaError_t launch_rows(Int4Params pp, uint8_t *ws, int sms, cudaStream_t stream
     AttnParams &p = pp.a;
     const int64_t rows = static_cast<int64_t>(p.next_n) * p.group;
     p.row_tiles = static_cast<int32_t>((rows + R - 1) / R);
-    p.request_units = p.kv_heads * p.row_tiles;
+    const int grid = sms < kMaxGrid ? sms : kMaxGrid;
+    // a gang: as many units as divide a request's and leave at most 7 blocks over
+    pp.units = p.kv_heads * p.row_tiles;
+    for (pp.gang = pp.units < 8 ? pp.units : 8; pp.units % pp.gang != 0 || pp.gang > grid; --pp.gang) {
+    }
+    p.request_units = pp.units / pp.gang;
     place_parts(p, ws);
     pp.codes = int4_codes(p.dim);
     pp.row = int4_row(p.dim);
@@ -703,9 +714,9 @@ cudaError_t launch_rows(Int4Params pp, uint8_t *ws, int sms, cudaStream_t stream
     auto kernel = attention_int4_kernel<F16, R, WIDE>;
     cudaError_t e = allow_smem(kernel, kMaxSmemBytes, allowed);
     if (e != cudaSuccess) return e;
-    const int grid = sms < kMaxGrid ? sms : kMaxGrid;
-    e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid)), kThreads4, bytes, stream, 1, pp);
+    e = launch_pdl(kernel, dim3(static_cast<unsigned>(grid / pp.gang * pp.gang)), kThreads4, bytes, stream, 1, pp);
     if (e != cudaSuccess) return e;
+    p.request_units = pp.units;
     if constexpr (WIDE) return launch_join<!F16, 256>(p, R, kTile, sms, stream);
     else return p.dim <= 64 ? launch_join<!F16, 64>(p, R, kTile, sms, stream) : launch_join<!F16, 128>(p, R, kTile, sms, stream);
 }

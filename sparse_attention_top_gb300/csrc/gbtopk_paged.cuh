@@ -164,13 +164,13 @@ __device__ int64_t sum_cost(const AttnParams &p, int32_t b, int64_t *before, Sca
     return all * p.request_units;
 }
 
-// The blockIdx.x-th of gridDim.x equal shares.
+// The index-th of `count` equal shares (the block's of the grid's).
 template <int KT, int THREADS>
-__device__ Share block_share(const AttnParams &p, ScanScratch *scratch) {
+__device__ Share block_share(const AttnParams &p, ScanScratch *scratch, int64_t index, int64_t count) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     int64_t before;
     const int64_t total = sum_cost<KT, THREADS>(p, 0, &before, scratch);
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x, start = per * blockIdx.x;
+    const int64_t per = (total + count - 1) / count, start = per * index;
     Share s{0, start >= total ? 0 : (start + per < total ? per : total - start), 0};
     if (s.cost == 0) return s;
     if (!p.seq_lens) {
@@ -208,6 +208,11 @@ __device__ Share block_share(const AttnParams &p, ScanScratch *scratch) {
     s.b = scratch->b;
     s.off = scratch->off;
     return s;
+}
+
+template <int KT, int THREADS>
+__device__ Share block_share(const AttnParams &p, ScanScratch *scratch) {
+    return block_share<KT, THREADS>(p, scratch, blockIdx.x, gridDim.x);
 }
 
 // Copies one tile's rows, of which each of four warps has KT / 4: eight lanes
