@@ -31,6 +31,7 @@
 #include <cfloat>
 #include <cmath>
 #include <numeric>
+#include <type_traits>
 
 #include "gbtopk_int4.cuh"
 #include "gbtopk_join.cuh"
@@ -63,11 +64,11 @@ struct Shared4 {
     uint64_t key_full[2], s_full[2], p_full[2], v_full[2], v_free[2], pv_done[2];
     uint64_t drain;
     uint32_t mask[kMasks][4];       // positions of a tile with a slot: bit b of word w is position 4 b + w
-    uint64_t tree[32];              // tree masks of the unit's rows
-    int64_t row_at[32];             // (row, head) of the output, -1: none
-    float4 less_m[8];               // rows' references, negated; kFar: none yet
-    float4 scale[8];                // factors of a move, of the output
-    float part[4][32];              // a warp's maxima or sums
+    uint64_t tree[64];              // tree masks of the unit's rows
+    int64_t row_at[64];             // (row, head) of the output, -1: none
+    float4 less_m[16];              // rows' references, negated; kFar: none yet
+    float4 scale[16];               // factors of a move, of the output
+    float part[4][64];              // a warp's maxima or sums
     ScanScratch scan;
     uint32_t tmem;
     uint32_t abort;
@@ -196,10 +197,16 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
     const int32_t rows = p.next_n * p.group;   // of a (request, kv head)
     bool ok = true;
 
-    // The softmax warps hold sums and scores of 32 rows: 152 registers a thread
-    // for them and 80 for the other four warpgroups are 472 of the launch's 480.
-    if (warp < kKeyWarp) asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
-    else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    // The softmax warps hold a sum and a score a row: 152 registers a thread for
+    // them (184 with 64 rows) and 80 (72) for the other four warpgroups are 472 of
+    // the launch's 480.
+    if (warp < kKeyWarp) {
+        if constexpr (R > 32) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+    } else {
+        if constexpr (R > 32) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    }
 
     if (warp < kKeyWarp) {
         // ------------------------------------------------ softmax, output
@@ -241,16 +248,18 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
                 tc_fence_after();
                 const uint32_t t_s = tmem + lanes + kS + sb * N;
                 const bool is = (reinterpret_cast<volatile uint32_t *>(sh.mask[job % kMasks])[at & 3] >> (at >> 2)) & 1;
-                uint32_t sees = is ? ~0u : 0;     // rows that see the thread's position
+                using Rows = std::conditional_t<(R > 32), uint64_t, uint32_t>;
+                constexpr Rows kEvery = ~static_cast<Rows>(0);
+                Rows sees = is ? kEvery : 0;     // rows that see the thread's position
                 if (i * kTile > u.span.ctx - kTile) {
                     const int32_t draft = i * kTile + at - u.span.ctx;
                     if (is && draft >= 0) {
                         sees = 0;
 #pragma unroll 1
-                        for (int r = 0; r < here; ++r) sees |= (draft < 64 ? static_cast<uint32_t>(sh.tree[r] >> draft) & 1 : 0) << r;
+                        for (int r = 0; r < here; ++r) sees |= static_cast<Rows>(draft < 64 ? (sh.tree[r] >> draft) & 1 : 0) << r;
                     }
                 }
-                const bool all = __all_sync(~0u, sees == ~0u);
+                const bool all = __all_sync(~0u, sees == kEvery);
                 // scores of the thread's position less their rows' references, base 2
                 float d[R];
                 auto scores = [&]() {
@@ -721,14 +730,19 @@ cudaError_t launch_rows(Int4Params pp, uint8_t *ws, int sms, cudaStream_t stream
     else return p.dim <= 64 ? launch_join<!F16, 64>(p, R, kTile, sms, stream) : launch_join<!F16, 128>(p, R, kTile, sms, stream);
 }
 
-// By the rows of a head: 8, 16, 32.  More rows are more units, each of which
-// decodes the cache.
+// By the rows of a head: 8, 16, 32, and 64 where they are a column each and one
+// block of the head dimension.  More rows are more units, each of which decodes
+// the cache (4 requests x 8 drafts over 131072 positions, 64 rows a head: 263 us
+// by two units of 32).
 template <bool F16>
 cudaError_t launch_int4(const Int4Params &pp, uint8_t *ws, int sms, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(pp.a.next_n) * pp.a.group;
     if (pp.a.dim > 128) return rows <= 16 ? launch_rows<F16, 16, true>(pp, ws, sms, s) : launch_rows<F16, 32, true>(pp, ws, sms, s);
     if (rows <= 8) return launch_rows<F16, 8, false>(pp, ws, sms, s);
-    return rows <= 16 ? launch_rows<F16, 16, false>(pp, ws, sms, s) : launch_rows<F16, 32, false>(pp, ws, sms, s);
+    if (rows <= 16) return launch_rows<F16, 16, false>(pp, ws, sms, s);
+    if constexpr (!F16)
+        if (rows > 32) return launch_rows<F16, 64, false>(pp, ws, sms, s);
+    return launch_rows<F16, 32, false>(pp, ws, sms, s);
 }
 
 int attend_int4(Int4Params &pp, int dtype, const void *q, int64_t num_rows, int64_t q_row_stride, int64_t q_head_stride,
