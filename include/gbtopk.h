@@ -608,6 +608,10 @@ int gbtopk_cache_read_int4(const void *cache, int64_t slot_stride, int64_t head_
  * and units as above and head_dim a multiple of 16.  Keys and values are the
  * exact elements.  Arithmetic as there, but fp16 probabilities keep 16 bits and
  * have no scale to share.
+ *
+ * The greatest common divisor of the slot and head strides is at least a row (as
+ * in every view of a contiguous tensor whose innermost axis is the row), and
+ * divides the cache into at most 2^31 - 1 lines: GBTOPK_EUNSUPPORTED otherwise.
  */
 int gbtopk_tree_attention_int4(const void *q, int dtype, int64_t num_rows, int64_t q_row_stride,
                                int64_t q_head_stride, int32_t q_heads, int32_t kv_heads,
@@ -638,7 +642,8 @@ int gbtopk_selected_attention_int4(const void *q, int dtype, int64_t num_rows, i
  *
  * Keys and values that a row does not see do not reach it, whatever they hold:
  * infinities and NaN of later tokens and of other sequences are left out.
- * Offsets are clamped to 0 .. num_rows (num_keys) and to ascending order.  Rows
+ * Offsets are clamped to 0 .. num_rows (num_keys), a sequence's end to its start
+ * at least; sequences that share query rows leave either's result there.  Rows
  * of out and lse that no sequence has are left as they were.  Arithmetic as for
  * gbtopk_tree_attention (in fp16 the tiles are 128 consecutive keys, 64 above
  * head_dim 128).

@@ -19,7 +19,7 @@
 // each a column of its own, and so is its probability (16 bits of it); S and O
 // are the sums of the two columns.  So fp16 needs no scaling against its
 // range, and its probabilities are more exact than fp16's own.  With bf16
-// inputs each probability is rounded to bf16 (2^-9 of itself) for its product,
+// inputs each probability is rounded to bf16 (2^-8 of itself) for its product,
 // as the 16-bit kernels' are.  S, m, l and O are 32 bits.
 //
 // A block, one an SM: four warps of softmax and output, four that turn the codes
@@ -47,6 +47,7 @@ constexpr int kMasks = 16;          // tiles whose validity bits are kept: the r
 constexpr float kRise = 8.f;        // rise of a score over its row's reference (base 2) that moves it
 constexpr float kFar = 0x1p100f;
 constexpr int kKeyWarp = 4, kValueWarp = 8, kCopyWarp = 12, kCopyWarps = 7, kIssueWarp = 19;
+static_assert(kMaxStages <= 2 * kCopyWarps, "two stages a copy warp at most");
 
 struct Int4Params {
     CUtensorMap rows;               // the cache: a line of `row` bytes every pitch
@@ -517,10 +518,9 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
         }
     } else if (warp != kIssueWarp) {
         // ------------------------------------------------ slots and copies, the warps in turn; queries
-        // As many warps take tiles as there are stages, at most: a warp that waits
-        // for a stage to be empty has then seen the tile before its last one there
-        // emptied, so that the parity it waits for is of this lap and not of the
-        // one before.
+        // A stage is one warp's, so that the parities that a warp waits for, of its
+        // stage emptied and in the end of its last copy there, are never two phases
+        // behind.
         const uint32_t turn = warp - kCopyWarp, turns = pp.stages < kCopyWarps ? pp.stages : kCopyWarps;
         int32_t last_b = -1;
         uint64_t seen = ~0ull;   // drafted tokens that some row of the request sees
@@ -538,8 +538,8 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
             }
             last_b = u.b;
             const int64_t head = (u.hm / p.row_tiles) * p.k_head;
-            // a tile a warp before the unit's queries, so that copies start (no more:
-            // their stages are the last unit's, whose queries are there)
+            // some tiles before the unit's queries, so that copies start (no more than
+            // there are stages: theirs are the last unit's, whose queries are there)
             const int32_t q_at = u.t1 - u.t0 < static_cast<int32_t>(turns) ? u.t1 : u.t0 + static_cast<int32_t>(turns);
             for (int32_t t = u.t0; ok; ++t) {
                 if (t == q_at) {
@@ -579,7 +579,7 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
                 }
                 if (t >= u.t1) break;
                 const uint32_t n = tile++;
-                if (n % turns == turn) {
+                if (stage == turn || stage == turn + turns) {   // (fewer stages than twice the warps)
                     Paging::Place place[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {

@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(1024) order_kernel(const __grid_constant__ Pro
                 const int64_t end = (static_cast<int64_t>(t) + 1) * tokens;
                 const int32_t b = kBuckets - 1 - key_tiles<KT>(s, end < s.rows ? static_cast<int32_t>(end) : s.rows) / per;
                 const int32_t n = atomicAdd(&at[b], 1);
-                if (pass && n < p.room) p.list[n] = make_int2(i, t);
+                if (pass && static_cast<uint32_t>(n) < static_cast<uint32_t>(p.room)) p.list[n] = make_int2(i, t);
             }
         }
         __syncthreads();
@@ -125,7 +125,8 @@ __global__ void __launch_bounds__(1024) order_kernel(const __grid_constant__ Pro
         }
         at[2 * threadIdx.x] = before + inc - a - b;
         at[2 * threadIdx.x + 1] = before + inc - b;
-        if (threadIdx.x == 0) *p.count = all < p.room ? all : p.room;
+        // (counts as unsigned: offsets that are not ascending can ask for more than int32 holds)
+        if (threadIdx.x == 0) *p.count = static_cast<uint32_t>(all) < static_cast<uint32_t>(p.room) ? all : p.room;
         __syncthreads();
     }
 }

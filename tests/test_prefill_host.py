@@ -134,6 +134,13 @@ def test_selected_attention_int4_refuses(kw, status):
     assert selected4(**kw) == status
 
 
+@pytest.mark.parametrize("f", [tree4, selected4])
+@pytest.mark.parametrize("kw", [dict(slot=208, head=96), dict(slot=176, head=80), dict(slot=64, kv_heads=1), dict(slot=(1 << 37) + 80, n=1 << 30)])
+def test_attention_int4_refuses_strides_without_lines(f, kw):
+    """No pitch of a row's length or more has every row on it, or too many lines."""
+    assert f(**kw) == gb.EUNSUPPORTED
+
+
 def prompt(**kw):
     return call("gbtopk_prompt_attention",
                 "q dtype rows q_row q_head q_heads kv_heads dim k k_row k_head v v_row v_head keys cu cu_k seqs".split() + TAIL,
