@@ -7,7 +7,9 @@ Bindings of ``gbtopk_rotate_and_cache``, ``gbtopk_rotate_and_cache_int4``,
 ``gbtopk_selected_attention_int4`` and ``gbtopk_prompt_attention`` (``include/gbtopk.h``, which states the formulas and
 the rows of a 4-bit cache).  Slots are those of the decode step's calls.  A
 4-bit cache is a uint8 tensor [num_slots, kv_heads, int4_row_bytes(head_dim)]
-whose slot and head strides are multiples of 16 bytes.
+whose slot and head strides are multiples of 16 bytes.  (For attention over it
+their greatest common divisor is a row or more, as in any view of a contiguous
+tensor whose last axis is the row.)
 """
 from __future__ import annotations
 
@@ -22,7 +24,7 @@ import sparse_attention_top_gb300 as _gb
 from .decode import (_F32, _HALF, _I32, _I64, _PAGE_RULE, _PAGES, _QUERY, MAX_PAGE_SIZE, _attention_bytes, _dense, _f, _i32,
                      _i64, _maybe, _outputs, _query, _refuse, _requests, _scratch, _sz, _table, _vp)
 
-__all__ = ["rotate_and_cache", "rotate_and_cache_int4", "read_cache_int4", "CachedRows", "int4_row_bytes",
+__all__ = ["rotate_and_cache", "rotate_and_cache_int4", "read_cache_int4", "CachedRows", "int4_row_bytes", "int4_parts",
            "tree_attention_int4", "selected_attention_int4", "prompt_attention", "gbtopk_prompt_workspace_bytes"]
 
 _TOKENS = [_vp, ctypes.c_int, _i64, _i64, _i64] + [_vp, _i64, _i64] * 2 + [_i32] * 3 + [_vp, _vp, _i32, ctypes.c_int] \
@@ -197,6 +199,19 @@ def rotate_and_cache_int4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos
     if status < 0:
         _gb._check(status)
     return q_out
+
+
+def int4_parts(cache: torch.Tensor):
+    """A 4-bit cache as ``evict_cache`` takes it: two views of its rows, of one
+    shape, in place of keys and values.  They overlap where half a row is no
+    multiple of 16 bytes; what lies in both is moved twice, to the same place."""
+    if not (isinstance(cache, torch.Tensor) and cache.dtype is torch.uint8 and cache.dim() == 3 and cache.shape[2] % 16 == 0
+            and cache.stride(2) == 1 and cache.shape[2] > 0):
+        raise ValueError("cache must be a 4-bit cache: uint8 [num_slots, kv_heads, row bytes], inner stride 1")
+    words = cache.view(torch.int32)
+    n = words.shape[2]
+    half = (n // 4 + 1) // 2 * 4
+    return words[:, :, :half], words[:, :, n - half:]
 
 
 class CachedRows(NamedTuple):
