@@ -16,9 +16,10 @@ page-table API quoted on the SGLang PR #33237 page.
 ``decode`` holds the rest of a speculative decode step over the same paged
 cache (``tree_attention``, ``selected_attention``,
 ``accumulate_cache_weights``, ``evict_cache``, ``verify_drafts``); ``prefill`` holds what
-fills that cache, and caches held in 4 bits (``rotate_and_cache``,
-``rotate_and_cache_int4``, ``read_cache_int4``).  The names of both are
-exported here too.
+fills that cache and answers prompts (``rotate_and_cache``,
+``prompt_attention``), and caches held in 4 bits (``rotate_and_cache_int4``,
+``read_cache_int4``, ``tree_attention_int4``, ``selected_attention_int4``).
+The names of both are exported here too.
 """
 from __future__ import annotations
 

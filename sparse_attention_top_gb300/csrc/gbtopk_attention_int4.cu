@@ -26,8 +26,17 @@
 // of keys into tensor memory, four that turn those of values into a
 // shared-memory tile, seven that look up slots and have the rows copied into a
 // ring (each a tile in turn; a lane gathers four rows by a tensor map), one that
-// issues products.  Shares, units and the join are
-// those of gbtopk_attention.cu.
+// issues products.  Shares, units and the join are those of gbtopk_attention.cu,
+// but that a gang of blocks takes the units of one request (its heads and row
+// tiles) over the same positions at once: a 128-byte line of the cache holds parts
+// of two heads' rows, which are then read from memory together.
+//
+// Measured: 64 requests x 4 drafts, 1..8192 positions of 8 heads of 128, fp16: 136
+// us, the 300 MB of the cache read once (45 us at the copy rate); 4 requests x 8
+// drafts over 131072 positions of 4 heads, 64 rows a head, bf16: 223 us (45).  Bound by the roles'
+// own instructions: a tile of 128 positions takes about 2400 cycles, in which the
+// ALU pipes are busy for 1100, the values' decoding, the issue of products and the
+// softmax each for most of it.
 #include <cfloat>
 #include <cmath>
 #include <numeric>
@@ -198,12 +207,12 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
     const int32_t rows = p.next_n * p.group;   // of a (request, kv head)
     bool ok = true;
 
-    // The softmax warps hold a sum and a score a row: 152 registers a thread for
-    // them (184 with 64 rows) and 80 (72) for the other four warpgroups are 472 of
-    // the launch's 480.
+    // The softmax warps hold a sum and a score a row: 160 registers a thread for
+    // them (184 with 64 rows) and 80 (72) for the other four warpgroups are 480
+    // (472) of the launch's 480.
     if (warp < kKeyWarp) {
         if constexpr (R > 32) asm volatile("setmaxnreg.inc.sync.aligned.u32 184;");
-        else asm volatile("setmaxnreg.inc.sync.aligned.u32 152;");
+        else asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
     } else {
         if constexpr (R > 32) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         else asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
@@ -698,6 +707,7 @@ cudaError_t launch_rows(Int4Params pp, uint8_t *ws, int sms, cudaStream_t stream
     p.row_tiles = static_cast<int32_t>((rows + R - 1) / R);
     const int grid = sms < kMaxGrid ? sms : kMaxGrid;
     // a gang: as many units as divide a request's and leave at most 7 blocks over
+    // (64 requests, 8 heads: 135 us, by single blocks 145 and 516 MB for 300)
     pp.units = p.kv_heads * p.row_tiles;
     for (pp.gang = pp.units < 8 ? pp.units : 8; pp.units % pp.gang != 0 || pp.gang > grid; --pp.gang) {
     }
@@ -731,9 +741,10 @@ cudaError_t launch_rows(Int4Params pp, uint8_t *ws, int sms, cudaStream_t stream
 }
 
 // By the rows of a head: 8, 16, 32, and 64 where they are a column each and one
-// block of the head dimension.  More rows are more units, each of which decodes
-// the cache (4 requests x 8 drafts over 131072 positions, 64 rows a head: 263 us
-// by two units of 32).
+// block of the head dimension.  Fewer rows are less work a tile (one request of
+// 4 rows a head: 22.4 us a call, as 16 rows 23.3; 16 rows 30.6 us, as 32 36.7);
+// more rows are more units, each of which decodes the cache (4 requests x 8 drafts
+// over 131072 positions, 64 rows a head: 223 us, by two units of 32 263).
 template <bool F16>
 cudaError_t launch_int4(const Int4Params &pp, uint8_t *ws, int sms, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(pp.a.next_n) * pp.a.group;
