@@ -47,6 +47,7 @@ struct RotateParams {
     int32_t tokens, groups;           // of a block
     FastDiv by_half;
     float eps, inv_dim, unit[2], inv_unit[2];
+    double inv_dim_wide;
 };
 
 template <bool BF16>
@@ -125,77 +126,118 @@ __device__ __forceinline__ void turn_wide(double x, double *sine, double *cosine
     *cosine = q == 0 ? c : q == 1 ? -s : q == 2 ? -c : s;
 }
 
-// Codes and scale of the lane's eight elements from the normalised and rotated
-// row in 64 bits, one row a group of LP lanes; every lane of the warp takes part.
-// Rare (a few in 100,000 elements) and by one warp alone, whose time is mostly
-// that of its instructions' way to the SM: loops that are not unrolled, no
-// division.
+// The lane's eight codes and the block's scale once more, where 32 bits leave a
+// doubt: word and *byte as stored, in which the elements in doubt (all eight where
+// the scale is) are replaced by those of 64 bits.  One row a group of LP lanes;
+// every lane of the warp takes part.  Rare (a few in 100,000 elements) and by one
+// warp alone at its end, whose time is mostly that of cold instructions (without
+// the doubts 2000 tokens would take 33 us, not 50): loops that are not unrolled,
+// no division.  An element's angle and rotation are taken in 64 bits only where 32
+// bits, with a bound eight times as wide as the one that raised the doubt, find it
+// near a border (2000 tokens 50 us a call, all eight elements 53).
 template <bool BF16, int LP, bool PAIRS>
-__device__ __noinline__ uint32_t encode_again(const RotateParams &p, const Row &row, const void *w, bool w_wide, double position,
-                                              double inv_unit, uint32_t *byte) {
+__device__ __noinline__ uint32_t encode_again(const RotateParams &p, const Row &row, const void *w, bool w_wide, int32_t position,
+                                              const float2 *turn, uint32_t word, uint32_t *byte) {
     const int lane = threadIdx.x & (LP - 1);
-    double sum = 0, y[8];
-    float f[8];
+    const bool in = row.there && row.at < 2 * p.half, second = !PAIRS && row.at >= p.half;
+    const int from = in && !PAIRS ? (second ? lane - p.half / 8 : lane + p.half / 8) : lane;
+    float x[8], f[8] = {};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const float2 t = Half2<BF16>::up(row.raw[i]);
-        y[2 * i] = t.x;
-        y[2 * i + 1] = t.y;
+        x[2 * i] = t.x;
+        x[2 * i + 1] = t.y;
     }
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) sum = fma(y[i], y[i], sum);
+    double r = 1;
     if (w) {
+        double sum = 0;
+#pragma unroll 1
+        for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), sum);
 #pragma unroll 1
         for (int o = LP / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        const double v = sum / p.dim + static_cast<double>(p.eps);
-        double r = rsqrtf(static_cast<float>(v));      // two steps of Newton's method from 22 bits
+        const double v = fma(sum, p.inv_dim_wide, static_cast<double>(p.eps));
+        r = rsqrtf(static_cast<float>(v));      // two steps of Newton's method from 22 bits
         r = r * fma(-0.5 * v * r, r, 1.5);
         r = r * fma(-0.5 * v * r, r, 1.5);
         if (row.there) load_weights<BF16>(w, w_wide, row.at, f);
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) y[i] = row.there ? y[i] * r * f[i] : 0;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) f[i] = 1.f;
     }
-    const bool in = row.there && row.at < 2 * p.half, second = !PAIRS && row.at >= p.half;
-    const int32_t k0 = !in ? 0 : PAIRS ? row.at / 2 : row.at - (second ? p.half : 0);
-    const int from = in && !PAIRS ? (second ? lane - p.half / 8 : lane + p.half / 8) : lane;
-    double top = 0, s, c;
-#pragma unroll 1
+    // ---- in 32 bits: which elements, and is it the scale
+    const float inv_unit = p.inv_unit[0];
+    float z[8], terms[8], most = 0.f, top = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] = x[i] * (static_cast<float>(r) * f[i]);
+#pragma unroll
     for (int i = 0; i < 8; ++i) {
-        if (p.half && !(PAIRS && (i & 1))) {
+        const float other = PAIRS ? x[i ^ 1] * (static_cast<float>(r) * f[i ^ 1]) : __shfl_sync(~0u, x[i] * (static_cast<float>(r) * f[i]), from, LP);
+        terms[i] = fabsf(z[i]);
+        if (in) {
+            const float2 cs = turn[PAIRS ? i / 2 : i];
+            terms[i] += fabsf(other);
+            z[i] = fmaf((PAIRS ? i & 1 : second) ? other : -other, cs.y, z[i] * cs.x);
+        }
+        most = fmaxf(most, terms[i]);
+        top = fmaxf(top, fabsf(z[i]));
+    }
+    most = fmaxf(most, __shfl_xor_sync(~0u, most, 1)) * inv_unit;
+    top = fmaxf(top, __shfl_xor_sync(~0u, top, 1)) * inv_unit;
+    float near;
+    const float small = block_scale(fminf(top, 4096.f), &near), small_per = small > 0.f ? inv_unit / small : 0.f;
+    const bool wide = near <= most * 0x1p-17f;
+    uint32_t need = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float t = z[i] * small_per;
+        if (wide || fabsf(fabsf(t - rintf(t)) - 0.5f) <= terms[i] * small_per * 0x1p-17f) need |= 1u << i;
+    }
+    // ---- in 64 bits, an element of every lane where one has it in doubt
+    const int32_t k0 = !in ? 0 : PAIRS ? row.at / 2 : row.at - (second ? p.half : 0);
+    const uint32_t any = __reduce_or_sync(~0u, need);
+    double y[8], tops = 0;
+#pragma unroll 1
+    for (uint32_t left = any; left; left &= left - 1) {
+        const int i = __ffs(static_cast<int>(left)) - 1;
+        const double mine = static_cast<double>(x[i]) * r * f[i];
+        double v = mine;
+        if (p.half) {
+            const float ox = PAIRS ? x[i ^ 1] : __shfl_sync(~0u, x[i], from, LP), of = PAIRS ? f[i ^ 1] : __shfl_sync(~0u, f[i], from, LP);
             const double a = position * (static_cast<double>(p.inv_freq[k0 + (PAIRS ? i / 2 : i)]) * 0.15915494309189533577);
-            turn_wide(a - rint(a), &s, &c);
-            const double other = PAIRS ? y[i + 1] : __shfl_sync(~0u, y[i], from, LP), mine = y[i];
-            if (in) {
-                y[i] = second ? mine * c + other * s : mine * c - other * s;
-                if (PAIRS) y[i + 1] = other * c + mine * s;
-            }
+            double sine, cosine;
+            turn_wide(a - rint(a), &sine, &cosine);
+            const double other = static_cast<double>(ox) * r * of;
+            if (in) v = fma(mine, cosine, (PAIRS ? i & 1 : second) ? other * sine : -(other * sine));
+        }
+        y[i] = v * inv_unit;
+        tops = fmax(tops, fabs(y[i]));
+    }
+    double scale = small;
+    if (__any_sync(~0u, wide)) {      // (then every element has been taken)
+        tops = fmax(tops, __shfl_xor_sync(~0u, tops, 1));
+        // as block_scale
+        tops = fmin(tops, 4096.0);
+        int e = static_cast<int>(static_cast<unsigned long long>(__double_as_longlong(tops * (1.0 / 7.0))) >> 52) - 1023;
+        e = e < -6 ? -6 : e;
+        const double step = __longlong_as_double(static_cast<long long>(e - 3 + 1023) << 52), steps = __longlong_as_double(static_cast<long long>(3 - e + 1023) << 52);
+        const double low = floor(tops * (1.0 / 7.0) * steps), off = tops * steps - 7 * (low + 0.5);
+        const bool up = off > 0 || (off == 0 && (static_cast<int>(low) & 1));
+        if (wide) {
+            scale = fmin((low + (up ? 1 : 0)) * step, 448.0);
+            *byte = scale_byte(static_cast<float>(scale));
+            if (scale == 0) word = need = 0;
         }
     }
-#pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-        y[i] *= inv_unit;
-        top = fmax(top, fabs(y[i]));
-    }
-    top = fmax(top, __shfl_xor_sync(~0u, top, 1));
-    // as block_scale
-    top = fmin(top, 4096.0);
-    int e = static_cast<int>(static_cast<unsigned long long>(__double_as_longlong(top * (1.0 / 7.0))) >> 52) - 1023;
-    e = e < -6 ? -6 : e;
-    const double step = __longlong_as_double(static_cast<long long>(e - 3 + 1023) << 52), steps = __longlong_as_double(static_cast<long long>(3 - e + 1023) << 52);
-    const double low = floor(top * (1.0 / 7.0) * steps), off = top * steps - 7 * (low + 0.5);
-    const bool up = off > 0 || (off == 0 && (static_cast<int>(low) & 1));
-    const double scale = fmin((low + (up ? 1 : 0)) * step, 448.0);
-    *byte = scale_byte(static_cast<float>(scale));
     double per = scale > 0 ? 1.f / static_cast<float>(scale) : 0.f;
     per = per * fma(-scale, per, 2.0);
-    uint32_t word = 0;
 #pragma unroll 1
-    for (int i = 0; i < 8; ++i) {
-        double x = rint(y[i] * per);
-        const double rest = fma(-x, scale, y[i]);
-        if (fabs(rest) == 0.5 * scale) x = 2 * rint(0.5 * (x + copysign(0.5, rest)));
-        x = x > 7 ? 7 : x < -7 ? -7 : x == x ? x : 0;
-        word |= put_code(i, static_cast<float>(x));
+    for (uint32_t left = any; left; left &= left - 1) {
+        const int i = __ffs(static_cast<int>(left)) - 1;
+        double c = rint(y[i] * per);
+        const double rest = fma(-c, scale, y[i]);
+        if (fabs(rest) == 0.5 * scale) c = 2 * rint(0.5 * (c + copysign(0.5, rest)));
+        c = c > 7 ? 7 : c < -7 ? -7 : c == c ? c : 0;
+        if ((need >> i) & 1) word = (word & ~put_code(i, -7.f)) | put_code(i, static_cast<float>(c));
     }
     return word;
 }
@@ -402,14 +444,14 @@ __global__ void __launch_bounds__(kRowThreads, 4) rotate_kernel(const __grid_con
                 row.raw[1] = v.y;
                 row.raw[2] = v.z;
                 row.raw[3] = v.w;
-                uint32_t byte;
+                // (keys: only they have doubts)
+                uint8_t *to = dst + slots[t] * dst_step, *to_scale = to + 2 * int4_codes(p.dim) - at / 2 + at / 16;
+                uint32_t byte = there ? *to_scale : 0;
                 const uint32_t word = encode_again<BF16, LP, PAIRS>(p, row, w, w_wide != 0, p.half ? p.positions[token0 + t] : 0,
-                                                                    p.inv_unit[kind - 1], &byte);
-                uint8_t *to = dst + slots[t] * dst_step;
+                                                                    mine + t * p.half, there ? *reinterpret_cast<uint32_t *>(to) : 0, &byte);
                 if (there) {
                     *reinterpret_cast<uint32_t *>(to) = word;
-                    if (!(lane & 1))
-                        to[(3 - kind) * int4_codes(p.dim) - at / 2 + (kind - 1) * int4_scales(p.dim) + at / 16] = static_cast<uint8_t>(byte);
+                    if (!(lane & 1)) *to_scale = static_cast<uint8_t>(byte);
                 }
             }
         }
@@ -545,6 +587,7 @@ RotateParams fill(const void *q, int64_t q_row, int64_t q_head, const void *k, i
     p.half = half;
     p.eps = eps;
     p.inv_dim = 1.f / static_cast<float>(dim > 0 ? dim : 1);
+    p.inv_dim_wide = 1.0 / (dim > 0 ? dim : 1);
     return p;
 }
 
