@@ -22,7 +22,6 @@
 // once a token, and short rows take the rest).  Into 4 bits the codes bind: 8,192
 // tokens of such heads 100 us, of which the bytes are 26; 32,769 slots read back
 // 36 us (25).
-#include <cfloat>
 #include <cmath>
 
 #include "gbtopk_int4.cuh"
@@ -245,11 +244,19 @@ __device__ __noinline__ uint32_t encode_again(const RotateParams &p, const Row &
 // The same from 32-bit numbers, keys with errors of at most err[i]; *doubt where
 // an error could have changed a code or the scale.
 template <bool KEYS>
-__device__ __forceinline__ uint32_t encode(const float *y, const float *err, float unit, float inv_unit, uint32_t *byte, bool *doubt) {
+__device__ __forceinline__ uint32_t encode(float *y, const float *err, float unit, float inv_unit, bool wild, uint32_t *byte, bool *doubt) {
     float top = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) top = fmaxf(top, fabsf(y[i]));   // (a NaN is no maximum)
     top = fmaxf(top, __shfl_xor_sync(~0u, top, 1)) * inv_unit;
+    // A NaN is stored as 0.  What lies beyond the largest scale's range comes back
+    // to where its code is the largest all the same: its quotient could be infinite,
+    // and the correction then a NaN without the number's sign.
+    if (__any_sync(~0u, wild || top > 4096.f)) {
+        const float most = 4096.f * unit;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = y[i] == y[i] ? fminf(fmaxf(y[i], -most), most) : 0.f;
+    }
     float near;
     const float steps = block_scale(fminf(top, 4096.f), &near);   // (saturated from 7 * 464 on)
     *byte = scale_byte(steps);
@@ -413,14 +420,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) rotate_kernel(const __grid_con
                         *reinterpret_cast<uint4 *>(to) = make_uint4(Half2<BF16>::down(y[0], y[1]), Half2<BF16>::down(y[2], y[3]),
                                                                     Half2<BF16>::down(y[4], y[5]), Half2<BF16>::down(y[6], y[7]));
                 } else if constexpr (INT4) {
-                    if (__any_sync(~0u, !(sum < INFINITY))) {      // (a NaN is stored as 0, an infinity as the largest)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) y[j] = y[j] == y[j] ? fminf(fmaxf(y[j], -FLT_MAX), FLT_MAX) : 0.f;
-                    }
                     uint32_t byte;
                     bool doubt = false;
+                    const bool wild = !(sum < INFINITY);
                     const float unit = p.unit[kind - 1], inv_unit = p.inv_unit[kind - 1];
-                    const uint32_t word = kind == 1 ? encode<true>(y, err, unit, inv_unit, &byte, &doubt) : encode<false>(y, err, unit, inv_unit, &byte, &doubt);
+                    const uint32_t word = kind == 1 ? encode<true>(y, err, unit, inv_unit, wild, &byte, &doubt)
+                                                    : encode<false>(y, err, unit, inv_unit, wild, &byte, &doubt);
                     if (there) {
                         *reinterpret_cast<uint32_t *>(to) = word;
                         // (the scales lie behind both codes)
