@@ -543,8 +543,8 @@ int64_t gbtopk_int4_row_bytes(int32_t head_dim);
  * caches at slots[token]; a token whose slot is < 0 or >= num_slots writes no
  * key and value.  Slots of one call differ from one another: where a slot is
  * listed twice its contents are some mixture of the two tokens'.  Sums and
- * products are 32 bits, the angles' turns are reduced in 64, and each element
- * is rounded once.
+ * products are 32 bits (64 where a row's mean square is below 2^-96 or above
+ * 2^120), the angles' turns are reduced in 64, and each element is rounded once.
  *
  *  q, k, v      device [num_tokens, q_heads or kv_heads, head_dim] of dtype
  *               (bf16 or fp16), inner stride 1, the other strides multiples of

@@ -22,6 +22,7 @@
 // once a token, and short rows take the rest).  Into 4 bits the codes bind: 8,192
 // tokens of such heads 100 us, of which the bytes are 26; 32,769 slots read back
 // 36 us (25).
+#include <cfloat>
 #include <cmath>
 
 #include "gbtopk_int4.cuh"
@@ -125,6 +126,69 @@ __device__ __forceinline__ void turn_wide(double x, double *sine, double *cosine
     *cosine = q == 0 ? c : q == 1 ? -s : q == 2 ? -c : s;
 }
 
+// Mean squares of 2^-96 .. 2^120 (a NaN is neither) are those whose root 32 bits
+// take: no square that counts, and no sum of 256 of them, is beyond their range.
+// Other rows' norms are computed in 64 bits (the test costs a long prompt 1.2 of 77 us).
+__device__ __forceinline__ bool far_mean(float mean) {
+    constexpr uint32_t kLeast = (127u - 96u) << 23, kMost = (127u + 120u) << 23;
+    return __float_as_uint(mean) - kLeast >= kMost - kLeast;
+}
+
+// A row's mean square and eps in 64 bits, in every lane of its group.
+template <int LP>
+__device__ __forceinline__ double mean_wide(const RotateParams &p, const float *x) {
+    double sum = 0;
+#pragma unroll 1
+    for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), sum);
+#pragma unroll 1
+    for (int o = LP / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
+    return fma(sum, p.inv_dim_wide, static_cast<double>(p.eps));
+}
+
+// 1 / sqrt(v) of a number that 32 bits may not hold: v = m 4^h with 1 <= m < 4, and
+// two steps of Newton's method from 22 bits of m's root.
+__device__ __noinline__ double root_far(double v) {
+    if (!(v > 0 && v <= DBL_MAX)) return rsqrtf(static_cast<float>(v));      // of 0, infinity, NaN
+    const int h = (static_cast<int>(static_cast<unsigned long long>(__double_as_longlong(v)) >> 52) - 1023) >> 1;
+    const double m = v * __longlong_as_double(static_cast<long long>(1023 - 2 * h) << 52);
+    double r = rsqrtf(static_cast<float>(m));
+    r = r * fma(-0.5 * m * r, r, 1.5);
+    r = r * fma(-0.5 * m * r, r, 1.5);
+    return r * __longlong_as_double(static_cast<long long>(1023 - h) << 52);
+}
+
+// The lane's eight elements of a query or a 16-bit key once more, where 32 bits do
+// not hold the row's mean square.  One row a group of LP lanes; every lane of the
+// warp takes part.
+template <bool BF16, int LP, bool PAIRS>
+__device__ __noinline__ uint4 norm_again(const RotateParams &p, const Row &row, const void *w, bool w_wide, const float2 *turn) {
+    const int lane = threadIdx.x & (LP - 1);
+    const bool in = row.there && row.at < 2 * p.half, second = !PAIRS && row.at >= p.half;
+    const int from = in && !PAIRS ? (second ? lane - p.half / 8 : lane + p.half / 8) : lane;
+    float x[8], f[8] = {};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 t = Half2<BF16>::up(row.raw[i]);
+        x[2 * i] = t.x;
+        x[2 * i + 1] = t.y;
+    }
+    const double r = root_far(mean_wide<LP>(p, x));
+    if (row.there) load_weights<BF16>(w, w_wide, row.at, f);
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = static_cast<float>(static_cast<double>(x[i]) * r * f[i]);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float other = PAIRS ? x[i ^ 1] : __shfl_sync(~0u, x[i], from, LP);
+        y[i] = x[i];
+        if (in) {
+            const float2 cs = turn[PAIRS ? i / 2 : i];
+            y[i] = fmaf((PAIRS ? i & 1 : second) ? other : -other, cs.y, x[i] * cs.x);
+        }
+    }
+    return make_uint4(Half2<BF16>::down(y[0], y[1]), Half2<BF16>::down(y[2], y[3]), Half2<BF16>::down(y[4], y[5]), Half2<BF16>::down(y[6], y[7]));
+}
+
 // The lane's eight codes and the block's scale once more, where 32 bits leave a
 // doubt: word and *byte as stored, in which the elements in doubt (all eight where
 // the scale is) are replaced by those of 64 bits.  One row a group of LP lanes;
@@ -148,16 +212,15 @@ __device__ __noinline__ uint32_t encode_again(const RotateParams &p, const Row &
         x[2 * i + 1] = t.y;
     }
     double r = 1;
+    bool far = false;
     if (w) {
-        double sum = 0;
-#pragma unroll 1
-        for (int i = 0; i < 8; ++i) sum = fma(static_cast<double>(x[i]), static_cast<double>(x[i]), sum);
-#pragma unroll 1
-        for (int o = LP / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
-        const double v = fma(sum, p.inv_dim_wide, static_cast<double>(p.eps));
+        const double v = mean_wide<LP>(p, x);
+        const float low = static_cast<float>(v) * 0.5f, high = static_cast<float>(v) * 2.f;
+        far = far_mean(low) || far_mean(high);      // (32 bits may have found it on the other side)
         r = rsqrtf(static_cast<float>(v));      // two steps of Newton's method from 22 bits
         r = r * fma(-0.5 * v * r, r, 1.5);
         r = r * fma(-0.5 * v * r, r, 1.5);
+        if (far) r = root_far(v);
         if (row.there) load_weights<BF16>(w, w_wide, row.at, f);
     } else {
 #pragma unroll
@@ -184,7 +247,7 @@ __device__ __noinline__ uint32_t encode_again(const RotateParams &p, const Row &
     top = fmaxf(top, __shfl_xor_sync(~0u, top, 1)) * inv_unit;
     float near;
     const float small = block_scale(fminf(top, 4096.f), &near), small_per = small > 0.f ? inv_unit / small : 0.f;
-    const bool wide = near <= most * 0x1p-17f;
+    const bool wide = far || near <= most * 0x1p-17f;     // (all of a far row)
     uint32_t need = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -349,7 +412,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) rotate_kernel(const __grid_con
         const void *w = kind < 2 ? p.w[kind] : nullptr;
         float f[8];
         if (w && there) load_weights<BF16>(w, w_wide != 0, at, f);
-        uint32_t doubts = 0;      // tokens whose codes need 64 bits
+        uint32_t again = 0;       // tokens whose row of this lane needs 64 bits
         for (int32_t t0 = 0; t0 < tokens; t0 += kAhead) {
             uint4 raw[kAhead];
 #pragma unroll
@@ -376,9 +439,12 @@ __global__ void __launch_bounds__(kRowThreads, 4) rotate_kernel(const __grid_con
                     pair[j] = fmaf(z.x, z.x, z.y * z.y);
                 }
                 float sum = (pair[0] + pair[1]) + (pair[2] + pair[3]);
+                bool far = false;
                 if (w) {
                     for (int o = LP / 2; o; o >>= 1) sum += __shfl_xor_sync(~0u, sum, o);
                     const float mean = fmaf(sum, p.inv_dim, p.eps);
+                    far = far_mean(mean);
+                    if (far) again |= 1u << t;
                     float r = rsqrtf(mean);
                     if (INT4 && kind == 1) r = fmaf(0.5f * r, fmaf(-mean * r, r, 1.f), r);    // (a step of Newton's method)
 #pragma unroll
@@ -416,49 +482,54 @@ __global__ void __launch_bounds__(kRowThreads, 4) rotate_kernel(const __grid_con
                     }
                 }
                 if (!INT4 || kind == 0) {
-                    if (there)
+                    if (there && !far)      // (q may be q_out: its row is read again)
                         *reinterpret_cast<uint4 *>(to) = make_uint4(Half2<BF16>::down(y[0], y[1]), Half2<BF16>::down(y[2], y[3]),
                                                                     Half2<BF16>::down(y[4], y[5]), Half2<BF16>::down(y[6], y[7]));
                 } else if constexpr (INT4) {
                     uint32_t byte;
                     bool doubt = false;
-                    const bool wild = !(sum < INFINITY);
+                    const bool odd = !(sum < INFINITY);
                     const float unit = p.unit[kind - 1], inv_unit = p.inv_unit[kind - 1];
-                    const uint32_t word = kind == 1 ? encode<true>(y, err, unit, inv_unit, wild, &byte, &doubt)
-                                                    : encode<false>(y, err, unit, inv_unit, wild, &byte, &doubt);
+                    const uint32_t word = kind == 1 ? encode<true>(y, err, unit, inv_unit, odd, &byte, &doubt)
+                                                    : encode<false>(y, err, unit, inv_unit, odd, &byte, &doubt);
                     if (there) {
                         *reinterpret_cast<uint32_t *>(to) = word;
                         // (the scales lie behind both codes)
                         if (!(lane & 1))
                             to[(3 - kind) * int4_codes(p.dim) - at / 2 + (kind - 1) * int4_scales(p.dim) + at / 16] = static_cast<uint8_t>(byte);
                     }
-                    if (__any_sync(~0u, doubt && there)) doubts |= 1u << t;
+                    if (doubt && there) again |= 1u << t;
                 }
             }
         }
-        if constexpr (INT4) {
-            // (behind the loop, whose registers it would take)
+        // (behind the loop, whose registers it would take)
 #pragma unroll 1
-            for (; doubts; doubts &= doubts - 1) {
-                const int32_t t = __ffs(static_cast<int>(doubts)) - 1;
-                Row row;
-                row.at = at;
-                row.there = there;
-                const uint4 v = there ? *reinterpret_cast<const uint4 *>(src + t * step) : make_uint4(0, 0, 0, 0);
-                row.raw[0] = v.x;
-                row.raw[1] = v.y;
-                row.raw[2] = v.z;
-                row.raw[3] = v.w;
-                // (keys: only they have doubts)
-                uint8_t *to = dst + slots[t] * dst_step, *to_scale = to + 2 * int4_codes(p.dim) - at / 2 + at / 16;
-                uint32_t byte = there ? *to_scale : 0;
-                const uint32_t word = encode_again<BF16, LP, PAIRS>(p, row, w, w_wide != 0, p.half ? p.positions[token0 + t] : 0,
-                                                                    mine + t * p.half, there ? *reinterpret_cast<uint32_t *>(to) : 0, &byte);
-                if (there) {
-                    *reinterpret_cast<uint32_t *>(to) = word;
-                    if (!(lane & 1)) *to_scale = static_cast<uint8_t>(byte);
+        for (uint32_t left = __reduce_or_sync(~0u, there ? again : 0); left; left &= left - 1) {
+            const int32_t t = __ffs(static_cast<int>(left)) - 1;
+            Row row;
+            row.at = at;
+            row.there = there;
+            const uint4 v = there ? *reinterpret_cast<const uint4 *>(src + t * step) : make_uint4(0, 0, 0, 0);
+            row.raw[0] = v.x;
+            row.raw[1] = v.y;
+            row.raw[2] = v.z;
+            row.raw[3] = v.w;
+            const float2 *turn = mine + t * p.half;
+            if constexpr (INT4) {
+                if (kind > 0) {      // (keys: only they have doubts)
+                    uint8_t *to = dst + slots[t] * dst_step, *to_scale = to + 2 * int4_codes(p.dim) - at / 2 + at / 16;
+                    uint32_t byte = there ? *to_scale : 0;
+                    const uint32_t word = encode_again<BF16, LP, PAIRS>(p, row, w, w_wide != 0, p.half ? p.positions[token0 + t] : 0, turn,
+                                                                        there ? *reinterpret_cast<uint32_t *>(to) : 0, &byte);
+                    if (there) {
+                        *reinterpret_cast<uint32_t *>(to) = word;
+                        if (!(lane & 1)) *to_scale = static_cast<uint8_t>(byte);
+                    }
+                    continue;
                 }
             }
+            const uint4 y = norm_again<BF16, LP, PAIRS>(p, row, w, w_wide != 0, turn);
+            if (there && ((again >> t) & 1)) *reinterpret_cast<uint4 *>(dst + (kind > 0 ? slots[t] : t) * dst_step) = y;
         }
     }
 }
