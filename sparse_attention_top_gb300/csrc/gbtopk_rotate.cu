@@ -375,6 +375,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) rotate_kernel(const __grid_con
     const int32_t at = lane * 8, rotary = 2 * p.half;
     const int32_t end = gq + 2 * gk < (static_cast<int32_t>(blockIdx.y) + 1) * p.groups ? gq + 2 * gk : (static_cast<int32_t>(blockIdx.y) + 1) * p.groups;
     if (static_cast<int32_t>(threadIdx.x) < tokens) slots[threadIdx.x] = p.slots[token0 + threadIdx.x];
+    bool bad = false;      // some angle is a NaN
     for (int k = threadIdx.x; k < tokens * p.half; k += kRowThreads) {
         const int32_t t = static_cast<int32_t>(p.by_half.div(static_cast<uint32_t>(k)));
         const double a = static_cast<double>(p.positions[token0 + t]) * (static_cast<double>(p.inv_freq[k - t * p.half]) * 0.15915494309189533577);
@@ -383,8 +384,10 @@ __global__ void __launch_bounds__(kRowThreads, 4) rotate_kernel(const __grid_con
         const float near = static_cast<float>(rest), off = static_cast<float>(rest - near) * 6.2831853f;
         sincospif(2.f * near, &s, &c);
         turns[k] = make_float2(fmaf(-s, off, c), fmaf(c, off, s));     // (what the 32-bit turns leave out)
+        if constexpr (INT4) bad |= !(fabsf(near) <= 0.5f);
     }
-    __syncthreads();
+    if constexpr (INT4) bad = __syncthreads_or(bad);
+    else __syncthreads();
     // the lane's partner in the rotation, its angles, the sign of its sine
     const bool in = at < rotary, second = !PAIRS && at >= p.half;
     const int from = in ? (second ? lane - p.half / 8 : lane + p.half / 8) : lane;
@@ -411,7 +414,14 @@ __global__ void __launch_bounds__(kRowThreads, 4) rotate_kernel(const __grid_con
         }
         const void *w = kind < 2 ? p.w[kind] : nullptr;
         float f[8];
-        if (w && there) load_weights<BF16>(w, w_wide != 0, at, f);
+        bool wild = bad;          // some weight or angle is a NaN: some of the keys may be
+        if (w && there) {
+            load_weights<BF16>(w, w_wide != 0, at, f);
+            if constexpr (INT4) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) wild |= f[j] != f[j];
+            }
+        }
         uint32_t again = 0;       // tokens whose row of this lane needs 64 bits
         for (int32_t t0 = 0; t0 < tokens; t0 += kAhead) {
             uint4 raw[kAhead];
@@ -488,7 +498,7 @@ __global__ void __launch_bounds__(kRowThreads, 4) rotate_kernel(const __grid_con
                 } else if constexpr (INT4) {
                     uint32_t byte;
                     bool doubt = false;
-                    const bool odd = !(sum < INFINITY);
+                    const bool odd = wild || !(sum < INFINITY);
                     const float unit = p.unit[kind - 1], inv_unit = p.inv_unit[kind - 1];
                     const uint32_t word = kind == 1 ? encode<true>(y, err, unit, inv_unit, odd, &byte, &doubt)
                                                     : encode<false>(y, err, unit, inv_unit, odd, &byte, &doubt);

@@ -1,6 +1,6 @@
 """Writes into 4-bit caches at the ends of their range on the GPU: numbers beyond
-the scales, of either sign and at every unit, against the formula in 64 bits, byte
-by byte."""
+the scales, of either sign and at every unit, and weights and frequencies that are
+no numbers, against the formula in 64 bits, byte by byte."""
 import math
 
 import numpy as np
@@ -77,3 +77,25 @@ def test_signs_of_the_largest(dev, dtype, dim, log2_unit):
         with np.errstate(invalid="ignore"):
             turned, _ = ref.turned(y, positions.numpy(), freqs.numpy(), pairs, None, 0.0)
         assert np.array_equal(got, rows_of(turned, y, unit, unit))
+
+
+@pytest.mark.parametrize("pairs", [False, True])
+def test_weights_and_frequencies_that_are_no_numbers(dev, pairs):
+    """A NaN is stored as 0, an infinity as the largest code, wherever it comes from."""
+    dim = 64
+    g = torch.Generator().manual_seed(5)
+    k = torch.randn((5, 3, dim), generator=g).to(BF)
+    w = torch.ones(dim)
+    w[1], w[20], w[40], w[63] = math.nan, math.inf, -math.inf, 3e38
+    freqs = torch.tensor([1.0, math.nan, 0.5, math.inf] + [0.1] * 4)
+    positions = torch.tensor([0, 1, 7, -2, 900], dtype=torch.int32)
+    kd, slots = k.to(dev), torch.arange(5, dtype=torch.int32, device=dev)
+    for weight, inv in ((w, None), (None, freqs), (w, freqs)):
+        cache = torch.zeros((5, 3, gb.int4_row_bytes(dim)), dtype=torch.uint8, device=dev)
+        gb.rotate_and_cache_int4(kd, kd, kd, positions.to(dev), slots, None if inv is None else inv.to(dev), cache,
+                                 k_weight=None if weight is None else weight.to(dev), interleaved=pairs)
+        with np.errstate(invalid="ignore", over="ignore"):
+            y, _ = ref.turned(k.double().numpy(), positions.numpy(), None if inv is None else inv.numpy(), pairs,
+                              None if weight is None else weight.double().numpy(), float(np.float32(1e-6)))
+        want = ref.row_bytes(*ref.codes(y), *ref.codes(k.double().numpy()))
+        assert np.array_equal(cache.cpu().numpy()[..., used_bytes(dim)], want[..., used_bytes(dim)])
