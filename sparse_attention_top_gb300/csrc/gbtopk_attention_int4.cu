@@ -54,7 +54,7 @@ constexpr int kThreads4 = 640;
 constexpr int kMaxStages = 12;
 constexpr int kMasks = 16;          // tiles whose validity bits are kept: the ring's and the two that are decoded
 constexpr float kRise = 8.f;        // rise of a score over its row's reference (base 2) that moves it
-constexpr float kFar = 0x1p100f;
+constexpr float kFar = FLT_MAX;     // a score's distance from a reference that is not there: above kRise for every number
 constexpr int kKeyWarp = 4, kValueWarp = 8, kCopyWarp = 12, kCopyWarps = 7, kIssueWarp = 19;
 static_assert(kMaxStages <= 2 * kCopyWarps, "two stages a copy warp at most");
 
@@ -270,7 +270,12 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
                     }
                 }
                 const bool all = __all_sync(~0u, sees == kEvery);
-                // scores of the thread's position less their rows' references, base 2
+                // Scores of the thread's position less their rows' references, base 2.  The
+                // product is rounded before the difference, as the reference was: fused, the
+                // difference of the largest would be what its rounding left off, up to 2^-24 of
+                // it, and a power beyond 32 bits from 2^31 on.  (Sums one at a time: a packed
+                // product and a packed sum do get fused.  64 x 4 drafts 134 -> 135 us, 64 rows a
+                // head over 131072 positions 224 -> 226.)
                 float d[R];
                 auto scores = [&]() {
 #pragma unroll
@@ -286,10 +291,14 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
                             const float4 m = sh.less_m[(c + k) / 4];
                             const float mm[4] = {m.x, m.y, m.z, m.w};
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                float v = __uint_as_float(x[k + j]);
-                                if constexpr (F16) v += __uint_as_float(CH == 8 ? x[(k + j + 8) & 15] : y[k + j]);
-                                d[c + k + j] = fmaf(v, pp.k_mul, mm[j]);
+                            for (int j = 0; j < 4; j += 2) {
+                                float2 v = make_float2(__uint_as_float(x[k + j]), __uint_as_float(x[k + j + 1]));
+                                if constexpr (F16 && CH == 8) add2(v, __uint_as_float(x[(k + j + 8) & 15]), __uint_as_float(x[(k + j + 9) & 15]));
+                                if constexpr (F16 && CH == 16) add2(v, __uint_as_float(y[k + j]), __uint_as_float(y[k + j + 1]));
+                                v = mul2(v.x, v.y, pp.k_mul);
+                                v = make_float2(__fadd_rn(v.x, mm[j]), __fadd_rn(v.y, mm[j + 1]));
+                                d[c + k + j] = v.x;
+                                d[c + k + j + 1] = v.y;
                             }
                         }
                         if (!all) {
@@ -317,8 +326,9 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
                         break;
                     }
                     tc_fence_after();
+                    // (the new reference is a score itself, no sum of differences)
                     const float before = at < R ? less_m[at] : 0.f;
-                    if (at < R && before == kFar) less_m[at] = 0.f;
+                    if (at < R) less_m[at] = 0.f;
                     softmax_sync();
                     scores();
 #pragma unroll
@@ -332,16 +342,15 @@ __global__ void __launch_bounds__(kThreads4, 1) attention_int4_kernel(const __gr
                     }
                     softmax_sync();
                     if (at < R) {
-                        float f = 1.f;
+                        float f = 1.f, now = before;
                         if (at < here) {
-                            const float rise = fmaxf(fmaxf(sh.part[0][at], sh.part[1][at]), fmaxf(sh.part[2][at], sh.part[3][at]));
-                            if (before == kFar) {
-                                less_m[at] = rise > -INFINITY ? -rise : kFar;
-                            } else if (rise > kRise) {
-                                less_m[at] = before - rise;
-                                f = exp2_fast((before - rise) - before);
+                            const float best = fmaxf(fmaxf(sh.part[0][at], sh.part[1][at]), fmaxf(sh.part[2][at], sh.part[3][at]));
+                            if (best + before > kRise) {
+                                now = -best;
+                                if (before != kFar) f = exp2_fast(now - before);
                             }
                         }
+                        less_m[at] = now;
                         scale[at] = f;
                     }
                     softmax_sync();

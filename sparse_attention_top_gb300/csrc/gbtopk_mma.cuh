@@ -200,13 +200,20 @@ __device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t *v) {
         : "memory");
 }
 
-// Two products and sums, two sums, as one instruction.
+// Two products and sums, two products, two sums, as one instruction.
 __device__ __forceinline__ float2 fma2(float x, float y, float k, float n) {   // k x + n, k y + n
     float2 r;
     asm("{\n .reg .b64 v, k, n;\n mov.b64 v, {%2, %3};\n mov.b64 k, {%4, %4};\n mov.b64 n, {%5, %5};\n"
         " fma.rn.f32x2 v, v, k, n;\n mov.b64 {%0, %1}, v;\n}"
         : "=f"(r.x), "=f"(r.y)
         : "f"(x), "f"(y), "f"(k), "f"(n));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float x, float y, float k) {   // k x, k y, rounded
+    float2 r;
+    asm("{\n .reg .b64 v, k;\n mov.b64 v, {%2, %3};\n mov.b64 k, {%4, %4};\n mul.rn.f32x2 v, v, k;\n mov.b64 {%0, %1}, v;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(x), "f"(y), "f"(k));
     return r;
 }
 __device__ __forceinline__ void add2(float2 &s, float x, float y) {
