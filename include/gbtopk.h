@@ -612,6 +612,7 @@ int gbtopk_cache_read_int4(const void *cache, int64_t slot_stride, int64_t head_
  * The greatest common divisor of the slot and head strides is at least a row (as
  * in every view of a contiguous tensor whose innermost axis is the row), and
  * divides the cache into at most 2^31 - 1 lines: GBTOPK_EUNSUPPORTED otherwise.
+ * So is a scale that with k_scale comes to more than 2^112.
  */
 int gbtopk_tree_attention_int4(const void *q, int dtype, int64_t num_rows, int64_t q_row_stride,
                                int64_t q_head_stride, int32_t q_heads, int32_t kv_heads,

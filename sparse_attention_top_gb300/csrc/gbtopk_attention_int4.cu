@@ -774,6 +774,9 @@ int attend_int4(Int4Params &pp, int dtype, const void *q, int64_t num_rows, int6
     if ((rc = check_rows(q, q_row_stride, q_head_stride, true)) != GBTOPK_OK) return rc;
     if ((rc = check_int4(cache, slot_stride, head_stride, p.pages.num_slots, head_dim)) != GBTOPK_OK) return rc;
     if (!int4_unit(k_scale) || !int4_unit(v_scale)) return GBTOPK_EINVAL;
+    // what a product of queries and keys' codes is multiplied by; a scale of 0 stays a product that ignores no mask
+    pp.k_mul = fmaxf(fabsf(scale) * (kLog2e * k_scale * kInt4Lift), FLT_MIN);
+    if (pp.k_mul > FLT_MAX) return GBTOPK_EUNSUPPORTED;
     if (!out) return GBTOPK_EINVAL;
     if (!aligned_to(out, 16) || !aligned_to(lse, 4)) return GBTOPK_EALIGN;
     if (!workspace || !aligned_to(workspace, 256) ||
@@ -801,7 +804,6 @@ int attend_int4(Int4Params &pp, int dtype, const void *q, int64_t num_rows, int6
     p.kv_heads = kv_heads;
     p.group = q_heads / kv_heads;
     p.dim = head_dim;
-    pp.k_mul = fmaxf(fabsf(scale) * kLog2e * k_scale * kInt4Lift, FLT_MIN);   // a scale of 0 stays a product that ignores no mask
     pp.v_mul = v_scale * kInt4Lift;
     p.negative = scale < 0.f;
     p.out = out;
