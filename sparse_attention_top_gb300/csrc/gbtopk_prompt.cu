@@ -39,6 +39,12 @@
 namespace gbtopk {
 namespace {
 
+// References up to which a score's product and its difference from the reference are
+// one operation.  The difference of the largest is then what the product's rounding
+// left off, up to 2^-24 of it: next to nothing here, and from 2^31 on a power beyond
+// 32 bits.  Tiles with a row beyond it take products and differences one by one, in a
+// loop of their own.  (All tiles so: 16 prompts 229 -> 237 us, the long one 607 -> 642.)
+constexpr float kFused = 0x1p20f;
 constexpr int kOddUnits = 8, kOddTiles = 4;   // units and their tiles whose marks are kept
 constexpr int kBuckets = 2048;
 
@@ -442,6 +448,7 @@ __global__ void __launch_bounds__(Prompt<DP>::kThreads, 1) prompt_kernel(const _
             }
             float m = -INFINITY, l = 0.f;
             uint32_t before = ~0u;   // the unit's latest job of this warpgroup
+            bool far = false;        // some row's reference is beyond kFused
             for (int32_t i = 0; i < deal.tiles; ++i, job += W) {
                 const uint32_t sb = job & 1;
                 ok = warp_wait(&sh.s_full[sb], (job >> 1) & 1, abort);
@@ -476,14 +483,19 @@ __global__ void __launch_bounds__(Prompt<DP>::kThreads, 1) prompt_kernel(const _
                         m = best - kLift<BF16>;
                     } else if (move) {
                         // a whole number k lower; m - k is rounded where it is the larger
-                        const float k = rintf(m + kLift<BF16> - best), to = m - k;
-                        const float g = exp2_whole(k) * exp2_fast(m - (to + k));
-                        if (k < 0.f || l * g <= kMostSum) {
+                        const float k = rintf(m + kLift<BF16> - best);
+                        float to = m - k, g = exp2_whole(k) * exp2_fast(m - (to + k));
+                        if (fabsf(best) > kFused) {      // (whose own steps are whole numbers or nearly)
+                            to = best - kLift<BF16>;
+                            g = exp2_fast(m - to);
+                        }
+                        if (to > m || l * g <= kMostSum) {
                             f = g;
                             l *= f;
                             m = to;
                         }
                     }
+                    if constexpr (DP == 64) far = __any_sync(~0u, fabsf(m) > kFused && m != -INFINITY);
                     if (__any_sync(~0u, f != 1.f)) {
                         // O is complete up to the row's last job
                         ok = warp_wait(&sh.pv_done[before & 1], (before >> 1) & 1, abort);
@@ -502,17 +514,38 @@ __global__ void __launch_bounds__(Prompt<DP>::kThreads, 1) prompt_kernel(const _
                 }
                 const float mm = m == -INFINITY ? 0.f : m;
                 float2 sum[2] = {};
+                // (at dimension 64 a vote a tile costs more than the flag does: 2 chunks over 16384
+                // keys 460 us, with the flag 443, without either 429; else less: one of 10007 tokens
+                // 606, 614, 607)
+                if (DP == 64 ? far : __any_sync(~0u, fabsf(mm) > kFused)) {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < KT; c0 += 16) {
+                        uint32_t z[16], y[8];
+                        tmem_load16(t_s + c0, z);
+                        tc_wait_ld();
 #pragma unroll
-                for (int c0 = 0; c0 < KT; c0 += 32) {
-                    uint32_t y[16];
-#pragma unroll
-                    for (int c = 0; c < 32; c += 2) {
-                        const float2 e = fma2(__uint_as_float(x[c0 + c]), __uint_as_float(x[c0 + c + 1]), p.c, -mm);
-                        const float a = exp2_fast(e.x), b = exp2_fast(e.y);
-                        add2(sum[c / 2 & 1], a, b);
-                        y[c / 2] = Half2<BF16>::down(a, b);
+                        for (int c = 0; c < 16; c += 2) {
+                            const int32_t seen = i < deal.whole ? KT : last - i * KT - c0;
+                            const float a = c > seen ? 0.f : exp2_fast(__fmul_rn(__uint_as_float(z[c]), p.c) - mm);
+                            const float b = c + 1 > seen ? 0.f : exp2_fast(__fmul_rn(__uint_as_float(z[c + 1]), p.c) - mm);
+                            add2(sum[c / 2 & 1], a, b);
+                            y[c / 2] = Half2<BF16>::down(a, b);
+                        }
+                        tmem_store8(t_s + c0 / 2, y);      // (over scores that have been read)
                     }
-                    tmem_store16(t_s + c0 / 2, y);
+                } else {
+#pragma unroll
+                    for (int c0 = 0; c0 < KT; c0 += 32) {
+                        uint32_t y[16];
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2) {
+                            const float2 e = fma2(__uint_as_float(x[c0 + c]), __uint_as_float(x[c0 + c + 1]), p.c, -mm);
+                            const float a = exp2_fast(e.x), b = exp2_fast(e.y);
+                            add2(sum[c / 2 & 1], a, b);
+                            y[c / 2] = Half2<BF16>::down(a, b);
+                        }
+                        tmem_store16(t_s + c0 / 2, y);
+                    }
                 }
                 l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
                 tc_wait_st();
@@ -550,7 +583,8 @@ __global__ void __launch_bounds__(Prompt<DP>::kThreads, 1) prompt_kernel(const _
                                 s = fmaf(qq.x, kk.x, fmaf(qq.y, kk.y, s));
                             }
                         }
-                        const float pr = sees ? exp2_fast((p.negative ? -s : s) * p.c - m) : 0.f;
+                        // (no larger than the softmax lets it be: s is another sum than its, of other roundings)
+                        const float pr = sees ? exp2_fast(fminf(__fmul_rn(p.negative ? -s : s, p.c) - m, kRescale + kLift<BF16>)) : 0.f;
                         __syncwarp();
 #pragma unroll 1
                         for (int c = 0; c < p.dim; c += 16) {

@@ -1,4 +1,5 @@
-"""Attention over 4-bit caches where scores are far from 0, on the GPU: next to such scores a probability is 1 or 0, so each row's output is the
+"""Attention over 4-bit caches and packed prompts where scores are far from 0, on
+the GPU: next to such scores a probability is 1 or 0, so each row's output is the
 mean of the values at its largest score.  The scores are products of whole
 numbers that 32 bits hold, times one factor: equal ones stay equal.
 
@@ -75,3 +76,28 @@ def test_int4_scores_far_from_zero(dev, dtype, factor, heads, next_n, dim, signs
         seen = pages[i, :lens[i] - next_n + t + 1].long().numpy()
         for h in range(heads):
             check(out[r, h], lse[r, h], (kv[seen, 0, 0] * float(q[r, h, 0]), scale * unit), vv[seen, 0], dtype, (r, h))
+
+
+@pytest.mark.parametrize("dtype", [BF, HF])
+@pytest.mark.parametrize("scale", [f for f, unit in FACTORS if unit == 1.0])
+@pytest.mark.parametrize("heads,kv,dim", [(4, 2, 64), (2, 2, 128), (3, 1, 256)])
+@pytest.mark.parametrize("signs", ["all below", "both"])
+def test_prompt_scores_far_from_zero(dev, dtype, scale, heads, kv, dim, signs):
+    g = torch.Generator().manual_seed(dim + heads)
+    lens = [400, 1, 130]
+    n = sum(lens)
+    k = torch.zeros((n, kv, dim))
+    k[:, :, 0] = torch.randint(1 if signs == "all below" else -7, 8, (n, kv), generator=g).float()
+    v = torch.randn((n, kv, dim), generator=g).to(dtype)
+    q = torch.randn((n, heads, dim), generator=g) * 0
+    q[:, :, 0] = torch.randint(1, 4, (n, heads), generator=g) * (-1.0 if (scale > 0) == (signs == "all below") else 1.0)
+    cu = np.cumsum([0] + lens)
+    out, lse = gb.prompt_attention(q.to(dtype).to(dev), k.to(dtype).to(dev), v.to(dev), torch.from_numpy(cu).to(torch.int32).to(dev),
+                                   scale=scale, return_lse=True)
+    out, lse, kk, vv = out.cpu().double().numpy(), lse.cpu().double().numpy(), k.double().numpy(), v.double().numpy()
+    for i in range(3):
+        for t in list(range(0, lens[i], 37)) + [lens[i] - 1]:
+            r, seen = cu[i] + t, slice(cu[i], cu[i] + t + 1)
+            for h in range(heads):
+                c = h // (heads // kv)
+                check(out[r, h], lse[r, h], (kk[seen, c, 0] * float(q[r, h, 0]), scale), vv[seen, c], dtype, (i, t, h))
