@@ -310,7 +310,8 @@ def gbtopk_prompt_workspace_bytes(num_rows: int, num_seqs: int, q_heads: int, kv
     return int(_lib().gbtopk_prompt_workspace_bytes(num_rows, num_seqs, q_heads, kv_heads, head_dim))
 
 
-_prompt_bytes = functools.lru_cache(maxsize=None)(gbtopk_prompt_workspace_bytes)
+# (packed prompts have another number of rows in nearly every call)
+_prompt_bytes = functools.lru_cache(maxsize=256)(gbtopk_prompt_workspace_bytes)
 
 
 def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor,
