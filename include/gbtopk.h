@@ -643,8 +643,9 @@ int gbtopk_selected_attention_int4(const void *q, int dtype, int64_t num_rows, i
  *
  * Keys and values that a row does not see do not reach it, whatever they hold:
  * infinities and NaN of later tokens and of other sequences are left out.
- * Offsets are clamped to 0 .. num_rows (num_keys), a sequence's end to its start
- * at least; sequences that share query rows leave either's result there.  Rows
+ * Offsets ascend, from 0 to num_rows (num_keys) at most.  Others are clamped to
+ * that range and a sequence's end to its start, so that nothing is read or
+ * written out of place, but which rows are then answered is not defined.  Rows
  * of out and lse that no sequence has are left as they were.  Arithmetic as for
  * gbtopk_tree_attention (in fp16 the tiles are 128 consecutive keys, 64 above
  * head_dim 128).

@@ -322,8 +322,8 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     cu_seqlens[i + 1]`` of ``q`` [rows, q_heads, head_dim] over the keys and
     values of the same offsets, or of ``cu_seqlens_k``, aligned at their ends
     (a chunk of a prompt behind its earlier context; rows that see nothing are
-    zero with ``lse`` -inf).  int32 offsets, on the device: a captured call
-    follows them.  Rows behind the last sequence are left as they were in
+    zero with ``lse`` -inf).  int32 offsets that ascend, on the device: a
+    captured call follows them.  Rows behind the last sequence are left as they were in
     ``out`` and ``lse`` (undefined where those are made here).  Everything else
     as for ``tree_attention``."""
     rows, heads, kv, dim = _heads(q, k, v, False)
