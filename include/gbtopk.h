@@ -333,6 +333,9 @@ int gbtopk_varlen_static_ws(const void *logits, int dtype, int64_t num_rows, int
  * In fp16 the positions of a tile (128 consecutive ones, 64 above dimension
  * 128) have one scale: probabilities below 2^-13 of the tile's largest (2^-20
  * where that is the row's largest) are off by up to 2^-24 (2^-31) of it.
+ * Scores of 2^26 (fp16) or 2^31 (bf16) and more, in base 2 and of either sign,
+ * whose own rounding is then more than a power can hold, give NaN or zeros here
+ * (not in the calls over 4-bit caches and over prompts).
  *
  *  q            device [num_rows, q_heads, head_dim], inner stride 1, row and
  *               head strides multiples of 8, 16-byte aligned.
@@ -576,7 +579,9 @@ int gbtopk_rotate_and_cache(const void *q, int dtype, int64_t num_tokens, int64_
  * gbtopk_rotate_and_cache_int4 — the same into a 4-bit cache (head_dim a
  * multiple of 16; strides in bytes).  The codes are those of the unrounded
  * keys: where 32-bit arithmetic cannot tell on which side of a border an
- * element lies, the row is computed again in 64 bits.
+ * element lies, the row is computed again in 64 bits.  Any strides that are
+ * multiples of 16 will do here and for gbtopk_cache_read_int4; the attention
+ * calls below ask for more.
  */
 int gbtopk_rotate_and_cache_int4(const void *q, int dtype, int64_t num_tokens, int64_t q_row_stride,
                                  int64_t q_head_stride, const void *k, int64_t k_row_stride,

@@ -31,9 +31,9 @@
 // tiles) over the same positions at once: a 128-byte line of the cache holds parts
 // of two heads' rows, which are then read from memory together.
 //
-// Measured: 64 requests x 4 drafts, 1..8192 positions of 8 heads of 128, fp16: 136
+// Measured: 64 requests x 4 drafts, 1..8192 positions of 8 heads of 128, fp16: 132
 // us, the 300 MB of the cache read once (45 us at the copy rate); 4 requests x 8
-// drafts over 131072 positions of 4 heads, 64 rows a head, bf16: 223 us (45).  Bound by the roles'
+// drafts over 131072 positions of 4 heads, 64 rows a head, bf16: 224 us (45).  Bound by the roles'
 // own instructions: a tile of 128 positions takes about 2400 cycles, in which the
 // ALU pipes are busy for 1100, the values' decoding, the issue of products and the
 // softmax each for most of it.

@@ -15,7 +15,7 @@
 // Units are sorted by their number of key tiles (a counting sort by one block,
 // in front of the kernel, 4.8 us) and dealt out to the persistent blocks in snake
 // order, longest first: equal shares without a counter that blocks would race for
-// (16 prompts 230 us, shortest first 260; one of 10007 tokens 585, 674).
+// (16 prompts 229 us a call, shortest first 256; one of 10007 tokens 605, 672).
 //
 // A block: two warpgroups of softmax and output (a row a thread), one warp that
 // issues products, one that has tiles copied by tensor maps, one that cleans the
@@ -24,11 +24,11 @@
 // not see them); the softmax warps add the latter to the rows that do, at the
 // unit's end.
 //
-// Measured, 32 over 8 heads of 128, bf16: one prompt of 10007 tokens 611 us, 1342
-// TFLOP/s (71% of the burst rate; the products' own issue would take 547 us); 16
-// prompts up to 2048 tokens 230 us; 2 chunks up to 2048 tokens over 16384 keys of
-// 64, 32 over 4 heads, 432 us: at 64 columns a product's issue costs as much as at
-// 128, 375 us of them.  Bound by the tensor pipe, and where units are short by their
+// Measured a call, 32 over 8 heads of 128, bf16: one prompt of 10007 tokens 604 us
+// (the kernel alone 584), 1358 TFLOP/s (72% of the burst rate; the products' own
+// issue would take 547 us); 16 prompts up to 2048 tokens 228 us; 2 chunks up to 2048
+// tokens over 16384 keys of 64, 32 over 4 heads, 443 us: at 64 columns a product's
+// issue costs as much as at 128, 375 us of them.  Bound by the tensor pipe, and where units are short by their
 // starts and ends and the diagonal's masked halves.
 #include <cfloat>
 #include <cmath>
@@ -671,7 +671,7 @@ int launch_prompt(const PromptParams &p, int sms, cudaStream_t s) {
 }
 
 // Query heads of a unit: the largest power of two up to 128 that divides the group
-// (groups of 4, 16 prompts: 230 us, a head a unit 328; one of 10007 tokens 585, 662).
+// (groups of 4, 16 prompts: 229 us a call, a head a unit 330; one of 10007 tokens 605, 668).
 int log2_pack(int32_t group) {
     int shift = 0;
     while (shift < 7 && group % (2 << shift) == 0) ++shift;

@@ -18,10 +18,11 @@
 // order of sums, and two builds agree bit for bit.
 //
 // Bound by the bytes read and written: 16,001 tokens of 32 + 2 x 8 heads of 128
-// move 393 MB in 75 us (77% of the copy rate; the angles, worked out in 64 bits
+// move 393 MB in 77 us (75% of the copy rate; the angles, worked out in 64 bits
 // once a token, and short rows take the rest).  Into 4 bits the codes bind: 8,192
-// tokens of such heads 100 us, of which the bytes are 26; 32,769 slots read back
-// 36 us (25).
+// tokens of such heads 102 us on the GPU, of which the bytes are 26 and the rows
+// in doubt 23; 32,769 slots read back 36 us (25), a word and a scale byte a thread
+// and so two loads for 16 bytes out.
 #include <cfloat>
 #include <cmath>
 

@@ -189,7 +189,8 @@ def rotate_and_cache_int4(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, pos
                           q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
                           eps: float = 1e-6, interleaved: bool = False, k_scale: float = 1.0, v_scale: float = 1.0,
                           q_out: Optional[torch.Tensor] = None) -> torch.Tensor:
-    """``rotate_and_cache`` into a 4-bit cache (``head_dim`` a multiple of 16).
+    """``rotate_and_cache`` into a 4-bit cache (``head_dim`` a multiple of 16;
+    attention over it wants rows on lines of one pitch, see the module).
     ``k_scale`` / ``v_scale``: powers of two, the unit of the cache's scales
     (whose own range, 2^-9 to 448, as a rule needs no other than 1)."""
     args, q_out, kv, dim = _tokens(q, k, v, positions, slots, inv_freq, q_weight, k_weight, eps, interleaved, q_out)
